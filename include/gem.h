@@ -68,6 +68,8 @@ typedef enum gem_status {
 /* Device-side flag bits. */
 #define GEM_DEVFLAG_POS_RANGE 1 /* pos[b] < 0, or pos[b] >= cache_cap for full attention */
 #define GEM_DEVFLAG_TIMEOUT 2   /* a bounded wait on an asynchronous copy gave up */
+#define GEM_DEVFLAG_PAGE_RANGE 4 /* a page or slot index outside the pool, or ring counters apart */
+#define GEM_DEVFLAG_NO_ROOM 8   /* gem_kv_block_tables refused a request: lengths, tokens or pages */
 
 /* Static description of a status code. */
 GEM_API const char *gem_status_string(int status);
@@ -385,6 +387,137 @@ GEM_API gem_status gem_gqa_decode_attn_noalloc(const float *q, int64_t ldq,
                                                int64_t cache_cap, const int32_t *pos, int window,
                                                float scale, float *out, int64_t ldo,
                                                int32_t *status, void *stream);
+
+/*
+ * The paged 4-bit KV cache: gem_kv_block_tables, gem_qknorm_mrope, gem_kv4_append,
+ * gem_kv4_gather and gem_kv4_attn.  The pages have no counterpart of these calls; they are the
+ * form of [GELO] 02/05's cached attention for many requests whose caches share one pool, each
+ * holding pages of it, with K and V in the 4-bit blocks of the weights (Q4_0, [GEM]).
+ * A serving step of one layer: tables once per step; then per layer the QKV projection,
+ * gem_qknorm_mrope, gem_kv4_append, gem_kv4_attn, the O projection.
+ *
+ * Pool: n_pages pages of gem_kv4_page_bytes(n_kv, d, page) = 1.125 * page * n_kv * d bytes each,
+ * 16-byte aligned; one pool per layer.  A page holds `page` tokens (16, 32, 64, 128 or 256) of
+ * every KV head: [n_kv][page / 16] tiles.  A tile is 16 tokens of one head, 18 * d bytes:
+ *     K codes [d / 32][16 tokens][16 bytes], V codes likewise,
+ *     K scales [d / 32][16 tokens] binary16, V scales likewise.
+ * 16 bytes of codes are 32 consecutive values of a row in the nibble order of a Q4_0 block (byte
+ * j: element j low, element j + 16 high); value = (code - 8) * scale.  A token's slot is
+ * page_index * page + its position mod page; n_pages * page < 2^31.  gem_kv4_page_bytes is 0 for
+ * sizes that the calls reject.
+ */
+GEM_API size_t gem_kv4_page_bytes(int n_kv, int d, int page);
+
+/*
+ * Block tables and slot maps from request lengths, on the device: pages for the new tokens of a
+ * batch of requests, and the slot, position and request of every token.
+ *   cached  [B] int32: tokens already cached;  fresh [B] int32: new tokens of this step (>= 0), or
+ *           -1 where the request has ended and gives its pages back.
+ *   table   [B][max_pages] int32 in/out: request b's pages; the first ceil(cached / page) are its
+ *           own on entry.
+ *   ring    [n_pages] int32 in/out: free page indices, a ring; the free ones are at
+ *           (ring_in[0] + i) mod n_pages, i < ring_in[1] - ring_in[0] (int64 counters that only
+ *           grow; ring_in[1] - ring_in[0] in 0..n_pages).  ring_out [2] receives the new counters.
+ *   Requests are served in order of b.  Request b is taken when
+ *     0 <= cached, -1 <= fresh, cached + max(fresh, 0) <= max_pages * page, and
+ *     fresh == 0, or the new tokens of the requests up to b that pass the line above <= T_cap, and
+ *     it needs no new page, or the pages needed by the requests up to b that pass the lines above
+ *     <= the free pages, and
+ *     for an ended request, the pages given back by the ended requests up to b fit the ring as it
+ *     was on entry (n_pages less the free ones).
+ *   A taken request gets its new pages from the head of the ring in order and kv_len = cached +
+ *   fresh; an ended one puts its pages, in order, at the tail (they are handed out by later calls)
+ *   and gets kv_len = 0; a refused one keeps its pages, gets kv_len = cached and no tokens, and
+ *   sets GEM_DEVFLAG_NO_ROOM.  Counters that are out of range set GEM_DEVFLAG_PAGE_RANGE, and the
+ *   ring counts as having no free pages and no room.
+ *   cu_tokens [B + 1] int32: tokens before request b; slot, pos, seq [T_cap] int32: slot, position
+ *           and request of token t, all -1 for t >= cu_tokens[B].
+ *   B in 0..4096, else GEM_ERR_UNSUPPORTED_SHAPE.  Outputs must not overlap inputs (ring_out is
+ *   not ring_in, kv_len is not cached): a step takes the last one's outputs and writes the others.
+ *   Deterministic.
+ */
+GEM_API gem_status gem_kv_block_tables(const int32_t *cached, const int32_t *fresh, int B, int page,
+                                       int32_t *table, int64_t max_pages, int32_t *ring,
+                                       int64_t n_pages, const int64_t *ring_in, int64_t *ring_out,
+                                       int32_t *kv_len, int32_t *cu_tokens, int32_t *slot,
+                                       int32_t *pos, int32_t *seq, int64_t T_cap, int32_t *status,
+                                       void *stream);
+
+/*
+ * Per-head QK-norm and RoPE of T tokens, with one or several position axes (text: one; images and
+ * video: time, height, width).  Same norm, pairing and frequencies as gem_rmsnorm_qknorm_rope:
+ *   y = x / sqrt(mean x^2 + eps) * gamma (gamma NULL: y = x), R = 2 * (sum of sections),
+ *   pair (i, i + R/2), i < R/2, rotated by pos[axis(i)][t] * theta^(-2i/R); dims from R on kept.
+ *   qkv      [T][ldqkv] fp32: Q heads, then K heads (what follows them is not touched).
+ *   out      [T][ldo] fp32, the rotated Q and K heads in the same columns; may be qkv itself with
+ *            ldo == ldqkv (in place), else must not overlap it.
+ *   pos      [n_axes][ldpos] int32 device, n_axes 1..4.  A row whose first position is -1 is
+ *            padding and is skipped; any other negative position sets GEM_DEVFLAG_POS_RANGE and
+ *            skips its row.
+ *   sections HOST [n_axes]: frequencies of each axis, 2 <= R <= d.
+ *   interleaved 0: the first sections[0] frequencies follow axis 0, the next sections[1] axis 1, ...
+ *            1: axis a >= 1 takes i = a, a + n_axes, ... (sections[a] of them, which must lie below
+ *            R/2: GEM_ERR_INVALID_ARG), axis 0 the rest.
+ *   d        even, 2..512.  The angle is reduced exactly (64-bit fixed point turns).
+ */
+GEM_API gem_status gem_qknorm_mrope(const float *qkv, int64_t ldqkv, int64_t T, int n_q, int n_kv,
+                                    int d, const float *gamma_q, const float *gamma_k, float eps,
+                                    const int32_t *pos, int64_t ldpos, int n_axes,
+                                    const int32_t *sections, int interleaved, float theta, float *out,
+                                    int64_t ldo, int32_t *status, void *stream);
+
+/*
+ * Append K and V rows to the pool, quantised: row t into slot[t].
+ *   k, v   [T][ldk], [T][ldv] fp32: n_kv heads of d (rotated K; column ranges of a QKV row do).
+ *   Block of 32: m = its value of largest magnitude (the first such), scale = binary16(m / -8)
+ *   (nearest even, held to +-65504), code = min(8 + rint(x / scale), 15) with ties to even, decided
+ *   exactly; scale 0: code 8.  A block with a NaN or an infinity gets a NaN scale.
+ *   slot   [T] int32, each slot at most once (a slot named twice is left with parts of either
+ *          row); -1: the row is skipped; any other value outside the pool sets
+ *          GEM_DEVFLAG_PAGE_RANGE and skips the row.
+ *   d 64, 128, 256 or 512.  Other tokens of the pages are left as they were.
+ */
+GEM_API gem_status gem_kv4_append(const float *k, int64_t ldk, const float *v, int64_t ldv, int64_t T,
+                                  int n_kv, int d, const int32_t *slot, void *pool, int64_t n_pages,
+                                  int page, int32_t *status, void *stream);
+
+/*
+ * Read rows of the pool back as fp32 values: the inverse of gem_kv4_append (k or v may be NULL).
+ * Slots may repeat.  A row whose slot is -1 is left as it was; any other slot outside the pool sets
+ * GEM_DEVFLAG_PAGE_RANGE and leaves its row.
+ */
+GEM_API gem_status gem_kv4_gather(const void *pool, int64_t n_pages, int page, int n_kv, int d,
+                                  const int32_t *slot, int64_t T, float *k, int64_t ldk, float *v,
+                                  int64_t ldv, int32_t *status, void *stream);
+
+/*
+ * Grouped-query attention over the paged 4-bit cache, for one or more new tokens per request.
+ *   Request b has n = cu_tokens[b + 1] - cu_tokens[b] query rows, from row cu_tokens[b] on; row i
+ *   stands at p = kv_len[b] - n + i and attends positions max(0, p - window + 1) .. p (window 0: all
+ *   of 0 .. p), which the pool must already hold:
+ *     out[t][h*d + e] = sum_j softmax_j(scale * q_h . K[j]) * V[j][e],  KV head h / (n_q / n_kv).
+ *   q      [T][ldq] fp32, 16-byte aligned, ldq % 4 == 0;  out [T][ldo] fp32.  Rows from
+ *          cu_tokens[B] on are neither read nor written.
+ *   table  [B][max_pages] int32; entries from ceil(kv_len / page) on are not read, nor those that
+ *          lie before every row's window.
+ *   d 64, 128, 256 or 512; n_q % n_kv == 0, n_q / n_kv <= 8; B in 0..4096.
+ *   Device checks: cu_tokens out of order or beyond T, kv_len[b] < n or beyond max_pages * page set
+ *   GEM_DEVFLAG_POS_RANGE and leave the request's rows as they were; a table entry outside
+ *   [0, n_pages) sets GEM_DEVFLAG_PAGE_RANGE and its positions count as masked (a row with no
+ *   position left is 0).
+ *   workspace  gem_kv4_attn_workspace(T, B, n_q, n_kv, d) bytes, 256-byte aligned, no
+ *          initialisation; calls that can run at the same time need one each.
+ *   Accumulation is fp32: q and the probabilities enter the tensor cores as binary16 hi + lo pairs
+ *   under power-of-two scales (about 22 bits), the codes exactly.  Deterministic: the split of the
+ *   range depends on the lengths, the shape and the device, and partial results are merged in order.
+ */
+GEM_API size_t gem_kv4_attn_workspace(int64_t T, int B, int n_q, int n_kv, int d);
+GEM_API gem_status gem_kv4_attn(const float *q, int64_t ldq, int64_t T, const int32_t *cu_tokens,
+                                const int32_t *kv_len, int B, int n_q, int n_kv, int d,
+                                const int32_t *table, int64_t max_pages, const void *pool,
+                                int64_t n_pages, int page, int window, float scale, float *out,
+                                int64_t ldo, void *workspace, size_t ws_bytes, int32_t *status,
+                                void *stream);
 
 /*
  * Gated FFN activation  [GELO] 04/05 (Qwen3 SwiGLU; Gemma gelu_pytorch_tanh).

@@ -21,10 +21,13 @@ ACT_SILU = 0
 ACT_GELU_TANH = 1
 DEVFLAG_POS_RANGE = 1
 DEVFLAG_TIMEOUT = 2
+DEVFLAG_PAGE_RANGE = 4
+DEVFLAG_NO_ROOM = 8
 
 __all__ = ["GemError", "q4_0_gemv", "q4_0_gemv_workspace", "q4_0_gemv_fused", "q8_0_gemv", "argmax", "argmax_workspace", "rmsnorm", "rmsnorm_qknorm_rope", "gqa_decode_attn",
            "gqa_decode_attn_workspace", "gqa_decode_attn_fused", "swiglu", "decode_layer", "decode_layer_workspace",
-           "DeviceLayer", "device_status", "status_from_flags", "set_wait_limit",
+           "kv4_page_bytes", "kv_block_tables", "qknorm_mrope", "kv4_append", "kv4_gather", "kv4_attn",
+           "kv4_attn_workspace", "DeviceLayer", "device_status", "status_from_flags", "set_wait_limit",
            "set_test_injection", "LayerDesc"]
 
 
@@ -381,6 +384,163 @@ def swiglu(gate: torch.Tensor, up: torch.Tensor, act: int, out: torch.Tensor,
     st = lib.gem_swiglu(_dev(gate, torch.float32, "gate"), _dev(up, torch.float32, "up"), B,
                         gate.shape[-1], act, _dev(out, torch.float32, "out"), _stream(stream))
     _check(st, "gem_swiglu")
+    return out
+
+
+# ---- paged 4-bit KV cache -------------------------------------------------------------------
+
+
+def _here(t: torch.Tensor, dtype, name: str, dim: int, device: int):
+    """Pointer of a contiguous tensor of `dim` dimensions on the current device."""
+    if not t.is_cuda or t.get_device() != device:
+        raise ValueError("%s must be on the current CUDA device" % name)
+    if t.dtype != dtype or t.dim() != dim or not t.is_contiguous():
+        raise ValueError("%s must be contiguous %s with %d dimension(s), got %s %s" % (
+            name, dtype, dim, t.dtype, tuple(t.shape)))
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, cols: int, name: str, device: int):
+    """(pointer, row stride) of an fp32 [rows, >= cols] tensor whose rows are contiguous; a column
+    range of a wider tensor will do."""
+    if not t.is_cuda or t.get_device() != device:
+        raise ValueError("%s must be on the current CUDA device" % name)
+    if t.dtype != torch.float32 or t.dim() != 2 or t.shape[1] < cols or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("%s must be fp32 [rows, >= %d] with contiguous rows, got %s %s strides %s" % (
+            name, cols, t.dtype, tuple(t.shape), t.stride()))
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 3) // 4 * 4)
+
+
+def _status(status: torch.Tensor | None, device: int):
+    return None if status is None else _here(status, torch.int32, "status", 1, device)
+
+
+def _pool(pool: torch.Tensor, n_kv: int, d: int, page: int, device: int):
+    """(pointer, pages) of a pool [n_pages, kv4_page_bytes(n_kv, d, page)]."""
+    ptr = _here(pool, torch.uint8, "pool", 2, device)
+    need = lib.gem_kv4_page_bytes(n_kv, d, page)
+    if need and pool.shape[1] != need:
+        raise ValueError("pool must be [n_pages, %d] for %d KV heads of %d and pages of %d, got %s" % (
+            need, n_kv, d, page, tuple(pool.shape)))
+    return ptr, pool.shape[0]
+
+
+def kv4_page_bytes(n_kv: int, d: int, page: int) -> int:
+    """Bytes of one page of the 4-bit KV cache; 0 for sizes that the calls reject."""
+    return int(lib.gem_kv4_page_bytes(n_kv, d, page))
+
+
+def kv_block_tables(cached: torch.Tensor, fresh: torch.Tensor, page: int, table: torch.Tensor, ring: torch.Tensor,
+                    ring_in: torch.Tensor, ring_out: torch.Tensor, kv_len: torch.Tensor, cu_tokens: torch.Tensor,
+                    slot: torch.Tensor, pos: torch.Tensor, seq: torch.Tensor, status: torch.Tensor | None = None,
+                    stream=None) -> None:
+    """Pages for the new tokens of B requests (or back from ended ones, fresh -1), and every token's
+    slot, position and request.  int32 tensors cached, fresh, kv_len [B], cu_tokens [B + 1],
+    table [B, max_pages], ring [n_pages], slot, pos, seq [T_cap]; int64 ring_in, ring_out [2]."""
+    dev = torch.cuda.current_device()
+    i32, i64 = torch.int32, torch.int64
+    B, T = cached.shape[0], slot.shape[0]
+    if fresh.shape[0] != B or kv_len.shape[0] != B or cu_tokens.shape[0] != B + 1 or table.shape[0] != B:
+        raise ValueError("fresh and kv_len must be [B=%d], cu_tokens [B + 1] and table [B, max_pages]" % B)
+    if pos.shape[0] != T or seq.shape[0] != T:
+        raise ValueError("slot, pos and seq must have the same length")
+    if ring_in.numel() != 2 or ring_out.numel() != 2:
+        raise ValueError("ring_in and ring_out must hold two counters")
+    st = lib.gem_kv_block_tables(
+        _here(cached, i32, "cached", 1, dev), _here(fresh, i32, "fresh", 1, dev), B, page,
+        _here(table, i32, "table", 2, dev), table.shape[1], _here(ring, i32, "ring", 1, dev), ring.shape[0],
+        _here(ring_in, i64, "ring_in", 1, dev), _here(ring_out, i64, "ring_out", 1, dev),
+        _here(kv_len, i32, "kv_len", 1, dev), _here(cu_tokens, i32, "cu_tokens", 1, dev),
+        _here(slot, i32, "slot", 1, dev), _here(pos, i32, "pos", 1, dev), _here(seq, i32, "seq", 1, dev), T,
+        _status(status, dev), _stream(stream))
+    _check(st, "gem_kv_block_tables")
+
+
+def qknorm_mrope(qkv: torch.Tensor, n_q: int, n_kv: int, d: int, gamma_q: torch.Tensor | None,
+                 gamma_k: torch.Tensor | None, eps: float, pos: torch.Tensor, sections, theta: float,
+                 out: torch.Tensor, interleaved: bool = False, status: torch.Tensor | None = None,
+                 stream=None) -> torch.Tensor:
+    """QK-norm and RoPE of the Q and K heads of T rows.  qkv, out: fp32 [T, >= (n_q + n_kv) * d] (out may
+    be qkv); pos int32 [n_axes, T]; sections: the number of frequencies of each axis (their sum is half
+    of the rotated dims); interleaved: the axes take turns along the frequencies."""
+    dev = torch.cuda.current_device()
+    T, cols = qkv.shape[0], (n_q + n_kv) * d
+    xp, ldx = _rows(qkv, cols, "qkv", dev)
+    op, ldo = _rows(out, cols, "out", dev)
+    if out.shape[0] != T or pos.dim() != 2 or pos.shape[1] != T or pos.shape[0] != len(sections):
+        raise ValueError("out must have T=%d rows and pos be [%d, T]" % (T, len(sections)))
+    gp = []
+    for name, g in (("gamma_q", gamma_q), ("gamma_k", gamma_k)):
+        gp.append(None if g is None else _here(g, torch.float32, name, 1, dev))
+        if g is not None and g.shape[0] != d:
+            raise ValueError("%s must be [d=%d]" % (name, d))
+    st = lib.gem_qknorm_mrope(xp, ldx, T, n_q, n_kv, d, gp[0], gp[1], eps, _here(pos, torch.int32, "pos", 2, dev), T,
+                              len(sections), (C.c_int32 * len(sections))(*sections), int(interleaved), theta, op,
+                              ldo, _status(status, dev), _stream(stream))
+    _check(st, "gem_qknorm_mrope")
+    return out
+
+
+def kv4_append(k: torch.Tensor, v: torch.Tensor, n_kv: int, d: int, slot: torch.Tensor, pool: torch.Tensor,
+               page: int, status: torch.Tensor | None = None, stream=None) -> None:
+    """Quantise the rows of k and v (fp32 [T, >= n_kv * d], columns of a wider tensor will do) into the
+    slots int32 [T] (-1: none) of pool (uint8 [n_pages, kv4_page_bytes(n_kv, d, page)])."""
+    dev = torch.cuda.current_device()
+    kp, ldk = _rows(k, n_kv * d, "k", dev)
+    vp, ldv = _rows(v, n_kv * d, "v", dev)
+    pp, n_pages = _pool(pool, n_kv, d, page, dev)
+    T = k.shape[0]
+    if v.shape[0] != T or slot.shape[0] != T:
+        raise ValueError("k, v and slot must have the same number of rows")
+    st = lib.gem_kv4_append(kp, ldk, vp, ldv, T, n_kv, d, _here(slot, torch.int32, "slot", 1, dev), pp, n_pages,
+                            page, _status(status, dev), _stream(stream))
+    _check(st, "gem_kv4_append")
+
+
+def kv4_gather(pool: torch.Tensor, page: int, n_kv: int, d: int, slot: torch.Tensor, k: torch.Tensor | None,
+               v: torch.Tensor | None, status: torch.Tensor | None = None, stream=None):
+    """Read the rows at the slots int32 [T] back into k and v (fp32 [T, >= n_kv * d], either may be None)."""
+    dev = torch.cuda.current_device()
+    pp, n_pages = _pool(pool, n_kv, d, page, dev)
+    T = slot.shape[0]
+    (kp, ldk), (vp, ldv) = ((None, 0) if x is None else _rows(x, n_kv * d, name, dev)
+                            for name, x in (("k", k), ("v", v)))
+    if any(x is not None and x.shape[0] != T for x in (k, v)):
+        raise ValueError("k and v must have one row for each slot")
+    st = lib.gem_kv4_gather(pp, n_pages, page, n_kv, d, _here(slot, torch.int32, "slot", 1, dev), T, kp, ldk, vp,
+                            ldv, _status(status, dev), _stream(stream))
+    _check(st, "gem_kv4_gather")
+    return k, v
+
+
+def kv4_attn_workspace(T: int, B: int, n_q: int, n_kv: int, d: int) -> int:
+    return int(lib.gem_kv4_attn_workspace(T, B, n_q, n_kv, d))
+
+
+def kv4_attn(q: torch.Tensor, n_q: int, n_kv: int, d: int, cu_tokens: torch.Tensor, kv_len: torch.Tensor,
+             table: torch.Tensor, pool: torch.Tensor, page: int, window: int, scale: float, out: torch.Tensor,
+             workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
+             stream=None) -> torch.Tensor:
+    """Attention of the rows of q (fp32 [T, >= n_q * d]) over the paged 4-bit cache: request b's rows are
+    cu_tokens[b] .. cu_tokens[b + 1] (int32 [B + 1]), the last positions of its kv_len[b] (int32 [B]);
+    table int32 [B, max_pages].  workspace: uint8, at least kv4_attn_workspace(...) bytes (allocated when
+    not given)."""
+    dev = torch.cuda.current_device()
+    qp, ldq = _rows(q, n_q * d, "q", dev)
+    op, ldo = _rows(out, n_q * d, "out", dev)
+    pp, n_pages = _pool(pool, n_kv, d, page, dev)
+    B, T = kv_len.shape[0], q.shape[0]
+    if cu_tokens.shape[0] != B + 1 or table.shape[0] != B or out.shape[0] != T:
+        raise ValueError("cu_tokens must be [B + 1], table [B=%d, max_pages] and out have T=%d rows" % (B, T))
+    if workspace is None:
+        need = lib.gem_kv4_attn_workspace(T, B, n_q, n_kv, d)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    st = lib.gem_kv4_attn(qp, ldq, T, _here(cu_tokens, torch.int32, "cu_tokens", 1, dev),
+                          _here(kv_len, torch.int32, "kv_len", 1, dev), B, n_q, n_kv, d,
+                          _here(table, torch.int32, "table", 2, dev), table.shape[1], pp, n_pages, page, window,
+                          scale, op, ldo, None if workspace is None else _here(workspace, torch.uint8, "workspace", 1, dev),
+                          0 if workspace is None else workspace.shape[0], _status(status, dev), _stream(stream))
+    _check(st, "gem_kv4_attn")
     return out
 
 

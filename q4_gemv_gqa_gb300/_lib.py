@@ -60,6 +60,15 @@ PROTOTYPES = {
                                           C.c_float, p, i64, p, C.c_size_t, p, p]),
     "gem_gqa_decode_attn_noalloc": (i32, [p, i64, p, p, i32, i32, i32, i32, i64, p, i32,
                                           C.c_float, p, i64, p, p]),
+    "gem_kv4_page_bytes": (C.c_size_t, [i32, i32, i32]),
+    "gem_kv_block_tables": (i32, [p, p, i32, i32, p, i64, p, i64, p, p, p, p, p, p, p, i64, p, p]),
+    "gem_qknorm_mrope": (i32, [p, i64, i64, i32, i32, i32, p, p, C.c_float, p, i64, i32, p, i32, C.c_float,
+                               p, i64, p, p]),
+    "gem_kv4_append": (i32, [p, i64, p, i64, i64, i32, i32, p, p, i64, i32, p, p]),
+    "gem_kv4_gather": (i32, [p, i64, i32, i32, i32, p, i64, p, i64, p, i64, p, p]),
+    "gem_kv4_attn_workspace": (C.c_size_t, [i64, i32, i32, i32, i32]),
+    "gem_kv4_attn": (i32, [p, i64, i64, p, p, i32, i32, i32, i32, p, i64, p, i64, i32, i32, C.c_float, p, i64,
+                           p, C.c_size_t, p, p]),
     "gem_swiglu": (i32, [p, p, i32, i64, i32, p, p]),
     "gem_decode_layer_workspace": (C.c_size_t, [C.POINTER(LayerDesc), i32, i64]),
     "gem_decode_layer": (i32, [C.POINTER(LayerDesc), i32, p, p, p, i64, p, p, C.c_size_t, p, p]),

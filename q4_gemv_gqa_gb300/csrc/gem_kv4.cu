@@ -1,0 +1,219 @@
+// gem_kv4.cu — rows into and out of the paged 4-bit KV cache: quantising append, gather.
+#include "gem_device.cuh"
+#include "gem_kv4.cuh"
+
+namespace gem {
+namespace kv4 {
+namespace {
+
+struct RowsParams {
+    const float *k, *v;      // append: the rows
+    float *ko, *vo;          // gather: the rows (nullable)
+    int64_t ldk, ldv, T;
+    const int32_t* slot;
+    uint8_t* pool;
+    int64_t n_slots;
+    int n_kv, d, nb;         // nb = d / 32
+    int lpage;               // log2 of the page size
+    int vec_k, vec_v;        // rows may be read or written 16 bytes at a time
+    int* status;
+};
+
+// Four threads hold one block of 32 values: thread u elements 4u .. 4u + 3 and 16 + 4u .. 16 + 4u + 3,
+// which are the low and the high nibbles of word u of the block's 16 bytes of codes.  The eight
+// blocks of a warp are eight consecutive tokens of one (K or V, head, block), so that the codes and
+// the scales of a prompt's tokens are written next to one another.
+struct Place {
+    int64_t t;
+    int which, head, blk, u;
+    uint8_t *code, *scale;   // nullptr: nothing to do for this row
+};
+
+__device__ __forceinline__ bool place_of(const RowsParams& P, int64_t gid, int* status, Place& o) {
+    o.u = static_cast<int>(gid & 3);
+    const int64_t g = gid >> 2;
+    const int per = 2 * P.n_kv * P.nb;
+    const int64_t rest = g >> 3;
+    const int part = static_cast<int>(rest % per);
+    o.t = (rest / per) * 8 + (g & 7);
+    if (o.t >= P.T) return false;
+    o.blk = part % P.nb;
+    o.head = part / P.nb % P.n_kv;
+    o.which = part / (P.nb * P.n_kv);
+    const int32_t s = P.slot[o.t];
+    if (s < 0 || s >= P.n_slots) {
+        if (s != -1 && part == 0 && o.u == 0) atomicOr(status, GEM_DEVFLAG_PAGE_RANGE);
+        return false;
+    }
+    const int page_tiles = (1 << P.lpage) / kTileTokens;
+    const int64_t tile = (static_cast<int64_t>(s >> P.lpage) * P.n_kv + o.head) * page_tiles +
+                         ((s & ((1 << P.lpage) - 1)) / kTileTokens);
+    const int row = s % kTileTokens;
+    uint8_t* base = P.pool + tile * tile_bytes(P.d);
+    o.code = base + codes_off(P.d, o.which) + (o.blk * kTileTokens + row) * 16 + o.u * 4;
+    o.scale = base + scales_off(P.d, o.which) + (o.blk * kTileTokens + row) * 2;
+    return true;
+}
+
+__device__ __forceinline__ void load4(const float* p, bool vec, float (&x)[4]) {
+    if (vec) {
+        const float4 f = *reinterpret_cast<const float4*>(p);
+        x[0] = f.x, x[1] = f.y, x[2] = f.z, x[3] = f.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = p[i];
+    }
+}
+
+// 8 + rint(x / s), ties to even, clamped to 0..15, decided exactly: the first guess from a
+// reciprocal is off by less than one step beyond the nearest code, and x - q s is exact in fp32
+// (both are multiples of the smaller of their last places, and the difference is no larger than x).
+__device__ __forceinline__ int code_of(float x, float s, float inv) {
+    float q = fminf(fmaxf(rintf(x * inv), -9.f), 8.f);   // beyond: clamped to the same codes
+    const float r = fmaf(-q, s, x), h = 0.5f * fabsf(s);
+    const bool over = fabsf(r) > h, tie = fabsf(r) == h;
+    if (over || (tie && (static_cast<int>(q) & 1))) q += (r < 0.f) == (s < 0.f) ? 1.f : -1.f;
+    return min(max(static_cast<int>(q) + 8, 0), 15);
+}
+
+__global__ void __launch_bounds__(256) kv4_append_kernel(const RowsParams P) {
+    pdl_wait_trigger();
+    const int64_t gid = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
+    Place o;
+    const bool live = place_of(P, gid, P.status, o);
+    float x[8];
+    if (live) {
+        const float* src = (o.which ? P.v + o.t * P.ldv : P.k + o.t * P.ldk) + o.head * P.d + o.blk * 32 + o.u * 4;
+        const bool vec = o.which ? P.vec_v : P.vec_k;
+        load4(src, vec, reinterpret_cast<float(&)[4]>(x[0]));
+        load4(src + 16, vec, reinterpret_cast<float(&)[4]>(x[4]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = 0.f;
+    }
+    // the value of largest magnitude, the first of equal ones: magnitude, then 31 - index, then sign
+    // (a NaN's magnitude bits are above an infinity's)
+    uint64_t key = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t bits = __float_as_uint(x[i]);
+        const uint32_t e = (i < 4 ? 0 : 16) + o.u * 4 + (i & 3);
+        const uint64_t k = (static_cast<uint64_t>(bits & 0x7fffffffu) << 32) | ((31u - e) << 1) | (bits >> 31);
+        key = k > key ? k : key;
+    }
+#pragma unroll
+    for (int m = 1; m < 4; m <<= 1) {
+        const uint64_t k = __shfl_xor_sync(0xffffffffu, key, m);
+        key = k > key ? k : key;
+    }
+    if (!live) return;
+    const uint32_t mag = static_cast<uint32_t>(key >> 32);
+    __half s16;
+    uint32_t word = 0x88888888u;
+    if (mag >= 0x7f800000u) {
+        s16 = __ushort_as_half(0x7fff);
+    } else {
+        const float m = __uint_as_float(mag | (static_cast<uint32_t>(key & 1) << 31));
+        s16 = __float2half_rn(fminf(fmaxf(m * -0.125f, -65504.f), 65504.f));
+        const float s = __half2float(s16);
+        if (s != 0.f) {
+            const float inv = 1.0f / s;
+            word = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                word |= static_cast<uint32_t>(code_of(x[i], s, inv) | (code_of(x[4 + i], s, inv) << 4)) << (8 * i);
+        }
+    }
+    *reinterpret_cast<uint32_t*>(o.code) = word;
+    if (o.u == 0) *reinterpret_cast<__half*>(o.scale) = s16;
+}
+
+__global__ void __launch_bounds__(256) kv4_gather_kernel(const RowsParams P) {
+    pdl_wait_trigger();
+    const int64_t gid = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
+    Place o;
+    if (!place_of(P, gid, P.status, o)) return;
+    float* dst = o.which ? P.vo : P.ko;
+    if (!dst) return;
+    dst += o.t * (o.which ? P.ldv : P.ldk) + o.head * P.d + o.blk * 32 + o.u * 4;
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(o.code);
+    const float s = __half2float(*reinterpret_cast<const __half*>(o.scale));
+    float lo[4], hi[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        lo[i] = static_cast<float>(static_cast<int>((w >> (8 * i)) & 15) - 8) * s;
+        hi[i] = static_cast<float>(static_cast<int>((w >> (8 * i + 4)) & 15) - 8) * s;
+    }
+    if (o.which ? P.vec_v : P.vec_k) {
+        *reinterpret_cast<float4*>(dst) = make_float4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<float4*>(dst + 16) = make_float4(hi[0], hi[1], hi[2], hi[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dst[i] = lo[i], dst[16 + i] = hi[i];
+    }
+}
+
+bool vec_ok(const float* p, int64_t ld) { return !(reinterpret_cast<uintptr_t>(p) & 15) && ld % 4 == 0; }
+
+gem_status rows_launch(const void* kernel, RowsParams& P, cudaStream_t stream) {
+    const gem_status st = flag_word(&P.status);
+    if (st != GEM_OK) return st;
+    const int64_t threads = (P.T + 7) / 8 * 8 * 4 * 2 * P.n_kv * P.nb;
+    const int64_t blocks = (threads + 255) / 256;
+    if (blocks > INT32_MAX) return GEM_ERR_UNSUPPORTED_SHAPE;
+    void* args[] = {&P};
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, args);
+}
+
+}  // namespace
+}  // namespace kv4
+}  // namespace gem
+
+extern "C" {
+
+size_t gem_kv4_page_bytes(int n_kv, int d, int page) {
+    if (n_kv <= 0 || n_kv > 65535 || !gem::kv4::head_dim_ok(d) || !gem::kv4::page_ok(page)) return 0;
+    return static_cast<size_t>(n_kv) * (page / gem::kv4::kTileTokens) * gem::kv4::tile_bytes(d);
+}
+
+gem_status gem_kv4_append(const float* k, int64_t ldk, const float* v, int64_t ldv, int64_t T, int n_kv, int d,
+                          const int32_t* slot, void* pool, int64_t n_pages, int page, int32_t* status,
+                          void* stream) {
+    using namespace gem::kv4;
+    const gem_status st = pool_check(pool, n_pages, page, n_kv, d);
+    if (st != GEM_OK) return st;
+    if (T < 0) return GEM_ERR_INVALID_ARG;
+    if (T == 0 || n_kv == 0) return GEM_OK;
+    if (!k || !v || !slot || ldk < static_cast<int64_t>(n_kv) * d || ldv < static_cast<int64_t>(n_kv) * d)
+        return GEM_ERR_INVALID_ARG;
+    RowsParams P{};
+    P.k = k, P.v = v, P.ldk = ldk, P.ldv = ldv, P.T = T, P.slot = slot;
+    P.pool = static_cast<uint8_t*>(pool);
+    P.n_slots = n_pages * page;
+    P.n_kv = n_kv, P.d = d, P.nb = d / 32, P.lpage = log2_of(page);
+    P.vec_k = vec_ok(k, ldk), P.vec_v = vec_ok(v, ldv);
+    P.status = status;
+    return rows_launch(reinterpret_cast<const void*>(kv4_append_kernel), P, static_cast<cudaStream_t>(stream));
+}
+
+gem_status gem_kv4_gather(const void* pool, int64_t n_pages, int page, int n_kv, int d, const int32_t* slot,
+                          int64_t T, float* k, int64_t ldk, float* v, int64_t ldv, int32_t* status,
+                          void* stream) {
+    using namespace gem::kv4;
+    const gem_status st = pool_check(pool, n_pages, page, n_kv, d);
+    if (st != GEM_OK) return st;
+    if (T < 0) return GEM_ERR_INVALID_ARG;
+    if (T == 0 || n_kv == 0 || (!k && !v)) return GEM_OK;
+    if (!slot || (k && ldk < static_cast<int64_t>(n_kv) * d) || (v && ldv < static_cast<int64_t>(n_kv) * d))
+        return GEM_ERR_INVALID_ARG;
+    RowsParams P{};
+    P.ko = k, P.vo = v, P.ldk = ldk, P.ldv = ldv, P.T = T, P.slot = slot;
+    P.pool = static_cast<uint8_t*>(const_cast<void*>(pool));
+    P.n_slots = n_pages * page;
+    P.n_kv = n_kv, P.d = d, P.nb = d / 32, P.lpage = log2_of(page);
+    P.vec_k = vec_ok(k, ldk), P.vec_v = vec_ok(v, ldv);
+    P.status = status;
+    return rows_launch(reinterpret_cast<const void*>(kv4_gather_kernel), P, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,152 @@
+// gem_mrope.cu — per-head QK-norm and rotary positions with one or several axes, for T tokens.
+#include <cmath>
+
+#include "gem_device.cuh"
+#include "gem_kv4.cuh"
+
+namespace gem {
+namespace kv4 {
+namespace {
+
+constexpr int kMaxAxes = 4;
+
+// theta^(-2i/R) / (2 pi) in turns, 64-bit fixed point; the two lowest bits hold the frequency's axis
+// (they change an angle by less than 2^-29 turns at the largest position).
+struct MropeFreq {
+    uint64_t f[kMaxHeadDim / 2];
+};
+
+struct MropeParams {
+    const float* x;
+    int64_t ldx;
+    float* out;
+    int64_t ldo, T;
+    int n_q, nheads, d, R;
+    const float *gamma_q, *gamma_k;
+    float eps;
+    const int32_t* pos;
+    int64_t ldpos;
+    int n_axes;
+    int* status;
+};
+
+// cos and sin of pos * frequency.  The product is taken modulo one turn in 64-bit integers, which
+// is exact; what is left, 32 bits of a turn, goes through fp32.
+__device__ __forceinline__ void turn_cos_sin(const MropeParams& P, int64_t t, uint64_t f, float& c, float& s) {
+    const int axis = static_cast<int>(f & 3);
+    const uint32_t p = static_cast<uint32_t>(P.pos[axis * P.ldpos + t]);
+    const uint64_t turns = static_cast<uint64_t>(p) * f;
+    const int32_t top = static_cast<int32_t>((turns + 0x80000000ull) >> 32);
+    sincospif(static_cast<float>(top) * 4.656612873077393e-10f, &s, &c);   // 2^-31: half turns
+}
+
+// 0: rotate row t; 1: padding; 2: a position out of range
+__device__ __forceinline__ int row_state(const MropeParams& P, int64_t t) {
+    const int32_t p0 = P.pos[t];
+    if (p0 == -1) return 1;
+    bool bad = p0 < 0;
+    for (int a = 1; a < P.n_axes; ++a) bad |= P.pos[a * P.ldpos + t] < 0;
+    return bad ? 2 : 0;
+}
+
+// One warp per (token, head).  Any even d and R.
+__global__ void __launch_bounds__(128) mrope_kernel(const MropeParams P, const __grid_constant__ MropeFreq F) {
+    __shared__ float buf[4][kMaxHeadDim];
+    pdl_wait_trigger();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int64_t unit = blockIdx.x * 4ll + w;
+    const int64_t t = unit / P.nheads;
+    if (t >= P.T) return;
+    const int head = static_cast<int>(unit % P.nheads);
+    const int state = row_state(P, t);
+    if (state) {
+        if (state == 2 && head == 0 && lane == 0) atomicOr(P.status, GEM_DEVFLAG_POS_RANGE);
+        return;
+    }
+    const float* x = P.x + t * P.ldx + static_cast<int64_t>(head) * P.d;
+    float* out = P.out + t * P.ldo + static_cast<int64_t>(head) * P.d;
+    const float* gamma = head < P.n_q ? P.gamma_q : P.gamma_k;
+    float* sb = buf[w];
+    float ss = 0.f;
+    for (int e = lane; e < P.d; e += 32) {
+        const float v = x[e];
+        sb[e] = v;
+        ss = fmaf(v, v, ss);
+    }
+    __syncwarp();
+    if (gamma) {
+        const float r = rsqrtf(warp_sum(ss) / static_cast<float>(P.d) + P.eps);
+        for (int e = lane; e < P.d; e += 32) sb[e] = sb[e] * r * gamma[e];
+        __syncwarp();
+    }
+    const int half = P.R / 2;
+    for (int i = lane; i < half; i += 32) {
+        float c, s;
+        turn_cos_sin(P, t, F.f[i], c, s);
+        const float a = sb[i], b = sb[i + half];
+        out[i] = fmaf(a, c, -b * s);
+        out[i + half] = fmaf(a, s, b * c);
+    }
+    for (int e = P.R + lane; e < P.d; e += 32) out[e] = sb[e];
+}
+
+}  // namespace
+}  // namespace kv4
+}  // namespace gem
+
+extern "C" gem_status gem_qknorm_mrope(const float* qkv, int64_t ldqkv, int64_t T, int n_q, int n_kv, int d,
+                                       const float* gamma_q, const float* gamma_k, float eps,
+                                       const int32_t* pos, int64_t ldpos, int n_axes, const int32_t* sections,
+                                       int interleaved, float theta, float* out, int64_t ldo, int32_t* status,
+                                       void* stream) {
+    using namespace gem;
+    using namespace gem::kv4;
+    if (T < 0 || n_q < 0 || n_kv < 0 || d <= 0 || !(eps >= 0.f) || interleaved < 0 || interleaved > 1)
+        return GEM_ERR_INVALID_ARG;
+    if (d > kMaxHeadDim || (d & 1) || n_axes < 1 || n_axes > kMaxAxes || n_q > 65535 || n_kv > 65535)
+        return GEM_ERR_UNSUPPORTED_SHAPE;
+    if (!sections || !(theta > 0.f) || !std::isfinite(theta)) return GEM_ERR_INVALID_ARG;
+    int64_t half = 0;
+    for (int a = 0; a < n_axes; ++a) {
+        if (sections[a] < 0) return GEM_ERR_INVALID_ARG;
+        half += sections[a];
+    }
+    if (half < 1 || 2 * half > d) return GEM_ERR_INVALID_ARG;
+    const int R = static_cast<int>(2 * half);
+    for (int a = 1; interleaved && a < n_axes; ++a)
+        if (sections[a] && a + static_cast<int64_t>(sections[a] - 1) * n_axes >= half) return GEM_ERR_INVALID_ARG;
+    const int64_t cols = static_cast<int64_t>(n_q + n_kv) * d;
+    if (T == 0 || cols == 0) return GEM_OK;
+    if (!qkv || !out || !pos || ldqkv < cols || ldo < cols || ldpos < T) return GEM_ERR_INVALID_ARG;
+    if (out == qkv && ldo != ldqkv) return GEM_ERR_INVALID_ARG;
+
+    MropeFreq F;
+    for (int i = 0, a = 0, left = sections[0]; i < half; ++i) {
+        int axis;
+        if (interleaved) {
+            axis = i % n_axes;
+            if (axis && i >= n_axes * static_cast<int64_t>(sections[axis])) axis = 0;
+        } else {
+            while (left == 0) left = sections[++a];
+            --left;
+            axis = a;
+        }
+        // theta < 1 gives more than a turn a position: the whole turns drop out
+        const double turns = std::pow(static_cast<double>(theta), -2.0 * i / R) * 0.15915494309189535;
+        const double part = turns - std::floor(turns);
+        uint64_t f = static_cast<uint64_t>(std::ldexp(part, 63)) << 1;
+        F.f[i] = (f & ~3ull) | static_cast<uint64_t>(axis);
+    }
+    MropeParams P{};
+    P.x = qkv, P.ldx = ldqkv, P.out = out, P.ldo = ldo, P.T = T;
+    P.n_q = n_q, P.nheads = n_q + n_kv, P.d = d, P.R = R;
+    P.gamma_q = gamma_q, P.gamma_k = gamma_k, P.eps = eps;
+    P.pos = pos, P.ldpos = ldpos, P.n_axes = n_axes, P.status = status;
+    gem_status st = flag_word(&P.status);
+    if (st != GEM_OK) return st;
+    const int64_t blocks = (T * P.nheads + 3) / 4;
+    if (blocks > INT32_MAX) return GEM_ERR_UNSUPPORTED_SHAPE;
+    void* args[] = {&P, &F};
+    return launch_pdl(reinterpret_cast<const void*>(mrope_kernel), dim3(static_cast<unsigned>(blocks)), dim3(128), 0,
+                      static_cast<cudaStream_t>(stream), args);
+}
