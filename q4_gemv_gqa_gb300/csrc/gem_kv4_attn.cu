@@ -1,5 +1,35 @@
 // gem_kv4_attn.cu — grouped-query attention over the paged 4-bit KV cache.
+//
+// Mathematics.  For a query row q (one token, one query head) and the cached rows of its KV head,
+//   out = sum_j p_j V_j / sum_j p_j,   p_j = 2^(c q.K_j - m),  c = scale * log2(e),
+// in one pass with a running maximum m.  K and V are (code - 8) * s with one scale s per position and
+// 32 dims, so with blocks b of 32 dims
+//   q.K_j  = sum_b sK[j][b] sum_{e in b} q_e (code_je - 8)
+//   out_e ~  sum_j (p_j sV[j][b]) (code_je - 8),  e in b.
+//
+// Tensor cores.  mma.sync m16n8k16 with the codes as the 16-row operand.  A nibble put into the low
+// mantissa bits of 1024 is the binary16 number 1024 + code (1024 + 16 code for the next nibble), and
+// one packed add or fma leaves code - 8, exactly: 9 instructions for 8 codes, 4 of them not on the
+// integer pipe.  (The codes could enter as they are, as subnormals code * 2^-24 in 5 instructions, with
+// the 8 taken out of the sums; measured, that costs 7 bits: products are aligned by their operands'
+// exponent fields before they are added, and a relative error of 1.2e-5 was left.)  q, and p times V's
+// scale, are fp32 and enter as binary16 hi + lo pairs (about 22 bits) under powers of two that keep
+// them in binary16's range; up to four query rows put both halves into the eight columns of one
+// instruction, more rows take two.
+// The wide tcgen05 path wants both operands in binary16 or fp8 tiles in shared memory: here one operand
+// is 4-bit codes and would first be written out four times as large, for eight columns of output, so
+// the unpacking, not the multiply rate, would bound it just the same.
+//
+// Schedule.  The work is (request, KV head, group of query rows) units of steps of 32 positions.  Their
+// number is known on the device only, so a fixed grid of warps takes equal contiguous shares of all
+// steps.  A warp streams its tiles with cp.async.bulk through a ring of its own and keeps its own
+// running maximum, sum and output; a unit inside one share is written out at once, the parts of one
+// that crosses shares are joined first inside the CTA, then, in order, by a second kernel.
+#include <algorithm>
 #include <cmath>
+#include <mutex>
+#include <set>
+#include <utility>
 
 #include "gem_device.cuh"
 #include "gem_kv4.cuh"
@@ -9,123 +39,818 @@ namespace kv4 {
 namespace {
 
 constexpr int kMaxGroup = 8;
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kStepTiles = 2;
+constexpr int kStepTokens = kStepTiles * kTileTokens;
+constexpr int kStages = 2;
+constexpr int kProbRow = kStepTokens + 8;   // floats; 8 modulo 32 keeps the rows in banks of their own
 
 struct AttnParams {
     const float* q;
     int64_t ldq, T;
     const int32_t *cu, *kv_len;
-    int B, n_q, n_kv, G;
+    int B, n_q, n_kv, G, GT;      // GT: tokens of a unit (GT * G query rows)
     const int32_t* table;
     int64_t max_pages;
     const uint8_t* pool;
     int64_t n_pages;
-    int page, lpage, window;
+    int lpage, window;
     float scale;
     float* out;
     int64_t ldo;
+    int64_t* plan;                // workspace: steps before request b, [B + 1]
+    float* part;                  // workspace: 2 slots a worker
+    int workers;
     int* status;
 };
 
-// One CTA per (query row, KV head), one cached position per warp at a time, the lanes across d.
-template <int D>
-__global__ void __launch_bounds__(128) kv4_attn_rows_kernel(const AttnParams P) {
-    constexpr int kWarps = 4, E = D / 32;
-    __shared__ float qs[kMaxGroup][D];
-    __shared__ float acc_s[kMaxGroup][D];
-    __shared__ float ml[kWarps][kMaxGroup][2];
-    __shared__ int found;
-    pdl_wait_trigger();
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int64_t t = blockIdx.x;
-    const int h = blockIdx.y;
-    if (threadIdx.x == 0) found = -1;
-    __syncthreads();
-    for (int b = threadIdx.x; b < P.B; b += blockDim.x) {
-        const int64_t c0 = P.cu[b], c1 = P.cu[b + 1], L = P.kv_len[b];
-        const bool ok = c0 >= 0 && c0 <= c1 && c1 <= P.T && L >= c1 - c0 && L <= P.max_pages * P.page;
-        if (!ok) {
-            if (t == 0 && h == 0) atomicOr(P.status, GEM_DEVFLAG_POS_RANGE);
-        } else if (c0 <= t && t < c1) {
-            atomicMax(&found, b);
+// ---- what a request asks for ---------------------------------------------------------------------
+
+struct Request {
+    int row0, n, L;       // first query row, query rows, cached positions
+    int tile0, steps;     // first tile that any row attends, steps from there on
+    int groups;           // units of one KV head
+};
+
+__device__ __forceinline__ bool request_of(const AttnParams& P, int b, Request& r) {
+    const int64_t c0 = P.cu[b], c1 = P.cu[b + 1], L = P.kv_len[b];
+    r.row0 = static_cast<int>(c0);
+    r.n = 0, r.L = 0, r.tile0 = 0, r.steps = 0, r.groups = 0;
+    if (c0 < 0 || c0 > c1 || c1 > P.T || L < c1 - c0 || L > (P.max_pages << P.lpage)) return false;
+    r.n = static_cast<int>(c1 - c0);
+    r.L = static_cast<int>(L);
+    if (r.n == 0) return true;
+    r.tile0 = P.window ? max(0, r.L - r.n + 1 - P.window) / kTileTokens : 0;
+    r.steps = ((r.L - 1) / kTileTokens - r.tile0) / kStepTiles + 1;
+    r.groups = (r.n + P.GT - 1) / P.GT;
+    return true;
+}
+
+// A place in the sequence of all steps: request, unit of it, step of the unit.
+struct Walk {
+    int b, u, i;
+    Request r;
+    __device__ __forceinline__ void seek(const AttnParams& P, const int64_t* plan, int64_t step) {
+        int lo = 0, hi = P.B - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (plan[mid] <= step) lo = mid;
+            else hi = mid - 1;
         }
+        b = lo;
+        request_of(P, b, r);
+        const int64_t in = step - plan[b];
+        u = static_cast<int>(in / r.steps);
+        i = static_cast<int>(in % r.steps);
     }
-    __syncthreads();
-    const int b = found;
-    if (b < 0) return;
-    const int p = P.kv_len[b] - P.cu[b + 1] + static_cast<int>(t);
-    const int first = P.window ? max(0, p - P.window + 1) : 0;
-    for (int i = threadIdx.x; i < P.G * D; i += blockDim.x)
-        qs[i / D][i % D] = P.q[t * P.ldq + static_cast<int64_t>(h) * P.G * D + i] * P.scale;
-    __syncthreads();
-    float m[kMaxGroup], l[kMaxGroup], acc[kMaxGroup][E];
-#pragma unroll
-    for (int g = 0; g < kMaxGroup; ++g) {
-        m[g] = -INFINITY, l[g] = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[g][e] = 0.f;
+    __device__ __forceinline__ void next(const AttnParams& P, const int64_t* plan) {
+        if (++i < r.steps) return;
+        i = 0;
+        if (++u < P.n_kv * r.groups) return;
+        u = 0;
+        do ++b;
+        while (b < P.B && plan[b + 1] == plan[b]);
+        if (b < P.B) request_of(P, b, r);
     }
-    const int page_tiles = P.page / kTileTokens;
-    for (int j = first + w; j <= p; j += kWarps) {
-        const int32_t id = P.table[b * P.max_pages + (j >> P.lpage)];
-        if (id < 0 || id >= P.n_pages) {
-            if (lane == 0) atomicOr(P.status, GEM_DEVFLAG_PAGE_RANGE);
-            continue;
-        }
-        const uint8_t* tile = P.pool + ((static_cast<int64_t>(id) * P.n_kv + h) * page_tiles +
-                                        (j & (P.page - 1)) / kTileTokens) * tile_bytes(D);
-        const int row = j % kTileTokens;
-        float kv[2][E];
-#pragma unroll
-        for (int which = 0; which < 2; ++which)
-#pragma unroll
-            for (int e = 0; e < E; ++e) {   // element 32 e + lane
-                const int at = e * kTileTokens + row;
-                const uint32_t byte = tile[codes_off(D, which) + at * 16 + (lane & 15)];
-                const float s = __half2float(reinterpret_cast<const __half*>(tile + scales_off(D, which))[at]);
-                kv[which][e] = static_cast<float>(static_cast<int>(lane < 16 ? byte & 15 : byte >> 4) - 8) * s;
-            }
-#pragma unroll
-        for (int g = 0; g < kMaxGroup; ++g) {
-            if (g >= P.G) break;
-            float s = 0.f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) s = fmaf(qs[g][e * 32 + lane], kv[0][e], s);
-            s = warp_sum(s);
-            const float mn = fmaxf(m[g], s);
-            const float corr = m[g] == mn ? 1.f : expf(m[g] - mn), pr = s == -INFINITY ? 0.f : expf(s - mn);
-            m[g] = mn;
-            l[g] = l[g] * corr + pr;
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[g][e] = fmaf(pr, kv[1][e], acc[g][e] * corr);
-        }
+};
+
+// The query rows of a unit: tokens j0 .. j0 + tokens - 1 of the request, positions p0 on.
+struct Unit {
+    int h, j0, tokens, p0;
+    int lo_all, hi_all;    // first and last position that any row attends
+    int lo_max;            // from here to p0 every row attends
+    __device__ __forceinline__ Unit(const AttnParams& P, const Walk& w) {
+        h = w.u / w.r.groups;
+        j0 = (w.u - h * w.r.groups) * P.GT;
+        tokens = min(P.GT, w.r.n - j0);
+        p0 = w.r.L - w.r.n + j0;
+        hi_all = p0 + tokens - 1;
+        lo_all = P.window ? max(0, p0 - P.window + 1) : 0;
+        lo_max = P.window ? max(0, hi_all - P.window + 1) : 0;
     }
-    for (int g = 0; g < P.G; ++g)
-        for (int e = threadIdx.x; e < D; e += blockDim.x) acc_s[g][e] = 0.f;
+};
+
+// ---- small pieces ----------------------------------------------------------------------------------
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// D = A B
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// Word of 8 codes, nibbles n0 .. n7 from the low end -> (n0, n4), (n1, n5), (n2, n6), (n3, n7), less 8 each.
+struct Codes {
+    uint32_t v[4];
+};
+__device__ __forceinline__ Codes codes_of(uint32_t w) {
+    constexpr uint32_t kMagic = 0x64006400u;   // 1024, 1024
+    uint32_t x[4];
+    asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(x[0]) : "r"(w), "r"(kMagic));   // (a & b) | c
+    asm("lop3.b32 %0, %1, 0x00f000f0, %2, 0xea;" : "=r"(x[1]) : "r"(w), "r"(kMagic));
+    const uint32_t u = w >> 8;
+    asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(x[2]) : "r"(u), "r"(kMagic));
+    asm("lop3.b32 %0, %1, 0x00f000f0, %2, 0xea;" : "=r"(x[3]) : "r"(u), "r"(kMagic));
+    Codes c;
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        asm("add.rn.f16x2 %0, %1, %2;" : "=r"(c.v[i]) : "r"(x[i]), "r"(0xe408e408u));                       // - 1032
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(c.v[i + 1]) : "r"(x[i + 1]), "r"(0x2c002c00u), "r"(0xd480d480u));   // / 16 - 72
+    }
+    return c;
+}
+
+// (lo, hi) halves of a register, rounded toward zero
+__device__ __forceinline__ uint32_t pack_rz(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_rn(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float round_f16(float x) { return __half2float(__float2half_rn(x)); }
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+    uint64_t ra, rb, rd;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(ra) : "f"(a.x), "f"(a.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(rb) : "f"(b.x), "f"(b.y));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(rd) : "l"(ra), "l"(rb));
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(rd));
+    return d;
+}
+// the 11 leading significant bits, negated where flip is the sign bit
+__device__ __forceinline__ float lead(float x, uint32_t flip) {
+    return __uint_as_float((__float_as_uint(x) & 0xffffe000u) ^ flip);
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// A partial result in memory: rows of D sums, then (maximum, sum) of each row.
+template <int D, int ROWS>
+struct Part {
+    static constexpr int kFloats = ROWS * (D + 2);
+};
+
+template <int D, int NT, bool PACK>
+struct Cfg {
+    static constexpr int kRows = PACK ? 4 : 8 * NT;      // query rows of a unit
+    static constexpr int kDims = D < 256 ? D : 256;      // dims of one warp
+    static constexpr int kPair = D / kDims;              // warps of a worker
+    static constexpr int kBlocks = kDims / 32;
+    static constexpr int kTile = tile_bytes(kDims);      // a tile's bytes in one warp's ring
+    static constexpr int kStage = kStepTiles * kTile;
+    static constexpr int kPartBytes = Part<D, kRows>::kFloats * 4;
+    static constexpr int kRingNeed = (kPartBytes / kPair + 127) / 128 * 128;   // the ring later holds a partial result
+    static constexpr int kRing = kStages * kStage > kRingNeed ? kStages * kStage : kRingNeed;
+    static constexpr int kScales = kStepTiles * kBlocks * 128;
+    static constexpr int kProbs = kRows * kProbRow * 4;
+    static constexpr int kSwap = kPair > 1 ? 2 * kStepTiles * NT * 32 * 16 : 0;
+    static constexpr int kWarpBytes = kRing + kScales + kProbs + kSwap;
+    static constexpr int kWorkers = kWarps / kPair;      // of a CTA
+    static size_t smem(int B) { return kWarps * static_cast<size_t>(kWarpBytes) + kWarps * kStages * 8 + (B + 1) * 8; }
+};
+
+// ---- the kernel ------------------------------------------------------------------------------------
+
+template <int D, int NT, bool PACK, int CTAS>
+__global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnParams P) {
+    using C = Cfg<D, NT, PACK>;
+    constexpr int NB = C::kBlocks, ROWS = C::kRows, PAIR = C::kPair;
+    constexpr int NH = PACK ? 1 : 2;                     // B operands of a product: (hi | lo) or hi, lo
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int64_t sums[kWarps];
+    __shared__ int64_t tail_unit[kWarps];
+
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const int member = warp % PAIR;                      // which dims of the head this warp has
+    const int worker = blockIdx.x * C::kWorkers + warp / PAIR;
+    uint8_t* ring = smem + warp * C::kWarpBytes;
+    float* scales = reinterpret_cast<float*>(ring + C::kRing);
+    float* probs = reinterpret_cast<float*>(ring + C::kRing + C::kScales);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kWarps * C::kWarpBytes) + warp * kStages;
+    int64_t* plan = reinterpret_cast<int64_t*>(smem + kWarps * C::kWarpBytes + kWarps * kStages * 8);
+
     if (lane == 0) {
-#pragma unroll
-        for (int g = 0; g < kMaxGroup; ++g) ml[w][g][0] = m[g], ml[w][g][1] = l[g];
+        for (int i = 0; i < kStages; ++i) mbar_init(&bars[i], 1);
+        fence_mbar_init();
     }
-    __syncthreads();
-    for (int k = 0; k < kWarps; ++k) {   // the warps add their share in order
-#pragma unroll
-        for (int g = 0; g < kMaxGroup; ++g) {
-            if (w != k || g >= P.G) break;
-            float mx = -INFINITY;
-            for (int i = 0; i < kWarps; ++i) mx = fmaxf(mx, ml[i][g][0]);
-            const float c = m[g] == mx ? 1.f : expf(m[g] - mx);
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc_s[g][e * 32 + lane] += c * acc[g][e];
+    pdl_wait_trigger();
+
+    // steps before each request
+    int64_t carry = 0;
+    if (threadIdx.x == 0) plan[0] = 0;
+    for (int base = 0; base < P.B; base += kThreads) {
+        const int b = base + threadIdx.x;
+        Request r;
+        int64_t v = 0;
+        if (b < P.B) {
+            if (!request_of(P, b, r) && blockIdx.x == 0) atomicOr(P.status, GEM_DEVFLAG_POS_RANGE);
+            v = static_cast<int64_t>(r.steps) * r.groups * P.n_kv;
         }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += x;
+        }
+        if (lane == 31) sums[warp] = v;
+        __syncthreads();
+        int64_t before = 0, all = 0;
+        for (int i = 0; i < kWarps; ++i) {
+            before += i < warp ? sums[i] : 0;
+            all += sums[i];
+        }
+        if (b < P.B) plan[b + 1] = carry + before + v;
+        carry += all;
         __syncthreads();
     }
-    for (int i = threadIdx.x; i < P.G * D; i += blockDim.x) {
-        const int g = i / D, e = i % D;
-        float mx = -INFINITY, den = 0.f;
-        for (int k = 0; k < kWarps; ++k) mx = fmaxf(mx, ml[k][g][0]);
-        for (int k = 0; k < kWarps; ++k) den += (ml[k][g][0] == mx ? 1.f : expf(ml[k][g][0] - mx)) * ml[k][g][1];
-        P.out[t * P.ldo + static_cast<int64_t>(h) * P.G * D + i] = den == 0.f ? 0.f : acc_s[g][e] / den;
+    __syncthreads();
+    if (blockIdx.x == 0)
+        for (int b = threadIdx.x; b <= P.B; b += kThreads) P.plan[b] = plan[b];
+    const int64_t total = plan[P.B];
+    const int64_t share = (total + P.workers - 1) / P.workers;
+    const int64_t begin = min(total, worker * share), end = min(total, begin + share);
+
+    Walk put, get;             // the step to request next, the step to compute next
+    int64_t put_step = begin;
+    int pbase = 0, pid = -1, pb = -1;   // table entries pbase .. pbase + 31 of request pb, one a lane
+    uint32_t lost = 0;         // tiles of the ring's stages that hold nothing
+    bool dead = false;
+    const int lpt = P.lpage - 4;
+
+    auto request_step = [&](int stage) {
+        const Unit un(P, put);
+        const int tile = put.r.tile0 + put.i * kStepTiles + lane;
+        const bool want = lane < kStepTiles && tile >= un.lo_all / kTileTokens && tile <= un.hi_all / kTileTokens;
+        const int first = (put.r.tile0 + put.i * kStepTiles) >> lpt;
+        if (pb != put.b || first < pbase || first + kStepTiles - 1 > pbase + 31) {   // a step's tiles lie in at most as many pages
+            pb = put.b, pbase = first;
+            const int64_t at = pbase + lane;
+            pid = at < P.max_pages && at <= ((put.r.L - 1) >> P.lpage)
+                      ? P.table[put.b * P.max_pages + at] : -1;
+        }
+        const int32_t id = __shfl_sync(0xffffffffu, pid, ((tile >> lpt) - pbase) & 31);
+        const bool in = id >= 0 && id < P.n_pages;
+        if (want && !in) atomicOr(P.status, GEM_DEVFLAG_PAGE_RANGE);
+        const uint32_t have = __ballot_sync(0xffffffffu, want && in);
+        constexpr uint32_t kMask = (1u << kStepTiles) - 1;
+        lost = (lost & ~(kMask << (stage * kStepTiles))) | ((~have & kMask) << (stage * kStepTiles));
+        if (lane == 0) {
+            uint32_t bytes = __popc(have) * C::kTile;
+            if (test_inject() & GEM_INJECT_RING_SHORTFALL) bytes += worker == 0 && put_step == 0 ? 16 : 0;
+            mbar_arrive_expect_tx(&bars[stage], bytes);
+        }
+        __syncwarp();
+        if (want && in) {
+            const uint8_t* src = P.pool + (((static_cast<int64_t>(id) * P.n_kv + un.h) << lpt) +
+                                           (tile & ((1 << lpt) - 1))) * tile_bytes(D);
+            const uint32_t dst = smem_u32(ring + stage * C::kStage + lane * C::kTile);
+            if (PAIR == 1) {
+                bulk_load(dst, src, C::kTile, &bars[stage]);
+            } else {
+                constexpr int kCodes = 8 * C::kDims, kScale = C::kDims;
+                bulk_load(dst, src + member * kCodes, kCodes, &bars[stage]);
+                bulk_load(dst + kCodes, src + codes_off(D, 1) + member * kCodes, kCodes, &bars[stage]);
+                bulk_load(dst + 2 * kCodes, src + scales_off(D, 0) + member * kScale, kScale, &bars[stage]);
+                bulk_load(dst + 2 * kCodes + kScale, src + scales_off(D, 1) + member * kScale, kScale, &bars[stage]);
+            }
+        }
+        ++put_step;
+        if (put_step < end) put.next(P, plan);
+    };
+
+    // state of the unit at hand
+    uint32_t bq[NB][2][NT][NH][2];        // q: [block][low or high byte pair][column tile][hi, lo][register]
+    float acc[NB][2][NT][4];              // output sums
+    float cmul[NT][2], m[NT][2], l[NT][2];
+    int prow[NT][2];                      // positions of this lane's two rows of each column tile
+    int E = 0;
+
+    // rows of the S and output fragments: columns 2t, 2t + 1
+    auto col_row = [&](int nt, int e) { return PACK ? (2 * t + e) & 3 : nt * 8 + 2 * t + e; };
+
+    auto begin_unit = [&](const Unit& un) {
+        const float c = P.scale * 1.4426950408889634f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int row = PACK ? g & 3 : nt * 8 + g;
+            const int tok = row / P.G;
+            const bool live = tok < un.tokens;
+            const float* src = P.q + (un.j0 + tok + static_cast<int64_t>(get.r.row0)) * P.ldq +
+                               (static_cast<int64_t>(un.h) * P.G + (row - tok * P.G)) * D + member * C::kDims + 4 * t;
+            float x[NB][8], top = 0.f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const float4 lo = live ? *reinterpret_cast<const float4*>(src + b * 32) : make_float4(0, 0, 0, 0);
+                const float4 hi = live ? *reinterpret_cast<const float4*>(src + b * 32 + 16) : make_float4(0, 0, 0, 0);
+                x[b][0] = lo.x, x[b][1] = lo.y, x[b][2] = lo.z, x[b][3] = lo.w;
+                x[b][4] = hi.x, x[b][5] = hi.y, x[b][6] = hi.z, x[b][7] = hi.w;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[b][k]));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // the row times 2^e has its largest value in [2^13, 2^14)
+            const int e = max(-96, min(120, 13 - (static_cast<int>(__float_as_uint(top) >> 23) - 127)));
+            const float f = pow2(e);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                float y[2][8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float v = x[b][k] * f;
+                    y[0][k] = round_f16(v);
+                    y[1][k] = round_f16(v - y[0][k]);
+                    if (PACK) y[0][k] = g < 4 ? y[0][k] : y[1][k];
+                }
+#pragma unroll
+                for (int hl = 0; hl < NH; ++hl)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        bq[b][j][nt][hl][0] = pack_rn(y[hl][j], y[hl][j + 2]);
+                        bq[b][j][nt][hl][1] = pack_rn(y[hl][4 + j], y[hl][6 + j]);
+                    }
+            }
+            const float back = c * pow2(-e);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                cmul[nt][k] = __shfl_sync(0xffffffffu, back, ((PACK ? (2 * t + k) & 3 : 2 * t + k)) * 4);
+                const int tk = col_row(nt, k) / P.G;
+                prow[nt][k] = un.p0 + min(tk, un.tokens - 1);
+                m[nt][k] = -INFINITY;
+                l[nt][k] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[b][0][nt][k] = acc[b][1][nt][k] = 0.f;
+        E = 60;
+    };
+
+    // The unit's sums so far, in true units: put_row(row, maximum, sum of p) for every row, and
+    // put_pair(row, dim, values of dim and dim + 1, sum of p) for its dims.
+    auto finish = [&](auto&& put_pair, auto&& put_row) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], o);
+                if (PACK) l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], 2);
+            }
+            const float down = pow2(-E);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                l[nt][k] *= down;
+                if (g == 0 && (!PACK || t < 2)) put_row(col_row(nt, k), m[nt][k], l[nt][k]);
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float v[4];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        float a0 = acc[b][j][nt][k], a1 = acc[b][j][nt][2 + k];
+                        if (PACK) {
+                            a0 += __shfl_xor_sync(0xffffffffu, a0, 2);
+                            a1 += __shfl_xor_sync(0xffffffffu, a1, 2);
+                        }
+                        v[j] = a0 * down;
+                        v[2 + j] = a1 * down;
+                    }
+                    if (!PACK || t < 2) {
+                        const int dim = member * C::kDims + b * 32 + 2 * g;
+                        put_pair(col_row(nt, k), dim, make_float2(v[0], v[1]), l[nt][k]);
+                        put_pair(col_row(nt, k), dim + 16, make_float2(v[2], v[3]), l[nt][k]);
+                    }
+                }
+            }
+        }
+    };
+
+    // ---- one step: kStepTiles tiles in stage `stage` ----
+    auto compute = [&](int stage, const Unit& un, int pos0) {
+        const uint8_t* st = ring + stage * C::kStage;
+        const uint32_t gone = (lost >> (stage * kStepTiles)) & ((1u << kStepTiles) - 1);
+        const bool clean = gone == 0 && pos0 >= un.lo_max && pos0 + kStepTokens - 1 <= un.p0;
+        // scales in fp32: K's as pairs (row g, row g + 8), V's as quads (2t, 2t + 1, 2t + 8, 2t + 9)
+#pragma unroll
+        for (int it = lane; it < kStepTiles * NB * 8; it += 32) {
+            const int s = it / (NB * 8), b = it / 8 % NB, r = it & 7;
+            const __half* ks = reinterpret_cast<const __half*>(st + s * C::kTile + scales_off(C::kDims, 0)) + b * 16;
+            reinterpret_cast<float2*>(scales + (s * NB + b) * 32)[r] =
+                make_float2(__half2float(ks[r]), __half2float(ks[r + 8]));
+        }
+        uint32_t big = 0;
+#pragma unroll
+        for (int it = lane; it < kStepTiles * NB * 4; it += 32) {
+            const int s = it / (NB * 4), b = it / 4 % NB, r = it & 3;
+            const __half2* vs = reinterpret_cast<const __half2*>(st + s * C::kTile + scales_off(C::kDims, 1)) + b * 8;
+            const float2 a = __half22float2(vs[r]), c = __half22float2(vs[r + 4]);
+            float v[4] = {a.x, a.y, c.x, c.y};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (!clean) {   // what no row attends may be anything
+                    const int pos = pos0 + s * kTileTokens + 2 * r + (k & 1) + (k >> 1) * 8;
+                    if (pos < un.lo_all || pos > un.hi_all || (gone >> s & 1)) v[k] = 0.f;
+                }
+                const uint32_t bits = __float_as_uint(v[k]) & 0x7fffffffu;
+                big = max(big, bits < 0x7f800000u ? bits : 0u);
+            }
+            reinterpret_cast<float4*>(scales + (s * NB + b) * 32 + 16)[r] = make_float4(v[0], v[1], v[2], v[3]);
+        }
+        big = __reduce_max_sync(0xffffffffu, big);
+        // p 2^E sV stays below 2^15
+        const int e_step = min(60, 14 - (static_cast<int>(big >> 23) - 127));
+        __syncwarp();
+
+        // scores
+        float sc[kStepTiles][NT][4];
+#pragma unroll
+        for (int s = 0; s < kStepTiles; ++s) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sc[s][nt][k] = 0.f;
+            const uint32_t codes = smem_u32(st + s * C::kTile) + lane * 16;
+#pragma unroll
+            for (int b2 = 0; b2 < NB; b2 += 2) {
+                uint32_t w[4];
+                ldmatrix_x4(w[0], w[1], w[2], w[3], codes + b2 * 256);
+#pragma unroll
+                for (int b = b2; b < b2 + 2; ++b) {
+                    const uint32_t wa = w[2 * (b - b2)], wb = w[2 * (b - b2) + 1];
+                    const float2 ks = reinterpret_cast<const float2*>(scales + (s * NB + b) * 32)[g];
+                    const Codes ca = codes_of(wa), cb = codes_of(wb);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float d[4];
+                        mma_first(d, ca.v[0], cb.v[0], ca.v[1], cb.v[1], bq[b][0][nt][0][0], bq[b][0][nt][0][1]);
+                        mma_16816(d, ca.v[2], cb.v[2], ca.v[3], cb.v[3], bq[b][1][nt][0][0], bq[b][1][nt][0][1]);
+                        if (!PACK) {
+                            mma_16816(d, ca.v[0], cb.v[0], ca.v[1], cb.v[1], bq[b][0][nt][NH - 1][0], bq[b][0][nt][NH - 1][1]);
+                            mma_16816(d, ca.v[2], cb.v[2], ca.v[3], cb.v[3], bq[b][1][nt][NH - 1][0], bq[b][1][nt][NH - 1][1]);
+                        }
+                        sc[s][nt][0] = fmaf(ks.x, d[0], sc[s][nt][0]);
+                        sc[s][nt][1] = fmaf(ks.x, d[1], sc[s][nt][1]);
+                        sc[s][nt][2] = fmaf(ks.y, d[2], sc[s][nt][2]);
+                        sc[s][nt][3] = fmaf(ks.y, d[3], sc[s][nt][3]);
+                    }
+                }
+            }
+        }
+        if (PAIR > 1) {   // the other half of the dims is the other warp's; buffers alternate by stage
+            float4* mine = reinterpret_cast<float4*>(ring + C::kRing + C::kScales + C::kProbs) + stage * kStepTiles * NT * 32;
+            float4* other = mine + (member ? -1 : 1) * (C::kWarpBytes / 16);
+#pragma unroll
+            for (int s = 0; s < kStepTiles; ++s)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sc[s][nt][k] *= cmul[nt][k & 1];   // the members' powers of two differ
+                    mine[(s * NT + nt) * 32 + lane] = make_float4(sc[s][nt][0], sc[s][nt][1], sc[s][nt][2], sc[s][nt][3]);
+                }
+            asm volatile("bar.sync %0, 64;" ::"r"(1 + warp / PAIR) : "memory");
+#pragma unroll
+            for (int s = 0; s < kStepTiles; ++s)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float4 o = other[(s * NT + nt) * 32 + lane];
+                    sc[s][nt][0] += o.x, sc[s][nt][1] += o.y, sc[s][nt][2] += o.z, sc[s][nt][3] += o.w;
+                }
+        }
+
+        // p: in log2 units; PACK: the two halves' sums, lanes t < 2 keep row g, the others row g + 8
+        constexpr int NV = PACK ? 2 : 4;
+        float x[kStepTiles][NT][NV];
+        bool up = false;
+#pragma unroll
+        for (int s = 0; s < kStepTiles; ++s)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                if (PACK) {
+                    const float g0 = t < 2 ? sc[s][nt][2] : sc[s][nt][0], g1 = t < 2 ? sc[s][nt][3] : sc[s][nt][1];
+                    const float k0 = t < 2 ? sc[s][nt][0] : sc[s][nt][2], k1 = t < 2 ? sc[s][nt][1] : sc[s][nt][3];
+                    x[s][nt][0] = (k0 + __shfl_xor_sync(0xffffffffu, g0, 2)) * (PAIR > 1 ? 1.f : cmul[nt][0]);
+                    x[s][nt][1] = (k1 + __shfl_xor_sync(0xffffffffu, g1, 2)) * (PAIR > 1 ? 1.f : cmul[nt][1]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < NV; ++k) x[s][nt][k] = sc[s][nt][k] * (PAIR > 1 ? 1.f : cmul[nt][k & 1]);
+                }
+                if (!clean) {
+#pragma unroll
+                    for (int k = 0; k < NV; ++k) {
+                        const int pos = pos0 + s * kTileTokens + g + (PACK ? (t >> 1) : (k >> 1)) * 8;
+                        const int p = prow[nt][k & 1];
+                        const bool in = pos <= p && (P.window == 0 || pos > p - P.window) && !(gone >> s & 1);
+                        if (!in) x[s][nt][k] = -INFINITY;
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < NV; ++k) up |= x[s][nt][k] > m[nt][k & 1];
+            }
+        if (__any_sync(0xffffffffu, up) || e_step < E) {   // new maxima, or larger scales: rescale the sums
+            const int e_new = min(E, e_step);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float corr[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float mx = m[nt][k];
+#pragma unroll
+                    for (int s = 0; s < kStepTiles; ++s)
+#pragma unroll
+                        for (int v = k; v < NV; v += 2) mx = fmaxf(mx, x[s][nt][v]);
+#pragma unroll
+                    for (int o = PACK ? 2 : 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    corr[k] = (m[nt][k] == mx ? 1.f : ex2(m[nt][k] - mx)) * pow2(e_new - E);
+                    m[nt][k] = mx;
+                    l[nt][k] *= corr[k];
+                }
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        acc[b][j][nt][0] *= corr[0], acc[b][j][nt][1] *= corr[1];
+                        acc[b][j][nt][2] *= corr[0], acc[b][j][nt][3] *= corr[1];
+                    }
+                }
+            }
+            E = e_new;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const float mb[2] = {m[nt][0] == -INFINITY ? 0.f : m[nt][0] - E, m[nt][1] == -INFINITY ? 0.f : m[nt][1] - E};
+#pragma unroll
+            for (int s = 0; s < kStepTiles; ++s)
+#pragma unroll
+                for (int k = 0; k < NV; ++k) {
+                    const float p = ex2(x[s][nt][k] - mb[k & 1]);
+                    l[nt][k & 1] += p;
+                    probs[col_row(nt, k & 1) * kProbRow + s * kTileTokens + g + (PACK ? (t >> 1) : (k >> 1)) * 8] = p;
+                }
+        }
+        __syncwarp();
+
+        // values
+        const uint32_t flip = !PACK || g >= 4 ? 0x80000000u : 0u;
+        const float2 keep = !PACK || g >= 4 ? make_float2(1.f, 1.f) : make_float2(0.f, 0.f);
+#pragma unroll
+        for (int s = 0; s < kStepTiles; ++s) {
+            float2 pr[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const float* row = probs + (PACK ? g & 3 : nt * 8 + g) * kProbRow + s * kTileTokens + 2 * t;
+                pr[nt][0] = *reinterpret_cast<const float2*>(row);
+                pr[nt][1] = *reinterpret_cast<const float2*>(row + 8);
+            }
+            const uint32_t codes = smem_u32(st + s * C::kTile + codes_off(C::kDims, 1)) + lane * 16;
+#pragma unroll
+            for (int b2 = 0; b2 < NB; b2 += 2) {
+                uint32_t w[4];
+                ldmatrix_x4_trans(w[0], w[1], w[2], w[3], codes + b2 * 256);
+#pragma unroll
+                for (int b = b2; b < b2 + 2; ++b) {
+                    const uint32_t wa = w[2 * (b - b2)], wb = w[2 * (b - b2) + 1];
+                    const float4 vs = reinterpret_cast<const float4*>(scales + (s * NB + b) * 32 + 16)[t];
+                    const Codes ca = codes_of(wa), cb = codes_of(wb);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float2 v0 = fmul2(pr[nt][0], make_float2(vs.x, vs.y));
+                        float2 v1 = fmul2(pr[nt][1], make_float2(vs.z, vs.w));
+                        if (!clean) {   // a row leaves out a position whatever V's scale is there
+                            v0.x = pr[nt][0].x == 0.f ? 0.f : v0.x, v0.y = pr[nt][0].y == 0.f ? 0.f : v0.y;
+                            v1.x = pr[nt][1].x == 0.f ? 0.f : v1.x, v1.y = pr[nt][1].y == 0.f ? 0.f : v1.y;
+                        }
+                        // hi: the leading 11 bits; lo: what they leave.  PACK: this lane's column is one of the two
+                        const float2 r0 = ffma2(v0, keep, make_float2(lead(v0.x, flip), lead(v0.y, flip)));
+                        const float2 r1 = ffma2(v1, keep, make_float2(lead(v1.x, flip), lead(v1.y, flip)));
+                        const uint32_t lo0 = pack_rn(r0.x, r0.y), lo1 = pack_rn(r1.x, r1.y);
+                        if (!PACK) {
+                            const uint32_t hi0 = pack_rz(v0.x, v0.y), hi1 = pack_rz(v1.x, v1.y);
+                            mma_16816(acc[b][0][nt], ca.v[0], ca.v[1], cb.v[0], cb.v[1], hi0, hi1);
+                            mma_16816(acc[b][1][nt], ca.v[2], ca.v[3], cb.v[2], cb.v[3], hi0, hi1);
+                        }
+                        mma_16816(acc[b][0][nt], ca.v[0], ca.v[1], cb.v[0], cb.v[1], lo0, lo1);
+                        mma_16816(acc[b][1][nt], ca.v[2], ca.v[3], cb.v[2], cb.v[3], lo0, lo1);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    };
+
+    // ---- the share ----
+    int64_t tail = -1;
+    if (begin < end) {
+        put.seek(P, plan, begin);
+        get = put;
+        for (int i = 0; i < kStages && put_step < end; ++i) request_step(i);
+        int stage = 0;
+        uint32_t parity = 0;
+        bool fresh = true;
+        for (int64_t step = begin; step < end; ++step) {
+            const Unit un(P, get);
+            if (fresh) begin_unit(un);
+            if (!dead) {
+                dead = __any_sync(0xffffffffu, !mbar_wait(&bars[stage], parity, P.status));
+                if (dead && lane == 0)   // a copy never landed: give those in flight a bounded chance to
+                    for (int i = 0; i < kStages; ++i)
+                        (void)mbar_wait(&bars[(stage + i) % kStages], parity ^ (stage + i >= kStages ? 1u : 0u), nullptr);
+            }
+            const int pos0 = (get.r.tile0 + get.i * kStepTiles) * kTileTokens;
+            if (!dead) {
+                if (pos0 <= un.hi_all && pos0 + kStepTokens > un.lo_all) compute(stage, un, pos0);
+                else if (PAIR > 1) asm volatile("bar.sync %0, 64;" ::"r"(1 + warp / PAIR) : "memory");
+                if (put_step < end) request_step(stage);
+            } else {   // leave without touching the outputs
+                if (PAIR > 1) asm volatile("bar.sync %0, 64;" ::"r"(1 + warp / PAIR) : "memory");
+            }
+            if (++stage == kStages) stage = 0, parity ^= 1;
+            const bool first = get.i == step - begin || step - begin > get.i;   // the unit began in this share
+            fresh = get.i == get.r.steps - 1;
+            if (fresh && !dead) {
+                if (first) {   // the whole unit
+                    float* rows = P.out + static_cast<int64_t>(un.h) * P.G * D;
+                    const int64_t row0 = get.r.row0 + un.j0;
+                    finish([&](int row, int dim, float2 v, float sum) {
+                        const int tok = row / P.G;
+                        if (tok >= un.tokens) return;
+                        float* o = rows + (row0 + tok) * P.ldo + (row - tok * P.G) * D + dim;
+                        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                        o[0] = v.x * inv, o[1] = v.y * inv;
+                    }, [](int, float, float) {});
+                } else {
+                    float* slot = P.part + static_cast<int64_t>(worker) * Part<D, ROWS>::kFloats;
+                    finish([&](int row, int dim, float2 v, float) { *reinterpret_cast<float2*>(slot + row * D + dim) = v; },
+                           [&](int row, float mx, float sum) {
+                               if (member == 0) slot[ROWS * D + 2 * row] = mx, slot[ROWS * D + 2 * row + 1] = sum;
+                           });
+                }
+            } else if (step == end - 1) {
+                tail = step - get.i;
+            }
+            if (step < end - 1) get.next(P, plan);
+        }
+        if (dead) tail = -1;
+    }
+    // units that go on in the next share: join the parts of this CTA's workers (the rings are empty now)
+    constexpr int kLocal = C::kRing / 4;
+    if (tail >= 0) {
+        __syncwarp();
+        float* mine = reinterpret_cast<float*>(ring);
+        finish([&](int row, int dim, float2 v, float) {
+                   *reinterpret_cast<float2*>(mine + row * C::kDims + (dim - member * C::kDims)) = v;
+               },
+               [&](int row, float mx, float sum) {
+                   mine[ROWS * C::kDims + 2 * row] = mx, mine[ROWS * C::kDims + 2 * row + 1] = sum;
+               });
+    }
+    static_assert(ROWS * (C::kDims + 2) <= kLocal, "a partial result fits the ring");
+    if (lane == 0) tail_unit[warp] = tail;
+    __syncthreads();
+    for (int f = 0; f < kWarps; f += PAIR) {
+        const int64_t id = tail_unit[f];
+        if (id < 0 || (f > 0 && tail_unit[f - PAIR] == id)) continue;
+        int last = f;
+        while (last + PAIR < kWarps && tail_unit[last + PAIR] == id) last += PAIR;
+        float* slot = P.part + (static_cast<int64_t>(P.workers) + blockIdx.x * C::kWorkers + f / PAIR) * Part<D, ROWS>::kFloats;
+        for (int i = threadIdx.x; i < ROWS * D / 2; i += kThreads) {
+            const int row = i / (D / 2), dim = i % (D / 2) * 2;
+            const int half = dim / C::kDims, at = dim % C::kDims;
+            float mx = -INFINITY, sum = 0.f;
+            float2 v = make_float2(0.f, 0.f);
+            for (int w = f; w <= last; w += PAIR)
+                mx = fmaxf(mx, reinterpret_cast<const float*>(smem + w * C::kWarpBytes)[ROWS * C::kDims + 2 * row]);
+            for (int w = f; w <= last; w += PAIR) {
+                const float* ml = reinterpret_cast<const float*>(smem + w * C::kWarpBytes) + ROWS * C::kDims + 2 * row;
+                const float* o = reinterpret_cast<const float*>(smem + (w + half) * C::kWarpBytes) + row * C::kDims + at;
+                const float c = ml[0] == mx ? 1.f : ex2(ml[0] - mx);
+                sum = fmaf(c, ml[1], sum);
+                v.x = fmaf(c, o[0], v.x), v.y = fmaf(c, o[1], v.y);
+            }
+            *reinterpret_cast<float2*>(slot + row * D + dim) = v;
+            if (dim == 0) slot[ROWS * D + 2 * row] = mx, slot[ROWS * D + 2 * row + 1] = sum;
+        }
     }
 }
+
+// Joins the parts of units that cross CTAs: one warp a query row and head.  The parts lie in order: one
+// for each CTA whose workers the unit goes on from, then the last worker's own.
+template <int D>
+__global__ void __launch_bounds__(128) kv4_attn_merge_kernel(const AttnParams P, int rows, int cta_workers) {
+    pdl_wait_trigger();
+    const int lane = threadIdx.x & 31;
+    const int64_t unit = blockIdx.x * 4ll + (threadIdx.x >> 5);
+    const int64_t t = unit / P.n_q;
+    if (t >= P.T) return;
+    const int head = static_cast<int>(unit % P.n_q);
+    // the request whose rows hold t (requests that were refused have no steps)
+    int lo = 0, hi = P.B;          // cu[lo] <= t < cu[hi]
+    if (t < P.cu[0] || t >= P.cu[P.B]) return;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (P.cu[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    const int64_t steps0 = P.plan[lo], steps1 = P.plan[lo + 1], total = P.plan[P.B];
+    Request r;
+    if (steps0 == steps1 || !request_of(P, lo, r) || t - r.row0 >= r.n) return;
+    const int j = static_cast<int>(t - r.row0), h = head / P.G;
+    const int64_t s0 = steps0 + (static_cast<int64_t>(h) * r.groups + j / P.GT) * r.steps, s1 = s0 + r.steps;
+    const int64_t share = (total + P.workers - 1) / P.workers;
+    const int64_t w0 = s0 / share, w1 = (s1 - 1) / share;
+    if (w0 == w1) return;          // written by its worker
+    const int row = j % P.GT * P.G + head % P.G;
+    const int64_t floats = static_cast<int64_t>(rows) * (D + 2);
+    const int64_t c0 = w0 / cta_workers, c1 = (w1 - 1) / cta_workers;
+    const int parts = static_cast<int>(c1 - c0 + 2);
+    auto slot = [&](int k) {
+        const int64_t c = c0 + k;
+        return P.part + (c > c1 ? w1 : P.workers + max(w0, c * cta_workers)) * floats;
+    };
+    float mx = -INFINITY;
+    for (int k = lane; k < parts; k += 32) mx = fmaxf(mx, slot(k)[rows * D + 2 * row]);
+    mx = warp_max(mx);
+    float sum = 0.f, v[D / 32];
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) v[e] = 0.f;
+    for (int k = 0; k < parts; ++k) {
+        const float* s = slot(k);
+        const float2 ml = *reinterpret_cast<const float2*>(s + rows * D + 2 * row);
+        const float c = ml.x == mx ? 1.f : ex2(ml.x - mx);
+        sum = fmaf(c, ml.y, sum);
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) v[e] = fmaf(c, s[row * D + e * 32 + lane], v[e]);
+    }
+    float* o = P.out + t * P.ldo + static_cast<int64_t>(head) * D;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) o[e * 32 + lane] = v[e] * inv;
+}
+
+// ---- host ------------------------------------------------------------------------------------------
+
+struct Variant {
+    const void *kernel, *merge;
+    int rows, ctas, cta_workers, part_floats;
+    size_t (*smem)(int);
+};
+
+template <int D, int NT, bool PACK, int CTAS>
+Variant variant() {
+    using C = Cfg<D, NT, PACK>;
+    return {reinterpret_cast<const void*>(kv4_attn_kernel<D, NT, PACK, CTAS>),
+            reinterpret_cast<const void*>(kv4_attn_merge_kernel<D>), C::kRows, CTAS, C::kWorkers,
+            Part<D, C::kRows>::kFloats, C::smem};
+}
+
+// Query rows a unit has: one token's heads, or as many tokens as the batch brings on average while
+// the sums of a warp stay in registers.
+Variant pick(int64_t T, int B, int G, int d) {
+    const int64_t tokens = std::max<int64_t>(1, (T + B - 1) / std::max(B, 1));
+    const int64_t want = tokens * G;
+    switch (d) {
+        case 64: return want <= 4 ? variant<64, 1, true, 2>() : want <= 8 ? variant<64, 1, false, 2>() : variant<64, 2, false, 1>();
+        case 128: return want <= 4 ? variant<128, 1, true, 2>() : want <= 8 ? variant<128, 1, false, 1>() : variant<128, 2, false, 1>();
+        case 256: return want <= 4 ? variant<256, 1, true, 1>() : variant<256, 1, false, 1>();
+        default: return want <= 4 ? variant<512, 1, true, 1>() : variant<512, 1, false, 1>();
+    }
+}
+
+// Once for each kernel and device: the dynamic shared memory of the largest batch.
+gem_status allow_smem(const void* kernel, const DeviceInfo& di, size_t bytes) {
+    static std::mutex mu;
+    static std::set<std::pair<int, const void*>> done;
+    std::lock_guard<std::mutex> lk(mu);
+    if (done.count({di.device, kernel})) return GEM_OK;
+    GEM_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      static_cast<int>(std::min(bytes, di.smem_optin))));
+    done.insert({di.device, kernel});
+    return GEM_OK;
+}
+
+size_t plan_bytes(int B) { return align_up((B + 1) * sizeof(int64_t), 256); }
 
 }  // namespace
 }  // namespace kv4
@@ -134,8 +859,15 @@ __global__ void __launch_bounds__(128) kv4_attn_rows_kernel(const AttnParams P) 
 extern "C" {
 
 size_t gem_kv4_attn_workspace(int64_t T, int B, int n_q, int n_kv, int d) {
-    (void)T, (void)B, (void)n_q, (void)n_kv, (void)d;
-    return 0;
+    using namespace gem;
+    using namespace gem::kv4;
+    if (T <= 0 || B <= 0 || B > kMaxRequests || n_q <= 0 || n_kv <= 0 || n_q % n_kv || n_q / n_kv > kMaxGroup ||
+        !head_dim_ok(d))
+        return 0;
+    DeviceInfo di;
+    if (device_info(&di) != GEM_OK) return 0;
+    const Variant v = pick(T, B, n_q / n_kv, d);
+    return plan_bytes(B) + align_up(2ull * di.num_sms * v.ctas * v.cta_workers * v.part_floats * sizeof(float), 256);
 }
 
 gem_status gem_kv4_attn(const float* q, int64_t ldq, int64_t T, const int32_t* cu_tokens, const int32_t* kv_len,
@@ -154,22 +886,32 @@ gem_status gem_kv4_attn(const float* q, int64_t ldq, int64_t T, const int32_t* c
     if (T == 0 || B == 0 || n_q == 0) return GEM_OK;
     if (!q || !out || !cu_tokens || !kv_len || (max_pages && !table)) return GEM_ERR_INVALID_ARG;
     if (ldq < static_cast<int64_t>(n_q) * d || ldo < static_cast<int64_t>(n_q) * d) return GEM_ERR_INVALID_ARG;
-    if ((reinterpret_cast<uintptr_t>(q) & 15) || ldq % 4) return GEM_ERR_MISALIGNED;
-    (void)workspace, (void)ws_bytes;
+    if ((reinterpret_cast<uintptr_t>(q) & 15) || ldq % 4 || (reinterpret_cast<uintptr_t>(workspace) & 255))
+        return GEM_ERR_MISALIGNED;
+    DeviceInfo di;
+    if ((st = device_info(&di)) != GEM_OK) return st;
+    const Variant v = pick(T, B, n_q / n_kv, d);
+    if (!workspace || ws_bytes < gem_kv4_attn_workspace(T, B, n_q, n_kv, d)) return GEM_ERR_WORKSPACE;
     AttnParams P{};
     P.q = q, P.ldq = ldq, P.T = T, P.cu = cu_tokens, P.kv_len = kv_len;
-    P.B = B, P.n_q = n_q, P.n_kv = n_kv, P.G = n_q / n_kv;
+    P.B = B, P.n_q = n_q, P.n_kv = n_kv, P.G = n_q / n_kv, P.GT = v.rows / P.G;
     P.table = table, P.max_pages = max_pages, P.pool = static_cast<const uint8_t*>(pool), P.n_pages = n_pages;
-    P.page = page, P.lpage = log2_of(page), P.window = window, P.scale = scale;
-    P.out = out, P.ldo = ldo, P.status = status;
-    if ((st = flag_word(&P.status)) != GEM_OK) return st;
-    const void* kernel = d == 64    ? reinterpret_cast<const void*>(kv4_attn_rows_kernel<64>)
-                         : d == 128 ? reinterpret_cast<const void*>(kv4_attn_rows_kernel<128>)
-                         : d == 256 ? reinterpret_cast<const void*>(kv4_attn_rows_kernel<256>)
-                                    : reinterpret_cast<const void*>(kv4_attn_rows_kernel<512>);
+    P.lpage = log2_of(page), P.window = window, P.scale = scale;
+    P.out = out, P.ldo = ldo, P.status = status ? status : di.status_word;
+    P.plan = static_cast<int64_t*>(workspace);
+    P.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan_bytes(B));
+    const int ctas = di.num_sms * v.ctas;
+    P.workers = ctas * v.cta_workers;
+    const size_t smem = v.smem(B);
+    const int64_t blocks = (T * n_q + 3) / 4;
+    if (smem > di.smem_optin || blocks > INT32_MAX) return GEM_ERR_UNSUPPORTED_SHAPE;
+    if ((st = allow_smem(v.kernel, di, v.smem(kMaxRequests))) != GEM_OK) return st;
     void* args[] = {&P};
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(T), static_cast<unsigned>(n_kv)), dim3(128), 0,
-                      static_cast<cudaStream_t>(stream), args);
+    if ((st = launch_pdl(v.kernel, dim3(ctas), dim3(kThreads), smem, static_cast<cudaStream_t>(stream), args)) != GEM_OK)
+        return st;
+    int rows = v.rows, cta_workers = v.cta_workers;
+    void* margs[] = {&P, &rows, &cta_workers};
+    return launch_pdl(v.merge, dim3(static_cast<unsigned>(blocks)), dim3(128), 0, static_cast<cudaStream_t>(stream), margs);
 }
 
 }  // extern "C"

@@ -615,3 +615,29 @@ def test_attention_on_two_streams_with_a_workspace_each(env):
     t.cuda.synchronize()
     for _, out, _, want in cases:
         assert_close(out.cpu().numpy(), want, "attention")
+
+
+def test_attention_reports_a_copy_that_never_lands(env):
+    """The first step of the first warp waits for 16 bytes more than its copies bring (nothing faults and
+    nothing hangs: the wait runs out after the limit set here), and the next call is right again."""
+    g, t = env
+    for n_q, n_kv, d in ((8, 2, 128), (8, 1, 512)):
+        r = np.random.RandomState(30)
+        kv_len, page = [200], 32
+        pool, table, cu, q = _attn_case(r, t, kv_len, [1], n_q, n_kv, d, page)
+        args = (pool, table, cu, q, kv_len, n_q, n_kv, d, page, 0, d ** -0.5)
+        status = t.zeros(1, dtype=t.int32, device="cuda")
+        t.cuda.synchronize()
+        g.set_wait_limit(1_000_000)
+        g.set_test_injection(g.INJECT_RING_SHORTFALL)
+        try:
+            _attn_run(g, t, *args, status=status)
+            t.cuda.synchronize()
+        finally:
+            g.set_test_injection(0)
+            g.set_wait_limit(0)
+        assert g.status_from_flags(int(status)) == 6
+        status.zero_()
+        got = _attn_run(g, t, *args, status=status)
+        assert int(status) == 0
+        assert_close(got, _attn_want(pool, table, cu, q, kv_len, n_q, n_kv, d, page, 0, d ** -0.5), "the call after")
