@@ -29,6 +29,7 @@
 #include <cmath>
 #include <mutex>
 #include <set>
+#include <type_traits>
 #include <utility>
 
 #include "gem_device.cuh"
@@ -87,49 +88,35 @@ __device__ __forceinline__ bool request_of(const AttnParams& P, int b, Request& 
     return true;
 }
 
-// A place in the sequence of all steps: request, unit of it, step of the unit.
-struct Walk {
-    int b, u, i;
-    Request r;
-    __device__ __forceinline__ void seek(const AttnParams& P, const int64_t* plan, int64_t step) {
-        int lo = 0, hi = P.B - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (plan[mid] <= step) lo = mid;
-            else hi = mid - 1;
-        }
-        b = lo;
-        request_of(P, b, r);
-        const int64_t in = step - plan[b];
-        u = static_cast<int>(in / r.steps);
-        i = static_cast<int>(in % r.steps);
-    }
-    __device__ __forceinline__ void next(const AttnParams& P, const int64_t* plan) {
-        if (++i < r.steps) return;
-        i = 0;
-        if (++u < P.n_kv * r.groups) return;
-        u = 0;
-        do ++b;
-        while (b < P.B && plan[b + 1] == plan[b]);
-        if (b < P.B) request_of(P, b, r);
-    }
-};
-
-// The query rows of a unit: tokens j0 .. j0 + tokens - 1 of the request, positions p0 on.
+// The query rows of unit u of request b: tokens j0 .. j0 + tokens - 1 of the request, positions p0 on.
 struct Unit {
-    int h, j0, tokens, p0;
+    int row0, h, j0, tokens, p0;
     int lo_all, hi_all;    // first and last position that any row attends
     int lo_max;            // from here to p0 every row attends
-    __device__ __forceinline__ Unit(const AttnParams& P, const Walk& w) {
-        h = w.u / w.r.groups;
-        j0 = (w.u - h * w.r.groups) * P.GT;
-        tokens = min(P.GT, w.r.n - j0);
-        p0 = w.r.L - w.r.n + j0;
+    int L, tile0, steps;   // of the request
+    __device__ __forceinline__ Unit(const AttnParams& P, int b, int u) {
+        Request r;
+        request_of(P, b, r);
+        h = u / r.groups;
+        j0 = (u - h * r.groups) * P.GT;
+        tokens = min(P.GT, r.n - j0);
+        row0 = r.row0 + j0;
+        p0 = r.L - r.n + j0;
         hi_all = p0 + tokens - 1;
         lo_all = P.window ? max(0, p0 - P.window + 1) : 0;
         lo_max = P.window ? max(0, hi_all - P.window + 1) : 0;
+        L = r.L, tile0 = r.tile0, steps = r.steps;
     }
 };
+
+// The unit after unit u of request b (b = B: none).
+__device__ __forceinline__ void next_unit(const AttnParams& P, const int64_t* plan, int steps, int& b, int& u) {
+    const int64_t units = (plan[b + 1] - plan[b]) / steps;
+    if (++u < units) return;
+    u = 0;
+    do ++b;
+    while (b < P.B && plan[b + 1] == plan[b]);
+}
 
 // ---- small pieces ----------------------------------------------------------------------------------
 
@@ -287,38 +274,46 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
     const int64_t share = (total + P.workers - 1) / P.workers;
     const int64_t begin = min(total, worker * share), end = min(total, begin + share);
 
-    Walk put, get;             // the step to request next, the step to compute next
+    // the step to request next: unit, steps left of it, first tile, and the tiles that its rows attend
+    int put_b = 0, put_u = 0, put_left = 0, put_tile = 0, put_lo = 0, put_hi = 0, put_h = 0, put_last_page = 0, put_steps = 1;
     int64_t put_step = begin;
-    int pbase = 0, pid = -1, pb = -1;   // table entries pbase .. pbase + 31 of request pb, one a lane
+    int pbase = 0, pid = -1;   // table entries pbase .. pbase + 31 of the request, one a lane
     uint32_t lost = 0;         // tiles of the ring's stages that hold nothing
     bool dead = false;
     const int lpt = P.lpage - 4;
+    constexpr uint32_t kMask = (1u << kStepTiles) - 1;
 
+    auto put_unit = [&](int i) {   // enter unit put_u of request put_b at its step i
+        const Unit un(P, put_b, put_u);
+        put_left = un.steps - i;
+        put_steps = un.steps;
+        put_tile = un.tile0 + i * kStepTiles;
+        put_lo = un.lo_all / kTileTokens, put_hi = un.hi_all / kTileTokens;
+        put_h = un.h;
+        put_last_page = (un.L - 1) >> P.lpage;
+        pbase = -64;
+    };
     auto request_step = [&](int stage) {
-        const Unit un(P, put);
-        const int tile = put.r.tile0 + put.i * kStepTiles + lane;
-        const bool want = lane < kStepTiles && tile >= un.lo_all / kTileTokens && tile <= un.hi_all / kTileTokens;
-        const int first = (put.r.tile0 + put.i * kStepTiles) >> lpt;
-        if (pb != put.b || first < pbase || first + kStepTiles - 1 > pbase + 31) {   // a step's tiles lie in at most as many pages
-            pb = put.b, pbase = first;
+        const int tile = put_tile + lane;
+        const bool want = lane < kStepTiles && tile >= put_lo && tile <= put_hi;
+        const int first = put_tile >> lpt;
+        if (first - pbase + kStepTiles - 1 > 31) {   // a step's tiles lie in at most as many pages
+            pbase = first;
             const int64_t at = pbase + lane;
-            pid = at < P.max_pages && at <= ((put.r.L - 1) >> P.lpage)
-                      ? P.table[put.b * P.max_pages + at] : -1;
+            pid = at < P.max_pages && at <= put_last_page ? P.table[put_b * P.max_pages + at] : -1;
         }
         const int32_t id = __shfl_sync(0xffffffffu, pid, ((tile >> lpt) - pbase) & 31);
-        const bool in = id >= 0 && id < P.n_pages;
-        if (want && !in) atomicOr(P.status, GEM_DEVFLAG_PAGE_RANGE);
-        const uint32_t have = __ballot_sync(0xffffffffu, want && in);
-        constexpr uint32_t kMask = (1u << kStepTiles) - 1;
+        const bool in = want && id >= 0 && id < P.n_pages;
+        const uint32_t have = __ballot_sync(0xffffffffu, in);
         lost = (lost & ~(kMask << (stage * kStepTiles))) | ((~have & kMask) << (stage * kStepTiles));
         if (lane == 0) {
             uint32_t bytes = __popc(have) * C::kTile;
-            if (test_inject() & GEM_INJECT_RING_SHORTFALL) bytes += worker == 0 && put_step == 0 ? 16 : 0;
+            if (put_step == 0 && (test_inject() & GEM_INJECT_RING_SHORTFALL)) bytes += 16;
             mbar_arrive_expect_tx(&bars[stage], bytes);
         }
         __syncwarp();
-        if (want && in) {
-            const uint8_t* src = P.pool + (((static_cast<int64_t>(id) * P.n_kv + un.h) << lpt) +
+        if (in) {
+            const uint8_t* src = P.pool + (((static_cast<int64_t>(id) * P.n_kv + put_h) << lpt) +
                                            (tile & ((1 << lpt) - 1))) * tile_bytes(D);
             const uint32_t dst = smem_u32(ring + stage * C::kStage + lane * C::kTile);
             if (PAIR == 1) {
@@ -330,9 +325,14 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
                 bulk_load(dst + 2 * kCodes, src + scales_off(D, 0) + member * kScale, kScale, &bars[stage]);
                 bulk_load(dst + 2 * kCodes + kScale, src + scales_off(D, 1) + member * kScale, kScale, &bars[stage]);
             }
+        } else if (want) {
+            atomicOr(P.status, GEM_DEVFLAG_PAGE_RANGE);
         }
-        ++put_step;
-        if (put_step < end) put.next(P, plan);
+        put_tile += kStepTiles;
+        if (++put_step < end && --put_left == 0) {
+            next_unit(P, plan, put_steps, put_b, put_u);
+            put_unit(0);
+        }
     };
 
     // state of the unit at hand
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
             const int row = PACK ? g & 3 : nt * 8 + g;
             const int tok = row / P.G;
             const bool live = tok < un.tokens;
-            const float* src = P.q + (un.j0 + tok + static_cast<int64_t>(get.r.row0)) * P.ldq +
+            const float* src = P.q + (un.row0 + tok + 0ll) * P.ldq +
                                (static_cast<int64_t>(un.h) * P.G + (row - tok * P.G)) * D + member * C::kDims + 4 * t;
             float x[NB][8], top = 0.f;
 #pragma unroll
@@ -449,10 +449,11 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
     };
 
     // ---- one step: kStepTiles tiles in stage `stage` ----
-    auto compute = [&](int stage, const Unit& un, int pos0) {
+    // (clean: every row of the unit attends every position of it)
+    auto compute = [&](int stage, auto clean_c, int pos0, int lo_all, int hi_all) {
+        constexpr bool clean = decltype(clean_c)::value;
         const uint8_t* st = ring + stage * C::kStage;
-        const uint32_t gone = (lost >> (stage * kStepTiles)) & ((1u << kStepTiles) - 1);
-        const bool clean = gone == 0 && pos0 >= un.lo_max && pos0 + kStepTokens - 1 <= un.p0;
+        const uint32_t gone = (lost >> (stage * kStepTiles)) & kMask;
         // scales in fp32: K's as pairs (row g, row g + 8), V's as quads (2t, 2t + 1, 2t + 8, 2t + 9)
 #pragma unroll
         for (int it = lane; it < kStepTiles * NB * 8; it += 32) {
@@ -472,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
             for (int k = 0; k < 4; ++k) {
                 if (!clean) {   // what no row attends may be anything
                     const int pos = pos0 + s * kTileTokens + 2 * r + (k & 1) + (k >> 1) * 8;
-                    if (pos < un.lo_all || pos > un.hi_all || (gone >> s & 1)) v[k] = 0.f;
+                    if (pos < lo_all || pos > hi_all || (gone >> s & 1)) v[k] = 0.f;
                 }
                 const uint32_t bits = __float_as_uint(v[k]) & 0x7fffffffu;
                 big = max(big, bits < 0x7f800000u ? bits : 0u);
@@ -663,40 +664,59 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
     // ---- the share ----
     int64_t tail = -1;
     if (begin < end) {
-        put.seek(P, plan, begin);
-        get = put;
-        for (int i = 0; i < kStages && put_step < end; ++i) request_step(i);
+        int b = 0, u, i;
+        {
+            int hi = P.B - 1;      // the last request that begins at or before the share
+            while (b < hi) {
+                const int mid = (b + hi + 1) >> 1;
+                if (plan[mid] <= begin) b = mid;
+                else hi = mid - 1;
+            }
+            Request r;
+            request_of(P, b, r);
+            u = static_cast<int>((begin - plan[b]) / r.steps);
+            i = static_cast<int>((begin - plan[b]) % r.steps);
+        }
+        put_b = b, put_u = u;
+        put_unit(i);
+        for (int k = 0; k < kStages && put_step < end; ++k) request_step(k);
         int stage = 0;
         uint32_t parity = 0;
-        bool fresh = true;
-        for (int64_t step = begin; step < end; ++step) {
-            const Unit un(P, get);
-            if (fresh) begin_unit(un);
-            if (!dead) {
-                dead = __any_sync(0xffffffffu, !mbar_wait(&bars[stage], parity, P.status));
-                if (dead && lane == 0)   // a copy never landed: give those in flight a bounded chance to
-                    for (int i = 0; i < kStages; ++i)
-                        (void)mbar_wait(&bars[(stage + i) % kStages], parity ^ (stage + i >= kStages ? 1u : 0u), nullptr);
+        int64_t step = begin;
+        while (step < end) {
+            const Unit un(P, b, u);
+            const int64_t unit_end = min(end, step + (un.steps - i));
+            const bool starts = i == 0, ends = step + (un.steps - i) <= end;
+            if (!ends) tail = step - i;
+            begin_unit(un);
+            int pos0 = (un.tile0 + i * kStepTiles) * kTileTokens;
+            for (; step < unit_end; ++step, pos0 += kStepTokens) {
+                if (!dead) {
+                    dead = __any_sync(0xffffffffu, !mbar_wait(&bars[stage], parity, P.status));
+                    if (dead && lane == 0)   // a copy never landed: give those in flight a bounded chance to
+                        for (int k = 0; k < kStages; ++k)
+                            (void)mbar_wait(&bars[(stage + k) % kStages], parity ^ (stage + k >= kStages ? 1u : 0u), nullptr);
+                }
+                if (!dead) {
+                    if (((lost >> (stage * kStepTiles)) & kMask) == 0 && pos0 >= un.lo_max && pos0 + kStepTokens - 1 <= un.p0)
+                        compute(stage, std::true_type{}, pos0, un.lo_all, un.hi_all);
+                    else if (pos0 <= un.hi_all && pos0 + kStepTokens > un.lo_all)
+                        compute(stage, std::false_type{}, pos0, un.lo_all, un.hi_all);
+                    else if (PAIR > 1)
+                        asm volatile("bar.sync %0, 64;" ::"r"(1 + warp / PAIR) : "memory");
+                    if (put_step < end) request_step(stage);
+                } else if (PAIR > 1) {   // leave without touching the outputs
+                    asm volatile("bar.sync %0, 64;" ::"r"(1 + warp / PAIR) : "memory");
+                }
+                if (++stage == kStages) stage = 0, parity ^= 1;
             }
-            const int pos0 = (get.r.tile0 + get.i * kStepTiles) * kTileTokens;
-            if (!dead) {
-                if (pos0 <= un.hi_all && pos0 + kStepTokens > un.lo_all) compute(stage, un, pos0);
-                else if (PAIR > 1) asm volatile("bar.sync %0, 64;" ::"r"(1 + warp / PAIR) : "memory");
-                if (put_step < end) request_step(stage);
-            } else {   // leave without touching the outputs
-                if (PAIR > 1) asm volatile("bar.sync %0, 64;" ::"r"(1 + warp / PAIR) : "memory");
-            }
-            if (++stage == kStages) stage = 0, parity ^= 1;
-            const bool first = get.i == step - begin || step - begin > get.i;   // the unit began in this share
-            fresh = get.i == get.r.steps - 1;
-            if (fresh && !dead) {
-                if (first) {   // the whole unit
-                    float* rows = P.out + static_cast<int64_t>(un.h) * P.G * D;
-                    const int64_t row0 = get.r.row0 + un.j0;
+            if (ends && !dead) {
+                if (starts) {   // the whole unit
                     finish([&](int row, int dim, float2 v, float sum) {
                         const int tok = row / P.G;
                         if (tok >= un.tokens) return;
-                        float* o = rows + (row0 + tok) * P.ldo + (row - tok * P.G) * D + dim;
+                        float* o = P.out + (un.row0 + static_cast<int64_t>(tok)) * P.ldo +
+                                   (static_cast<int64_t>(un.h) * P.G + (row - tok * P.G)) * D + dim;
                         const float inv = sum == 0.f ? 0.f : 1.f / sum;
                         o[0] = v.x * inv, o[1] = v.y * inv;
                     }, [](int, float, float) {});
@@ -707,10 +727,9 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
                                if (member == 0) slot[ROWS * D + 2 * row] = mx, slot[ROWS * D + 2 * row + 1] = sum;
                            });
                 }
-            } else if (step == end - 1) {
-                tail = step - get.i;
             }
-            if (step < end - 1) get.next(P, plan);
+            i = 0;
+            if (step < end) next_unit(P, plan, un.steps, b, u);
         }
         if (dead) tail = -1;
     }
