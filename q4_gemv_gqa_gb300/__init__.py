@@ -392,7 +392,7 @@ def swiglu(gate: torch.Tensor, up: torch.Tensor, act: int, out: torch.Tensor,
 
 def _here(t: torch.Tensor, dtype, name: str, dim: int, device: int):
     """Pointer of a contiguous tensor of `dim` dimensions on the current device."""
-    if not t.is_cuda or t.get_device() != device:
+    if t.get_device() != device:   # -1 on the host
         raise ValueError("%s must be on the current CUDA device" % name)
     if t.dtype != dtype or t.dim() != dim or not t.is_contiguous():
         raise ValueError("%s must be contiguous %s with %d dimension(s), got %s %s" % (
@@ -403,12 +403,19 @@ def _here(t: torch.Tensor, dtype, name: str, dim: int, device: int):
 def _rows(t: torch.Tensor, cols: int, name: str, device: int):
     """(pointer, row stride) of an fp32 [rows, >= cols] tensor whose rows are contiguous; a column
     range of a wider tensor will do."""
-    if not t.is_cuda or t.get_device() != device:
+    if t.get_device() != device:
         raise ValueError("%s must be on the current CUDA device" % name)
-    if t.dtype != torch.float32 or t.dim() != 2 or t.shape[1] < cols or (t.shape[1] > 1 and t.stride(1) != 1):
+    rows, have = t.shape if t.dim() == 2 else (0, -1)
+    ld, step = t.stride() if have >= 0 else (0, 0)
+    if t.dtype != torch.float32 or have < cols or (step != 1 and have > 1):
         raise ValueError("%s must be fp32 [rows, >= %d] with contiguous rows, got %s %s strides %s" % (
             name, cols, t.dtype, tuple(t.shape), t.stride()))
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 3) // 4 * 4)
+    return t.data_ptr(), (ld if rows > 1 else (have + 3) // 4 * 4)
+
+
+def _stream_on(stream, device: int) -> int:
+    """Handle of `stream`, or of the current stream of `device` (the current one)."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def _status(status: torch.Tensor | None, device: int):
@@ -418,8 +425,8 @@ def _status(status: torch.Tensor | None, device: int):
 def _pool(pool: torch.Tensor, n_kv: int, d: int, page: int, device: int):
     """(pointer, pages) of a pool [n_pages, kv4_page_bytes(n_kv, d, page)]."""
     ptr = _here(pool, torch.uint8, "pool", 2, device)
-    need = lib.gem_kv4_page_bytes(n_kv, d, page)
-    if need and pool.shape[1] != need:
+    need = n_kv * d * page * 9 // 8   # the library rejects the sizes that have no pages
+    if pool.shape[1] != need:
         raise ValueError("pool must be [n_pages, %d] for %d KV heads of %d and pages of %d, got %s" % (
             need, n_kv, d, page, tuple(pool.shape)))
     return ptr, pool.shape[0]
@@ -452,7 +459,7 @@ def kv_block_tables(cached: torch.Tensor, fresh: torch.Tensor, page: int, table:
         _here(ring_in, i64, "ring_in", 1, dev), _here(ring_out, i64, "ring_out", 1, dev),
         _here(kv_len, i32, "kv_len", 1, dev), _here(cu_tokens, i32, "cu_tokens", 1, dev),
         _here(slot, i32, "slot", 1, dev), _here(pos, i32, "pos", 1, dev), _here(seq, i32, "seq", 1, dev), T,
-        _status(status, dev), _stream(stream))
+        _status(status, dev), _stream_on(stream, dev))
     _check(st, "gem_kv_block_tables")
 
 
@@ -476,7 +483,7 @@ def qknorm_mrope(qkv: torch.Tensor, n_q: int, n_kv: int, d: int, gamma_q: torch.
             raise ValueError("%s must be [d=%d]" % (name, d))
     st = lib.gem_qknorm_mrope(xp, ldx, T, n_q, n_kv, d, gp[0], gp[1], eps, _here(pos, torch.int32, "pos", 2, dev), T,
                               len(sections), (C.c_int32 * len(sections))(*sections), int(interleaved), theta, op,
-                              ldo, _status(status, dev), _stream(stream))
+                              ldo, _status(status, dev), _stream_on(stream, dev))
     _check(st, "gem_qknorm_mrope")
     return out
 
@@ -493,7 +500,7 @@ def kv4_append(k: torch.Tensor, v: torch.Tensor, n_kv: int, d: int, slot: torch.
     if v.shape[0] != T or slot.shape[0] != T:
         raise ValueError("k, v and slot must have the same number of rows")
     st = lib.gem_kv4_append(kp, ldk, vp, ldv, T, n_kv, d, _here(slot, torch.int32, "slot", 1, dev), pp, n_pages,
-                            page, _status(status, dev), _stream(stream))
+                            page, _status(status, dev), _stream_on(stream, dev))
     _check(st, "gem_kv4_append")
 
 
@@ -508,7 +515,7 @@ def kv4_gather(pool: torch.Tensor, page: int, n_kv: int, d: int, slot: torch.Ten
     if any(x is not None and x.shape[0] != T for x in (k, v)):
         raise ValueError("k and v must have one row for each slot")
     st = lib.gem_kv4_gather(pp, n_pages, page, n_kv, d, _here(slot, torch.int32, "slot", 1, dev), T, kp, ldk, vp,
-                            ldv, _status(status, dev), _stream(stream))
+                            ldv, _status(status, dev), _stream_on(stream, dev))
     _check(st, "gem_kv4_gather")
     return k, v
 
@@ -539,7 +546,7 @@ def kv4_attn(q: torch.Tensor, n_q: int, n_kv: int, d: int, cu_tokens: torch.Tens
                           _here(kv_len, torch.int32, "kv_len", 1, dev), B, n_q, n_kv, d,
                           _here(table, torch.int32, "table", 2, dev), table.shape[1], pp, n_pages, page, window,
                           scale, op, ldo, None if workspace is None else _here(workspace, torch.uint8, "workspace", 1, dev),
-                          0 if workspace is None else workspace.shape[0], _status(status, dev), _stream(stream))
+                          0 if workspace is None else workspace.shape[0], _status(status, dev), _stream_on(stream, dev))
     _check(st, "gem_kv4_attn")
     return out
 

@@ -60,7 +60,7 @@ struct AttnParams {
     float scale;
     float* out;
     int64_t ldo;
-    int64_t* plan;                // workspace: steps before request b, [B + 1]
+    int4* tasks;                  // workspace: one a worker, see the joining kernel
     float* part;                  // workspace: 2 slots a worker
     int workers;
     int* status;
@@ -88,6 +88,12 @@ __device__ __forceinline__ bool request_of(const AttnParams& P, int b, Request& 
     return true;
 }
 
+// a / b; the usual case in 32 bits
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 // The query rows of unit u of request b: tokens j0 .. j0 + tokens - 1 of the request, positions p0 on.
 struct Unit {
     int row0, h, j0, tokens, p0;
@@ -111,7 +117,7 @@ struct Unit {
 
 // The unit after unit u of request b (b = B: none).
 __device__ __forceinline__ void next_unit(const AttnParams& P, const int64_t* plan, int steps, int& b, int& u) {
-    const int64_t units = (plan[b + 1] - plan[b]) / steps;
+    const int64_t units = quotient(plan[b + 1] - plan[b], steps);
     if (++u < units) return;
     u = 0;
     do ++b;
@@ -167,7 +173,6 @@ __device__ __forceinline__ uint32_t pack_rn(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ float round_f16(float x) { return __half2float(__float2half_rn(x)); }
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -205,7 +210,7 @@ struct Cfg {
     static constexpr int kPartBytes = Part<D, kRows>::kFloats * 4;
     static constexpr int kRingNeed = (kPartBytes / kPair + 127) / 128 * 128;   // the ring later holds a partial result
     static constexpr int kRing = kStages * kStage > kRingNeed ? kStages * kStage : kRingNeed;
-    static constexpr int kScales = kStepTiles * kBlocks * 128;
+    static constexpr int kScales = kStepTiles * kBlocks * 192;   // fp32: K's 16 twice, V's 16
     static constexpr int kProbs = kRows * kProbRow * 4;
     static constexpr int kSwap = kPair > 1 ? 2 * kStepTiles * NT * 32 * 16 : 0;
     static constexpr int kWarpBytes = kRing + kScales + kProbs + kSwap;
@@ -268,10 +273,8 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
         __syncthreads();
     }
     __syncthreads();
-    if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b <= P.B; b += kThreads) P.plan[b] = plan[b];
     const int64_t total = plan[P.B];
-    const int64_t share = (total + P.workers - 1) / P.workers;
+    const int64_t share = quotient(total + P.workers - 1, P.workers);
     const int64_t begin = min(total, worker * share), end = min(total, begin + share);
 
     // the step to request next: unit, steps left of it, first tile, and the tiles that its rows attend
@@ -371,20 +374,16 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
             const float f = pow2(e);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                float y[2][8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float v = x[b][k] * f;
-                    y[0][k] = round_f16(v);
-                    y[1][k] = round_f16(v - y[0][k]);
-                    if (PACK) y[0][k] = g < 4 ? y[0][k] : y[1][k];
-                }
+                for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int hl = 0; hl < NH; ++hl)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        bq[b][j][nt][hl][0] = pack_rn(y[hl][j], y[hl][j + 2]);
-                        bq[b][j][nt][hl][1] = pack_rn(y[hl][4 + j], y[hl][6 + j]);
+                    for (int k = 0; k < 2; ++k) {
+                        const float v0 = x[b][4 * k + j] * f, v1 = x[b][4 * k + j + 2] * f;
+                        const uint32_t hi = pack_rn(v0, v1);
+                        const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+                        const uint32_t lo = pack_rn(v0 - h.x, v1 - h.y);
+                        bq[b][j][nt][0][k] = !PACK || g < 4 ? hi : lo;
+                        if (!PACK) bq[b][j][nt][NH - 1][k] = lo;
                     }
             }
             const float back = c * pow2(-e);
@@ -454,35 +453,37 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
         constexpr bool clean = decltype(clean_c)::value;
         const uint8_t* st = ring + stage * C::kStage;
         const uint32_t gone = (lost >> (stage * kStepTiles)) & kMask;
-        // scales in fp32: K's as pairs (row g, row g + 8), V's as quads (2t, 2t + 1, 2t + 8, 2t + 9)
+        // scales in fp32: K's as (row g, row g, row g + 8, row g + 8), V's as (2t, 2t + 1, 2t + 8, 2t + 9)
 #pragma unroll
-        for (int it = lane; it < kStepTiles * NB * 8; it += 32) {
-            const int s = it / (NB * 8), b = it / 8 % NB, r = it & 7;
+        for (int it = 0; it < kStepTiles * NB * 8; it += 32) {
+            const int at = it + lane, sb = at >> 3, r = at & 7, s = sb / NB, b = sb % NB;
             const __half* ks = reinterpret_cast<const __half*>(st + s * C::kTile + scales_off(C::kDims, 0)) + b * 16;
-            reinterpret_cast<float2*>(scales + (s * NB + b) * 32)[r] =
-                make_float2(__half2float(ks[r]), __half2float(ks[r + 8]));
+            const float k0 = __half2float(ks[r]), k1 = __half2float(ks[r + 8]);
+            reinterpret_cast<float4*>(scales + sb * 48)[r] = make_float4(k0, k0, k1, k1);
         }
-        uint32_t big = 0;
+        __half2 big2 = __float2half2_rn(0.f);
 #pragma unroll
-        for (int it = lane; it < kStepTiles * NB * 4; it += 32) {
-            const int s = it / (NB * 4), b = it / 4 % NB, r = it & 3;
-            const __half2* vs = reinterpret_cast<const __half2*>(st + s * C::kTile + scales_off(C::kDims, 1)) + b * 8;
-            const float2 a = __half22float2(vs[r]), c = __half22float2(vs[r + 4]);
-            float v[4] = {a.x, a.y, c.x, c.y};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
+        for (int it = 0; it < kStepTiles * NB * 4; it += 32) {
+            const int at = it + lane, sb = at >> 2, r = at & 3, s = sb / NB, b = sb % NB;
+            if (kStepTiles * NB * 4 % 32 == 0 || sb < kStepTiles * NB) {
+                const __half2* vs = reinterpret_cast<const __half2*>(st + s * C::kTile + scales_off(C::kDims, 1)) + b * 8;
+                __half2 v0 = vs[r], v1 = vs[r + 4];
                 if (!clean) {   // what no row attends may be anything
-                    const int pos = pos0 + s * kTileTokens + 2 * r + (k & 1) + (k >> 1) * 8;
-                    if (pos < lo_all || pos > hi_all || (gone >> s & 1)) v[k] = 0.f;
+                    const int pos = pos0 + s * kTileTokens + 2 * r;
+                    auto in = [&](int p) { return p >= lo_all && p <= hi_all && !(gone >> s & 1); };
+                    const __half zero = __float2half_rn(0.f);
+                    v0 = __halves2half2(in(pos) ? __low2half(v0) : zero, in(pos + 1) ? __high2half(v0) : zero);
+                    v1 = __halves2half2(in(pos + 8) ? __low2half(v1) : zero, in(pos + 9) ? __high2half(v1) : zero);
                 }
-                const uint32_t bits = __float_as_uint(v[k]) & 0x7fffffffu;
-                big = max(big, bits < 0x7f800000u ? bits : 0u);
+                big2 = __hmax2(big2, __hmax2(__habs2(v0), __habs2(v1)));   // a NaN is passed over
+                const float2 f0 = __half22float2(v0), f1 = __half22float2(v1);
+                reinterpret_cast<float4*>(scales + sb * 48 + 32)[r] = make_float4(f0.x, f0.y, f1.x, f1.y);
             }
-            reinterpret_cast<float4*>(scales + (s * NB + b) * 32 + 16)[r] = make_float4(v[0], v[1], v[2], v[3]);
         }
-        big = __reduce_max_sync(0xffffffffu, big);
-        // p 2^E sV stays below 2^15
-        const int e_step = min(60, 14 - (static_cast<int>(big >> 23) - 127));
+        // p 2^E sV stays below 2^15 (binary16 numbers that are not negative order as their bits do)
+        const uint32_t big = __reduce_max_sync(
+            0xffffffffu, static_cast<uint32_t>(__half_as_ushort(__hmax(__low2half(big2), __high2half(big2)))));
+        const int e_step = min(60, 29 - static_cast<int>(big >> 10));
         __syncwarp();
 
         // scores
@@ -501,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
 #pragma unroll
                 for (int b = b2; b < b2 + 2; ++b) {
                     const uint32_t wa = w[2 * (b - b2)], wb = w[2 * (b - b2) + 1];
-                    const float2 ks = reinterpret_cast<const float2*>(scales + (s * NB + b) * 32)[g];
+                    const float4 ks = reinterpret_cast<const float4*>(scales + (s * NB + b) * 48)[g];
                     const Codes ca = codes_of(wa), cb = codes_of(wb);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
@@ -512,10 +513,9 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
                             mma_16816(d, ca.v[0], cb.v[0], ca.v[1], cb.v[1], bq[b][0][nt][NH - 1][0], bq[b][0][nt][NH - 1][1]);
                             mma_16816(d, ca.v[2], cb.v[2], ca.v[3], cb.v[3], bq[b][1][nt][NH - 1][0], bq[b][1][nt][NH - 1][1]);
                         }
-                        sc[s][nt][0] = fmaf(ks.x, d[0], sc[s][nt][0]);
-                        sc[s][nt][1] = fmaf(ks.x, d[1], sc[s][nt][1]);
-                        sc[s][nt][2] = fmaf(ks.y, d[2], sc[s][nt][2]);
-                        sc[s][nt][3] = fmaf(ks.y, d[3], sc[s][nt][3]);
+                        float2* to = reinterpret_cast<float2*>(sc[s][nt]);
+                        to[0] = ffma2(make_float2(ks.x, ks.y), make_float2(d[0], d[1]), to[0]);
+                        to[1] = ffma2(make_float2(ks.z, ks.w), make_float2(d[2], d[3]), to[1]);
                     }
                 }
             }
@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
 #pragma unroll
                 for (int b = b2; b < b2 + 2; ++b) {
                     const uint32_t wa = w[2 * (b - b2)], wb = w[2 * (b - b2) + 1];
-                    const float4 vs = reinterpret_cast<const float4*>(scales + (s * NB + b) * 32 + 16)[t];
+                    const float4 vs = reinterpret_cast<const float4*>(scales + (s * NB + b) * 48 + 32)[t];
                     const Codes ca = codes_of(wa), cb = codes_of(wb);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
@@ -663,6 +663,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
 
     // ---- the share ----
     int64_t tail = -1;
+    int4 task = make_int4(-1, 0, 0, 0);
     if (begin < end) {
         int b = 0, u, i;
         {
@@ -674,8 +675,9 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
             }
             Request r;
             request_of(P, b, r);
-            u = static_cast<int>((begin - plan[b]) / r.steps);
-            i = static_cast<int>((begin - plan[b]) % r.steps);
+            const int64_t in = begin - plan[b], q = quotient(in, r.steps);
+            u = static_cast<int>(q);
+            i = static_cast<int>(in - q * r.steps);
         }
         put_b = b, put_u = u;
         put_unit(i);
@@ -721,6 +723,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
                         o[0] = v.x * inv, o[1] = v.y * inv;
                     }, [](int, float, float) {});
                 } else {
+                    task = make_int4(static_cast<int>(quotient(step - un.steps, share)), un.row0, un.tokens, un.h);
                     float* slot = P.part + static_cast<int64_t>(worker) * Part<D, ROWS>::kFloats;
                     finish([&](int row, int dim, float2 v, float) { *reinterpret_cast<float2*>(slot + row * D + dim) = v; },
                            [&](int row, float mx, float sum) {
@@ -731,8 +734,9 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
             i = 0;
             if (step < end) next_unit(P, plan, un.steps, b, u);
         }
-        if (dead) tail = -1;
+        if (dead) tail = task.x = -1;
     }
+    if (lane == 0 && member == 0) P.tasks[worker] = task;
     // units that go on in the next share: join the parts of this CTA's workers (the rings are empty now)
     constexpr int kLocal = C::kRing / 4;
     if (tail >= 0) {
@@ -774,58 +778,80 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
     }
 }
 
-// Joins the parts of units that cross CTAs: one warp a query row and head.  The parts lie in order: one
-// for each CTA whose workers the unit goes on from, then the last worker's own.
+// Joins the parts of units that cross shares: one CTA for each row of a unit and the workers of one CTA
+// of the first kernel.  A worker whose share holds the end of a unit that began earlier left a task:
+// the first worker of the unit, its first query row, its tokens, its KV head.  The parts lie in order:
+// one for each CTA whose workers the unit goes on from, then the last worker's own.  D / 4 threads hold
+// four dims each; the groups of so many threads take every kSlices-th part and are joined in order.
+constexpr int kMergeThreads = 256;
 template <int D>
-__global__ void __launch_bounds__(128) kv4_attn_merge_kernel(const AttnParams P, int rows, int cta_workers) {
+__global__ void __launch_bounds__(kMergeThreads) kv4_attn_merge_kernel(const AttnParams P, int rows, int cta_workers) {
+    constexpr int kCols = D / 4, kSlices = kMergeThreads / kCols, kAhead = 4;
+    __shared__ float4 v_s[kSlices][kCols];
+    __shared__ float2 ml_s[kSlices];
     pdl_wait_trigger();
-    const int lane = threadIdx.x & 31;
-    const int64_t unit = blockIdx.x * 4ll + (threadIdx.x >> 5);
-    const int64_t t = unit / P.n_q;
-    if (t >= P.T) return;
-    const int head = static_cast<int>(unit % P.n_q);
-    // the request whose rows hold t (requests that were refused have no steps)
-    int lo = 0, hi = P.B;          // cu[lo] <= t < cu[hi]
-    if (t < P.cu[0] || t >= P.cu[P.B]) return;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (P.cu[mid] <= t) lo = mid;
-        else hi = mid;
-    }
-    const int64_t steps0 = P.plan[lo], steps1 = P.plan[lo + 1], total = P.plan[P.B];
-    Request r;
-    if (steps0 == steps1 || !request_of(P, lo, r) || t - r.row0 >= r.n) return;
-    const int j = static_cast<int>(t - r.row0), h = head / P.G;
-    const int64_t s0 = steps0 + (static_cast<int64_t>(h) * r.groups + j / P.GT) * r.steps, s1 = s0 + r.steps;
-    const int64_t share = (total + P.workers - 1) / P.workers;
-    const int64_t w0 = s0 / share, w1 = (s1 - 1) / share;
-    if (w0 == w1) return;          // written by its worker
-    const int row = j % P.GT * P.G + head % P.G;
+    const int row = blockIdx.y, tok = row / P.G;
     const int64_t floats = static_cast<int64_t>(rows) * (D + 2);
-    const int64_t c0 = w0 / cta_workers, c1 = (w1 - 1) / cta_workers;
-    const int parts = static_cast<int>(c1 - c0 + 2);
-    auto slot = [&](int k) {
-        const int64_t c = c0 + k;
-        return P.part + (c > c1 ? w1 : P.workers + max(w0, c * cta_workers)) * floats;
-    };
-    float mx = -INFINITY;
-    for (int k = lane; k < parts; k += 32) mx = fmaxf(mx, slot(k)[rows * D + 2 * row]);
-    mx = warp_max(mx);
-    float sum = 0.f, v[D / 32];
+    const int col = threadIdx.x % kCols, slice = threadIdx.x / kCols;
+    const int lane = threadIdx.x & 31;
+    int4 mine = make_int4(-1, 0, 0, 0);
+    if (lane < cta_workers) mine = P.tasks[blockIdx.x * cta_workers + lane];
+    for (uint32_t todo = __ballot_sync(0xffffffffu, mine.x >= 0 && tok < mine.z); todo; todo &= todo - 1) {
+        const int from = __ffs(todo) - 1, w1 = blockIdx.x * cta_workers + from;
+        int4 task;
+        task.x = __shfl_sync(0xffffffffu, mine.x, from), task.y = __shfl_sync(0xffffffffu, mine.y, from);
+        task.w = __shfl_sync(0xffffffffu, mine.w, from);
+        const int w0 = task.x, c0 = w0 / cta_workers, c1 = (w1 - 1) / cta_workers, parts = c1 - c0 + 2;
+        float mx = -INFINITY, sum = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = slice; k0 < parts; k0 += kSlices * kAhead) {
+            float2 ml[kAhead], ol[kAhead], oh[kAhead];
 #pragma unroll
-    for (int e = 0; e < D / 32; ++e) v[e] = 0.f;
-    for (int k = 0; k < parts; ++k) {
-        const float* s = slot(k);
-        const float2 ml = *reinterpret_cast<const float2*>(s + rows * D + 2 * row);
-        const float c = ml.x == mx ? 1.f : ex2(ml.x - mx);
-        sum = fmaf(c, ml.y, sum);
+            for (int a = 0; a < kAhead; ++a) {
+                const int k = k0 + a * kSlices, c = c0 + k;
+                ml[a] = make_float2(-INFINITY, 0.f), ol[a] = oh[a] = make_float2(0.f, 0.f);
+                if (k < parts) {
+                    const float* s = P.part + (c > c1 ? w1 : P.workers + max(w0, c * cta_workers)) * floats;
+                    ml[a] = *reinterpret_cast<const float2*>(s + rows * D + 2 * row);
+                    ol[a] = *reinterpret_cast<const float2*>(s + row * D + 4 * col);
+                    oh[a] = *reinterpret_cast<const float2*>(s + row * D + 4 * col + 2);
+                }
+            }
+            float top = mx;
 #pragma unroll
-        for (int e = 0; e < D / 32; ++e) v[e] = fmaf(c, s[row * D + e * 32 + lane], v[e]);
+            for (int a = 0; a < kAhead; ++a) top = fmaxf(top, ml[a].x);
+            const float c = mx == top ? 1.f : ex2(mx - top);
+            mx = top;
+            sum *= c, v.x *= c, v.y *= c, v.z *= c, v.w *= c;
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a) {
+                const float f = ml[a].x == mx ? 1.f : ex2(ml[a].x - mx);
+                sum = fmaf(f, ml[a].y, sum);
+                v.x = fmaf(f, ol[a].x, v.x), v.y = fmaf(f, ol[a].y, v.y);
+                v.z = fmaf(f, oh[a].x, v.z), v.w = fmaf(f, oh[a].y, v.w);
+            }
+        }
+        v_s[slice][col] = v;
+        if (col == 0) ml_s[slice] = make_float2(mx, sum);
+        __syncthreads();
+        if (slice == 0) {
+            mx = ml_s[0].x;
+            for (int k = 1; k < kSlices; ++k) mx = fmaxf(mx, ml_s[k].x);
+            sum = 0.f, v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kSlices; ++k) {
+                const float f = ml_s[k].x == mx ? 1.f : ex2(ml_s[k].x - mx);
+                sum = fmaf(f, ml_s[k].y, sum);
+                const float4 o = v_s[k][col];
+                v.x = fmaf(f, o.x, v.x), v.y = fmaf(f, o.y, v.y), v.z = fmaf(f, o.z, v.z), v.w = fmaf(f, o.w, v.w);
+            }
+            float* o = P.out + (task.y + static_cast<int64_t>(tok)) * P.ldo +
+                       (static_cast<int64_t>(task.w) * P.G + (row - tok * P.G)) * D + 4 * col;
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            o[0] = v.x * inv, o[1] = v.y * inv, o[2] = v.z * inv, o[3] = v.w * inv;
+        }
+        __syncthreads();
     }
-    float* o = P.out + t * P.ldo + static_cast<int64_t>(head) * D;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) o[e * 32 + lane] = v[e] * inv;
 }
 
 // ---- host ------------------------------------------------------------------------------------------
@@ -869,7 +895,7 @@ gem_status allow_smem(const void* kernel, const DeviceInfo& di, size_t bytes) {
     return GEM_OK;
 }
 
-size_t plan_bytes(int B) { return align_up((B + 1) * sizeof(int64_t), 256); }
+size_t task_bytes(int workers) { return align_up(workers * sizeof(int4), 256); }
 
 }  // namespace
 }  // namespace kv4
@@ -886,7 +912,8 @@ size_t gem_kv4_attn_workspace(int64_t T, int B, int n_q, int n_kv, int d) {
     DeviceInfo di;
     if (device_info(&di) != GEM_OK) return 0;
     const Variant v = pick(T, B, n_q / n_kv, d);
-    return plan_bytes(B) + align_up(2ull * di.num_sms * v.ctas * v.cta_workers * v.part_floats * sizeof(float), 256);
+    const int workers = di.num_sms * v.ctas * v.cta_workers;
+    return task_bytes(workers) + align_up(2ull * workers * v.part_floats * sizeof(float), 256);
 }
 
 gem_status gem_kv4_attn(const float* q, int64_t ldq, int64_t T, const int32_t* cu_tokens, const int32_t* kv_len,
@@ -917,20 +944,20 @@ gem_status gem_kv4_attn(const float* q, int64_t ldq, int64_t T, const int32_t* c
     P.table = table, P.max_pages = max_pages, P.pool = static_cast<const uint8_t*>(pool), P.n_pages = n_pages;
     P.lpage = log2_of(page), P.window = window, P.scale = scale;
     P.out = out, P.ldo = ldo, P.status = status ? status : di.status_word;
-    P.plan = static_cast<int64_t*>(workspace);
-    P.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + plan_bytes(B));
     const int ctas = di.num_sms * v.ctas;
     P.workers = ctas * v.cta_workers;
+    P.tasks = static_cast<int4*>(workspace);
+    P.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + task_bytes(P.workers));
     const size_t smem = v.smem(B);
-    const int64_t blocks = (T * n_q + 3) / 4;
-    if (smem > di.smem_optin || blocks > INT32_MAX) return GEM_ERR_UNSUPPORTED_SHAPE;
+    if (smem > di.smem_optin) return GEM_ERR_UNSUPPORTED_SHAPE;
     if ((st = allow_smem(v.kernel, di, v.smem(kMaxRequests))) != GEM_OK) return st;
     void* args[] = {&P};
     if ((st = launch_pdl(v.kernel, dim3(ctas), dim3(kThreads), smem, static_cast<cudaStream_t>(stream), args)) != GEM_OK)
         return st;
     int rows = v.rows, cta_workers = v.cta_workers;
     void* margs[] = {&P, &rows, &cta_workers};
-    return launch_pdl(v.merge, dim3(static_cast<unsigned>(blocks)), dim3(128), 0, static_cast<cudaStream_t>(stream), margs);
+    return launch_pdl(v.merge, dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(rows)),
+                      dim3(kMergeThreads), 0, static_cast<cudaStream_t>(stream), margs);
 }
 
 }  // extern "C"
