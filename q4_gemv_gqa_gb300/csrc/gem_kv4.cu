@@ -13,7 +13,7 @@ struct RowsParams {
     const int32_t* slot;
     uint8_t* pool;
     int64_t n_slots;
-    int n_kv, d, nb;         // nb = d / 32
+    int n_kv, d, lnb;        // log2 of d / 32
     int lpage;               // log2 of the page size
     int vec_k, vec_v;        // rows may be read or written 16 bytes at a time
     int* status;
@@ -21,33 +21,31 @@ struct RowsParams {
 
 // Four threads hold one block of 32 values: thread u elements 4u .. 4u + 3 and 16 + 4u .. 16 + 4u + 3,
 // which are the low and the high nibbles of word u of the block's 16 bytes of codes.  The eight
-// blocks of a warp are eight consecutive tokens of one (K or V, head, block), so that the codes and
-// the scales of a prompt's tokens are written next to one another.
+// blocks of a warp are eight consecutive tokens of one part (K or V, head, block), so that the codes and
+// the scales of a prompt's tokens are written next to one another, and the warps of a CTA have
+// consecutive parts, so that it reads whole 1 KB pieces of the rows.
+constexpr int kRowThreads = 256;
 struct Place {
     int64_t t;
     int which, head, blk, u;
-    uint8_t *code, *scale;   // nullptr: nothing to do for this row
+    uint8_t *code, *scale;
 };
 
-__device__ __forceinline__ bool place_of(const RowsParams& P, int64_t gid, int* status, Place& o) {
-    o.u = static_cast<int>(gid & 3);
-    const int64_t g = gid >> 2;
-    const int per = 2 * P.n_kv * P.nb;
-    const int64_t rest = g >> 3;
-    const int part = static_cast<int>(rest % per);
-    o.t = (rest / per) * 8 + (g & 7);
-    if (o.t >= P.T) return false;
-    o.blk = part % P.nb;
-    o.head = part / P.nb % P.n_kv;
-    o.which = part / (P.nb * P.n_kv);
+__device__ __forceinline__ bool place_of(const RowsParams& P, Place& o) {
+    o.u = threadIdx.x & 3;
+    o.t = blockIdx.x * 8ll + ((threadIdx.x >> 2) & 7);
+    const int part = blockIdx.y * (kRowThreads / 32) + (threadIdx.x >> 5), half = P.n_kv << P.lnb;
+    if (o.t >= P.T || part >= 2 * half) return false;
+    o.which = part >= half;
+    o.head = (part - (o.which ? half : 0)) >> P.lnb;
+    o.blk = part & ((1 << P.lnb) - 1);
     const int32_t s = P.slot[o.t];
     if (s < 0 || s >= P.n_slots) {
-        if (s != -1 && part == 0 && o.u == 0) atomicOr(status, GEM_DEVFLAG_PAGE_RANGE);
+        if (s != -1 && part == 0 && o.u == 0) atomicOr(P.status, GEM_DEVFLAG_PAGE_RANGE);
         return false;
     }
-    const int page_tiles = (1 << P.lpage) / kTileTokens;
-    const int64_t tile = (static_cast<int64_t>(s >> P.lpage) * P.n_kv + o.head) * page_tiles +
-                         ((s & ((1 << P.lpage) - 1)) / kTileTokens);
+    const int lpt = P.lpage - 4;
+    const int64_t tile = ((static_cast<int64_t>(s >> P.lpage) * P.n_kv + o.head) << lpt) + ((s >> 4) & ((1 << lpt) - 1));
     const int row = s % kTileTokens;
     uint8_t* base = P.pool + tile * tile_bytes(P.d);
     o.code = base + codes_off(P.d, o.which) + (o.blk * kTileTokens + row) * 16 + o.u * 4;
@@ -76,11 +74,10 @@ __device__ __forceinline__ int code_of(float x, float s, float inv) {
     return min(max(static_cast<int>(q) + 8, 0), 15);
 }
 
-__global__ void __launch_bounds__(256) kv4_append_kernel(const RowsParams P) {
+__global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const RowsParams P) {
     pdl_wait_trigger();
-    const int64_t gid = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
     Place o;
-    const bool live = place_of(P, gid, P.status, o);
+    const bool live = place_of(P, o);
     float x[8];
     if (live) {
         const float* src = (o.which ? P.v + o.t * P.ldv : P.k + o.t * P.ldk) + o.head * P.d + o.blk * 32 + o.u * 4;
@@ -128,11 +125,10 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(const RowsParams P) {
     if (o.u == 0) *reinterpret_cast<__half*>(o.scale) = s16;
 }
 
-__global__ void __launch_bounds__(256) kv4_gather_kernel(const RowsParams P) {
+__global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const RowsParams P) {
     pdl_wait_trigger();
-    const int64_t gid = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x;
     Place o;
-    if (!place_of(P, gid, P.status, o)) return;
+    if (!place_of(P, o)) return;
     float* dst = o.which ? P.vo : P.ko;
     if (!dst) return;
     dst += o.t * (o.which ? P.ldv : P.ldk) + o.head * P.d + o.blk * 32 + o.u * 4;
@@ -158,11 +154,10 @@ bool vec_ok(const float* p, int64_t ld) { return !(reinterpret_cast<uintptr_t>(p
 gem_status rows_launch(const void* kernel, RowsParams& P, cudaStream_t stream) {
     const gem_status st = flag_word(&P.status);
     if (st != GEM_OK) return st;
-    const int64_t threads = (P.T + 7) / 8 * 8 * 4 * 2 * P.n_kv * P.nb;
-    const int64_t blocks = (threads + 255) / 256;
-    if (blocks > INT32_MAX) return GEM_ERR_UNSUPPORTED_SHAPE;
+    const int64_t x = (P.T + 7) / 8, y = (2ll * (P.n_kv << P.lnb) + kRowThreads / 32 - 1) / (kRowThreads / 32);
+    if (x > INT32_MAX || y > 65535) return GEM_ERR_UNSUPPORTED_SHAPE;
     void* args[] = {&P};
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, args);
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(x), static_cast<unsigned>(y)), dim3(kRowThreads), 0, stream, args);
 }
 
 }  // namespace
@@ -190,7 +185,7 @@ gem_status gem_kv4_append(const float* k, int64_t ldk, const float* v, int64_t l
     P.k = k, P.v = v, P.ldk = ldk, P.ldv = ldv, P.T = T, P.slot = slot;
     P.pool = static_cast<uint8_t*>(pool);
     P.n_slots = n_pages * page;
-    P.n_kv = n_kv, P.d = d, P.nb = d / 32, P.lpage = log2_of(page);
+    P.n_kv = n_kv, P.d = d, P.lnb = log2_of(d / 32), P.lpage = log2_of(page);
     P.vec_k = vec_ok(k, ldk), P.vec_v = vec_ok(v, ldv);
     P.status = status;
     return rows_launch(reinterpret_cast<const void*>(kv4_append_kernel), P, static_cast<cudaStream_t>(stream));
@@ -210,7 +205,7 @@ gem_status gem_kv4_gather(const void* pool, int64_t n_pages, int page, int n_kv,
     P.ko = k, P.vo = v, P.ldk = ldk, P.ldv = ldv, P.T = T, P.slot = slot;
     P.pool = static_cast<uint8_t*>(const_cast<void*>(pool));
     P.n_slots = n_pages * page;
-    P.n_kv = n_kv, P.d = d, P.nb = d / 32, P.lpage = log2_of(page);
+    P.n_kv = n_kv, P.d = d, P.lnb = log2_of(d / 32), P.lpage = log2_of(page);
     P.vec_k = vec_ok(k, ldk), P.vec_v = vec_ok(v, ldv);
     P.status = status;
     return rows_launch(reinterpret_cast<const void*>(kv4_gather_kernel), P, static_cast<cudaStream_t>(stream));

@@ -1,5 +1,6 @@
 // gem_mrope.cu — per-head QK-norm and rotary positions with one or several axes, for T tokens.
 #include <cmath>
+#include <type_traits>
 
 #include "gem_device.cuh"
 #include "gem_kv4.cuh"
@@ -49,7 +50,90 @@ __device__ __forceinline__ int row_state(const MropeParams& P, int64_t t) {
     return bad ? 2 : 0;
 }
 
-// One warp per (token, head).  Any even d and R.
+// The head dims that the library's layers have, with rows that can be read VW floats at a time.  A warp
+// takes `heads` heads of one token; its lanes hold pairs (i, i + R/2) (and, past the rotated dims, pairs of
+// kept ones), the same for every head, so the angles are taken once and a head is two loads, one
+// reduction and two stores, with kAhead heads under way.
+template <int D>
+__global__ void __launch_bounds__(256) mrope_rows_kernel(const MropeParams P, const __grid_constant__ MropeFreq F, int heads,
+                                                         int chunks) {
+    constexpr int NP = D / 64, VW = NP < 4 ? NP : 4, NC = NP / VW, kAhead = NP <= 4 ? 4 : 2;
+    using Vec = std::conditional_t<VW == 1, float, std::conditional_t<VW == 2, float2, float4>>;
+    pdl_wait_trigger();
+    const int lane = threadIdx.x & 31;
+    const uint32_t unit = blockIdx.x * 8u + (threadIdx.x >> 5);
+    const uint32_t token = unit / static_cast<uint32_t>(chunks);
+    const int64_t t = token;
+    if (t >= P.T) return;
+    const int chunk = static_cast<int>(unit - token * chunks);
+    const int state = row_state(P, t);
+    if (state) {
+        if (state == 2 && chunk == 0 && lane == 0) atomicOr(P.status, GEM_DEVFLAG_POS_RANGE);
+        return;
+    }
+    const int half = P.R / 2, h0 = chunk * heads, h1 = min(P.nheads, h0 + heads);
+    int at0[NC], at1[NC];
+    float co[NC][VW], si[NC][VW];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int j = (c * 32 + lane) * VW;
+        at0[c] = j < half ? j : half + j;
+        at1[c] = at0[c] + (j < half ? half : (D - P.R) / 2);
+#pragma unroll
+        for (int v = 0; v < VW; ++v) {
+            co[c][v] = 1.f, si[c][v] = 0.f;
+            if (j < half) turn_cos_sin(P, t, F.f[j + v], co[c][v], si[c][v]);
+        }
+    }
+    const float* x = P.x + t * P.ldx;
+    float* out = P.out + t * P.ldo;
+    auto load = [](const float* p, float (&to)[VW]) { *reinterpret_cast<Vec*>(to) = *reinterpret_cast<const Vec*>(p); };
+    for (int h = h0; h < h1; h += kAhead) {
+        alignas(16) float a[kAhead][NC][VW], b[kAhead][NC][VW];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (h + k < h1)
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    load(x + (h + k) * D + at0[c], a[k][c]);
+                    load(x + (h + k) * D + at1[c], b[k][c]);
+                }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            if (h + k >= h1) break;
+            const float* gamma = h + k < P.n_q ? P.gamma_q : P.gamma_k;
+            if (gamma) {
+                float ss = 0.f;
+#pragma unroll
+                for (int c = 0; c < NC; ++c)
+#pragma unroll
+                    for (int v = 0; v < VW; ++v) ss = fmaf(a[k][c][v], a[k][c][v], fmaf(b[k][c][v], b[k][c][v], ss));
+                const float r = rsqrtf(warp_sum(ss) * (1.f / D) + P.eps);
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    alignas(16) float g0[VW], g1[VW];
+                    load(gamma + at0[c], g0);
+                    load(gamma + at1[c], g1);
+#pragma unroll
+                    for (int v = 0; v < VW; ++v) a[k][c][v] *= r * g0[v], b[k][c][v] *= r * g1[v];
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                alignas(16) float y0[VW], y1[VW];
+#pragma unroll
+                for (int v = 0; v < VW; ++v) {
+                    y0[v] = fmaf(a[k][c][v], co[c][v], -b[k][c][v] * si[c][v]);
+                    y1[v] = fmaf(a[k][c][v], si[c][v], b[k][c][v] * co[c][v]);
+                }
+                *reinterpret_cast<Vec*>(out + (h + k) * D + at0[c]) = *reinterpret_cast<Vec*>(y0);
+                *reinterpret_cast<Vec*>(out + (h + k) * D + at1[c]) = *reinterpret_cast<Vec*>(y1);
+            }
+        }
+    }
+}
+
+// Any even d and R: one warp per (token, head), the head in shared memory.
 __global__ void __launch_bounds__(128) mrope_kernel(const MropeParams P, const __grid_constant__ MropeFreq F) {
     __shared__ float buf[4][kMaxHeadDim];
     pdl_wait_trigger();
@@ -90,6 +174,41 @@ __global__ void __launch_bounds__(128) mrope_kernel(const MropeParams P, const _
     for (int e = P.R + lane; e < P.d; e += 32) out[e] = sb[e];
 }
 
+// The frequencies are a function of these alone; a thread keeps the last ones it computed (a model's
+// layers ask for the same), since their powers cost more than the launch.
+struct FreqKey {
+    float theta;
+    int n_axes, interleaved;
+    int32_t sections[kMaxAxes];
+    bool operator==(const FreqKey& o) const {
+        return theta == o.theta && n_axes == o.n_axes && interleaved == o.interleaved &&
+               std::equal(sections, sections + kMaxAxes, o.sections);
+    }
+};
+
+const MropeFreq& frequencies(const FreqKey& key, int R) {
+    thread_local FreqKey last{};
+    thread_local MropeFreq F;
+    if (key == last) return F;
+    for (int i = 0, a = 0, left = key.sections[0]; i < R / 2; ++i) {
+        int axis;
+        if (key.interleaved) {
+            axis = i % key.n_axes;
+            if (axis && i >= key.n_axes * static_cast<int64_t>(key.sections[axis])) axis = 0;
+        } else {
+            while (left == 0) left = key.sections[++a];
+            --left;
+            axis = a;
+        }
+        // theta < 1 gives more than a turn a position: the whole turns drop out
+        const double turns = std::pow(static_cast<double>(key.theta), -2.0 * i / R) * 0.15915494309189535;
+        const double part = turns - std::floor(turns);
+        F.f[i] = ((static_cast<uint64_t>(std::ldexp(part, 63)) << 1) & ~3ull) | static_cast<uint64_t>(axis);
+    }
+    last = key;
+    return F;
+}
+
 }  // namespace
 }  // namespace kv4
 }  // namespace gem
@@ -120,23 +239,9 @@ extern "C" gem_status gem_qknorm_mrope(const float* qkv, int64_t ldqkv, int64_t 
     if (!qkv || !out || !pos || ldqkv < cols || ldo < cols || ldpos < T) return GEM_ERR_INVALID_ARG;
     if (out == qkv && ldo != ldqkv) return GEM_ERR_INVALID_ARG;
 
-    MropeFreq F;
-    for (int i = 0, a = 0, left = sections[0]; i < half; ++i) {
-        int axis;
-        if (interleaved) {
-            axis = i % n_axes;
-            if (axis && i >= n_axes * static_cast<int64_t>(sections[axis])) axis = 0;
-        } else {
-            while (left == 0) left = sections[++a];
-            --left;
-            axis = a;
-        }
-        // theta < 1 gives more than a turn a position: the whole turns drop out
-        const double turns = std::pow(static_cast<double>(theta), -2.0 * i / R) * 0.15915494309189535;
-        const double part = turns - std::floor(turns);
-        uint64_t f = static_cast<uint64_t>(std::ldexp(part, 63)) << 1;
-        F.f[i] = (f & ~3ull) | static_cast<uint64_t>(axis);
-    }
+    const FreqKey key{theta, n_axes, interleaved, {sections[0], n_axes > 1 ? sections[1] : 0, n_axes > 2 ? sections[2] : 0,
+                                                   n_axes > 3 ? sections[3] : 0}};
+    const MropeFreq& F = frequencies(key, R);
     MropeParams P{};
     P.x = qkv, P.ldx = ldqkv, P.out = out, P.ldo = ldo, P.T = T;
     P.n_q = n_q, P.nheads = n_q + n_kv, P.d = d, P.R = R;
@@ -144,9 +249,31 @@ extern "C" gem_status gem_qknorm_mrope(const float* qkv, int64_t ldqkv, int64_t 
     P.pos = pos, P.ldpos = ldpos, P.n_axes = n_axes, P.status = status;
     gem_status st = flag_word(&P.status);
     if (st != GEM_OK) return st;
+    // the vectorised kernel where every piece of a row can be read so many floats at a time
+    const int vw = std::min(4, d / 64);
+    auto aligned = [&](const float* p, int64_t ld) { return reinterpret_cast<uintptr_t>(p) % (4 * vw) == 0 && ld % vw == 0; };
+    if (head_dim_ok(d) && half % vw == 0 && aligned(qkv, ldqkv) && aligned(out, ldo) && aligned(gamma_q, 0) &&
+        aligned(gamma_k, 0)) {
+        DeviceInfo di;
+        if ((st = device_info(&di)) != GEM_OK) return st;
+        // eight heads a warp share its angles, fewer while that leaves SMs without 32 warps
+        const int64_t all = T * P.nheads, warps = 32ll * di.num_sms;
+        int heads = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, all / warps)));
+        int chunks = (P.nheads + heads - 1) / heads;
+        const int64_t blocks = (T * chunks + 7) / 8;
+        if (blocks <= INT32_MAX / 8) {
+            const void* kernel = d == 64    ? reinterpret_cast<const void*>(mrope_rows_kernel<64>)
+                                 : d == 128 ? reinterpret_cast<const void*>(mrope_rows_kernel<128>)
+                                 : d == 256 ? reinterpret_cast<const void*>(mrope_rows_kernel<256>)
+                                            : reinterpret_cast<const void*>(mrope_rows_kernel<512>);
+            void* vargs[] = {&P, const_cast<MropeFreq*>(&F), &heads, &chunks};
+            return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, static_cast<cudaStream_t>(stream),
+                              vargs);
+        }
+    }
     const int64_t blocks = (T * P.nheads + 3) / 4;
     if (blocks > INT32_MAX) return GEM_ERR_UNSUPPORTED_SHAPE;
-    void* args[] = {&P, &F};
+    void* args[] = {&P, const_cast<MropeFreq*>(&F)};
     return launch_pdl(reinterpret_cast<const void*>(mrope_kernel), dim3(static_cast<unsigned>(blocks)), dim3(128), 0,
                       static_cast<cudaStream_t>(stream), args);
 }
