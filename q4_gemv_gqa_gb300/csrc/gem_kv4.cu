@@ -74,6 +74,48 @@ __device__ __forceinline__ int code_of(float x, float s, float inv) {
     return min(max(static_cast<int>(q) + 8, 0), 15);
 }
 
+// NaN where either is
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// The four low bytes of four words.
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
+// The codes of a thread's eight values for scale s (not 0), a word.  The common case rounds x / s + 8 by
+// adding it to 1.5 * 2^23, whose low byte then is the code (16, a value opposite to the largest, becomes
+// 15); it stands where every remainder is below half a step, that is, where no value is on a border or
+// within the reciprocal's error of one, and where s is a normal number, so that no ratio is past 8.01.
+__device__ __forceinline__ uint32_t word_of(const float (&x)[8], float s) {
+    const float inv = 1.0f / s, base = 12582912.f + 8.f;
+    float worst = 0.f;
+    uint32_t t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float u = fmaf(x[i], inv, base);
+        worst = fmaxf(worst, fabsf(fmaf(base - u, s, x[i])));
+        t[i] = __float_as_uint(u);
+    }
+    if (worst < 0.5f * fabsf(s) && fabsf(s) >= 6.103515625e-5f && fabsf(s) < 65504.f) {
+        const uint32_t lo = low_bytes(t[0], t[1], t[2], t[3]), hi = low_bytes(t[4], t[5], t[6], t[7]);
+        return (lo - (lo >> 4 & 0x01010101u)) | ((hi - (hi >> 4 & 0x01010101u)) << 4);
+    }
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w |= static_cast<uint32_t>(code_of(x[i], s, inv) | (code_of(x[4 + i], s, inv) << 4)) << (8 * i);
+    return w;
+}
+
 __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const RowsParams P) {
     pdl_wait_trigger();
     Place o;
@@ -88,38 +130,41 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const RowsParam
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = 0.f;
     }
-    // the value of largest magnitude, the first of equal ones: magnitude, then 31 - index, then sign
-    // (a NaN's magnitude bits are above an infinity's)
-    uint64_t key = 0;
+    float top = x[0], low = x[0];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t bits = __float_as_uint(x[i]);
-        const uint32_t e = (i < 4 ? 0 : 16) + o.u * 4 + (i & 3);
-        const uint64_t k = (static_cast<uint64_t>(bits & 0x7fffffffu) << 32) | ((31u - e) << 1) | (bits >> 31);
-        key = k > key ? k : key;
-    }
+    for (int i = 1; i < 8; ++i) top = max_nan(top, x[i]), low = min_nan(low, x[i]);
 #pragma unroll
     for (int m = 1; m < 4; m <<= 1) {
-        const uint64_t k = __shfl_xor_sync(0xffffffffu, key, m);
-        key = k > key ? k : key;
+        top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, m));
+        low = min_nan(low, __shfl_xor_sync(0xffffffffu, low, m));
+    }
+    float m = top > -low ? top : low;            // the value of largest magnitude
+    const bool both = top == -low && top != 0.f;
+    if (__any_sync(0xffffffffu, both)) {         // of either sign: the first of them
+        int first = 32;
+#pragma unroll
+        for (int i = 7; i >= 0; --i)
+            if (fabsf(x[i]) == top) first = (i < 4 ? 0 : 16) + o.u * 4 + (i & 3);
+        int at = first;
+#pragma unroll
+        for (int s = 1; s < 4; s <<= 1) at = min(at, __shfl_xor_sync(0xffffffffu, at, s));
+        bool minus = false;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if ((i < 4 ? 0 : 16) + o.u * 4 + (i & 3) == at) minus = x[i] < 0.f;
+        const uint32_t quad = 0xfu << (threadIdx.x & 28);
+        const bool any_minus = (__ballot_sync(0xffffffffu, minus) & quad) != 0;
+        if (both) m = any_minus ? low : top;
     }
     if (!live) return;
-    const uint32_t mag = static_cast<uint32_t>(key >> 32);
     __half s16;
     uint32_t word = 0x88888888u;
-    if (mag >= 0x7f800000u) {
+    if (!(fabsf(m) < INFINITY)) {
         s16 = __ushort_as_half(0x7fff);
     } else {
-        const float m = __uint_as_float(mag | (static_cast<uint32_t>(key & 1) << 31));
         s16 = __float2half_rn(fminf(fmaxf(m * -0.125f, -65504.f), 65504.f));
         const float s = __half2float(s16);
-        if (s != 0.f) {
-            const float inv = 1.0f / s;
-            word = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                word |= static_cast<uint32_t>(code_of(x[i], s, inv) | (code_of(x[4 + i], s, inv) << 4)) << (8 * i);
-        }
+        if (s != 0.f) word = word_of(x, s);
     }
     *reinterpret_cast<uint32_t*>(o.code) = word;
     if (o.u == 0) *reinterpret_cast<__half*>(o.scale) = s16;
