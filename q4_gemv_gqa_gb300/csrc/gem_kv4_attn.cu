@@ -45,6 +45,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kStepTiles = 2;
 constexpr int kStepTokens = kStepTiles * kTileTokens;
 constexpr int kStages = 2;
+constexpr int kSlack = 6;                   // log2 of how far a score may pass the maximum in use
 constexpr int kProbRow = kStepTokens + 8;   // floats; 8 modulo 32 keeps the rows in banks of their own
 
 struct AttnParams {
@@ -100,9 +101,8 @@ struct Unit {
     int lo_all, hi_all;    // first and last position that any row attends
     int lo_max;            // from here to p0 every row attends
     int L, tile0, steps;   // of the request
-    __device__ __forceinline__ Unit(const AttnParams& P, int b, int u) {
-        Request r;
-        request_of(P, b, r);
+    int units;             // of the request
+    __device__ __forceinline__ Unit(const AttnParams& P, const Request& r, int u) {
         h = u / r.groups;
         j0 = (u - h * r.groups) * P.GT;
         tokens = min(P.GT, r.n - j0);
@@ -111,17 +111,21 @@ struct Unit {
         hi_all = p0 + tokens - 1;
         lo_all = P.window ? max(0, p0 - P.window + 1) : 0;
         lo_max = P.window ? max(0, hi_all - P.window + 1) : 0;
-        L = r.L, tile0 = r.tile0, steps = r.steps;
+        L = r.L, tile0 = r.tile0, steps = r.steps, units = r.groups * P.n_kv;
     }
 };
 
-// The unit after unit u of request b (b = B: none).
-__device__ __forceinline__ void next_unit(const AttnParams& P, const int64_t* plan, int steps, int& b, int& u) {
-    const int64_t units = quotient(plan[b + 1] - plan[b], steps);
-    if (++u < units) return;
-    u = 0;
-    do ++b;
-    while (b < P.B && plan[b + 1] == plan[b]);
+// The unit after unit u of request b, which has `units`; there is one.
+__device__ __forceinline__ Unit next_unit(const AttnParams& P, int units, int& b, int& u) {
+    Request r;
+    if (++u == units) {
+        u = 0;
+        do request_of(P, ++b, r);
+        while (r.n == 0 && b < P.B - 1);
+    } else {
+        request_of(P, b, r);
+    }
+    return Unit(P, r, u);
 }
 
 // ---- small pieces ----------------------------------------------------------------------------------
@@ -199,10 +203,10 @@ struct Part {
     static constexpr int kFloats = ROWS * (D + 2);
 };
 
-template <int D, int NT, bool PACK>
+template <int D, int NT, bool PACK, int DW>
 struct Cfg {
     static constexpr int kRows = PACK ? 4 : 8 * NT;      // query rows of a unit
-    static constexpr int kDims = D < 256 ? D : 256;      // dims of one warp
+    static constexpr int kDims = DW;                     // dims of one warp
     static constexpr int kPair = D / kDims;              // warps of a worker
     static constexpr int kBlocks = kDims / 32;
     static constexpr int kTile = tile_bytes(kDims);      // a tile's bytes in one warp's ring
@@ -215,19 +219,22 @@ struct Cfg {
     static constexpr int kSwap = kPair > 1 ? 2 * kStepTiles * NT * 32 * 16 : 0;
     static constexpr int kWarpBytes = kRing + kScales + kProbs + kSwap;
     static constexpr int kWorkers = kWarps / kPair;      // of a CTA
-    static size_t smem(int B) { return kWarps * static_cast<size_t>(kWarpBytes) + kWarps * kStages * 8 + (B + 1) * 8; }
+    static size_t smem(int B) {
+        return kWarps * static_cast<size_t>(kWarpBytes) + kWarps * kStages * 8 + (B > 32 ? (B + 1) * 8 : 0);
+    }
 };
 
 // ---- the kernel ------------------------------------------------------------------------------------
 
-template <int D, int NT, bool PACK, int CTAS>
+template <int D, int NT, bool PACK, int DW, int CTAS>
 __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnParams P) {
-    using C = Cfg<D, NT, PACK>;
+    using C = Cfg<D, NT, PACK, DW>;
     constexpr int NB = C::kBlocks, ROWS = C::kRows, PAIR = C::kPair;
     constexpr int NH = PACK ? 1 : 2;                     // B operands of a product: (hi | lo) or hi, lo
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t sums[kWarps];
-    __shared__ int64_t tail_unit[kWarps];
+    __shared__ int tail_unit[C::kWorkers];
+    __shared__ float weight[C::kWorkers * ROWS];
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
@@ -245,40 +252,73 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
     }
     pdl_wait_trigger();
 
-    // steps before each request
-    int64_t carry = 0;
-    if (threadIdx.x == 0) plan[0] = 0;
-    for (int base = 0; base < P.B; base += kThreads) {
-        const int b = base + threadIdx.x;
+    // this worker's share of all steps, and the request and unit that it begins in
+    Request r0;
+    int b0 = 0;
+    int64_t total, in_b0 = 0;
+    auto split = [&]() { return quotient(total + P.workers - 1, P.workers); };
+    if (P.B <= 32) {           // every warp for itself, a request a lane
         Request r;
-        int64_t v = 0;
-        if (b < P.B) {
-            if (!request_of(P, b, r) && blockIdx.x == 0) atomicOr(P.status, GEM_DEVFLAG_POS_RANGE);
-            v = static_cast<int64_t>(r.steps) * r.groups * P.n_kv;
-        }
+        r.steps = r.groups = r.n = r.L = r.row0 = r.tile0 = 0;
+        if (lane < P.B && !request_of(P, lane, r) && worker == 0) atomicOr(P.status, GEM_DEVFLAG_POS_RANGE);
+        const int64_t v = static_cast<int64_t>(r.steps) * r.groups * P.n_kv;
+        int64_t upto = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += x;
+            const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += x;
         }
-        if (lane == 31) sums[warp] = v;
-        __syncthreads();
-        int64_t before = 0, all = 0;
-        for (int i = 0; i < kWarps; ++i) {
-            before += i < warp ? sums[i] : 0;
-            all += sums[i];
+        total = __shfl_sync(0xffffffffu, upto, 31);
+        const int64_t from = worker * split();
+        b0 = min(31, __popc(__ballot_sync(0xffffffffu, upto <= from)));
+        in_b0 = from - __shfl_sync(0xffffffffu, upto - v, b0);
+        r0.row0 = __shfl_sync(0xffffffffu, r.row0, b0), r0.n = __shfl_sync(0xffffffffu, r.n, b0);
+        r0.L = __shfl_sync(0xffffffffu, r.L, b0), r0.tile0 = __shfl_sync(0xffffffffu, r.tile0, b0);
+        r0.steps = __shfl_sync(0xffffffffu, r.steps, b0), r0.groups = __shfl_sync(0xffffffffu, r.groups, b0);
+    } else {
+        int64_t carry = 0;     // steps before each request, in shared memory
+        if (threadIdx.x == 0) plan[0] = 0;
+        for (int base = 0; base < P.B; base += kThreads) {
+            const int b = base + threadIdx.x;
+            Request r;
+            int64_t v = 0;
+            if (b < P.B) {
+                if (!request_of(P, b, r) && blockIdx.x == 0) atomicOr(P.status, GEM_DEVFLAG_POS_RANGE);
+                v = static_cast<int64_t>(r.steps) * r.groups * P.n_kv;
+            }
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t x = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += x;
+            }
+            if (lane == 31) sums[warp] = v;
+            __syncthreads();
+            int64_t before = 0, all = 0;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                before += i < warp ? sums[i] : 0;
+                all += sums[i];
+            }
+            if (b < P.B) plan[b + 1] = carry + before + v;
+            carry += all;
+            __syncthreads();
         }
-        if (b < P.B) plan[b + 1] = carry + before + v;
-        carry += all;
-        __syncthreads();
+        total = plan[P.B];
+        const int64_t from = worker * split();
+        int hi = P.B - 1;      // the last request that begins at or before the share
+        while (b0 < hi) {
+            const int mid = (b0 + hi + 1) >> 1;
+            if (plan[mid] <= from) b0 = mid;
+            else hi = mid - 1;
+        }
+        in_b0 = from - plan[b0];
+        request_of(P, b0, r0);
     }
-    __syncthreads();
-    const int64_t total = plan[P.B];
-    const int64_t share = quotient(total + P.workers - 1, P.workers);
+    const int64_t share = split();
     const int64_t begin = min(total, worker * share), end = min(total, begin + share);
 
     // the step to request next: unit, steps left of it, first tile, and the tiles that its rows attend
-    int put_b = 0, put_u = 0, put_left = 0, put_tile = 0, put_lo = 0, put_hi = 0, put_h = 0, put_last_page = 0, put_steps = 1;
+    int put_b = 0, put_u = 0, put_left = 0, put_tile = 0, put_lo = 0, put_hi = 0, put_h = 0, put_last_page = 0, put_units = 1;
     int64_t put_step = begin;
     int pbase = 0, pid = -1;   // table entries pbase .. pbase + 31 of the request, one a lane
     uint32_t lost = 0;         // tiles of the ring's stages that hold nothing
@@ -286,10 +326,9 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
     const int lpt = P.lpage - 4;
     constexpr uint32_t kMask = (1u << kStepTiles) - 1;
 
-    auto put_unit = [&](int i) {   // enter unit put_u of request put_b at its step i
-        const Unit un(P, put_b, put_u);
+    auto put_unit = [&](const Unit& un, int i) {   // go on at step i of a unit
         put_left = un.steps - i;
-        put_steps = un.steps;
+        put_units = un.units;
         put_tile = un.tile0 + i * kStepTiles;
         put_lo = un.lo_all / kTileTokens, put_hi = un.hi_all / kTileTokens;
         put_h = un.h;
@@ -332,10 +371,12 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
             atomicOr(P.status, GEM_DEVFLAG_PAGE_RANGE);
         }
         put_tile += kStepTiles;
-        if (++put_step < end && --put_left == 0) {
-            next_unit(P, plan, put_steps, put_b, put_u);
-            put_unit(0);
-        }
+        if (++put_step < end && --put_left == 0) put_unit(next_unit(P, put_units, put_b, put_u), 0);
+    };
+
+    // the warps of a worker; each step has one
+    auto member_sync = [&]() {
+        if (PAIR > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / PAIR), "n"(32 * PAIR) : "memory");
     };
 
     // state of the unit at hand
@@ -348,20 +389,31 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
     // rows of the S and output fragments: columns 2t, 2t + 1
     auto col_row = [&](int nt, int e) { return PACK ? (2 * t + e) & 3 : nt * 8 + 2 * t + e; };
 
-    auto begin_unit = [&](const Unit& un) {
-        const float c = P.scale * 1.4426950408889634f;
+    // q's values that go into this lane's operands: issued apart from their use
+    float4 qv[NT][NB][2];
+    auto load_q = [&](const Unit& un) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int row = PACK ? g & 3 : nt * 8 + g;
             const int tok = row / P.G;
             const bool live = tok < un.tokens;
-            const float* src = P.q + (un.row0 + tok + 0ll) * P.ldq +
+            const float* src = P.q + (un.row0 + static_cast<int64_t>(tok)) * P.ldq +
                                (static_cast<int64_t>(un.h) * P.G + (row - tok * P.G)) * D + member * C::kDims + 4 * t;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    qv[nt][b][k] = live ? *reinterpret_cast<const float4*>(src + b * 32 + 16 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    };
+    auto begin_unit = [&](const Unit& un) {
+        const float c = P.scale * 1.4426950408889634f;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
             float x[NB][8], top = 0.f;
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                const float4 lo = live ? *reinterpret_cast<const float4*>(src + b * 32) : make_float4(0, 0, 0, 0);
-                const float4 hi = live ? *reinterpret_cast<const float4*>(src + b * 32 + 16) : make_float4(0, 0, 0, 0);
+                const float4 lo = qv[nt][b][0], hi = qv[nt][b][1];
                 x[b][0] = lo.x, x[b][1] = lo.y, x[b][2] = lo.z, x[b][3] = lo.w;
                 x[b][4] = hi.x, x[b][5] = hi.y, x[b][6] = hi.z, x[b][7] = hi.w;
 #pragma unroll
@@ -402,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) acc[b][0][nt][k] = acc[b][1][nt][k] = 0.f;
-        E = 60;
+        E = 64;   // above any step's
     };
 
     // The unit's sums so far, in true units: put_row(row, maximum, sum of p) for every row, and
@@ -480,10 +532,11 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
                 reinterpret_cast<float4*>(scales + sb * 48 + 32)[r] = make_float4(f0.x, f0.y, f1.x, f1.y);
             }
         }
-        // p 2^E sV stays below 2^15 (binary16 numbers that are not negative order as their bits do)
+        // p 2^E sV stays below 2^15, p up to 2^kSlack (binary16 numbers that are not negative order as their
+        // bits do)
         const uint32_t big = __reduce_max_sync(
             0xffffffffu, static_cast<uint32_t>(__half_as_ushort(__hmax(__low2half(big2), __high2half(big2)))));
-        const int e_step = min(60, 29 - static_cast<int>(big >> 10));
+        const int e_step = 29 - kSlack - static_cast<int>(big >> 10);
         __syncwarp();
 
         // scores
@@ -520,24 +573,33 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
                 }
             }
         }
-        if (PAIR > 1) {   // the other half of the dims is the other warp's; buffers alternate by stage
-            float4* mine = reinterpret_cast<float4*>(ring + C::kRing + C::kScales + C::kProbs) + stage * kStepTiles * NT * 32;
-            float4* other = mine + (member ? -1 : 1) * (C::kWarpBytes / 16);
+        if (PAIR > 1) {   // the head's other dims are the other members'; the buffers alternate with the stage
+            constexpr int kBuf = kStepTiles * NT * 32;
+            auto buffer = [&](int of) {
+                return reinterpret_cast<float4*>(smem + (warp - member + of) * C::kWarpBytes + C::kRing + C::kScales + C::kProbs) +
+                       stage * kBuf;
+            };
 #pragma unroll
             for (int s = 0; s < kStepTiles; ++s)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) sc[s][nt][k] *= cmul[nt][k & 1];   // the members' powers of two differ
-                    mine[(s * NT + nt) * 32 + lane] = make_float4(sc[s][nt][0], sc[s][nt][1], sc[s][nt][2], sc[s][nt][3]);
+                    buffer(member)[(s * NT + nt) * 32 + lane] = make_float4(sc[s][nt][0], sc[s][nt][1], sc[s][nt][2], sc[s][nt][3]);
                 }
-            asm volatile("bar.sync %0, 64;" ::"r"(1 + warp / PAIR) : "memory");
+            member_sync();
 #pragma unroll
             for (int s = 0; s < kStepTiles; ++s)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const float4 o = other[(s * NT + nt) * 32 + lane];
-                    sc[s][nt][0] += o.x, sc[s][nt][1] += o.y, sc[s][nt][2] += o.z, sc[s][nt][3] += o.w;
+                    // in the members' order, so that all of them get the same sums
+                    float4 v = buffer(0)[(s * NT + nt) * 32 + lane];
+#pragma unroll
+                    for (int of = 1; of < PAIR; ++of) {
+                        const float4 o = buffer(of)[(s * NT + nt) * 32 + lane];
+                        v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+                    }
+                    sc[s][nt][0] = v.x, sc[s][nt][1] = v.y, sc[s][nt][2] = v.z, sc[s][nt][3] = v.w;
                 }
         }
 
@@ -568,10 +630,12 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
                     }
                 }
 #pragma unroll
-                for (int k = 0; k < NV; ++k) up |= x[s][nt][k] > m[nt][k & 1];
+                for (int k = 0; k < NV; ++k) up |= x[s][nt][k] > m[nt][k & 1] + kSlack;
             }
-        if (__any_sync(0xffffffffu, up) || e_step < E) {   // new maxima, or larger scales: rescale the sums
-            const int e_new = min(E, e_step);
+        // Scores well past the maxima so far, or larger scales: new maxima, and the sums are rescaled.  (Any
+        // maximum would make it half of the steps; p may pass 1 by kSlack powers of two instead.)
+        if (__any_sync(0xffffffffu, up) || e_step < E) {
+            const int e_new = e_step < E ? e_step - 1 : E;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float corr[2];
@@ -665,28 +729,17 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
     int64_t tail = -1;
     int4 task = make_int4(-1, 0, 0, 0);
     if (begin < end) {
-        int b = 0, u, i;
-        {
-            int hi = P.B - 1;      // the last request that begins at or before the share
-            while (b < hi) {
-                const int mid = (b + hi + 1) >> 1;
-                if (plan[mid] <= begin) b = mid;
-                else hi = mid - 1;
-            }
-            Request r;
-            request_of(P, b, r);
-            const int64_t in = begin - plan[b], q = quotient(in, r.steps);
-            u = static_cast<int>(q);
-            i = static_cast<int>(in - q * r.steps);
-        }
+        const int64_t q0 = quotient(in_b0, r0.steps);
+        int b = b0, u = static_cast<int>(q0), i = static_cast<int>(in_b0 - q0 * r0.steps);
+        Unit un(P, r0, u);
+        load_q(un);
         put_b = b, put_u = u;
-        put_unit(i);
+        put_unit(un, i);
         for (int k = 0; k < kStages && put_step < end; ++k) request_step(k);
         int stage = 0;
         uint32_t parity = 0;
         int64_t step = begin;
-        while (step < end) {
-            const Unit un(P, b, u);
+        while (true) {
             const int64_t unit_end = min(end, step + (un.steps - i));
             const bool starts = i == 0, ends = step + (un.steps - i) <= end;
             if (!ends) tail = step - i;
@@ -704,11 +757,11 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
                         compute(stage, std::true_type{}, pos0, un.lo_all, un.hi_all);
                     else if (pos0 <= un.hi_all && pos0 + kStepTokens > un.lo_all)
                         compute(stage, std::false_type{}, pos0, un.lo_all, un.hi_all);
-                    else if (PAIR > 1)
-                        asm volatile("bar.sync %0, 64;" ::"r"(1 + warp / PAIR) : "memory");
+                    else
+                        member_sync();
                     if (put_step < end) request_step(stage);
-                } else if (PAIR > 1) {   // leave without touching the outputs
-                    asm volatile("bar.sync %0, 64;" ::"r"(1 + warp / PAIR) : "memory");
+                } else {   // leave without touching the outputs
+                    member_sync();
                 }
                 if (++stage == kStages) stage = 0, parity ^= 1;
             }
@@ -731,8 +784,10 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
                            });
                 }
             }
+            if (step == end) break;
             i = 0;
-            if (step < end) next_unit(P, plan, un.steps, b, u);
+            un = next_unit(P, un.units, b, u);
+            load_q(un);
         }
         if (dead) tail = task.x = -1;
     }
@@ -750,30 +805,57 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
                });
     }
     static_assert(ROWS * (C::kDims + 2) <= kLocal, "a partial result fits the ring");
-    if (lane == 0) tail_unit[warp] = tail;
+    constexpr int kW = C::kWorkers;
+    auto state_of = [&](int w) {   // a worker's (maximum, sum) rows
+        return reinterpret_cast<const float2*>(smem + w * PAIR * C::kWarpBytes + ROWS * C::kDims * 4);
+    };
+    if (lane == 0 && member == 0) tail_unit[warp / PAIR] = tail < 0 ? -1 : static_cast<int>(tail & 0x7fffffff);
     __syncthreads();
-    for (int f = 0; f < kWarps; f += PAIR) {
-        const int64_t id = tail_unit[f];
-        if (id < 0 || (f > 0 && tail_unit[f - PAIR] == id)) continue;
-        int last = f;
-        while (last + PAIR < kWarps && tail_unit[last + PAIR] == id) last += PAIR;
-        float* slot = P.part + (static_cast<int64_t>(P.workers) + blockIdx.x * C::kWorkers + f / PAIR) * Part<D, ROWS>::kFloats;
-        for (int i = threadIdx.x; i < ROWS * D / 2; i += kThreads) {
-            const int row = i / (D / 2), dim = i % (D / 2) * 2;
-            const int half = dim / C::kDims, at = dim % C::kDims;
-            float mx = -INFINITY, sum = 0.f;
-            float2 v = make_float2(0.f, 0.f);
-            for (int w = f; w <= last; w += PAIR)
-                mx = fmaxf(mx, reinterpret_cast<const float*>(smem + w * C::kWarpBytes)[ROWS * C::kDims + 2 * row]);
-            for (int w = f; w <= last; w += PAIR) {
-                const float* ml = reinterpret_cast<const float*>(smem + w * C::kWarpBytes) + ROWS * C::kDims + 2 * row;
-                const float* o = reinterpret_cast<const float*>(smem + (w + half) * C::kWarpBytes) + row * C::kDims + at;
-                const float c = ml[0] == mx ? 1.f : ex2(ml[0] - mx);
-                sum = fmaf(c, ml[1], sum);
-                v.x = fmaf(c, o[0], v.x), v.y = fmaf(c, o[1], v.y);
-            }
-            *reinterpret_cast<float2*>(slot + row * D + dim) = v;
-            if (dim == 0) slot[ROWS * D + 2 * row] = mx, slot[ROWS * D + 2 * row + 1] = sum;
+    int ids[kW];
+#pragma unroll
+    for (int w = 0; w < kW; ++w) ids[w] = tail_unit[w];
+    auto slot_of = [&](int first) {
+        return P.part + (static_cast<int64_t>(P.workers) + blockIdx.x * kW + first) * Part<D, ROWS>::kFloats;
+    };
+    // each worker's weight in its unit's part, and the part's (maximum, sum)
+    for (int at = threadIdx.x; at < kW * ROWS; at += kThreads) {
+        const int w = at / ROWS, row = at % ROWS, id = tail_unit[w];
+        if (id < 0) continue;
+        float2 ml[kW];
+        float top = -INFINITY, sum = 0.f;
+        int first = kW;
+#pragma unroll
+        for (int k = kW - 1; k >= 0; --k) {
+            ml[k] = ids[k] == id ? state_of(k)[row] : make_float2(-INFINITY, 0.f);
+            top = fmaxf(top, ml[k].x);
+            if (ids[k] == id) first = k;
+        }
+#pragma unroll
+        for (int k = 0; k < kW; ++k) {
+            const float c = ml[k].x == top ? 1.f : ex2(ml[k].x - top);
+            sum = fmaf(c, ml[k].y, sum);
+            if (k == w) weight[w * ROWS + row] = c;
+        }
+        if (w == first) *reinterpret_cast<float2*>(slot_of(first) + ROWS * D + 2 * row) = make_float2(top, sum);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < ROWS * D / 2; i += kThreads) {
+        const int row = i / (D / 2), dim = i % (D / 2) * 2;
+        float2 o[kW], v = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kW; ++w)
+            if (ids[w] >= 0)
+                o[w] = *reinterpret_cast<const float2*>(smem + (w * PAIR + dim / C::kDims) * C::kWarpBytes +
+                                                        (row * C::kDims + dim % C::kDims) * 4);
+        int first = 0;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) {
+            if (ids[w] < 0) continue;
+            if (w == 0 || ids[w] != ids[w - 1]) first = w, v = make_float2(0.f, 0.f);
+            const float c = weight[w * ROWS + row];
+            v.x = fmaf(c, o[w].x, v.x), v.y = fmaf(c, o[w].y, v.y);
+            if (w == kW - 1 || ids[w] != ids[w + 1 < kW ? w + 1 : w])
+                *reinterpret_cast<float2*>(slot_of(first) + row * D + dim) = v;
         }
     }
 }
@@ -784,24 +866,24 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
 // one for each CTA whose workers the unit goes on from, then the last worker's own.  D / 4 threads hold
 // four dims each; the groups of so many threads take every kSlices-th part and are joined in order.
 constexpr int kMergeThreads = 256;
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads) kv4_attn_merge_kernel(const AttnParams P, int rows, int cta_workers) {
+template <int D, int ROWS, int CW>
+__global__ void __launch_bounds__(kMergeThreads) kv4_attn_merge_kernel(const AttnParams P) {
     constexpr int kCols = D / 4, kSlices = kMergeThreads / kCols, kAhead = 4;
     __shared__ float4 v_s[kSlices][kCols];
     __shared__ float2 ml_s[kSlices];
     pdl_wait_trigger();
     const int row = blockIdx.y, tok = row / P.G;
-    const int64_t floats = static_cast<int64_t>(rows) * (D + 2);
+    constexpr int64_t kFloats = Part<D, ROWS>::kFloats;
     const int col = threadIdx.x % kCols, slice = threadIdx.x / kCols;
     const int lane = threadIdx.x & 31;
     int4 mine = make_int4(-1, 0, 0, 0);
-    if (lane < cta_workers) mine = P.tasks[blockIdx.x * cta_workers + lane];
+    if (lane < CW) mine = P.tasks[blockIdx.x * CW + lane];
     for (uint32_t todo = __ballot_sync(0xffffffffu, mine.x >= 0 && tok < mine.z); todo; todo &= todo - 1) {
-        const int from = __ffs(todo) - 1, w1 = blockIdx.x * cta_workers + from;
+        const int from = __ffs(todo) - 1, w1 = blockIdx.x * CW + from;
         int4 task;
         task.x = __shfl_sync(0xffffffffu, mine.x, from), task.y = __shfl_sync(0xffffffffu, mine.y, from);
         task.w = __shfl_sync(0xffffffffu, mine.w, from);
-        const int w0 = task.x, c0 = w0 / cta_workers, c1 = (w1 - 1) / cta_workers, parts = c1 - c0 + 2;
+        const int w0 = task.x, c0 = w0 / CW, c1 = (w1 - 1) / CW, parts = c1 - c0 + 2;
         float mx = -INFINITY, sum = 0.f;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k0 = slice; k0 < parts; k0 += kSlices * kAhead) {
@@ -811,8 +893,8 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_attn_merge_kernel(const Att
                 const int k = k0 + a * kSlices, c = c0 + k;
                 ml[a] = make_float2(-INFINITY, 0.f), ol[a] = oh[a] = make_float2(0.f, 0.f);
                 if (k < parts) {
-                    const float* s = P.part + (c > c1 ? w1 : P.workers + max(w0, c * cta_workers)) * floats;
-                    ml[a] = *reinterpret_cast<const float2*>(s + rows * D + 2 * row);
+                    const float* s = P.part + (c > c1 ? w1 : P.workers + max(w0, c * CW)) * kFloats;
+                    ml[a] = *reinterpret_cast<const float2*>(s + ROWS * D + 2 * row);
                     ol[a] = *reinterpret_cast<const float2*>(s + row * D + 4 * col);
                     oh[a] = *reinterpret_cast<const float2*>(s + row * D + 4 * col + 2);
                 }
@@ -862,11 +944,11 @@ struct Variant {
     size_t (*smem)(int);
 };
 
-template <int D, int NT, bool PACK, int CTAS>
+template <int D, int NT, bool PACK, int DW, int CTAS>
 Variant variant() {
-    using C = Cfg<D, NT, PACK>;
-    return {reinterpret_cast<const void*>(kv4_attn_kernel<D, NT, PACK, CTAS>),
-            reinterpret_cast<const void*>(kv4_attn_merge_kernel<D>), C::kRows, CTAS, C::kWorkers,
+    using C = Cfg<D, NT, PACK, DW>;
+    return {reinterpret_cast<const void*>(kv4_attn_kernel<D, NT, PACK, DW, CTAS>),
+            reinterpret_cast<const void*>(kv4_attn_merge_kernel<D, C::kRows, C::kWorkers>), C::kRows, CTAS, C::kWorkers,
             Part<D, C::kRows>::kFloats, C::smem};
 }
 
@@ -876,10 +958,10 @@ Variant pick(int64_t T, int B, int G, int d) {
     const int64_t tokens = std::max<int64_t>(1, (T + B - 1) / std::max(B, 1));
     const int64_t want = tokens * G;
     switch (d) {
-        case 64: return want <= 4 ? variant<64, 1, true, 2>() : want <= 8 ? variant<64, 1, false, 2>() : variant<64, 2, false, 1>();
-        case 128: return want <= 4 ? variant<128, 1, true, 2>() : want <= 8 ? variant<128, 1, false, 1>() : variant<128, 2, false, 1>();
-        case 256: return want <= 4 ? variant<256, 1, true, 1>() : variant<256, 1, false, 1>();
-        default: return want <= 4 ? variant<512, 1, true, 1>() : variant<512, 1, false, 1>();
+        case 64: return want <= 4 ? variant<64, 1, true, 64, 2>() : want <= 8 ? variant<64, 1, false, 64, 2>() : variant<64, 2, false, 64, 1>();
+        case 128: return want <= 4 ? variant<128, 1, true, 128, 2>() : want <= 8 ? variant<128, 1, false, 128, 1>() : variant<128, 2, false, 128, 1>();
+        case 256: return want <= 4 ? variant<256, 1, true, 128, 2>() : variant<256, 1, false, 256, 1>();
+        default: return want <= 4 ? variant<512, 1, true, 128, 2>() : variant<512, 1, false, 256, 1>();
     }
 }
 
@@ -954,10 +1036,8 @@ gem_status gem_kv4_attn(const float* q, int64_t ldq, int64_t T, const int32_t* c
     void* args[] = {&P};
     if ((st = launch_pdl(v.kernel, dim3(ctas), dim3(kThreads), smem, static_cast<cudaStream_t>(stream), args)) != GEM_OK)
         return st;
-    int rows = v.rows, cta_workers = v.cta_workers;
-    void* margs[] = {&P, &rows, &cta_workers};
-    return launch_pdl(v.merge, dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(rows)),
-                      dim3(kMergeThreads), 0, static_cast<cudaStream_t>(stream), margs);
+    return launch_pdl(v.merge, dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(v.rows)),
+                      dim3(kMergeThreads), 0, static_cast<cudaStream_t>(stream), args);
 }
 
 }  // extern "C"
