@@ -216,7 +216,7 @@ struct Cfg {
     static constexpr int kRing = kStages * kStage > kRingNeed ? kStages * kStage : kRingNeed;
     static constexpr int kScales = kStepTiles * kBlocks * 192;   // fp32: K's 16 twice, V's 16
     static constexpr int kProbs = kRows * kProbRow * 4;
-    static constexpr int kSwap = kPair > 1 ? 2 * kStepTiles * NT * 32 * 16 : 0;
+    static constexpr int kSwap = kPair > 1 ? kStages * kStepTiles * NT * 32 * 16 : 0;   // a buffer for each stage
     static constexpr int kWarpBytes = kRing + kScales + kProbs + kSwap;
     static constexpr int kWorkers = kWarps / kPair;      // of a CTA
     static size_t smem(int B) {
@@ -323,6 +323,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
     int pbase = 0, pid = -1;   // table entries pbase .. pbase + 31 of the request, one a lane
     uint32_t lost = 0;         // tiles of the ring's stages that hold nothing
     bool dead = false;
+    const uint32_t short_by = worker == 0 && (test_inject() & GEM_INJECT_RING_SHORTFALL) ? 16 : 0;
     const int lpt = P.lpage - 4;
     constexpr uint32_t kMask = (1u << kStepTiles) - 1;
 
@@ -350,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
         lost = (lost & ~(kMask << (stage * kStepTiles))) | ((~have & kMask) << (stage * kStepTiles));
         if (lane == 0) {
             uint32_t bytes = __popc(have) * C::kTile;
-            if (put_step == 0 && (test_inject() & GEM_INJECT_RING_SHORTFALL)) bytes += 16;
+            if (put_step == 0) bytes += short_by;
             mbar_arrive_expect_tx(&bars[stage], bytes);
         }
         __syncwarp();
@@ -573,7 +574,8 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
                 }
             }
         }
-        if (PAIR > 1) {   // the head's other dims are the other members'; the buffers alternate with the stage
+        if (PAIR > 1) {   // the head's other dims are the other members'; the buffers alternate with the stage,
+                          // and a member that writes one again has passed the barrier after its last reading
             constexpr int kBuf = kStepTiles * NT * 32;
             auto buffer = [&](int of) {
                 return reinterpret_cast<float4*>(smem + (warp - member + of) * C::kWarpBytes + C::kRing + C::kScales + C::kProbs) +
@@ -804,6 +806,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
                    mine[ROWS * C::kDims + 2 * row] = mx, mine[ROWS * C::kDims + 2 * row + 1] = sum;
                });
     }
+    static_assert(kStages >= 2, "the members' buffers alternate");
     static_assert(ROWS * (C::kDims + 2) <= kLocal, "a partial result fits the ring");
     constexpr int kW = C::kWorkers;
     auto state_of = [&](int w) {   // a worker's (maximum, sum) rows
@@ -871,12 +874,12 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_attn_merge_kernel(const Att
     constexpr int kCols = D / 4, kSlices = kMergeThreads / kCols, kAhead = 4;
     __shared__ float4 v_s[kSlices][kCols];
     __shared__ float2 ml_s[kSlices];
-    pdl_wait_trigger();
     const int row = blockIdx.y, tok = row / P.G;
     constexpr int64_t kFloats = Part<D, ROWS>::kFloats;
     const int col = threadIdx.x % kCols, slice = threadIdx.x / kCols;
     const int lane = threadIdx.x & 31;
     int4 mine = make_int4(-1, 0, 0, 0);
+    pdl_wait_trigger();
     if (lane < CW) mine = P.tasks[blockIdx.x * CW + lane];
     for (uint32_t todo = __ballot_sync(0xffffffffu, mine.x >= 0 && tok < mine.z); todo; todo &= todo - 1) {
         const int from = __ffs(todo) - 1, w1 = blockIdx.x * CW + from;
