@@ -53,6 +53,7 @@ struct AttnParams {
     int64_t ldq, T;
     const int32_t *cu, *kv_len;
     int B, n_q, n_kv, G, GT;      // GT: tokens of a unit (GT * G query rows)
+    int inv_g;                    // 2^16 / G rounded up: a row's token is row * inv_g / 2^16
     const int32_t* table;
     int64_t max_pages;
     const uint8_t* pool;
@@ -85,7 +86,7 @@ __device__ __forceinline__ bool request_of(const AttnParams& P, int b, Request& 
     if (r.n == 0) return true;
     r.tile0 = P.window ? max(0, r.L - r.n + 1 - P.window) / kTileTokens : 0;
     r.steps = ((r.L - 1) / kTileTokens - r.tile0) / kStepTiles + 1;
-    r.groups = (r.n + P.GT - 1) / P.GT;
+    r.groups = P.GT == 1 ? r.n : (r.n + P.GT - 1) / P.GT;
     return true;
 }
 
@@ -103,7 +104,7 @@ struct Unit {
     int L, tile0, steps;   // of the request
     int units;             // of the request
     __device__ __forceinline__ Unit(const AttnParams& P, const Request& r, int u) {
-        h = u / r.groups;
+        h = r.groups == 1 ? u : u / r.groups;
         j0 = (u - h * r.groups) * P.GT;
         tokens = min(P.GT, r.n - j0);
         row0 = r.row0 + j0;
@@ -263,14 +264,13 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
         if (lane < P.B && !request_of(P, lane, r) && worker == 0) atomicOr(P.status, GEM_DEVFLAG_POS_RANGE);
         const int64_t v = static_cast<int64_t>(r.steps) * r.groups * P.n_kv;
         int64_t upto = v;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
+        for (int o = 1; o < P.B; o <<= 1) {
             const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
             if (lane >= o) upto += x;
         }
-        total = __shfl_sync(0xffffffffu, upto, 31);
+        total = __shfl_sync(0xffffffffu, upto, P.B - 1);
         const int64_t from = worker * split();
-        b0 = min(31, __popc(__ballot_sync(0xffffffffu, upto <= from)));
+        b0 = min(P.B - 1, __popc(__ballot_sync(0xffffffffu, lane < P.B && upto <= from)));
         in_b0 = from - __shfl_sync(0xffffffffu, upto - v, b0);
         r0.row0 = __shfl_sync(0xffffffffu, r.row0, b0), r0.n = __shfl_sync(0xffffffffu, r.n, b0);
         r0.L = __shfl_sync(0xffffffffu, r.L, b0), r0.tile0 = __shfl_sync(0xffffffffu, r.tile0, b0);
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int row = PACK ? g & 3 : nt * 8 + g;
-            const int tok = row / P.G;
+            const int tok = (row * P.inv_g) >> 16;
             const bool live = tok < un.tokens;
             const float* src = P.q + (un.row0 + static_cast<int64_t>(tok)) * P.ldq +
                                (static_cast<int64_t>(un.h) * P.G + (row - tok * P.G)) * D + member * C::kDims + 4 * t;
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 cmul[nt][k] = __shfl_sync(0xffffffffu, back, ((PACK ? (2 * t + k) & 3 : 2 * t + k)) * 4);
-                const int tk = col_row(nt, k) / P.G;
+                const int tk = (col_row(nt, k) * P.inv_g) >> 16;
                 prow[nt][k] = un.p0 + min(tk, un.tokens - 1);
                 m[nt][k] = -INFINITY;
                 l[nt][k] = 0.f;
@@ -541,6 +541,13 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
         __syncwarp();
 
         // scores
+        uint32_t kw[kStepTiles][NB / 2][4];
+#pragma unroll
+        for (int s = 0; s < kStepTiles; ++s)
+#pragma unroll
+            for (int b2 = 0; b2 < NB; b2 += 2)
+                ldmatrix_x4(kw[s][b2 / 2][0], kw[s][b2 / 2][1], kw[s][b2 / 2][2], kw[s][b2 / 2][3],
+                            smem_u32(st + s * C::kTile) + lane * 16 + b2 * 256);
         float sc[kStepTiles][NT][4];
 #pragma unroll
         for (int s = 0; s < kStepTiles; ++s) {
@@ -548,11 +555,9 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) sc[s][nt][k] = 0.f;
-            const uint32_t codes = smem_u32(st + s * C::kTile) + lane * 16;
 #pragma unroll
             for (int b2 = 0; b2 < NB; b2 += 2) {
-                uint32_t w[4];
-                ldmatrix_x4(w[0], w[1], w[2], w[3], codes + b2 * 256);
+                const uint32_t (&w)[4] = kw[s][b2 / 2];
 #pragma unroll
                 for (int b = b2; b < b2 + 2; ++b) {
                     const uint32_t wa = w[2 * (b - b2)], wb = w[2 * (b - b2) + 1];
@@ -604,6 +609,13 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
                     sc[s][nt][0] = v.x, sc[s][nt][1] = v.y, sc[s][nt][2] = v.z, sc[s][nt][3] = v.w;
                 }
         }
+
+        // the first tile's V codes are under way while the probabilities are taken
+        uint32_t vw[NB / 2][4];
+#pragma unroll
+        for (int b2 = 0; b2 < NB; b2 += 2)
+            ldmatrix_x4_trans(vw[b2 / 2][0], vw[b2 / 2][1], vw[b2 / 2][2], vw[b2 / 2][3],
+                              smem_u32(st + codes_off(C::kDims, 1)) + lane * 16 + b2 * 256);
 
         // p: in log2 units; PACK: the two halves' sums, lanes t < 2 keep row g, the others row g + 8
         constexpr int NV = PACK ? 2 : 4;
@@ -695,7 +707,12 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
 #pragma unroll
             for (int b2 = 0; b2 < NB; b2 += 2) {
                 uint32_t w[4];
-                ldmatrix_x4_trans(w[0], w[1], w[2], w[3], codes + b2 * 256);
+                if (s == 0) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) w[k] = vw[b2 / 2][k];
+                } else {
+                    ldmatrix_x4_trans(w[0], w[1], w[2], w[3], codes + b2 * 256);
+                }
 #pragma unroll
                 for (int b = b2; b < b2 + 2; ++b) {
                     const uint32_t wa = w[2 * (b - b2)], wb = w[2 * (b - b2) + 1];
@@ -770,7 +787,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
             if (ends && !dead) {
                 if (starts) {   // the whole unit
                     finish([&](int row, int dim, float2 v, float sum) {
-                        const int tok = row / P.G;
+                        const int tok = (row * P.inv_g) >> 16;
                         if (tok >= un.tokens) return;
                         float* o = P.out + (un.row0 + static_cast<int64_t>(tok)) * P.ldo +
                                    (static_cast<int64_t>(un.h) * P.G + (row - tok * P.G)) * D + dim;
@@ -874,7 +891,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_attn_merge_kernel(const Att
     constexpr int kCols = D / 4, kSlices = kMergeThreads / kCols, kAhead = 4;
     __shared__ float4 v_s[kSlices][kCols];
     __shared__ float2 ml_s[kSlices];
-    const int row = blockIdx.y, tok = row / P.G;
+    const int row = blockIdx.y, tok = (row * P.inv_g) >> 16;
     constexpr int64_t kFloats = Part<D, ROWS>::kFloats;
     const int col = threadIdx.x % kCols, slice = threadIdx.x / kCols;
     const int lane = threadIdx.x & 31;
@@ -1025,7 +1042,7 @@ gem_status gem_kv4_attn(const float* q, int64_t ldq, int64_t T, const int32_t* c
     if (!workspace || ws_bytes < gem_kv4_attn_workspace(T, B, n_q, n_kv, d)) return GEM_ERR_WORKSPACE;
     AttnParams P{};
     P.q = q, P.ldq = ldq, P.T = T, P.cu = cu_tokens, P.kv_len = kv_len;
-    P.B = B, P.n_q = n_q, P.n_kv = n_kv, P.G = n_q / n_kv, P.GT = v.rows / P.G;
+    P.B = B, P.n_q = n_q, P.n_kv = n_kv, P.G = n_q / n_kv, P.GT = v.rows / P.G, P.inv_g = (65536 + P.G - 1) / P.G;
     P.table = table, P.max_pages = max_pages, P.pool = static_cast<const uint8_t*>(pool), P.n_pages = n_pages;
     P.lpage = log2_of(page), P.window = window, P.scale = scale;
     P.out = out, P.ldo = ldo, P.status = status ? status : di.status_word;
