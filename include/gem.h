@@ -431,7 +431,9 @@ GEM_API size_t gem_kv4_page_bytes(int n_kv, int d, int page);
  *   sets GEM_DEVFLAG_NO_ROOM.  Counters that are out of range set GEM_DEVFLAG_PAGE_RANGE, and the
  *   ring counts as having no free pages and no room.
  *   cu_tokens [B + 1] int32: tokens before request b; slot, pos, seq [T_cap] int32: slot, position
- *           and request of token t, all -1 for t >= cu_tokens[B].
+ *           and request of token t, all -1 for t >= cu_tokens[B].  Page indices are copied as they
+ *           are; a token whose page is outside [0, n_pages) gets slot -2^31 (which the calls below
+ *           refuse) and sets GEM_DEVFLAG_PAGE_RANGE.
  *   B in 0..4096, else GEM_ERR_UNSUPPORTED_SHAPE.  Outputs must not overlap inputs (ring_out is
  *   not ring_in, kv_len is not cached): a step takes the last one's outputs and writes the others.
  *   Deterministic.
@@ -496,15 +498,17 @@ GEM_API gem_status gem_kv4_gather(const void *pool, int64_t n_pages, int page, i
  *   stands at p = kv_len[b] - n + i and attends positions max(0, p - window + 1) .. p (window 0: all
  *   of 0 .. p), which the pool must already hold:
  *     out[t][h*d + e] = sum_j softmax_j(scale * q_h . K[j]) * V[j][e],  KV head h / (n_q / n_kv).
- *   q      [T][ldq] fp32, 16-byte aligned, ldq % 4 == 0;  out [T][ldo] fp32.  Rows from
- *          cu_tokens[B] on are neither read nor written.
+ *   q      [T][ldq] fp32, 16-byte aligned, ldq % 4 == 0;  out [T][ldo] fp32, which must not
+ *          overlap q.  Rows from cu_tokens[B] on are neither read nor written.
  *   table  [B][max_pages] int32; entries from ceil(kv_len / page) on are not read, nor those that
  *          lie before every row's window.
  *   d 64, 128, 256 or 512; n_q % n_kv == 0, n_q / n_kv <= 8; B in 0..4096.
  *   Device checks: cu_tokens out of order or beyond T, kv_len[b] < n or beyond max_pages * page set
  *   GEM_DEVFLAG_POS_RANGE and leave the request's rows as they were; a table entry outside
  *   [0, n_pages) sets GEM_DEVFLAG_PAGE_RANGE and its positions count as masked (a row with no
- *   position left is 0).
+ *   position left is 0).  What lies in the pages behind kv_len or before the window may be
+ *   anything.  A position whose K scale is not finite makes NaN of the rows that attend it, one
+ *   whose V scale is not finite of their values in its block of 32 dims.
  *   workspace  gem_kv4_attn_workspace(T, B, n_q, n_kv, d) bytes, 256-byte aligned, no
  *          initialisation; calls that can run at the same time need one each.
  *   Accumulation is fp32: q and the probabilities enter the tensor cores as binary16 hi + lo pairs

@@ -125,7 +125,9 @@ def block_tables(cached, fresh, page, table, ring, ring_in, T_cap):
     for b in range(len(cached)):
         for i in range(cu[b + 1] - cu[b]):
             p = int(cached[b]) + i
-            slot[cu[b] + i], pos[cu[b] + i], seq[cu[b] + i] = table[b, p // page] * page + p % page, p, b
+            id_ = int(table[b, p // page])
+            slot[cu[b] + i] = id_ * page + p % page if 0 <= id_ < n_pages else -2 ** 31
+            pos[cu[b] + i], seq[cu[b] + i] = p, b
     return dict(table=table, ring=ring, ring_out=np.array([head + popped, tail + len(given)], np.int64),
                 kv_len=np.array(kv_len, np.int32), cu=np.array(cu, np.int32), slot=slot, pos=pos, seq=seq,
                 refused=refused, bad_ring=bad)

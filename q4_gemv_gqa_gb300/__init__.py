@@ -542,6 +542,8 @@ def kv4_attn(q: torch.Tensor, n_q: int, n_kv: int, d: int, cu_tokens: torch.Tens
     if workspace is None:
         need = lib.gem_kv4_attn_workspace(T, B, n_q, n_kv, d)
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+        if stream is not None and workspace is not None:
+            workspace.record_stream(stream)   # it is given back here, before that stream has used it
     st = lib.gem_kv4_attn(qp, ldq, T, _here(cu_tokens, torch.int32, "cu_tokens", 1, dev),
                           _here(kv_len, torch.int32, "kv_len", 1, dev), B, n_q, n_kv, d,
                           _here(table, torch.int32, "table", 2, dev), table.shape[1], pp, n_pages, page, window,

@@ -511,7 +511,9 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
         for (int it = 0; it < kStepTiles * NB * 8; it += 32) {
             const int at = it + lane, sb = at >> 3, r = at & 7, s = sb / NB, b = sb % NB;
             const __half* ks = reinterpret_cast<const __half*>(st + s * C::kTile + scales_off(C::kDims, 0)) + b * 16;
-            const float k0 = __half2float(ks[r]), k1 = __half2float(ks[r + 8]);
+            // an infinite scale becomes NaN (x + 0 x): times a negative sum it would hide its position
+            float k0 = __half2float(ks[r]), k1 = __half2float(ks[r + 8]);
+            k0 = fmaf(k0, 0.f, k0), k1 = fmaf(k1, 0.f, k1);
             reinterpret_cast<float4*>(scales + sb * 48)[r] = make_float4(k0, k0, k1, k1);
         }
         __half2 big2 = __float2half2_rn(0.f);
@@ -528,7 +530,9 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
                     v0 = __halves2half2(in(pos) ? __low2half(v0) : zero, in(pos + 1) ? __high2half(v0) : zero);
                     v1 = __halves2half2(in(pos + 8) ? __low2half(v1) : zero, in(pos + 9) ? __high2half(v1) : zero);
                 }
-                big2 = __hmax2(big2, __hmax2(__habs2(v0), __habs2(v1)));   // a NaN is passed over
+                // infinities become NaN (x + 0 x), which the maximum passes over
+                const __half2 zero2 = __float2half2_rn(0.f);
+                big2 = __hmax2(big2, __hmax2(__habs2(__hfma2(v0, zero2, v0)), __habs2(__hfma2(v1, zero2, v1))));
                 const float2 f0 = __half22float2(v0), f1 = __half22float2(v1);
                 reinterpret_cast<float4*>(scales + sb * 48 + 32)[r] = make_float4(f0.x, f0.y, f1.x, f1.y);
             }
@@ -1032,7 +1036,7 @@ gem_status gem_kv4_attn(const float* q, int64_t ldq, int64_t T, const int32_t* c
         (n_kv && n_q / n_kv > kMaxGroup))
         return GEM_ERR_UNSUPPORTED_SHAPE;
     if (T == 0 || B == 0 || n_q == 0) return GEM_OK;
-    if (!q || !out || !cu_tokens || !kv_len || (max_pages && !table)) return GEM_ERR_INVALID_ARG;
+    if (!q || !out || q == out || !cu_tokens || !kv_len || (max_pages && !table)) return GEM_ERR_INVALID_ARG;
     if (ldq < static_cast<int64_t>(n_q) * d || ldo < static_cast<int64_t>(n_q) * d) return GEM_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(q) & 15) || ldq % 4 || (reinterpret_cast<uintptr_t>(workspace) & 255))
         return GEM_ERR_MISALIGNED;

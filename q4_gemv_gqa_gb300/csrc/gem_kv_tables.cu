@@ -152,7 +152,12 @@ __global__ void __launch_bounds__(kTabThreads) kv_tables_kernel(const TableParam
             const int64_t p = cached + (t - cu_s[lo]), pi = p >> P.lpage;
             const int32_t id = pi < held ? P.table[lo * P.max_pages + pi]
                                          : P.ring[ring_at(head + first_s[lo] + (pi - held), P.n_pages)];
-            slot = static_cast<int32_t>(id * page + (p & (page - 1)));
+            if (id >= 0 && id < P.n_pages) {
+                slot = static_cast<int32_t>(id * page + (p & (page - 1)));
+            } else {   // not a page: a slot that every reader refuses
+                slot = INT32_MIN;
+                atomicOr(P.status, GEM_DEVFLAG_PAGE_RANGE);
+            }
             pos = static_cast<int32_t>(p);
             seq = lo;
         }

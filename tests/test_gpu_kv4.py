@@ -368,6 +368,9 @@ ATTN = [
     ([20000], [2], 2, 1, 128, 256, 0),
     ([90] * 40, [1] * 40, 4, 2, 64, 32, 0),
     ([33] * 5, [3, 1, 0, 2, 1], 3, 3, 64, 16, 0),
+    ([1000], [1000], 4, 2, 64, 16, 0),                        # a whole prompt
+    ([100, 61] * 18, [3, 1] * 18, 8, 2, 128, 16, 0),          # more than 32 requests, chunks among them
+    ([130] * 40, [2] * 40, 8, 1, 128, 32, 50),
 ]
 
 
@@ -641,3 +644,165 @@ def test_attention_reports_a_copy_that_never_lands(env):
         got = _attn_run(g, t, *args, status=status)
         assert int(status) == 0
         assert_close(got, _attn_want(pool, table, cu, q, kv_len, n_q, n_kv, d, page, 0, d ** -0.5), "the call after")
+
+
+# ---- what the documentation allows at its edges ---------------------------------------------------
+
+
+def test_tables_pass_pages_that_are_none_on_as_slots_that_are_refused(env):
+    g, t = env
+    table = np.array([[9, -1, 2 ** 27 + 1], [1, 2, -5]], np.int32)
+    ring = np.array([0, -7, 3, 2 ** 30], np.int32)
+    args = (np.array([20, 33], np.int32), np.array([30, 2], np.int32), 16, table, ring, np.array([1, 4], np.int64), 40)
+    want = kv4.block_tables(*args)
+    status = t.zeros(1, dtype=t.int32, device="cuda")
+    got = _run_tables(g, t, *args, status=status)
+    for k in got:
+        assert np.array_equal(got[k], want[k]), k
+    # (request 0 is refused as well: its 50 tokens do not fit its row)
+    assert (want["slot"] == -2 ** 31).any() and want["refused"] == [0]
+    assert int(status) == g.DEVFLAG_PAGE_RANGE | g.DEVFLAG_NO_ROOM
+
+
+@pytest.mark.parametrize("bits", [0x7e00, 0x7c00, 0xfc00])
+@pytest.mark.parametrize("case", [([70, 40], [5, 1], 8, 2, 128, 16, 0), ([90, 64], [6, 3], 4, 2, 64, 32, 20),
+                                  ([100], [9], 8, 1, 256, 16, 0), ([50], [2], 16, 2, 512, 16, 7)], ids=str)
+def test_attention_keeps_scales_that_are_not_finite_to_the_rows_that_attend_them(env, case, bits):
+    """A scale that is NaN or infinite at a position that some rows of a request attend and others mask
+    (the newest tokens, and the oldest of a window): the others are as if it were not there."""
+    g, t = env
+    kv_len, fresh, n_q, n_kv, d, page, window = case
+    r = np.random.RandomState(40 + d)
+    pool, table, cu, q = _attn_case(r, t, kv_len, fresh, n_q, n_kv, d, page)
+    want = _attn_want(pool, table, cu, q, kv_len, n_q, n_kv, d, page, window, d ** -0.5)
+    bad = np.zeros((len(q), n_q, d), bool)
+    G = n_q // n_kv
+    for b, L in enumerate(kv_len):
+        n = fresh[b]
+        spots = [L - 1 - n // 2] + ([L - window] if window else [])
+        for j in spots:
+            slot = table[b, j // page] * page + j % page
+            for which in range(2):
+                blk = int(r.randint(0, d // 32))
+                p, c, at = pool._at(slot, n_kv - 1, which, blk)
+                pool.bytes[p, at:at + 2] = np.array([bits], np.uint16).view(np.uint8)
+                for i in range(n):
+                    pos = L - n + i
+                    if j <= pos and (not window or j > pos - window):
+                        dims = slice(blk * 32, blk * 32 + 32) if which else slice(None)
+                        bad[cu[b] + i, (n_kv - 1) * G:, dims] = True
+    bad = bad.reshape(len(q), -1)
+    got = _attn_run(g, t, pool, table, cu, q, kv_len, n_q, n_kv, d, page, window, d ** -0.5)
+    assert not np.any(np.isfinite(got[bad])), "a row that attends the position hides it"
+    assert bad.any() and not bad.all()
+    assert_close(got[~bad], want[~bad], "the rows that do not")
+
+
+def test_attention_of_as_many_requests_as_allowed(env):
+    g, t = env
+    for n_q, n_kv, d, B in ((8, 1, 512, 4096), (4, 2, 64, 4096), (2, 2, 128, 33)):
+        page = 16
+        r = np.random.RandomState(B)
+        kv_len = r.randint(1, 20, B)
+        fresh = np.ones(B, np.int64)
+        fresh[r.rand(B) < 0.2] = 0
+        pool = _random_pool(r, t, 64, page, n_kv, d)
+        table = r.randint(0, 64, (B, 2)).astype(np.int32)      # requests may share pages
+        cu = np.concatenate([[0], np.cumsum(fresh)]).astype(np.int32)
+        q = (2 * r.randn(int(cu[-1]), n_q * d)).astype(np.float32)
+        x = _unpack(pool, d)
+        got = _attn_run(g, t, pool, table, cu, q, kv_len, n_q, n_kv, d, page, 0, d ** -0.5)
+        for b in r.permutation(np.nonzero(fresh)[0])[:60]:
+            j = np.arange(kv_len[b])
+            slots = table[b, j // page] * page + j % page
+            want = kv4.attention(q[cu[b]:cu[b + 1]].reshape(1, n_q, d), x[0, slots], x[1, slots], kv_len[b], 0, d ** -0.5)
+            assert_close(got[cu[b]], want.reshape(-1), "request %d of %d" % (b, B))
+    assert g.device_status(reset=True) == 0
+
+
+def test_attention_reads_and_writes_columns_of_wider_rows(env):
+    """q a column range of a QKV row, out a column range that is not 16-byte aligned; a stream of the
+    caller's with no workspace given."""
+    g, t = env
+    kv_len, fresh, n_q, n_kv, d, page = [300, 35], [1, 3], 6, 2, 128, 32
+    r = np.random.RandomState(50)
+    pool, table, cu, q = _attn_case(r, t, kv_len, fresh, n_q, n_kv, d, page)
+    want = _attn_want(pool, table, cu, q, kv_len, n_q, n_kv, d, page, 0, d ** -0.5)
+    wide = t.full((len(q), 8 + n_q * d + 512), float("nan"), device="cuda")
+    wide[:, 8:8 + n_q * d] = _cu(t, q)
+    out = t.full((len(q), n_q * d + 7), 4.0, device="cuda")
+    args = [_cu(t, cu), _cu(t, kv_len, np.int32), _cu(t, table), _cu(t, pool.bytes)]
+    s = t.cuda.Stream()
+    s.wait_stream(t.cuda.current_stream())
+    g.kv4_attn(wide[:, 8:], n_q, n_kv, d, *args, page, 0, d ** -0.5, out[:, 3:], stream=s)
+    s.synchronize()
+    got = out.cpu().numpy()
+    assert_close(got[:, 3:3 + n_q * d], want, "attention")
+    assert np.all(got[:, :3] == 4.0) and np.all(got[:, 3 + n_q * d:] == 4.0)
+    with pytest.raises(g.GemError) as e:
+        g.kv4_attn(wide[:, 8:], n_q, n_kv, d, *args, page, 0, d ** -0.5, wide[:, 8:])
+    assert e.value.status == 1
+
+
+def test_two_captured_steps_share_a_workspace_in_turn(env):
+    g, t = env
+    n_q, n_kv, d, page = 8, 2, 128, 16
+    ws = t.empty(g.kv4_attn_workspace(2, 2, n_q, n_kv, d), dtype=t.uint8, device="cuda")
+    graphs = []
+    for k in range(2):
+        r = np.random.RandomState(60 + k)
+        kv_len = [1500 - 1000 * k, 77]
+        pool, table, cu, q = _attn_case(r, t, kv_len, [1, 1], n_q, n_kv, d, page)
+        want = _attn_want(pool, table, cu, q, kv_len, n_q, n_kv, d, page, 0, d ** -0.5)
+        x = [_cu(t, q), _cu(t, cu), _cu(t, kv_len, np.int32), _cu(t, table), _cu(t, pool.bytes)]
+        out = t.zeros(2, n_q * d, device="cuda")
+        graph = t.cuda.CUDAGraph()
+        with t.cuda.graph(graph):
+            g.kv4_attn(x[0], n_q, n_kv, d, x[1], x[2], x[3], x[4], page, 0, d ** -0.5, out, workspace=ws)
+        graphs.append((graph, out, want, x))
+    for _ in range(10):
+        for graph, _, _, _ in graphs:
+            graph.replay()
+    t.cuda.synchronize()
+    for _, out, want, _ in graphs:
+        assert_close(out.cpu().numpy(), want, "attention")
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    """Nothing of the library has run in the process: every call's set-up happens under capture."""
+    import subprocess
+    import sys
+
+    from conftest import ROOT
+    code = """
+import torch as t, q4_gemv_gqa_gb300 as g
+i32 = dict(dtype=t.int32, device="cuda")
+n_q, n_kv, d, page = 4, 2, 64, 16
+pool = t.zeros((4, g.kv4_page_bytes(n_kv, d, page)), dtype=t.uint8, device="cuda")
+qkv = t.randn(2, (n_q + 2 * n_kv) * d, device="cuda")
+table, ring = t.full((1, 2), -1, **i32), t.arange(4, **i32)
+rin, rout = t.tensor([0, 4], device="cuda"), t.zeros(2, dtype=t.int64, device="cuda")
+cached, fresh, kv, cu = t.zeros(1, **i32), t.full((1,), 2, **i32), t.zeros(1, **i32), t.zeros(2, **i32)
+slot, pos, seq = (t.zeros(2, **i32) for _ in range(3))
+out = t.zeros(2, n_q * d, device="cuda")
+kk, vv = t.zeros(2, n_kv * d, device="cuda"), t.zeros(2, n_kv * d, device="cuda")
+ws = t.zeros(48 << 20, dtype=t.uint8, device="cuda")
+t.cuda.synchronize()
+graph = t.cuda.CUDAGraph()
+with t.cuda.graph(graph):
+    g.kv_block_tables(cached, fresh, page, table, ring, rin, rout, kv, cu, slot, pos, seq)
+    g.qknorm_mrope(qkv, n_q, n_kv, d, None, None, 1e-6, pos[None], [32], 1e4, qkv)
+    g.kv4_append(qkv[:, n_q * d:(n_q + n_kv) * d], qkv[:, (n_q + n_kv) * d:], n_kv, d, slot, pool, page)
+    g.kv4_gather(pool, page, n_kv, d, slot, kk, vv)
+    g.kv4_attn(qkv, n_q, n_kv, d, cu, kv, table, pool, page, 0, 0.125, out, workspace=ws)
+graph.replay()
+t.cuda.synchronize()
+# the first row attends itself alone: its output is its own value
+want = vv[0].view(n_kv, 1, d).expand(n_kv, n_q // n_kv, d).reshape(-1)
+assert kv.item() == 2 and slot.tolist() == [0, 1], (kv, slot)
+assert t.allclose(out[0], want, rtol=1e-5, atol=1e-6), (out[0] - want).abs().max()
+assert g.device_status() == 0
+print("captured")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=280)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stdout + r.stderr

@@ -197,7 +197,7 @@ def test_append_and_gather_refusals(lib):
 
 def _attn(lib, **kw):
     a = dict(q=D, ldq=256, T=3, cu=D, kv_len=D, B=2, n_q=4, n_kv=2, d=64, table=D, max_pages=4, pool=D, n_pages=4,
-             page=16, window=0, scale=0.125, out=D, ldo=256, ws=C.c_void_p(0x10000), ws_bytes=1 << 30)
+             page=16, window=0, scale=0.125, out=C.c_void_p(0x9000), ldo=256, ws=C.c_void_p(0x10000), ws_bytes=1 << 30)
     a.update(kw)
     return lib.gem_kv4_attn(*a.values(), None, None)
 
@@ -206,7 +206,7 @@ def test_attn_refusals(lib):
     assert _attn(lib, T=0) == OK and _attn(lib, B=0) == OK and _attn(lib, n_q=0) == OK
     for kw in (dict(T=-1), dict(B=-1), dict(n_q=-4), dict(n_kv=-2), dict(n_q=5), dict(n_kv=0), dict(window=-1),
                dict(max_pages=-1), dict(n_pages=-1), dict(q=None), dict(out=None), dict(cu=None), dict(kv_len=None),
-               dict(table=None), dict(pool=None), dict(ldq=252), dict(ldo=255), dict(d=0)):
+               dict(table=None), dict(pool=None), dict(ldq=252), dict(ldo=255), dict(d=0), dict(out=D, q=D)):
         assert _attn(lib, **kw) == INVALID, kw
     for kw in (dict(n_q=18, ldq=9999 * 4, ldo=9999), dict(d=96, ldq=800, ldo=800), dict(page=24), dict(B=4097),
                dict(T=1 << 31), dict(max_pages=1 << 27), dict(n_pages=1 << 27)):
