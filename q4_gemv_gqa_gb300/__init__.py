@@ -390,27 +390,26 @@ def swiglu(gate: torch.Tensor, up: torch.Tensor, act: int, out: torch.Tensor,
 # ---- paged 4-bit KV cache -------------------------------------------------------------------
 
 
-def _here(t: torch.Tensor, dtype, name: str, dim: int, device: int):
-    """Pointer of a contiguous tensor of `dim` dimensions on the current device."""
-    if t.get_device() != device:   # -1 on the host
-        raise ValueError("%s must be on the current CUDA device" % name)
-    if t.dtype != dtype or t.dim() != dim or not t.is_contiguous():
-        raise ValueError("%s must be contiguous %s with %d dimension(s), got %s %s" % (
-            name, dtype, dim, t.dtype, tuple(t.shape)))
+def _here(t: torch.Tensor, dtype, name: str, shape, device: int):
+    """Pointer of a contiguous tensor of this type and shape on the current device."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError("%s must be contiguous %s %s on the current CUDA device, got %s %s on %s" % (
+            name, dtype, tuple(shape), t.dtype, tuple(t.shape), t.device))
     return t.data_ptr()
 
 
 def _rows(t: torch.Tensor, cols: int, name: str, device: int):
-    """(pointer, row stride) of an fp32 [rows, >= cols] tensor whose rows are contiguous; a column
+    """(pointer, row stride, rows) of an fp32 [rows, >= cols] tensor whose rows are contiguous; a column
     range of a wider tensor will do."""
-    if t.get_device() != device:
-        raise ValueError("%s must be on the current CUDA device" % name)
-    rows, have = t.shape if t.dim() == 2 else (0, -1)
-    ld, step = t.stride() if have >= 0 else (0, 0)
-    if t.dtype != torch.float32 or have < cols or (step != 1 and have > 1):
-        raise ValueError("%s must be fp32 [rows, >= %d] with contiguous rows, got %s %s strides %s" % (
-            name, cols, t.dtype, tuple(t.shape), t.stride()))
-    return t.data_ptr(), (ld if rows > 1 else (have + 3) // 4 * 4)
+    if t.dim() != 2 or t.dtype is not torch.float32 or t.get_device() != device:
+        raise ValueError("%s must be fp32 [rows, >= %d] on the current CUDA device, got %s %s on %s" % (
+            name, cols, t.dtype, tuple(t.shape), t.device))
+    rows, have = t.shape
+    ld, step = t.stride()
+    if have < cols or (step != 1 and have > 1):
+        raise ValueError("%s must be fp32 [rows, >= %d] with contiguous rows, got %s strides %s" % (
+            name, cols, tuple(t.shape), t.stride()))
+    return t.data_ptr(), (ld if rows > 1 else (have + 3) // 4 * 4), rows
 
 
 def _stream_on(stream, device: int) -> int:
@@ -419,17 +418,14 @@ def _stream_on(stream, device: int) -> int:
 
 
 def _status(status: torch.Tensor | None, device: int):
-    return None if status is None else _here(status, torch.int32, "status", 1, device)
+    return None if status is None else _here(status, torch.int32, "status", status.shape, device)
 
 
 def _pool(pool: torch.Tensor, n_kv: int, d: int, page: int, device: int):
-    """(pointer, pages) of a pool [n_pages, kv4_page_bytes(n_kv, d, page)]."""
-    ptr = _here(pool, torch.uint8, "pool", 2, device)
-    need = n_kv * d * page * 9 // 8   # the library rejects the sizes that have no pages
-    if pool.shape[1] != need:
-        raise ValueError("pool must be [n_pages, %d] for %d KV heads of %d and pages of %d, got %s" % (
-            need, n_kv, d, page, tuple(pool.shape)))
-    return ptr, pool.shape[0]
+    """(pointer, pages) of a pool [n_pages, kv4_page_bytes(n_kv, d, page)]; the library rejects the sizes
+    that have no pages."""
+    n_pages = pool.shape[0]
+    return _here(pool, torch.uint8, "pool", (n_pages, n_kv * d * page * 9 // 8), device), n_pages
 
 
 def kv4_page_bytes(n_kv: int, d: int, page: int) -> int:
@@ -446,19 +442,13 @@ def kv_block_tables(cached: torch.Tensor, fresh: torch.Tensor, page: int, table:
     table [B, max_pages], ring [n_pages], slot, pos, seq [T_cap]; int64 ring_in, ring_out [2]."""
     dev = torch.cuda.current_device()
     i32, i64 = torch.int32, torch.int64
-    B, T = cached.shape[0], slot.shape[0]
-    if fresh.shape[0] != B or kv_len.shape[0] != B or cu_tokens.shape[0] != B + 1 or table.shape[0] != B:
-        raise ValueError("fresh and kv_len must be [B=%d], cu_tokens [B + 1] and table [B, max_pages]" % B)
-    if pos.shape[0] != T or seq.shape[0] != T:
-        raise ValueError("slot, pos and seq must have the same length")
-    if ring_in.numel() != 2 or ring_out.numel() != 2:
-        raise ValueError("ring_in and ring_out must hold two counters")
+    B, T, n_pages, max_pages = cached.shape[0], slot.shape[0], ring.shape[0], table.shape[-1]
     st = lib.gem_kv_block_tables(
-        _here(cached, i32, "cached", 1, dev), _here(fresh, i32, "fresh", 1, dev), B, page,
-        _here(table, i32, "table", 2, dev), table.shape[1], _here(ring, i32, "ring", 1, dev), ring.shape[0],
-        _here(ring_in, i64, "ring_in", 1, dev), _here(ring_out, i64, "ring_out", 1, dev),
-        _here(kv_len, i32, "kv_len", 1, dev), _here(cu_tokens, i32, "cu_tokens", 1, dev),
-        _here(slot, i32, "slot", 1, dev), _here(pos, i32, "pos", 1, dev), _here(seq, i32, "seq", 1, dev), T,
+        _here(cached, i32, "cached", (B,), dev), _here(fresh, i32, "fresh", (B,), dev), B, page,
+        _here(table, i32, "table", (B, max_pages), dev), max_pages, _here(ring, i32, "ring", (n_pages,), dev), n_pages,
+        _here(ring_in, i64, "ring_in", (2,), dev), _here(ring_out, i64, "ring_out", (2,), dev),
+        _here(kv_len, i32, "kv_len", (B,), dev), _here(cu_tokens, i32, "cu_tokens", (B + 1,), dev),
+        _here(slot, i32, "slot", (T,), dev), _here(pos, i32, "pos", (T,), dev), _here(seq, i32, "seq", (T,), dev), T,
         _status(status, dev), _stream_on(stream, dev))
     _check(st, "gem_kv_block_tables")
 
@@ -471,19 +461,16 @@ def qknorm_mrope(qkv: torch.Tensor, n_q: int, n_kv: int, d: int, gamma_q: torch.
     be qkv); pos int32 [n_axes, T]; sections: the number of frequencies of each axis (their sum is half
     of the rotated dims); interleaved: the axes take turns along the frequencies."""
     dev = torch.cuda.current_device()
-    T, cols = qkv.shape[0], (n_q + n_kv) * d
-    xp, ldx = _rows(qkv, cols, "qkv", dev)
-    op, ldo = _rows(out, cols, "out", dev)
-    if out.shape[0] != T or pos.dim() != 2 or pos.shape[1] != T or pos.shape[0] != len(sections):
-        raise ValueError("out must have T=%d rows and pos be [%d, T]" % (T, len(sections)))
-    gp = []
-    for name, g in (("gamma_q", gamma_q), ("gamma_k", gamma_k)):
-        gp.append(None if g is None else _here(g, torch.float32, name, 1, dev))
-        if g is not None and g.shape[0] != d:
-            raise ValueError("%s must be [d=%d]" % (name, d))
-    st = lib.gem_qknorm_mrope(xp, ldx, T, n_q, n_kv, d, gp[0], gp[1], eps, _here(pos, torch.int32, "pos", 2, dev), T,
-                              len(sections), (C.c_int32 * len(sections))(*sections), int(interleaved), theta, op,
-                              ldo, _status(status, dev), _stream_on(stream, dev))
+    cols, axes = (n_q + n_kv) * d, len(sections)
+    xp, ldx, T = _rows(qkv, cols, "qkv", dev)
+    op, ldo, rows = _rows(out, cols, "out", dev)
+    if rows != T:
+        raise ValueError("out must have T=%d rows, got %d" % (T, rows))
+    st = lib.gem_qknorm_mrope(
+        xp, ldx, T, n_q, n_kv, d, None if gamma_q is None else _here(gamma_q, torch.float32, "gamma_q", (d,), dev),
+        None if gamma_k is None else _here(gamma_k, torch.float32, "gamma_k", (d,), dev), eps,
+        _here(pos, torch.int32, "pos", (axes, T), dev), T, axes, (C.c_int32 * axes)(*sections), int(interleaved), theta,
+        op, ldo, _status(status, dev), _stream_on(stream, dev))
     _check(st, "gem_qknorm_mrope")
     return out
 
@@ -493,13 +480,12 @@ def kv4_append(k: torch.Tensor, v: torch.Tensor, n_kv: int, d: int, slot: torch.
     """Quantise the rows of k and v (fp32 [T, >= n_kv * d], columns of a wider tensor will do) into the
     slots int32 [T] (-1: none) of pool (uint8 [n_pages, kv4_page_bytes(n_kv, d, page)])."""
     dev = torch.cuda.current_device()
-    kp, ldk = _rows(k, n_kv * d, "k", dev)
-    vp, ldv = _rows(v, n_kv * d, "v", dev)
+    kp, ldk, T = _rows(k, n_kv * d, "k", dev)
+    vp, ldv, rows = _rows(v, n_kv * d, "v", dev)
     pp, n_pages = _pool(pool, n_kv, d, page, dev)
-    T = k.shape[0]
-    if v.shape[0] != T or slot.shape[0] != T:
-        raise ValueError("k, v and slot must have the same number of rows")
-    st = lib.gem_kv4_append(kp, ldk, vp, ldv, T, n_kv, d, _here(slot, torch.int32, "slot", 1, dev), pp, n_pages,
+    if rows != T:
+        raise ValueError("k and v must have the same number of rows, got %d and %d" % (T, rows))
+    st = lib.gem_kv4_append(kp, ldk, vp, ldv, T, n_kv, d, _here(slot, torch.int32, "slot", (T,), dev), pp, n_pages,
                             page, _status(status, dev), _stream_on(stream, dev))
     _check(st, "gem_kv4_append")
 
@@ -510,11 +496,11 @@ def kv4_gather(pool: torch.Tensor, page: int, n_kv: int, d: int, slot: torch.Ten
     dev = torch.cuda.current_device()
     pp, n_pages = _pool(pool, n_kv, d, page, dev)
     T = slot.shape[0]
-    (kp, ldk), (vp, ldv) = ((None, 0) if x is None else _rows(x, n_kv * d, name, dev)
-                            for name, x in (("k", k), ("v", v)))
-    if any(x is not None and x.shape[0] != T for x in (k, v)):
-        raise ValueError("k and v must have one row for each slot")
-    st = lib.gem_kv4_gather(pp, n_pages, page, n_kv, d, _here(slot, torch.int32, "slot", 1, dev), T, kp, ldk, vp,
+    kp, ldk, k_rows = (None, 0, T) if k is None else _rows(k, n_kv * d, "k", dev)
+    vp, ldv, v_rows = (None, 0, T) if v is None else _rows(v, n_kv * d, "v", dev)
+    if k_rows != T or v_rows != T:
+        raise ValueError("k and v must have one row for each of the %d slots" % T)
+    st = lib.gem_kv4_gather(pp, n_pages, page, n_kv, d, _here(slot, torch.int32, "slot", (T,), dev), T, kp, ldk, vp,
                             ldv, _status(status, dev), _stream_on(stream, dev))
     _check(st, "gem_kv4_gather")
     return k, v
@@ -533,22 +519,23 @@ def kv4_attn(q: torch.Tensor, n_q: int, n_kv: int, d: int, cu_tokens: torch.Tens
     table int32 [B, max_pages].  workspace: uint8, at least kv4_attn_workspace(...) bytes (allocated when
     not given)."""
     dev = torch.cuda.current_device()
-    qp, ldq = _rows(q, n_q * d, "q", dev)
-    op, ldo = _rows(out, n_q * d, "out", dev)
+    qp, ldq, T = _rows(q, n_q * d, "q", dev)
+    op, ldo, rows = _rows(out, n_q * d, "out", dev)
     pp, n_pages = _pool(pool, n_kv, d, page, dev)
-    B, T = kv_len.shape[0], q.shape[0]
-    if cu_tokens.shape[0] != B + 1 or table.shape[0] != B or out.shape[0] != T:
-        raise ValueError("cu_tokens must be [B + 1], table [B=%d, max_pages] and out have T=%d rows" % (B, T))
+    B, max_pages = kv_len.shape[0], table.shape[-1]
+    if rows != T:
+        raise ValueError("out must have T=%d rows, got %d" % (T, rows))
     if workspace is None:
         need = lib.gem_kv4_attn_workspace(T, B, n_q, n_kv, d)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-        if stream is not None and workspace is not None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        if stream is not None and need:
             workspace.record_stream(stream)   # it is given back here, before that stream has used it
-    st = lib.gem_kv4_attn(qp, ldq, T, _here(cu_tokens, torch.int32, "cu_tokens", 1, dev),
-                          _here(kv_len, torch.int32, "kv_len", 1, dev), B, n_q, n_kv, d,
-                          _here(table, torch.int32, "table", 2, dev), table.shape[1], pp, n_pages, page, window,
-                          scale, op, ldo, None if workspace is None else _here(workspace, torch.uint8, "workspace", 1, dev),
-                          0 if workspace is None else workspace.shape[0], _status(status, dev), _stream_on(stream, dev))
+    ws_bytes = workspace.shape[0]
+    st = lib.gem_kv4_attn(qp, ldq, T, _here(cu_tokens, torch.int32, "cu_tokens", (B + 1,), dev),
+                          _here(kv_len, torch.int32, "kv_len", (B,), dev), B, n_q, n_kv, d,
+                          _here(table, torch.int32, "table", (B, max_pages), dev), max_pages, pp, n_pages, page, window,
+                          scale, op, ldo, _here(workspace, torch.uint8, "workspace", (ws_bytes,), dev), ws_bytes,
+                          _status(status, dev), _stream_on(stream, dev))
     _check(st, "gem_kv4_attn")
     return out
 

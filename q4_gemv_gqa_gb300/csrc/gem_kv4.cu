@@ -31,9 +31,10 @@ struct Place {
     uint8_t *code, *scale;
 };
 
-__device__ __forceinline__ bool place_of(const RowsParams& P, Place& o) {
+// The `turn`-th of the `turns` octets of tokens that a CTA takes.
+__device__ __forceinline__ bool place_of(const RowsParams& P, int turns, int turn, Place& o) {
     o.u = threadIdx.x & 3;
-    o.t = blockIdx.x * 8ll + ((threadIdx.x >> 2) & 7);
+    o.t = (blockIdx.x * static_cast<int64_t>(turns) + turn) * 8 + ((threadIdx.x >> 2) & 7);
     const int part = blockIdx.y * (kRowThreads / 32) + (threadIdx.x >> 5), half = P.n_kv << P.lnb;
     if (o.t >= P.T || part >= 2 * half) return false;
     o.which = part >= half;
@@ -116,20 +117,8 @@ __device__ __forceinline__ uint32_t word_of(const float (&x)[8], float s) {
     return w;
 }
 
-__global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const RowsParams P) {
-    pdl_wait_trigger();
-    Place o;
-    const bool live = place_of(P, o);
-    float x[8];
-    if (live) {
-        const float* src = (o.which ? P.v + o.t * P.ldv : P.k + o.t * P.ldk) + o.head * P.d + o.blk * 32 + o.u * 4;
-        const bool vec = o.which ? P.vec_v : P.vec_k;
-        load4(src, vec, reinterpret_cast<float(&)[4]>(x[0]));
-        load4(src + 16, vec, reinterpret_cast<float(&)[4]>(x[4]));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    }
+// One block's eighth: the largest value of the block by its four threads, the scale, this thread's codes.
+__device__ __forceinline__ void quantise(const float (&x)[8], bool live, const Place& o) {
     float top = x[0], low = x[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) top = max_nan(top, x[i]), low = min_nan(low, x[i]);
@@ -170,36 +159,72 @@ __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const RowsParam
     if (o.u == 0) *reinterpret_cast<__half*>(o.scale) = s16;
 }
 
-__global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const RowsParams P) {
+// Bound by HBM and, close behind, by the quantisation's instructions: 4095 rows of 2 x 16 x 256 are 134 MB
+// read and 19 MB written, 36 us or 4.3 TB/s, 63 % of the measured copy rate.  (Two octets of tokens a
+// thread put more loads in flight and take 38 us.)
+__global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const RowsParams P) {
     pdl_wait_trigger();
     Place o;
-    if (!place_of(P, o)) return;
-    float* dst = o.which ? P.vo : P.ko;
-    if (!dst) return;
-    dst += o.t * (o.which ? P.ldv : P.ldk) + o.head * P.d + o.blk * 32 + o.u * 4;
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(o.code);
-    const float s = __half2float(*reinterpret_cast<const __half*>(o.scale));
-    float lo[4], hi[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        lo[i] = static_cast<float>(static_cast<int>((w >> (8 * i)) & 15) - 8) * s;
-        hi[i] = static_cast<float>(static_cast<int>((w >> (8 * i + 4)) & 15) - 8) * s;
-    }
-    if (o.which ? P.vec_v : P.vec_k) {
-        *reinterpret_cast<float4*>(dst) = make_float4(lo[0], lo[1], lo[2], lo[3]);
-        *reinterpret_cast<float4*>(dst + 16) = make_float4(hi[0], hi[1], hi[2], hi[3]);
+    const bool live = place_of(P, 1, 0, o);
+    float x[8];
+    if (live) {
+        const float* src = (o.which ? P.v + o.t * P.ldv : P.k + o.t * P.ldk) + o.head * P.d + o.blk * 32 + o.u * 4;
+        const bool vec = o.which ? P.vec_v : P.vec_k;
+        load4(src, vec, reinterpret_cast<float(&)[4]>(x[0]));
+        load4(src + 16, vec, reinterpret_cast<float(&)[4]>(x[4]));
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dst[i] = lo[i], dst[16 + i] = hi[i];
+        for (int i = 0; i < 8; ++i) x[i] = 0.f;
+    }
+    quantise(x, live, o);
+}
+
+// The same rows back: 19 MB read, 134 MB written in 27 us, 5.7 TB/s, 85 % of the measured copy rate with two
+// octets of tokens a thread (30 us with one).
+constexpr int kTurns = 2;
+__global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const RowsParams P) {
+    pdl_wait_trigger();
+    Place o[kTurns];
+    bool live[kTurns];
+    uint32_t w[kTurns];
+    float s[kTurns];
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+        live[k] = place_of(P, kTurns, k, o[k]) && (o[k].which ? P.vo : P.ko);
+        w[k] = 0, s[k] = 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k)
+        if (live[k]) {
+            w[k] = *reinterpret_cast<const uint32_t*>(o[k].code);
+            s[k] = __half2float(*reinterpret_cast<const __half*>(o[k].scale));
+        }
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+        if (!live[k]) continue;
+        float* dst = (o[k].which ? P.vo + o[k].t * P.ldv : P.ko + o[k].t * P.ldk) + o[k].head * P.d + o[k].blk * 32 + o[k].u * 4;
+        float lo[4], hi[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            lo[i] = static_cast<float>(static_cast<int>((w[k] >> (8 * i)) & 15) - 8) * s[k];
+            hi[i] = static_cast<float>(static_cast<int>((w[k] >> (8 * i + 4)) & 15) - 8) * s[k];
+        }
+        if (o[k].which ? P.vec_v : P.vec_k) {
+            *reinterpret_cast<float4*>(dst) = make_float4(lo[0], lo[1], lo[2], lo[3]);
+            *reinterpret_cast<float4*>(dst + 16) = make_float4(hi[0], hi[1], hi[2], hi[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dst[i] = lo[i], dst[16 + i] = hi[i];
+        }
     }
 }
 
 bool vec_ok(const float* p, int64_t ld) { return !(reinterpret_cast<uintptr_t>(p) & 15) && ld % 4 == 0; }
 
-gem_status rows_launch(const void* kernel, RowsParams& P, cudaStream_t stream) {
+gem_status rows_launch(const void* kernel, int turns, RowsParams& P, cudaStream_t stream) {
     const gem_status st = flag_word(&P.status);
     if (st != GEM_OK) return st;
-    const int64_t x = (P.T + 7) / 8, y = (2ll * (P.n_kv << P.lnb) + kRowThreads / 32 - 1) / (kRowThreads / 32);
+    const int64_t x = (P.T + 8 * turns - 1) / (8 * turns), y = (2ll * (P.n_kv << P.lnb) + kRowThreads / 32 - 1) / (kRowThreads / 32);
     if (x > INT32_MAX || y > 65535) return GEM_ERR_UNSUPPORTED_SHAPE;
     void* args[] = {&P};
     return launch_pdl(kernel, dim3(static_cast<unsigned>(x), static_cast<unsigned>(y)), dim3(kRowThreads), 0, stream, args);
@@ -233,7 +258,7 @@ gem_status gem_kv4_append(const float* k, int64_t ldk, const float* v, int64_t l
     P.n_kv = n_kv, P.d = d, P.lnb = log2_of(d / 32), P.lpage = log2_of(page);
     P.vec_k = vec_ok(k, ldk), P.vec_v = vec_ok(v, ldv);
     P.status = status;
-    return rows_launch(reinterpret_cast<const void*>(kv4_append_kernel), P, static_cast<cudaStream_t>(stream));
+    return rows_launch(reinterpret_cast<const void*>(kv4_append_kernel), 1, P, static_cast<cudaStream_t>(stream));
 }
 
 gem_status gem_kv4_gather(const void* pool, int64_t n_pages, int page, int n_kv, int d, const int32_t* slot,
@@ -253,7 +278,7 @@ gem_status gem_kv4_gather(const void* pool, int64_t n_pages, int page, int n_kv,
     P.n_kv = n_kv, P.d = d, P.lnb = log2_of(d / 32), P.lpage = log2_of(page);
     P.vec_k = vec_ok(k, ldk), P.vec_v = vec_ok(v, ldv);
     P.status = status;
-    return rows_launch(reinterpret_cast<const void*>(kv4_gather_kernel), P, static_cast<cudaStream_t>(stream));
+    return rows_launch(reinterpret_cast<const void*>(kv4_gather_kernel), kTurns, P, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

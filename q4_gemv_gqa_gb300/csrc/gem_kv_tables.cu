@@ -191,15 +191,14 @@ extern "C" gem_status gem_kv_block_tables(const int32_t* cached, const int32_t* 
     P.table = table, P.max_pages = max_pages, P.ring = ring, P.n_pages = n_pages;
     P.ring_in = ring_in, P.ring_out = ring_out, P.kv_len = kv_len, P.cu = cu_tokens;
     P.slot = slot, P.pos = pos, P.seq = seq, P.T_cap = T_cap, P.status = status;
-    const gem_status st = flag_word(&P.status);
+    DeviceInfo di;
+    const gem_status st = device_info(&di);
     if (st != GEM_OK) return st;
+    if (!status) P.status = di.status_word;
     void* args[] = {&P};
     // a thread for each token of a large step; a decode step's tokens fit a CTA of few threads, which starts
     // sooner
     const int threads = B <= 32 && T_cap <= 256 ? 256 : kTabThreads;
-    DeviceInfo di;
-    const gem_status st2 = device_info(&di);
-    if (st2 != GEM_OK) return st2;
     const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(di.num_sms, (T_cap + threads - 1) / threads));
     return launch_pdl(reinterpret_cast<const void*>(kv_tables_kernel), dim3(static_cast<unsigned>(ctas)), dim3(threads), 0,
                       static_cast<cudaStream_t>(stream), args);
