@@ -1,7 +1,7 @@
 /*
  * gem.h — C ABI of the GB300 (sm_103a) decoder-step library: Q4_0 dequantise-and-matvec,
  * RMSNorm / per-head QK-norm / RoPE / KV append, grouped-query split-K decode attention,
- * gated FFN activation, and one whole decoder layer step.
+ * gated FFN activation, one whole decoder layer step, and a paged 4-bit KV cache.
  *
  * Sources, cited by page title and section:
  *   [GEM]  "gem" engine research record (Gemma 4 native engine), sections "Verified model
@@ -31,7 +31,8 @@
  *     nibble and element j + 16 in its high nibble); weight = (q - 8) * d.  [GEM]
  *   - The fast path needs K % 256 == 0 and a 16-byte aligned matrix; other matrices with
  *     K % 32 == 0 go through a slower general kernel.  K % 32 != 0 is rejected.
- *   - Batch B is 0..8 (0 = nothing to do).  Larger batches are GEM_ERR_UNSUPPORTED_SHAPE.
+ *   - Batch B is 0..8 (0 = nothing to do).  Larger batches are GEM_ERR_UNSUPPORTED_SHAPE.  (The
+ *     paged cache's calls have limits of their own.)
  *   - Arguments are checked on the host before anything is enqueued; a rejected call has
  *     no effect.  Values only the device can see (positions) are checked by the kernels,
  *     which then skip the offending sequence and OR a GEM_DEVFLAG_* bit into *status
@@ -104,7 +105,8 @@ GEM_API gem_status gem_status_from_flags(int32_t flags);
  *         same synchronisation rules.  While set:
  *           GEM_INJECT_RING_SHORTFALL  the one-row Q4_0 GEMV (B = 1, K % 256 == 0) makes
  *             CTA 0 expect 16 bytes more than its last ring stage receives, so that stage's
- *             wait runs out after the wait limit (every copy still lands);
+ *             wait runs out after the wait limit (every copy still lands); gem_kv4_attn's first
+ *             warp does the same with its first stage;
  *           GEM_INJECT_GRID_ARRIVAL  gem_decode_step makes CTA 0 leave out its arrival at
  *             the step's first grid barrier, so every CTA's barrier wait runs out and the
  *             step is aborted (the plan must then be destroyed and created again).

