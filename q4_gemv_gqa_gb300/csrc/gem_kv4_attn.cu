@@ -660,7 +660,10 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
             }
         // Scores well past the maxima so far, or larger scales: new maxima, and the sums are rescaled.  (Any
         // maximum would make it half of the steps; p may pass 1 by kSlack powers of two instead.)
-        if (__any_sync(0xffffffffu, up) || e_step < E) {
+        // The scales are this warp's dims' alone, the scores the same for all warps of a head: a maximum moves
+        // for the scores only, so that it stays the same too, since parts are joined under one of them.
+        const bool rise = __any_sync(0xffffffffu, up);
+        if (rise || e_step < E) {
             const int e_new = e_step < E ? e_step - 1 : E;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -668,12 +671,14 @@ __global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnPara
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     float mx = m[nt][k];
+                    if (rise) {
 #pragma unroll
-                    for (int s = 0; s < kStepTiles; ++s)
+                        for (int s = 0; s < kStepTiles; ++s)
 #pragma unroll
-                        for (int v = k; v < NV; v += 2) mx = fmaxf(mx, x[s][nt][v]);
+                            for (int v = k; v < NV; v += 2) mx = fmaxf(mx, x[s][nt][v]);
 #pragma unroll
-                    for (int o = PACK ? 2 : 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                        for (int o = PACK ? 2 : 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    }
                     corr[k] = (m[nt][k] == mx ? 1.f : ex2(m[nt][k] - mx)) * pow2(e_new - E);
                     m[nt][k] = mx;
                     l[nt][k] *= corr[k];

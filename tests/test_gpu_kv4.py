@@ -806,3 +806,31 @@ print("captured")
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=280)
     assert r.returncode == 0 and "captured" in r.stdout, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("case", [(8, 4, 256, 6000, 16), (32, 4, 256, 6000, 16), (4, 2, 512, 6000, 12), (16, 2, 512, 6000, 12)], ids=str)
+def test_attention_whose_value_scales_grow_in_part_of_the_dims(env, case):
+    """The warps that share a head rescale their own sums when V's scales grow, and parts of a sequence
+    are joined under the maximum of one of them: it has to be the same for all.  The scales of the last
+    dims double every 32 positions for 256 positions, over and over, those of the first dims do not; the
+    batch is large enough for every warp to pass several of them (the requests share their pages)."""
+    g, t = env
+    n_q, n_kv, d, L, B = case
+    page = 64
+    r = np.random.RandomState(70 + d + n_q)
+    pool, table, _, _ = _attn_case(r, t, [L], [1], n_q, n_kv, d, page)
+    tiles = pool.bytes.reshape(len(pool.bytes), n_kv, page // 16, 18 * d)
+    scales = tiles[..., 16 * d:].view(np.float16).reshape(len(pool.bytes), n_kv, page // 16, 2, d // 32, 16)
+    for j in range(0, L // 16 * 16, 16):
+        at = scales[table[0, j // page], :, j % page // 16, 1, d // 64:]
+        at[:] = (at.astype(np.float64) * 2.0 ** (j % 256 // 32 - 4)).astype(np.float16)
+    x = _unpack(pool, d)
+    slots = table[0, np.arange(L) // page] * page + np.arange(L) % page
+    K, V = x[0, slots], x[1, slots]
+    q = (2 * r.randn(B, n_q * d)).astype(np.float32)
+    got = _attn_run(g, t, pool, np.repeat(table, B, 0), np.arange(B + 1, dtype=np.int32), q, [L] * B, n_q, n_kv, d, page, 0,
+                    d ** -0.5)
+    want = np.stack([kv4.attention(q[b].reshape(1, n_q, d), K, V, L, 0, d ** -0.5)[0] for b in range(B)])
+    got = got.reshape(want.shape)
+    for half in (slice(0, d // 2), slice(d // 2, d)):
+        assert_close(got[..., half], want[..., half], "dims %s" % half, max_abs=2e-4 * np.abs(want[..., half]).max(), rel_l2=1e-5)
