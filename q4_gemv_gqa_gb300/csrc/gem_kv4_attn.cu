@@ -40,8 +40,6 @@ namespace kv4 {
 namespace {
 
 constexpr int kMaxGroup = 8;
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 constexpr int kStepTiles = 2;
 constexpr int kStepTokens = kStepTiles * kTileTokens;
 constexpr int kStages = 2;
@@ -204,8 +202,9 @@ struct Part {
     static constexpr int kFloats = ROWS * (D + 2);
 };
 
-template <int D, int NT, bool PACK, int DW>
+template <int D, int NT, bool PACK, int DW, int WARPS>
 struct Cfg {
+    static constexpr int kWarps = WARPS, kThreads = 32 * WARPS;
     static constexpr int kRows = PACK ? 4 : 8 * NT;      // query rows of a unit
     static constexpr int kDims = DW;                     // dims of one warp
     static constexpr int kPair = D / kDims;              // warps of a worker
@@ -228,16 +227,19 @@ struct Cfg {
 // ---- the kernel ------------------------------------------------------------------------------------
 //
 // What bounds it: the warp instructions, about 800 a step of 32 positions at d 128 and four rows, of
-// which unpacking the codes is 290 and splitting p times V's scale 100; with 16 warps an SM (the sums, q
-// and a tile's operands are 128 registers) the issue slots are 58 % used.  8 requests of up to 32,768
-// positions (32 / 8 heads, d 128, 257 MB): 71 us, 3.6 TB/s, 53 % of the measured copy rate.  Short batches
-// are latency: 1 x 4097 positions take 9.9 us, 1 x 100 take 8.8.
-// Steps of 32 positions: with 16 the per-step work (waits, maxima, requests) weighs twice (85 us above),
-// and two stages of more do not fit twice in an SM's shared memory.
+// which unpacking the codes is 290 and splitting p times V's scale 100, and their latency, with three
+// warps a scheduler.  8 requests of up to 32,768 positions (32 / 8 heads, d 128, 257 MB): 67 us, 3.8 TB/s,
+// 57 % of the measured copy rate.  Short batches are latency: 1 x 4097 positions take 9 us.
+// One CTA of 12 warps an SM has 168 registers a thread for the sums, q and the operands under way; two of
+// 8 have 128, spill, and take 71 us there, 15.1 against 12.9 for 8 requests of up to 2049 positions; 10
+// warps take 76 and 12.1.
+// Steps of 32 positions: with 16 the per-step work (waits, maxima, requests) weighs twice (85 us against
+// 71), and longer ones do not fit shared memory twice for every warp.
 
-template <int D, int NT, bool PACK, int DW, int CTAS>
-__global__ void __launch_bounds__(kThreads, CTAS) kv4_attn_kernel(const AttnParams P) {
-    using C = Cfg<D, NT, PACK, DW>;
+template <int D, int NT, bool PACK, int DW, int WARPS, int CTAS>
+__global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnParams P) {
+    using C = Cfg<D, NT, PACK, DW, WARPS>;
+    constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
     constexpr int NB = C::kBlocks, ROWS = C::kRows, PAIR = C::kPair;
     constexpr int NH = PACK ? 1 : 2;                     // B operands of a product: (hi | lo) or hi, lo
     extern __shared__ __align__(128) uint8_t smem[];
@@ -978,32 +980,38 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_attn_merge_kernel(const Att
 
 struct Variant {
     const void *kernel, *merge;
-    int rows, ctas, cta_workers, part_floats;
+    int rows, threads, ctas, cta_workers, part_floats;
     size_t (*smem)(int);
 };
 
-template <int D, int NT, bool PACK, int DW, int CTAS>
+template <int D, int NT, bool PACK, int DW, int WARPS, int CTAS>
 Variant variant() {
-    using C = Cfg<D, NT, PACK, DW>;
-    return {reinterpret_cast<const void*>(kv4_attn_kernel<D, NT, PACK, DW, CTAS>),
-            reinterpret_cast<const void*>(kv4_attn_merge_kernel<D, C::kRows, C::kWorkers>), C::kRows, CTAS, C::kWorkers,
+    using C = Cfg<D, NT, PACK, DW, WARPS>;
+    return {reinterpret_cast<const void*>(kv4_attn_kernel<D, NT, PACK, DW, WARPS, CTAS>),
+            reinterpret_cast<const void*>(kv4_attn_merge_kernel<D, C::kRows, C::kWorkers>), C::kRows, C::kThreads, CTAS, C::kWorkers,
             Part<D, C::kRows>::kFloats, C::smem};
 }
 
 // Query rows a unit has: one token's heads, or as many tokens as the batch brings on average while
 // the sums of a warp stay in registers.  (Any batch is right with any of them: a request's tokens are cut
-// into units.)  Measured, 8 rows of d 128 with 16 warps an SM spill: 22 us against 16 with 8 warps
-// (8 x 16,384 positions, one KV head); at d 512 four warps of 128 dims a head likewise, 52 against 44
-// (1 x 32,769); 32 rows a unit in warps of 64 dims: 77 against 62 (4 chunks of 32 tokens).  Up to four
-// rows, 128 dims a warp and 16 warps an SM win: 25 against 28 (8 x window 1024, d 256).
+// into units.)  Measured: 8 rows of d 128 take 8 warps of 255 registers (4 x 32 new tokens: 63 us with 16
+// rows; 12 warps spill, 104; 32 rows in warps of 64 dims, 77); so do 8 rows at d 256 and 512, with 256
+// dims a warp (1 x 32,769, d 512: 36 us; 128 dims a warp: 37 with 12 warps, 52 with 16).  Up to four rows
+// take 128 dims a warp.
 Variant pick(int64_t T, int B, int G, int d) {
     const int64_t tokens = std::max<int64_t>(1, (T + B - 1) / std::max(B, 1));
     const int64_t want = tokens * G;
     switch (d) {
-        case 64: return want <= 4 ? variant<64, 1, true, 64, 2>() : want <= 8 ? variant<64, 1, false, 64, 2>() : variant<64, 2, false, 64, 1>();
-        case 128: return want <= 4 ? variant<128, 1, true, 128, 2>() : want <= 8 ? variant<128, 1, false, 128, 1>() : variant<128, 2, false, 128, 1>();
-        case 256: return want <= 4 ? variant<256, 1, true, 128, 2>() : variant<256, 1, false, 256, 1>();
-        default: return want <= 4 ? variant<512, 1, true, 128, 2>() : variant<512, 1, false, 256, 1>();
+        case 64:
+            return want <= 4   ? variant<64, 1, true, 64, 12, 1>()
+                   : want <= 8 ? variant<64, 1, false, 64, 12, 1>()
+                               : variant<64, 2, false, 64, 8, 1>();
+        case 128:
+            return want <= 4   ? variant<128, 1, true, 128, 12, 1>()
+                   : want <= 8 ? variant<128, 1, false, 128, 8, 1>()
+                               : variant<128, 2, false, 128, 8, 1>();
+        case 256: return want <= 4 ? variant<256, 1, true, 128, 12, 1>() : variant<256, 1, false, 256, 8, 1>();
+        default: return want <= 4 ? variant<512, 1, true, 128, 12, 1>() : variant<512, 1, false, 256, 8, 1>();
     }
 }
 
@@ -1076,7 +1084,7 @@ gem_status gem_kv4_attn(const float* q, int64_t ldq, int64_t T, const int32_t* c
     if (smem > di.smem_optin) return GEM_ERR_UNSUPPORTED_SHAPE;
     if ((st = allow_smem(v.kernel, di, v.smem(kMaxRequests))) != GEM_OK) return st;
     void* args[] = {&P};
-    if ((st = launch_pdl(v.kernel, dim3(ctas), dim3(kThreads), smem, static_cast<cudaStream_t>(stream), args)) != GEM_OK)
+    if ((st = launch_pdl(v.kernel, dim3(ctas), dim3(v.threads), smem, static_cast<cudaStream_t>(stream), args)) != GEM_OK)
         return st;
     return launch_pdl(v.merge, dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(v.rows)),
                       dim3(kMergeThreads), 0, static_cast<cudaStream_t>(stream), args);
