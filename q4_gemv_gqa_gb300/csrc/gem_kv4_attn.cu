@@ -516,23 +516,22 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
         constexpr bool clean = decltype(clean_c)::value;
         const uint8_t* st = ring + stage * C::kStage;
         const uint32_t gone = (lost >> (stage * kStepTiles)) & kMask;
-        // scales in fp32: K's as (row g, row g, row g + 8, row g + 8), V's as (2t, 2t + 1, 2t + 8, 2t + 9)
-#pragma unroll
-        for (int it = 0; it < kStepTiles * NB * 8; it += 32) {
-            const int at = it + lane, sb = at >> 3, r = at & 7, s = sb / NB, b = sb % NB;
-            const __half* ks = reinterpret_cast<const __half*>(st + s * C::kTile + scales_off(C::kDims, 0)) + b * 16;
-            // an infinite scale becomes NaN (x + 0 x): times a negative sum it would hide its position
-            float k0 = __half2float(ks[r]), k1 = __half2float(ks[r + 8]);
-            k0 = fmaf(k0, 0.f, k0), k1 = fmaf(k1, 0.f, k1);
-            reinterpret_cast<float4*>(scales + sb * 48)[r] = make_float4(k0, k0, k1, k1);
-        }
+        // scales in fp32: K's as (row g, row g, row g + 8, row g + 8), V's as (2t, 2t + 1, 2t + 8, 2t + 9); a lane
+        // takes positions 2r, 2r + 1, 2r + 8 and 2r + 9 of a block of both
         __half2 big2 = __float2half2_rn(0.f);
+        const __half2 zero2 = __float2half2_rn(0.f);
 #pragma unroll
         for (int it = 0; it < kStepTiles * NB * 4; it += 32) {
             const int at = it + lane, sb = at >> 2, r = at & 3, s = sb / NB, b = sb % NB;
             if (kStepTiles * NB * 4 % 32 == 0 || sb < kStepTiles * NB) {
-                const __half2* vs = reinterpret_cast<const __half2*>(st + s * C::kTile + scales_off(C::kDims, 1)) + b * 8;
-                __half2 v0 = vs[r], v1 = vs[r + 4];
+                const __half2* ks = reinterpret_cast<const __half2*>(st + s * C::kTile + scales_off(C::kDims, 0)) + b * 8 + r;
+                const __half2* vs = ks + C::kDims / 4;
+                // an infinite scale of K becomes NaN (x + 0 x): times a negative sum it would hide its position
+                const float2 k0 = __half22float2(__hfma2(ks[0], zero2, ks[0])), k1 = __half22float2(__hfma2(ks[4], zero2, ks[4]));
+                float4* to = reinterpret_cast<float4*>(scales + sb * 48);
+                to[2 * r] = make_float4(k0.x, k0.x, k1.x, k1.x);
+                to[2 * r + 1] = make_float4(k0.y, k0.y, k1.y, k1.y);
+                __half2 v0 = vs[0], v1 = vs[4];
                 if (!clean) {   // what no row attends may be anything
                     const int pos = pos0 + s * kTileTokens + 2 * r;
                     auto in = [&](int p) { return p >= lo_all && p <= hi_all && !(gone >> s & 1); };
@@ -540,11 +539,10 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
                     v0 = __halves2half2(in(pos) ? __low2half(v0) : zero, in(pos + 1) ? __high2half(v0) : zero);
                     v1 = __halves2half2(in(pos + 8) ? __low2half(v1) : zero, in(pos + 9) ? __high2half(v1) : zero);
                 }
-                // infinities become NaN (x + 0 x), which the maximum passes over
-                const __half2 zero2 = __float2half2_rn(0.f);
+                // infinities become NaN, which the maximum passes over
                 big2 = __hmax2(big2, __hmax2(__habs2(__hfma2(v0, zero2, v0)), __habs2(__hfma2(v1, zero2, v1))));
                 const float2 f0 = __half22float2(v0), f1 = __half22float2(v1);
-                reinterpret_cast<float4*>(scales + sb * 48 + 32)[r] = make_float4(f0.x, f0.y, f1.x, f1.y);
+                to[8 + r] = make_float4(f0.x, f0.y, f1.x, f1.y);
             }
         }
         // p 2^E sV stays below 2^15, p up to 2^kSlack (binary16 numbers that are not negative order as their
@@ -623,13 +621,6 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
                     sc[s][nt][0] = v.x, sc[s][nt][1] = v.y, sc[s][nt][2] = v.z, sc[s][nt][3] = v.w;
                 }
         }
-
-        // the first tile's V codes are under way while the probabilities are taken
-        uint32_t vw[NB / 2][4];
-#pragma unroll
-        for (int b2 = 0; b2 < NB; b2 += 2)
-            ldmatrix_x4_trans(vw[b2 / 2][0], vw[b2 / 2][1], vw[b2 / 2][2], vw[b2 / 2][3],
-                              smem_u32(st + codes_off(C::kDims, 1)) + lane * 16 + b2 * 256);
 
         // p: in log2 units; PACK: the two halves' sums, lanes t < 2 keep row g, the others row g + 8
         constexpr int NV = PACK ? 2 : 4;
@@ -712,6 +703,13 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
 
         // values
         const uint32_t flip = !PACK || g >= 4 ? 0x80000000u : 0u;
+        uint32_t vw[kStepTiles][NB / 2][4];
+#pragma unroll
+        for (int s = 0; s < kStepTiles; ++s)
+#pragma unroll
+            for (int b2 = 0; b2 < NB; b2 += 2)
+                ldmatrix_x4_trans(vw[s][b2 / 2][0], vw[s][b2 / 2][1], vw[s][b2 / 2][2], vw[s][b2 / 2][3],
+                                  smem_u32(st + s * C::kTile + codes_off(C::kDims, 1)) + lane * 16 + b2 * 256);
         const float2 keep = !PACK || g >= 4 ? make_float2(1.f, 1.f) : make_float2(0.f, 0.f);
 #pragma unroll
         for (int s = 0; s < kStepTiles; ++s) {
@@ -726,12 +724,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
 #pragma unroll
             for (int b2 = 0; b2 < NB; b2 += 2) {
                 uint32_t w[4];
-                if (s == 0) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) w[k] = vw[b2 / 2][k];
-                } else {
-                    ldmatrix_x4_trans(w[0], w[1], w[2], w[3], codes + b2 * 256);
-                }
+                for (int k = 0; k < 4; ++k) w[k] = vw[s][b2 / 2][k];
 #pragma unroll
                 for (int b = b2; b < b2 + 2; ++b) {
                     const uint32_t wa = w[2 * (b - b2)], wb = w[2 * (b - b2) + 1];
