@@ -226,10 +226,10 @@ struct Cfg {
 
 // ---- the kernel ------------------------------------------------------------------------------------
 //
-// What bounds it: the warp instructions, about 800 a step of 32 positions at d 128 and four rows, of
+// What bounds it: the warp instructions, about 730 a step of 32 positions at d 128 and four rows, of
 // which unpacking the codes is 290 and splitting p times V's scale 100, and their latency, with three
-// warps a scheduler.  8 requests of up to 32,768 positions (32 / 8 heads, d 128, 257 MB): 67 us, 3.8 TB/s,
-// 57 % of the measured copy rate.  Short batches are latency: 1 x 4097 positions take 9 us.
+// warps a scheduler issuing in 57 % of the cycles.  8 requests of up to 32,768 positions (32 / 8 heads,
+// d 128, 257 MB): 66 us, 3.9 TB/s, 58 % of the measured copy rate.  Short batches are latency: 1 x 4097 positions take 9 us.
 // One CTA of 12 warps an SM has 168 registers a thread for the sums, q and the operands under way; two of
 // 8 have 128, spill, and take 71 us there, 15.1 against 12.9 for 8 requests of up to 2049 positions; 10
 // warps take 76 and 12.1.
@@ -702,7 +702,6 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
         __syncwarp();
 
         // values
-        const uint32_t flip = !PACK || g >= 4 ? 0x80000000u : 0u;
         uint32_t vw[kStepTiles][NB / 2][4];
 #pragma unroll
         for (int s = 0; s < kStepTiles; ++s)
@@ -710,6 +709,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
             for (int b2 = 0; b2 < NB; b2 += 2)
                 ldmatrix_x4_trans(vw[s][b2 / 2][0], vw[s][b2 / 2][1], vw[s][b2 / 2][2], vw[s][b2 / 2][3],
                                   smem_u32(st + s * C::kTile + codes_off(C::kDims, 1)) + lane * 16 + b2 * 256);
+        const uint32_t flip = !PACK || g >= 4 ? 0x80000000u : 0u;
         const float2 keep = !PACK || g >= 4 ? make_float2(1.f, 1.f) : make_float2(0.f, 0.f);
 #pragma unroll
         for (int s = 0; s < kStepTiles; ++s) {
@@ -720,12 +720,9 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
                 pr[nt][0] = *reinterpret_cast<const float2*>(row);
                 pr[nt][1] = *reinterpret_cast<const float2*>(row + 8);
             }
-            const uint32_t codes = smem_u32(st + s * C::kTile + codes_off(C::kDims, 1)) + lane * 16;
 #pragma unroll
             for (int b2 = 0; b2 < NB; b2 += 2) {
-                uint32_t w[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) w[k] = vw[s][b2 / 2][k];
+                const uint32_t (&w)[4] = vw[s][b2 / 2];
 #pragma unroll
                 for (int b = b2; b < b2 + 2; ++b) {
                     const uint32_t wa = w[2 * (b - b2)], wb = w[2 * (b - b2) + 1];
