@@ -504,7 +504,7 @@ GEM_API gem_status gem_kv4_gather(const void *pool, int64_t n_pages, int page, i
  *          overlap q.  Rows from cu_tokens[B] on are neither read nor written.
  *   table  [B][max_pages] int32; entries from ceil(kv_len / page) on are not read, nor those that
  *          lie before every row's window.
- *   d 64, 128, 256 or 512; n_q % n_kv == 0, n_q / n_kv <= 8; B in 0..4096.
+ *   d 64, 128, 256 or 512; n_q % n_kv == 0, n_q / n_kv <= 8; B in 0..4096; T * n_kv < 2^31.
  *   Device checks: cu_tokens out of order or beyond T, kv_len[b] < n or beyond max_pages * page set
  *   GEM_DEVFLAG_POS_RANGE and leave the request's rows as they were; a table entry outside
  *   [0, n_pages) sets GEM_DEVFLAG_PAGE_RANGE and its positions count as masked (a row with no

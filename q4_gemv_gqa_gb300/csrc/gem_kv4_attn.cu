@@ -28,9 +28,7 @@
 #include <algorithm>
 #include <cmath>
 #include <mutex>
-#include <set>
 #include <type_traits>
-#include <utility>
 
 #include "gem_device.cuh"
 #include "gem_kv4.cuh"
@@ -1008,13 +1006,19 @@ Variant pick(int64_t T, int B, int G, int d) {
 
 // Once for each kernel and device: the dynamic shared memory of the largest batch.
 gem_status allow_smem(const void* kernel, const DeviceInfo& di, size_t bytes) {
+    struct Done {
+        int device;
+        const void* kernel;
+    };
     static std::mutex mu;
-    static std::set<std::pair<int, const void*>> done;
+    static Done done[256];     // (beyond these it is set at every call)
+    static int n = 0;
     std::lock_guard<std::mutex> lk(mu);
-    if (done.count({di.device, kernel})) return GEM_OK;
+    for (int i = 0; i < n; ++i)
+        if (done[i].device == di.device && done[i].kernel == kernel) return GEM_OK;
     GEM_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       static_cast<int>(std::min(bytes, di.smem_optin))));
-    done.insert({di.device, kernel});
+    if (n < 256) done[n++] = {di.device, kernel};
     return GEM_OK;
 }
 
@@ -1049,7 +1053,7 @@ gem_status gem_kv4_attn(const float* q, int64_t ldq, int64_t T, const int32_t* c
     if (st != GEM_OK) return st;
     if (T < 0 || B < 0 || n_q < 0 || max_pages < 0 || window < 0) return GEM_ERR_INVALID_ARG;
     if (n_kv == 0 ? n_q != 0 : n_q % n_kv != 0) return GEM_ERR_INVALID_ARG;
-    if (B > kMaxRequests || T > INT32_MAX || max_pages > (INT32_MAX - 255) / page ||
+    if (B > kMaxRequests || T > INT32_MAX / std::max(n_kv, 1) || max_pages > (INT32_MAX - 255) / page ||
         (n_kv && n_q / n_kv > kMaxGroup))
         return GEM_ERR_UNSUPPORTED_SHAPE;
     if (T == 0 || B == 0 || n_q == 0) return GEM_OK;

@@ -209,7 +209,7 @@ def test_attn_refusals(lib):
                dict(table=None), dict(pool=None), dict(ldq=252), dict(ldo=255), dict(d=0), dict(out=D, q=D)):
         assert _attn(lib, **kw) == INVALID, kw
     for kw in (dict(n_q=18, ldq=9999 * 4, ldo=9999), dict(d=96, ldq=800, ldo=800), dict(page=24), dict(B=4097),
-               dict(T=1 << 31), dict(max_pages=1 << 27), dict(n_pages=1 << 27)):
+               dict(T=1 << 31), dict(T=1 << 30), dict(max_pages=1 << 27), dict(n_pages=1 << 27)):
         assert _attn(lib, **kw) == UNSUPPORTED, kw
     for kw in (dict(q=ODD), dict(ldq=257), dict(pool=ODD)):
         assert _attn(lib, **kw) == MISALIGNED, kw
