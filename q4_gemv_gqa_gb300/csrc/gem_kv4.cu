@@ -19,38 +19,36 @@ struct RowsParams {
     int* status;
 };
 
-// Four threads hold one block of 32 values: thread u elements 4u .. 4u + 3 and 16 + 4u .. 16 + 4u + 3,
-// which are the low and the high nibbles of word u of the block's 16 bytes of codes.  The eight
-// blocks of a warp are eight consecutive tokens of one part (K or V, head, block), so that the codes and
-// the scales of a prompt's tokens are written next to one another, and the warps of a CTA have
-// consecutive parts, so that it reads whole 1 KB pieces of the rows.
+// Four threads hold one block of 32 values of K and of V: thread u elements 4u .. 4u + 3 and
+// 16 + 4u .. 16 + 4u + 3, which are the low and the high nibbles of word u of the block's 16 bytes of
+// codes.  The eight blocks of a warp are eight consecutive tokens of one (head, block), so that the codes
+// and the scales of a prompt's tokens are written next to one another, and the warps of a CTA have
+// consecutive ones, so that it reads whole 1 KB pieces of the rows.
 constexpr int kRowThreads = 256;
 struct Place {
     int64_t t;
-    int which, head, blk, u;
-    uint8_t *code, *scale;
+    int u, col;            // column of the row: the block's first plus 4 u
+    uint8_t *code, *scale; // K's; V's are 8 d and d bytes on
 };
 
-// The `turn`-th of the `turns` octets of tokens that a CTA takes.
-__device__ __forceinline__ bool place_of(const RowsParams& P, int turns, int turn, Place& o) {
+__device__ __forceinline__ bool place_of(const RowsParams& P, Place& o) {
     o.u = threadIdx.x & 3;
-    o.t = (blockIdx.x * static_cast<int64_t>(turns) + turn) * 8 + ((threadIdx.x >> 2) & 7);
-    const int part = blockIdx.y * (kRowThreads / 32) + (threadIdx.x >> 5), half = P.n_kv << P.lnb;
-    if (o.t >= P.T || part >= 2 * half) return false;
-    o.which = part >= half;
-    o.head = (part - (o.which ? half : 0)) >> P.lnb;
-    o.blk = part & ((1 << P.lnb) - 1);
+    o.t = blockIdx.x * 8ll + ((threadIdx.x >> 2) & 7);
+    const int part = blockIdx.y * (kRowThreads / 32) + (threadIdx.x >> 5);
+    if (o.t >= P.T || part >= P.n_kv << P.lnb) return false;
+    const int head = part >> P.lnb, blk = part & ((1 << P.lnb) - 1);
+    o.col = part * 32 + o.u * 4;
     const int32_t s = P.slot[o.t];
     if (s < 0 || s >= P.n_slots) {
         if (s != -1 && part == 0 && o.u == 0) atomicOr(P.status, GEM_DEVFLAG_PAGE_RANGE);
         return false;
     }
     const int lpt = P.lpage - 4;
-    const int64_t tile = ((static_cast<int64_t>(s >> P.lpage) * P.n_kv + o.head) << lpt) + ((s >> 4) & ((1 << lpt) - 1));
-    const int row = s % kTileTokens;
+    const int64_t tile = ((static_cast<int64_t>(s >> P.lpage) * P.n_kv + head) << lpt) + ((s >> 4) & ((1 << lpt) - 1));
+    const int at = blk * kTileTokens + s % kTileTokens;
     uint8_t* base = P.pool + tile * tile_bytes(P.d);
-    o.code = base + codes_off(P.d, o.which) + (o.blk * kTileTokens + row) * 16 + o.u * 4;
-    o.scale = base + scales_off(P.d, o.which) + (o.blk * kTileTokens + row) * 2;
+    o.code = base + at * 16 + o.u * 4;
+    o.scale = base + scales_off(P.d, 0) + at * 2;
     return true;
 }
 
@@ -118,7 +116,7 @@ __device__ __forceinline__ uint32_t word_of(const float (&x)[8], float s) {
 }
 
 // One block's eighth: the largest value of the block by its four threads, the scale, this thread's codes.
-__device__ __forceinline__ void quantise(const float (&x)[8], bool live, const Place& o) {
+__device__ __forceinline__ void quantise(const float (&x)[8], bool live, int u, uint8_t* code, uint8_t* scale) {
     float top = x[0], low = x[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) top = max_nan(top, x[i]), low = min_nan(low, x[i]);
@@ -133,14 +131,14 @@ __device__ __forceinline__ void quantise(const float (&x)[8], bool live, const P
         int first = 32;
 #pragma unroll
         for (int i = 7; i >= 0; --i)
-            if (fabsf(x[i]) == top) first = (i < 4 ? 0 : 16) + o.u * 4 + (i & 3);
+            if (fabsf(x[i]) == top) first = (i < 4 ? 0 : 16) + u * 4 + (i & 3);
         int at = first;
 #pragma unroll
         for (int s = 1; s < 4; s <<= 1) at = min(at, __shfl_xor_sync(0xffffffffu, at, s));
         bool minus = false;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if ((i < 4 ? 0 : 16) + o.u * 4 + (i & 3) == at) minus = x[i] < 0.f;
+            if ((i < 4 ? 0 : 16) + u * 4 + (i & 3) == at) minus = x[i] < 0.f;
         const uint32_t quad = 0xfu << (threadIdx.x & 28);
         const bool any_minus = (__ballot_sync(0xffffffffu, minus) & quad) != 0;
         if (both) m = any_minus ? low : top;
@@ -155,61 +153,59 @@ __device__ __forceinline__ void quantise(const float (&x)[8], bool live, const P
         const float s = __half2float(s16);
         if (s != 0.f) word = word_of(x, s);
     }
-    *reinterpret_cast<uint32_t*>(o.code) = word;
-    if (o.u == 0) *reinterpret_cast<__half*>(o.scale) = s16;
+    *reinterpret_cast<uint32_t*>(code) = word;
+    if (u == 0) *reinterpret_cast<__half*>(scale) = s16;
 }
 
-// Bound by HBM and, close behind, by the quantisation's instructions: 4095 rows of 2 x 16 x 256 are 134 MB
-// read and 19 MB written, 36 us or 4.3 TB/s, 63 % of the measured copy rate.  (Two octets of tokens a
-// thread put more loads in flight and take 38 us.)
+// Bound by HBM: 4095 rows of 2 x 16 x 256 are 134 MB read and 19 MB written, 34.5 us or 4.4 TB/s, 66 % of the
+// measured copy rate.  K and V of a block in one thread share the slot and the address (a thread for each
+// took 36 us, one with two octets of tokens 38).
 __global__ void __launch_bounds__(kRowThreads) kv4_append_kernel(const RowsParams P) {
     pdl_wait_trigger();
-    Place o;
-    const bool live = place_of(P, 1, 0, o);
-    float x[8];
-    if (live) {
-        const float* src = (o.which ? P.v + o.t * P.ldv : P.k + o.t * P.ldk) + o.head * P.d + o.blk * 32 + o.u * 4;
-        const bool vec = o.which ? P.vec_v : P.vec_k;
-        load4(src, vec, reinterpret_cast<float(&)[4]>(x[0]));
-        load4(src + 16, vec, reinterpret_cast<float(&)[4]>(x[4]));
-    } else {
+    Place o{};
+    const bool live = place_of(P, o);
+    float x[2][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = 0.f;
+    for (int w = 0; w < 2; ++w) {
+        if (live) {
+            const float* src = (w ? P.v + o.t * P.ldv : P.k + o.t * P.ldk) + o.col;
+            const bool vec = w ? P.vec_v : P.vec_k;
+            load4(src, vec, reinterpret_cast<float(&)[4]>(x[w][0]));
+            load4(src + 16, vec, reinterpret_cast<float(&)[4]>(x[w][4]));
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[w][i] = 0.f;
+        }
     }
-    quantise(x, live, o);
+#pragma unroll
+    for (int w = 0; w < 2; ++w)
+        quantise(x[w], live, o.u, o.code + codes_off(P.d, w), o.scale + w * P.d);
 }
 
-// The same rows back: 19 MB read, 134 MB written in 27 us, 5.7 TB/s, 85 % of the measured copy rate with two
-// octets of tokens a thread (30 us with one).
-constexpr int kTurns = 2;
+// The same rows back: 19 MB read, 134 MB written in 25.7 us, 6.0 TB/s, 88 % of the measured copy rate.
 __global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const RowsParams P) {
     pdl_wait_trigger();
-    Place o[kTurns];
-    bool live[kTurns];
-    uint32_t w[kTurns];
-    float s[kTurns];
+    Place o;
+    if (!place_of(P, o)) return;
+    uint32_t code[2];
+    float s[2];
 #pragma unroll
-    for (int k = 0; k < kTurns; ++k) {
-        live[k] = place_of(P, kTurns, k, o[k]) && (o[k].which ? P.vo : P.ko);
-        w[k] = 0, s[k] = 0.f;
+    for (int w = 0; w < 2; ++w) {
+        code[w] = *reinterpret_cast<const uint32_t*>(o.code + codes_off(P.d, w));
+        s[w] = __half2float(*reinterpret_cast<const __half*>(o.scale + w * P.d));
     }
 #pragma unroll
-    for (int k = 0; k < kTurns; ++k)
-        if (live[k]) {
-            w[k] = *reinterpret_cast<const uint32_t*>(o[k].code);
-            s[k] = __half2float(*reinterpret_cast<const __half*>(o[k].scale));
-        }
-#pragma unroll
-    for (int k = 0; k < kTurns; ++k) {
-        if (!live[k]) continue;
-        float* dst = (o[k].which ? P.vo + o[k].t * P.ldv : P.ko + o[k].t * P.ldk) + o[k].head * P.d + o[k].blk * 32 + o[k].u * 4;
+    for (int w = 0; w < 2; ++w) {
+        float* dst = w ? P.vo : P.ko;
+        if (!dst) continue;
+        dst += o.t * (w ? P.ldv : P.ldk) + o.col;
         float lo[4], hi[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            lo[i] = static_cast<float>(static_cast<int>((w[k] >> (8 * i)) & 15) - 8) * s[k];
-            hi[i] = static_cast<float>(static_cast<int>((w[k] >> (8 * i + 4)) & 15) - 8) * s[k];
+            lo[i] = static_cast<float>(static_cast<int>((code[w] >> (8 * i)) & 15) - 8) * s[w];
+            hi[i] = static_cast<float>(static_cast<int>((code[w] >> (8 * i + 4)) & 15) - 8) * s[w];
         }
-        if (o[k].which ? P.vec_v : P.vec_k) {
+        if (w ? P.vec_v : P.vec_k) {
             *reinterpret_cast<float4*>(dst) = make_float4(lo[0], lo[1], lo[2], lo[3]);
             *reinterpret_cast<float4*>(dst + 16) = make_float4(hi[0], hi[1], hi[2], hi[3]);
         } else {
@@ -221,10 +217,10 @@ __global__ void __launch_bounds__(kRowThreads) kv4_gather_kernel(const RowsParam
 
 bool vec_ok(const float* p, int64_t ld) { return !(reinterpret_cast<uintptr_t>(p) & 15) && ld % 4 == 0; }
 
-gem_status rows_launch(const void* kernel, int turns, RowsParams& P, cudaStream_t stream) {
+gem_status rows_launch(const void* kernel, RowsParams& P, cudaStream_t stream) {
     const gem_status st = flag_word(&P.status);
     if (st != GEM_OK) return st;
-    const int64_t x = (P.T + 8 * turns - 1) / (8 * turns), y = (2ll * (P.n_kv << P.lnb) + kRowThreads / 32 - 1) / (kRowThreads / 32);
+    const int64_t x = (P.T + 7) / 8, y = ((static_cast<int64_t>(P.n_kv) << P.lnb) + kRowThreads / 32 - 1) / (kRowThreads / 32);
     if (x > INT32_MAX || y > 65535) return GEM_ERR_UNSUPPORTED_SHAPE;
     void* args[] = {&P};
     return launch_pdl(kernel, dim3(static_cast<unsigned>(x), static_cast<unsigned>(y)), dim3(kRowThreads), 0, stream, args);
@@ -258,7 +254,7 @@ gem_status gem_kv4_append(const float* k, int64_t ldk, const float* v, int64_t l
     P.n_kv = n_kv, P.d = d, P.lnb = log2_of(d / 32), P.lpage = log2_of(page);
     P.vec_k = vec_ok(k, ldk), P.vec_v = vec_ok(v, ldv);
     P.status = status;
-    return rows_launch(reinterpret_cast<const void*>(kv4_append_kernel), 1, P, static_cast<cudaStream_t>(stream));
+    return rows_launch(reinterpret_cast<const void*>(kv4_append_kernel), P, static_cast<cudaStream_t>(stream));
 }
 
 gem_status gem_kv4_gather(const void* pool, int64_t n_pages, int page, int n_kv, int d, const int32_t* slot,
@@ -278,7 +274,7 @@ gem_status gem_kv4_gather(const void* pool, int64_t n_pages, int page, int n_kv,
     P.n_kv = n_kv, P.d = d, P.lnb = log2_of(d / 32), P.lpage = log2_of(page);
     P.vec_k = vec_ok(k, ldk), P.vec_v = vec_ok(v, ldv);
     P.status = status;
-    return rows_launch(reinterpret_cast<const void*>(kv4_gather_kernel), kTurns, P, static_cast<cudaStream_t>(stream));
+    return rows_launch(reinterpret_cast<const void*>(kv4_gather_kernel), P, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"
