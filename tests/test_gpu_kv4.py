@@ -834,3 +834,23 @@ def test_attention_whose_value_scales_grow_in_part_of_the_dims(env, case):
     got = got.reshape(want.shape)
     for half in (slice(0, d // 2), slice(d // 2, d)):
         assert_close(got[..., half], want[..., half], "dims %s" % half, max_abs=2e-4 * np.abs(want[..., half]).max(), rel_l2=1e-5)
+
+
+def test_attention_sums_do_not_drift_along_a_long_sequence(env):
+    """Every warp sums some 80 steps of 32 positions here.  Scores and probabilities carry some 2^-22 each and
+    the sums are rounded to nearest, 2^-24 a step, so their errors add up as a random walk: the result is
+    within 2e-6.  (Kept in the tensor cores, which cut off toward zero, they would drift by 2^-25 a
+    product, 5e-6 after 320.)"""
+    g, t = env
+    n_q, n_kv, d, page, L, B, new = 16, 8, 128, 128, 12000, 8, 26
+    r = np.random.RandomState(80)
+    pool, table, _, _ = _attn_case(r, t, [L], [1], n_q, n_kv, d, page)
+    cu = (np.arange(B + 1) * new).astype(np.int32)
+    q = (2 * r.randn(B * new, n_q * d)).astype(np.float32)
+    got = _attn_run(g, t, pool, np.repeat(table, B, 0), cu, q, [L] * B, n_q, n_kv, d, page, 0, d ** -0.5)
+    x = _unpack(pool, d)
+    slots = table[0, np.arange(L) // page] * page + np.arange(L) % page
+    K, V = x[0, slots], x[1, slots]
+    rows = r.permutation(B * new)[:24]
+    want = np.stack([kv4.attention(q[i].reshape(1, n_q, d), K, V, L - new + 1 + i % new, 0, d ** -0.5)[0] for i in rows])
+    assert_close(got[rows].reshape(want.shape), want, "attention", max_abs=1e-5 * np.abs(want).max(), rel_l2=2e-6)
