@@ -224,15 +224,15 @@ struct Cfg {
 
 // ---- the kernel ------------------------------------------------------------------------------------
 //
-// What bounds it: the warp instructions, about 730 a step of 32 positions at d 128 and four rows, of
+// What bounds it: the warp instructions, about 770 a step of 32 positions at d 128 and four rows, of
 // which unpacking the codes is 290 and splitting p times V's scale 100, and their latency, with three
-// warps a scheduler issuing in 57 % of the cycles.  8 requests of up to 32,768 positions (32 / 8 heads,
-// d 128, 257 MB): 66 us, 3.9 TB/s, 58 % of the measured copy rate.  Short batches are latency: 1 x 4097 positions take 9 us.
+// warps a scheduler issuing in 58 % of the cycles.  8 requests of up to 32,768 positions (32 / 8 heads,
+// d 128, 257 MB): 68 us, 3.8 TB/s, 56 % of the measured copy rate.  Short batches are latency: 1 x 4097 positions take 9 us.
 // One CTA of 12 warps an SM has 168 registers a thread for the sums, q and the operands under way; two of
-// 8 have 128, spill, and take 71 us there, 15.1 against 12.9 for 8 requests of up to 2049 positions; 10
-// warps take 76 and 12.1.
+// 8 have 128, spill, and took 71 us there against 66.7 at that point, 15.1 against 12.9 for 8 requests of up
+// to 2049 positions; 10 warps took 76 and 12.1.
 // Steps of 32 positions: with 16 the per-step work (waits, maxima, requests) weighs twice (85 us against
-// 71), and longer ones do not fit shared memory twice for every warp.
+// 71 with two CTAs), and longer ones do not fit shared memory twice for every warp.
 
 template <int D, int NT, bool PACK, int DW, int WARPS, int CTAS>
 __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnParams P) {
@@ -999,9 +999,9 @@ Variant variant() {
 
 // Query rows a unit has: one token's heads, or as many tokens as the batch brings on average while
 // the sums of a warp stay in registers.  (Any batch is right with any of them: a request's tokens are cut
-// into units.)  Measured: 8 rows of d 128 take 8 warps of 255 registers (4 x 32 new tokens: 63 us with 16
-// rows; 12 warps spill, 104; 32 rows in warps of 64 dims, 77); so do 8 rows at d 256 and 512, with 256
-// dims a warp (1 x 32,769, d 512: 36 us; 128 dims a warp: 37 with 12 warps, 52 with 16).  Up to four rows
+// into units.)  Measured: 8 rows of d 128 take 8 warps of 255 registers (4 x 32 new tokens: 62 us with 16
+// rows when these were compared, 65 now; 12 warps spill, 104; 32 rows in warps of 64 dims, 77); so do 8 rows at d 256 and 512, with 256
+// dims a warp (1 x 32,769, d 512: 36 us then, 38 now; 128 dims a warp: 37 with 12 warps, 52 with 16).  Up to four rows
 // take 128 dims a warp.
 Variant pick(int64_t T, int B, int G, int d) {
     const int64_t tokens = std::max<int64_t>(1, (T + B - 1) / std::max(B, 1));
