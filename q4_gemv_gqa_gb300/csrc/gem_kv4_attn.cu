@@ -192,6 +192,15 @@ __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
 __device__ __forceinline__ float lead(float x, uint32_t flip) {
     return __uint_as_float((__float_as_uint(x) & 0xffffe000u) ^ flip);
 }
+// The power of two that brings x >= 0 into [2^14, 2^15), and its inverse.  (Below 2^-112 the power stays; infinity
+// stays infinity.)
+struct Scale2 {
+    float up, down;
+};
+__device__ __forceinline__ Scale2 scale_to_2_14(float x) {
+    const uint32_t e = max(__float_as_uint(x) & 0x7f800000u, 15u << 23);
+    return {__uint_as_float((268u << 23) - e), __uint_as_float(e - (14u << 23))};
+}
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
 // A partial result in memory: rows of D sums, then (maximum, sum) of each row.
@@ -393,7 +402,6 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
     float acc[NB][2][NT][4];              // output sums
     float cmul[NT][2], m[NT][2], l[NT][2];
     int prow[NT][2];                      // positions of this lane's two rows of each column tile
-    int E = 0;
 
     // rows of the S and output fragments: columns 2t, 2t + 1
     auto col_row = [&](int nt, int e) { return PACK ? (2 * t + e) & 3 : nt * 8 + 2 * t + e; };
@@ -463,10 +471,9 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) acc[b][0][nt][k] = acc[b][1][nt][k] = 0.f;
-        E = 64;   // above any step's
     };
 
-    // The unit's sums so far, in true units: put_row(row, maximum, sum of p) for every row, and
+    // The unit's sums so far: put_row(row, maximum, sum of p) for every row, and
     // put_pair(row, dim, values of dim and dim + 1, sum of p) for its dims.
     auto finish = [&](auto&& put_pair, auto&& put_row) {
 #pragma unroll
@@ -477,12 +484,9 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
                 for (int o = 4; o < 32; o <<= 1) l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], o);
                 if (PACK) l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], 2);
             }
-            const float down = pow2(-E);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                l[nt][k] *= down;
+            for (int k = 0; k < 2; ++k)
                 if (g == 0 && (!PACK || t < 2)) put_row(col_row(nt, k), m[nt][k], l[nt][k]);
-            }
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
 #pragma unroll
@@ -495,8 +499,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
                             a0 += __shfl_xor_sync(0xffffffffu, a0, 2);
                             a1 += __shfl_xor_sync(0xffffffffu, a1, 2);
                         }
-                        v[j] = a0 * down;
-                        v[2 + j] = a1 * down;
+                        v[j] = a0;
+                        v[2 + j] = a1;
                     }
                     if (!PACK || t < 2) {
                         const int dim = member * C::kDims + b * 32 + 2 * g;
@@ -516,7 +520,6 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
         const uint32_t gone = (lost >> (stage * kStepTiles)) & kMask;
         // scales in fp32: K's as (row g, row g, row g + 8, row g + 8), V's as (2t, 2t + 1, 2t + 8, 2t + 9); a lane
         // takes positions 2r, 2r + 1, 2r + 8 and 2r + 9 of a block of both
-        __half2 big2 = __float2half2_rn(0.f);
         const __half2 zero2 = __float2half2_rn(0.f);
 #pragma unroll
         for (int it = 0; it < kStepTiles * NB * 4; it += 32) {
@@ -537,17 +540,10 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
                     v0 = __halves2half2(in(pos) ? __low2half(v0) : zero, in(pos + 1) ? __high2half(v0) : zero);
                     v1 = __halves2half2(in(pos + 8) ? __low2half(v1) : zero, in(pos + 9) ? __high2half(v1) : zero);
                 }
-                // infinities become NaN, which the maximum passes over
-                big2 = __hmax2(big2, __hmax2(__habs2(__hfma2(v0, zero2, v0)), __habs2(__hfma2(v1, zero2, v1))));
                 const float2 f0 = __half22float2(v0), f1 = __half22float2(v1);
                 to[8 + r] = make_float4(f0.x, f0.y, f1.x, f1.y);
             }
         }
-        // p 2^E sV stays below 2^15, p up to 2^kSlack (binary16 numbers that are not negative order as their
-        // bits do)
-        const uint32_t big = __reduce_max_sync(
-            0xffffffffu, static_cast<uint32_t>(__half_as_ushort(__hmax(__low2half(big2), __high2half(big2)))));
-        const int e_step = 29 - kSlack - static_cast<int>(big >> 10);
         __syncwarp();
 
         // scores
@@ -649,28 +645,23 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
 #pragma unroll
                 for (int k = 0; k < NV; ++k) up |= x[s][nt][k] > m[nt][k & 1] + kSlack;
             }
-        // Scores well past the maxima so far, or larger scales: new maxima, and the sums are rescaled.  (Any
-        // maximum would make it half of the steps; p may pass 1 by kSlack powers of two instead.)
-        // The scales are this warp's dims' alone, the scores the same for all warps of a head: a maximum moves
-        // for the scores only, so that it stays the same too, since parts are joined under one of them.
-        const bool rise = __any_sync(0xffffffffu, up);
-        if (rise || e_step < E) {
-            const int e_new = e_step < E ? e_step - 1 : E;
+        // Scores well past the maxima so far: new maxima, and the sums are rescaled.  (Any maximum would make
+        // it half of the steps; p may pass 1 by kSlack powers of two instead.)  The scores are the same for all
+        // warps of a head, so that the maxima are too: parts are joined under one of them.
+        if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float corr[2];
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     float mx = m[nt][k];
-                    if (rise) {
 #pragma unroll
-                        for (int s = 0; s < kStepTiles; ++s)
+                    for (int s = 0; s < kStepTiles; ++s)
 #pragma unroll
-                            for (int v = k; v < NV; v += 2) mx = fmaxf(mx, x[s][nt][v]);
+                        for (int v = k; v < NV; v += 2) mx = fmaxf(mx, x[s][nt][v]);
 #pragma unroll
-                        for (int o = PACK ? 2 : 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-                    }
-                    corr[k] = (m[nt][k] == mx ? 1.f : ex2(m[nt][k] - mx)) * pow2(e_new - E);
+                    for (int o = PACK ? 2 : 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                    corr[k] = m[nt][k] == mx ? 1.f : ex2(m[nt][k] - mx);
                     m[nt][k] = mx;
                     l[nt][k] *= corr[k];
                 }
@@ -683,11 +674,10 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
                     }
                 }
             }
-            E = e_new;
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const float mb[2] = {m[nt][0] == -INFINITY ? 0.f : m[nt][0] - E, m[nt][1] == -INFINITY ? 0.f : m[nt][1] - E};
+            const float mb[2] = {m[nt][0] == -INFINITY ? 0.f : m[nt][0], m[nt][1] == -INFINITY ? 0.f : m[nt][1]};
 #pragma unroll
             for (int s = 0; s < kStepTiles; ++s)
 #pragma unroll
@@ -720,17 +710,19 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
             }
         // A block's products of the step go into fresh accumulators and from there into the sums: the tensor
         // cores cut what they accumulate off toward zero, and a sum kept there through a long sequence drifts
-        // (after 450 products it was 6.5e-6 off).
+        // (after 450 products it was 6.5e-6 off).  So each row's block has a power of two of its own in each
+        // step, that of its largest product p sV, under which hi and lo fill binary16 whatever the scales and the
+        // probabilities of other blocks, rows and steps are.
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             float d[2][NT][4];
+            float2 v[kStepTiles][NT][2], back[NT];
 #pragma unroll
-            for (int s = 0; s < kStepTiles; ++s) {
-                const uint32_t wa = vw[s][b / 2][2 * (b & 1)], wb = vw[s][b / 2][2 * (b & 1) + 1];
-                const float4 vs = reinterpret_cast<const float4*>(scales + (s * NB + b) * 48 + 32)[t];
-                const Codes ca = codes_of(wa), cb = codes_of(wb);
+            for (int nt = 0; nt < NT; ++nt) {
+                float top = 0.f;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
+                for (int s = 0; s < kStepTiles; ++s) {
+                    const float4 vs = reinterpret_cast<const float4*>(scales + (s * NB + b) * 48 + 32)[t];
                     const float2 p0 = pr[s][nt][0], p1 = pr[s][nt][1];
                     float2 v0 = fmul2(p0, make_float2(vs.x, vs.y));
                     float2 v1 = fmul2(p1, make_float2(vs.z, vs.w));
@@ -738,6 +730,26 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
                         v0.x = p0.x == 0.f ? 0.f : v0.x, v0.y = p0.y == 0.f ? 0.f : v0.y;
                         v1.x = p1.x == 0.f ? 0.f : v1.x, v1.y = p1.y == 0.f ? 0.f : v1.y;
                     }
+                    top = fmaxf(top, fmaxf(fmaxf(fabsf(v0.x), fabsf(v0.y)), fmaxf(fabsf(v1.x), fabsf(v1.y))));
+                    v[s][nt][0] = v0, v[s][nt][1] = v1;
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const Scale2 f = scale_to_2_14(top);
+#pragma unroll
+                for (int s = 0; s < kStepTiles; ++s)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) v[s][nt][k] = fmul2(v[s][nt][k], make_float2(f.up, f.up));
+                back[nt].x = __shfl_sync(0xffffffffu, f.down, 8 * t);
+                back[nt].y = __shfl_sync(0xffffffffu, f.down, 8 * t + 4);
+            }
+#pragma unroll
+            for (int s = 0; s < kStepTiles; ++s) {
+                const uint32_t wa = vw[s][b / 2][2 * (b & 1)], wb = vw[s][b / 2][2 * (b & 1) + 1];
+                const Codes ca = codes_of(wa), cb = codes_of(wb);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const float2 v0 = v[s][nt][0], v1 = v[s][nt][1];
                     // hi: the leading 11 bits; lo: what they leave.  PACK: this lane's column is one of the two
                     const float2 r0 = ffma2(v0, keep, make_float2(lead(v0.x, flip), lead(v0.y, flip)));
                     const float2 r1 = ffma2(v1, keep, make_float2(lead(v1.x, flip), lead(v1.y, flip)));
@@ -761,8 +773,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     float2* to = reinterpret_cast<float2*>(acc[b][j][nt]);
-                    to[0] = fadd2(to[0], make_float2(d[j][nt][0], d[j][nt][1]));
-                    to[1] = fadd2(to[1], make_float2(d[j][nt][2], d[j][nt][3]));
+                    to[0] = ffma2(make_float2(d[j][nt][0], d[j][nt][1]), back[nt], to[0]);
+                    to[1] = ffma2(make_float2(d[j][nt][2], d[j][nt][3]), back[nt], to[1]);
                 }
         }
         __syncwarp();
