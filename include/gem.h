@@ -514,10 +514,11 @@ GEM_API gem_status gem_kv4_gather(const void *pool, int64_t n_pages, int page, i
  *   workspace  gem_kv4_attn_workspace(T, B, n_q, n_kv, d) bytes, 256-byte aligned, no
  *          initialisation; calls that can run at the same time need one each.
  *   Accumulation is fp32: q and the probabilities times V's scales enter the tensor cores as binary16
- *   hi + lo pairs (about 22 bits), the codes exactly.  Each row has a power of two of its own for every
- *   block of 32 dims and step of 32 positions, so that neither V's scales in other blocks nor those at
- *   positions of little weight take bits from it.  Deterministic: the split of the
- *   range depends on the lengths, the shape and the device, and partial results are merged in order.
+ *   hi + lo pairs (about 22 bits), the codes exactly.  Each row has powers of two of its own for every
+ *   block of 32 dims, of q and, in each step of 32 positions, of those products, so that neither other
+ *   blocks nor positions of little weight take bits from it, and q may have any finite size at which
+ *   q.K is finite.  Deterministic: the split of the range depends on the lengths, the shape and the
+ *   device, and partial results are merged in order.
  */
 GEM_API size_t gem_kv4_attn_workspace(int64_t T, int B, int n_q, int n_kv, int d);
 GEM_API gem_status gem_kv4_attn(const float *q, int64_t ldq, int64_t T, const int32_t *cu_tokens,

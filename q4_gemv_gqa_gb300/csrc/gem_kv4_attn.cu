@@ -15,7 +15,9 @@
 // exponent fields before they are added, and a relative error of 1.2e-5 was left.)  q, and p times V's
 // scale, are fp32 and enter as binary16 hi + lo pairs (about 22 bits) under powers of two that keep
 // them in binary16's range; up to four query rows put both halves into the eight columns of one
-// instruction, more rows take two.
+// instruction, more rows take two.  Each row has a power for every block of 32 dims, of q once a unit, of p sV in
+// each step: one for all blocks loses the bits of the small ones (blocks 2^24 apart were 1e-4 off for q, 2e-2
+// for V).
 // The wide tcgen05 path wants both operands in binary16 or fp8 tiles in shared memory: here one operand
 // is 4-bit codes and would first be written out four times as large, for eight columns of output, so
 // the unpacking, not the multiply rate, would bound it just the same.
@@ -42,7 +44,9 @@ constexpr int kStepTiles = 2;
 constexpr int kStepTokens = kStepTiles * kTileTokens;
 constexpr int kStages = 2;
 constexpr int kSlack = 6;                   // log2 of how far a score may pass the maximum in use
-constexpr int kProbRow = kStepTokens + 8;   // floats; 8 modulo 32 keeps the rows in banks of their own
+// A row of probabilities in shared memory, in floats.  8 modulo 32 keeps the rows in banks of their own; the 8 behind
+// the probabilities hold what takes q's powers of two back, for a block of dims and eight query rows.
+constexpr int kProbRow = kStepTokens + 8;
 
 struct AttnParams {
     const float* q;
@@ -201,7 +205,6 @@ __device__ __forceinline__ Scale2 scale_to_2_14(float x) {
     const uint32_t e = max(__float_as_uint(x) & 0x7f800000u, 15u << 23);
     return {__uint_as_float((268u << 23) - e), __uint_as_float(e - (14u << 23))};
 }
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
 // A partial result in memory: rows of D sums, then (maximum, sum) of each row.
 template <int D, int ROWS>
@@ -397,10 +400,12 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
         if (PAIR > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / PAIR), "n"(32 * PAIR) : "memory");
     };
 
+    const float to_log2 = P.scale * 1.4426950408889634f;
+
     // state of the unit at hand
     uint32_t bq[NB][2][NT][NH][2];        // q: [block][low or high byte pair][column tile][hi, lo][register]
     float acc[NB][2][NT][4];              // output sums
-    float cmul[NT][2], m[NT][2], l[NT][2];
+    float m[NT][2], l[NT][2];
     int prow[NT][2];                      // positions of this lane's two rows of each column tile
 
     // rows of the S and output fragments: columns 2t, 2t + 1
@@ -424,41 +429,33 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
         }
     };
     auto begin_unit = [&](const Unit& un) {
-        const float c = P.scale * 1.4426950408889634f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            float x[NB][8], top = 0.f;
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                const float4 lo = qv[nt][b][0], hi = qv[nt][b][1];
-                x[b][0] = lo.x, x[b][1] = lo.y, x[b][2] = lo.z, x[b][3] = lo.w;
-                x[b][4] = hi.x, x[b][5] = hi.y, x[b][6] = hi.z, x[b][7] = hi.w;
+                const float4 lo4 = qv[nt][b][0], hi4 = qv[nt][b][1];
+                const float x[8] = {lo4.x, lo4.y, lo4.z, lo4.w, hi4.x, hi4.y, hi4.z, hi4.w};
+                float top = 0.f;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[b][k]));
-            }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // the row times 2^e has its largest value in [2^13, 2^14)
-            const int e = max(-96, min(120, 13 - (static_cast<int>(__float_as_uint(top) >> 23) - 127)));
-            const float f = pow2(e);
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
+                for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[k]));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const Scale2 f = scale_to_2_14(top);   // a power of two for each row's block
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const float v0 = x[b][4 * k + j] * f, v1 = x[b][4 * k + j + 2] * f;
+                        const float v0 = x[4 * k + j] * f.up, v1 = x[4 * k + j + 2] * f.up;
                         const uint32_t hi = pack_rn(v0, v1);
                         const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
                         const uint32_t lo = pack_rn(v0 - h.x, v1 - h.y);
                         bq[b][j][nt][0][k] = !PACK || g < 4 ? hi : lo;
                         if (!PACK) bq[b][j][nt][NH - 1][k] = lo;
                     }
+                if (t == 0) probs[(b * NT + nt) * kProbRow + kStepTokens + g] = f.down;
             }
-            const float back = c * pow2(-e);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                cmul[nt][k] = __shfl_sync(0xffffffffu, back, ((PACK ? (2 * t + k) & 3 : 2 * t + k)) * 4);
                 const int tk = (col_row(nt, k) * P.inv_g) >> 16;
                 prow[nt][k] = un.p0 + min(tk, un.tokens - 1);
                 m[nt][k] = -INFINITY;
@@ -579,8 +576,9 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
                             mma_16816(d, ca.v[2], cb.v[2], ca.v[3], cb.v[3], bq[b][1][nt][NH - 1][0], bq[b][1][nt][NH - 1][1]);
                         }
                         float2* to = reinterpret_cast<float2*>(sc[s][nt]);
-                        to[0] = ffma2(make_float2(ks.x, ks.y), make_float2(d[0], d[1]), to[0]);
-                        to[1] = ffma2(make_float2(ks.z, ks.w), make_float2(d[2], d[3]), to[1]);
+                        const float2 down = *reinterpret_cast<const float2*>(probs + (b * NT + nt) * kProbRow + kStepTokens + 2 * t);
+                        to[0] = ffma2(fmul2(make_float2(ks.x, ks.y), make_float2(d[0], d[1])), down, to[0]);
+                        to[1] = ffma2(fmul2(make_float2(ks.z, ks.w), make_float2(d[2], d[3])), down, to[1]);
                     }
                 }
             }
@@ -595,11 +593,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
 #pragma unroll
             for (int s = 0; s < kStepTiles; ++s)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) sc[s][nt][k] *= cmul[nt][k & 1];   // the members' powers of two differ
+                for (int nt = 0; nt < NT; ++nt)
                     buffer(member)[(s * NT + nt) * 32 + lane] = make_float4(sc[s][nt][0], sc[s][nt][1], sc[s][nt][2], sc[s][nt][3]);
-                }
             member_sync();
 #pragma unroll
             for (int s = 0; s < kStepTiles; ++s)
@@ -627,11 +622,11 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
                 if (PACK) {
                     const float g0 = t < 2 ? sc[s][nt][2] : sc[s][nt][0], g1 = t < 2 ? sc[s][nt][3] : sc[s][nt][1];
                     const float k0 = t < 2 ? sc[s][nt][0] : sc[s][nt][2], k1 = t < 2 ? sc[s][nt][1] : sc[s][nt][3];
-                    x[s][nt][0] = (k0 + __shfl_xor_sync(0xffffffffu, g0, 2)) * (PAIR > 1 ? 1.f : cmul[nt][0]);
-                    x[s][nt][1] = (k1 + __shfl_xor_sync(0xffffffffu, g1, 2)) * (PAIR > 1 ? 1.f : cmul[nt][1]);
+                    x[s][nt][0] = (k0 + __shfl_xor_sync(0xffffffffu, g0, 2)) * to_log2;
+                    x[s][nt][1] = (k1 + __shfl_xor_sync(0xffffffffu, g1, 2)) * to_log2;
                 } else {
 #pragma unroll
-                    for (int k = 0; k < NV; ++k) x[s][nt][k] = sc[s][nt][k] * (PAIR > 1 ? 1.f : cmul[nt][k & 1]);
+                    for (int k = 0; k < NV; ++k) x[s][nt][k] = sc[s][nt][k] * to_log2;
                 }
                 if (!clean) {
 #pragma unroll
@@ -860,6 +855,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
                });
     }
     static_assert(kStages >= 2, "the members' buffers alternate");
+    static_assert(NB * NT <= ROWS, "a row of probabilities for each block and column tile");
     static_assert(ROWS * (C::kDims + 2) <= kLocal, "a partial result fits the ring");
     constexpr int kW = C::kWorkers;
     auto state_of = [&](int w) {   // a worker's (maximum, sum) rows

@@ -135,3 +135,24 @@ def test_rows_of_a_group_that_look_at_positions_of_different_sizes(env, case):
                 pool.write(slot, h, 0, codes, scales)
             vs[j][:] = (vs[j].astype(np.float64) * (2.0 ** 11 if j % 2 else 2.0 ** -9)).astype(np.float16)
     _go(env, case, pool, table, cu, q, scale)
+
+
+@pytest.mark.parametrize("case", SHAPES, ids=IDS)
+def test_blocks_of_q_and_k_that_differ_by_powers_of_two(env, case):
+    """q of each block of dims at a size of its own, 2^-12 to 2^12, K's scales at the inverse: every block has
+    the same part in the scores.  (Dims of V are left alone.)"""
+    r, pool, table, cu, q, heads, _, scale = _prepared(case, 4)
+    size = 2.0 ** np.linspace(-12, 12, pool.nb)[r.permutation(pool.nb)]
+    for b, L in enumerate(case[0]):
+        for s in _scales(pool, table, b, L, 0):
+            s[:] = (s.astype(np.float64) / size).astype(np.float16)
+    q.reshape(len(q), heads[0], pool.nb, 32)[:] *= size[:, None].astype(np.float32)
+    _go(env, case, pool, table, cu, q, scale)
+
+
+@pytest.mark.parametrize("power", [-100, 112, 118])
+@pytest.mark.parametrize("case", SHAPES, ids=IDS)
+def test_q_of_any_size_with_a_scale_to_match(env, case, power):
+    r, pool, table, cu, q, _, _, scale = _prepared(case, 5)
+    q *= np.float32(2.0 ** power)
+    _go(env, case, pool, table, cu, q, scale * 2.0 ** -power)
