@@ -614,6 +614,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
         // p: in log2 units; PACK: the two halves' sums, lanes t < 2 keep row g, the others row g + 8
         constexpr int NV = PACK ? 2 : 4;
         float x[kStepTiles][NT][NV];
+        uint32_t masked = 0;
         bool up = false;
 #pragma unroll
         for (int s = 0; s < kStepTiles; ++s)
@@ -634,7 +635,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
                         const int pos = pos0 + s * kTileTokens + g + (PACK ? (t >> 1) : (k >> 1)) * 8;
                         const int p = prow[nt][k & 1];
                         const bool in = pos <= p && (P.window == 0 || pos > p - P.window) && !(gone >> s & 1);
-                        if (!in) x[s][nt][k] = -INFINITY;
+                        if (!in) x[s][nt][k] = -INFINITY, masked |= 1u << ((s * NT + nt) * NV + k);
                     }
                 }
 #pragma unroll
@@ -677,7 +678,8 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
             for (int s = 0; s < kStepTiles; ++s)
 #pragma unroll
                 for (int k = 0; k < NV; ++k) {
-                    const float p = ex2(x[s][nt][k] - mb[k & 1]);
+                    float p = ex2(x[s][nt][k] - mb[k & 1]);
+                    if (!clean && (masked >> ((s * NT + nt) * NV + k) & 1)) p = -0.f;   // unlike one that underflowed
                     l[nt][k & 1] += p;
                     probs[col_row(nt, k & 1) * kProbRow + s * kTileTokens + g + (PACK ? (t >> 1) : (k >> 1)) * 8] = p;
                 }
@@ -722,8 +724,9 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
                     float2 v0 = fmul2(p0, make_float2(vs.x, vs.y));
                     float2 v1 = fmul2(p1, make_float2(vs.z, vs.w));
                     if (!clean) {   // a row leaves out a position whatever V's scale is there
-                        v0.x = p0.x == 0.f ? 0.f : v0.x, v0.y = p0.y == 0.f ? 0.f : v0.y;
-                        v1.x = p1.x == 0.f ? 0.f : v1.x, v1.y = p1.y == 0.f ? 0.f : v1.y;
+                        auto out = [](float p) { return __float_as_uint(p) == 0x80000000u; };
+                        v0.x = out(p0.x) ? 0.f : v0.x, v0.y = out(p0.y) ? 0.f : v0.y;
+                        v1.x = out(p1.x) ? 0.f : v1.x, v1.y = out(p1.y) ? 0.f : v1.y;
                     }
                     top = fmaxf(top, fmaxf(fmaxf(fabsf(v0.x), fabsf(v0.y)), fmaxf(fabsf(v1.x), fabsf(v1.y))));
                     v[s][nt][0] = v0, v[s][nt][1] = v1;

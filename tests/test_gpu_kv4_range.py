@@ -156,3 +156,29 @@ def test_q_of_any_size_with_a_scale_to_match(env, case, power):
     r, pool, table, cu, q, _, _, scale = _prepared(case, 5)
     q *= np.float32(2.0 ** power)
     _go(env, case, pool, table, cu, q, scale * 2.0 ** -power)
+
+
+@pytest.mark.parametrize("bits", [0x7e00, 0x7c00, 0xfc00])
+@pytest.mark.parametrize("case", SHAPES, ids=IDS)
+def test_value_scales_that_are_not_finite_show_at_positions_of_no_weight(env, case, bits):
+    """A scale of V that is not finite, at a position whose probability underflows to 0 in every row: the rows
+    that attend it have NaN in its block of dims, in the steps with masked positions as in the others."""
+    g, t = env
+    kv_len, fresh, n_q, n_kv, d, page, window = case
+    r, pool, table, cu, q, _, _, scale = _prepared(case, 6)
+    q.reshape(len(q), n_q, d)[..., 0] = 16.0
+    want = np.zeros((len(q), n_q, d), bool)
+    for b, L in enumerate(kv_len):
+        ks, vs = (_scales(pool, table, b, L, w) for w in (0, 1))
+        last = L - fresh[b] - 1                       # every row attends it, and it shares a step with later ones
+        first = max(0, L - window) if window else 0   # a step that may be whole
+        for j, blk in ((last, 0), (first + 40, 1)):
+            slot = table[b, j // page] * page + j % page
+            codes, scales = r.randint(0, 16, (pool.nb, 32)).astype(np.uint8), ks[j][n_kv - 1].copy()
+            codes[0], codes[0, 0] = 8, 0
+            scales[0] = np.float16(100.0 * np.sqrt(d / 64))             # a score of 16 * -8 * 100 / 8
+            pool.write(slot, n_kv - 1, 0, codes, scales)
+            vs[j][n_kv - 1, blk] = np.array([bits], np.uint16).view(np.float16)[0]
+            want[cu[b]:cu[b + 1], (n_kv - 1) * (n_q // n_kv):, blk * 32:blk * 32 + 32] = True
+    got = _attn_run(g, t, pool, table, cu, q, kv_len, n_q, n_kv, d, page, window, scale)
+    assert np.array_equal(np.isnan(got).reshape(want.shape), want)
