@@ -141,10 +141,11 @@ __global__ void __launch_bounds__(256, D < 512 ? 4 : 2) mrope_rows_kernel(const 
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 alignas(16) float y0[4], y1[4];
+                const bool kept = (c * kLanes + at) * 4 >= half;   // as they are: times 0 an infinity would be NaN
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
-                    y0[v] = fmaf(a[k][c][v], co[c][v], -b[k][c][v] * si[c][v]);
-                    y1[v] = fmaf(a[k][c][v], si[c][v], b[k][c][v] * co[c][v]);
+                    y0[v] = kept ? a[k][c][v] : fmaf(a[k][c][v], co[c][v], -b[k][c][v] * si[c][v]);
+                    y1[v] = kept ? b[k][c][v] : fmaf(a[k][c][v], si[c][v], b[k][c][v] * co[c][v]);
                 }
                 *reinterpret_cast<float4*>(out + hk * D + at0[c]) = *reinterpret_cast<float4*>(y0);
                 *reinterpret_cast<float4*>(out + hk * D + at1[c]) = *reinterpret_cast<float4*>(y1);
