@@ -511,6 +511,8 @@ GEM_API gem_status gem_kv4_gather(const void *pool, int64_t n_pages, int page, i
  *   position left is 0).  What lies in the pages behind kv_len or before the window may be
  *   anything.  A position whose K scale is not finite makes NaN of the rows that attend it, one
  *   whose V scale is not finite of their values in its block of 32 dims.
+ *   A wait for a copy that runs out sets GEM_DEVFLAG_TIMEOUT; query heads of a KV head whose sums are not
+ *   whole for it are left as they were, the others are right.
  *   workspace  gem_kv4_attn_workspace(T, B, n_q, n_kv, d) bytes, 256-byte aligned, no
  *          initialisation; calls that can run at the same time need one each.
  *   Accumulation is fp32: q and the probabilities times V's scales enter the tensor cores as binary16

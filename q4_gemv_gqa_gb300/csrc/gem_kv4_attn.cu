@@ -256,6 +256,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
     __shared__ int64_t sums[kWarps];
     __shared__ int tail_unit[C::kWorkers];
     __shared__ float weight[C::kWorkers * ROWS];
+    __shared__ volatile int gave_up[kWarps];             // a wait of this warp ran out
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
@@ -270,7 +271,9 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
     if (lane == 0) {
         for (int i = 0; i < kStages; ++i) mbar_init(&bars[i], 1);
         fence_mbar_init();
+        gave_up[warp] = 0;
     }
+    __syncwarp();
     pdl_wait_trigger();
 
     // this worker's share of all steps, and the request and unit that it begins in
@@ -401,6 +404,16 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
     };
 
     const float to_log2 = P.scale * 1.4426950408889634f;
+
+    // whether a wait of one of this worker's warps has run out (each sets its word before a step's barrier): then
+    // its units are not written
+    auto failed = [&]() {
+        bool any = dead;
+        if (PAIR > 1)
+#pragma unroll
+            for (int of = 0; of < PAIR; ++of) any |= gave_up[warp - member + of] != 0;
+        return PAIR > 1 ? __any_sync(0xffffffffu, any) != 0 : any;
+    };
 
     // state of the unit at hand
     uint32_t bq[NB][2][NT][NH][2];        // q: [block][low or high byte pair][column tile][hi, lo][register]
@@ -801,9 +814,12 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
             for (; step < unit_end; ++step, pos0 += kStepTokens) {
                 if (!dead) {
                     dead = __any_sync(0xffffffffu, !mbar_wait(&bars[stage], parity, P.status));
-                    if (dead && lane == 0)   // a copy never landed: give those in flight a bounded chance to
+                    if (dead && lane == 0) {   // a copy never landed: give those in flight a bounded chance to
+                        gave_up[warp] = 1;
                         for (int k = 0; k < kStages; ++k)
                             (void)mbar_wait(&bars[(stage + k) % kStages], parity ^ (stage + k >= kStages ? 1u : 0u), nullptr);
+                    }
+                    __syncwarp();
                 }
                 if (!dead) {
                     if (((lost >> (stage * kStepTiles)) & kMask) == 0 && pos0 >= un.lo_max && pos0 + kStepTokens - 1 <= un.p0)
@@ -813,12 +829,12 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
                     else
                         member_sync();
                     if (put_step < end) request_step(stage);
-                } else {   // leave without touching the outputs
+                } else {   // go through the steps without work
                     member_sync();
                 }
                 if (++stage == kStages) stage = 0, parity ^= 1;
             }
-            if (ends && !dead) {
+            if (ends && !failed()) {
                 if (starts) {   // the whole unit
                     finish([&](int row, int dim, float2 v, float sum) {
                         const int tok = (row * P.inv_g) >> 16;
@@ -842,7 +858,7 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
             un = next_unit(P, un.units, b, u);
             load_q(un);
         }
-        if (dead) tail = task.x = -1;
+        if (failed()) tail = task.x = -1;
     }
     if (lane == 0 && member == 0) P.tasks[worker] = task;
     // units that go on in the next share: join the parts of this CTA's workers (the rings are empty now)
@@ -865,13 +881,21 @@ __global__ void __launch_bounds__(32 * WARPS, CTAS) kv4_attn_kernel(const AttnPa
         return reinterpret_cast<const float2*>(smem + w * PAIR * C::kWarpBytes + ROWS * C::kDims * 4);
     };
     if (lane == 0 && member == 0) tail_unit[warp / PAIR] = tail < 0 ? -1 : static_cast<int>(tail & 0x7fffffff);
-    __syncthreads();
-    int ids[kW];
-#pragma unroll
-    for (int w = 0; w < kW; ++w) ids[w] = tail_unit[w];
+    const bool lost_one = __syncthreads_or(dead);
     auto slot_of = [&](int first) {
         return P.part + (static_cast<int64_t>(P.workers) + blockIdx.x * kW + first) * Part<D, ROWS>::kFloats;
     };
+    if (lost_one) {   // parts of this CTA may be missing: a maximum that is NaN, which no sum has, marks all of its slots
+        for (int at = threadIdx.x; at < kW * ROWS; at += kThreads) {
+            const int64_t up = ROWS * D + 2 * (at % ROWS);
+            slot_of(at / ROWS)[up] = NAN;
+            slot_of(at / ROWS - P.workers)[up] = NAN;
+        }
+        return;
+    }
+    int ids[kW];
+#pragma unroll
+    for (int w = 0; w < kW; ++w) ids[w] = tail_unit[w];
     // each worker's weight in its unit's part, and the part's (maximum, sum)
     for (int at = threadIdx.x; at < kW * ROWS; at += kThreads) {
         const int w = at / ROWS, row = at % ROWS, id = tail_unit[w];
@@ -941,6 +965,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_attn_merge_kernel(const Att
         task.w = __shfl_sync(0xffffffffu, mine.w, from);
         const int w0 = task.x, c0 = w0 / CW, c1 = (w1 - 1) / CW, parts = c1 - c0 + 2;
         float mx = -INFINITY, sum = 0.f;
+        bool whole = true;     // no part is marked as missing
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k0 = slice; k0 < parts; k0 += kSlices * kAhead) {
             float2 ml[kAhead], ol[kAhead], oh[kAhead];
@@ -957,7 +982,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_attn_merge_kernel(const Att
             }
             float top = mx;
 #pragma unroll
-            for (int a = 0; a < kAhead; ++a) top = fmaxf(top, ml[a].x);
+            for (int a = 0; a < kAhead; ++a) top = fmaxf(top, ml[a].x), whole &= ml[a].x == ml[a].x;
             const float c = mx == top ? 1.f : ex2(mx - top);
             mx = top;
             sum *= c, v.x *= c, v.y *= c, v.z *= c, v.w *= c;
@@ -970,11 +995,11 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_attn_merge_kernel(const Att
             }
         }
         v_s[slice][col] = v;
-        if (col == 0) ml_s[slice] = make_float2(mx, sum);
+        if (col == 0) ml_s[slice] = make_float2(whole ? mx : NAN, sum);
         __syncthreads();
         if (slice == 0) {
-            mx = ml_s[0].x;
-            for (int k = 1; k < kSlices; ++k) mx = fmaxf(mx, ml_s[k].x);
+            mx = ml_s[0].x, whole = mx == mx;
+            for (int k = 1; k < kSlices; ++k) mx = fmaxf(mx, ml_s[k].x), whole &= ml_s[k].x == ml_s[k].x;
             sum = 0.f, v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < kSlices; ++k) {
@@ -986,7 +1011,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_attn_merge_kernel(const Att
             float* o = P.out + (task.y + static_cast<int64_t>(tok)) * P.ldo +
                        (static_cast<int64_t>(task.w) * P.G + (row - tok * P.G)) * D + 4 * col;
             const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            o[0] = v.x * inv, o[1] = v.y * inv, o[2] = v.z * inv, o[3] = v.w * inv;
+            if (whole) o[0] = v.x * inv, o[1] = v.y * inv, o[2] = v.z * inv, o[3] = v.w * inv;
         }
         __syncthreads();
     }
