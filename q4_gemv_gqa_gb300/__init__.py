@@ -51,6 +51,15 @@ def _stream(stream) -> int:
     return stream.cuda_stream
 
 
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    """Bytes for a call on `stream` (None: the current one), of that stream's memory: a block of another
+    stream's may still be in use by work pending there, and would be given back to it at the end of the call."""
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 _HALF_BITS = (torch.int16, torch.uint16)   # binary16 bit patterns
 
 
@@ -140,7 +149,7 @@ def q4_0_gemv(W: torch.Tensor, N: int, K: int, x: torch.Tensor, y: torch.Tensor,
         _check(st, "gem_q4_0_gemv")
         return y
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _scratch(need, x.device, stream)
     st = lib.gem_q4_0_gemv_ws(_dev(W, torch.uint8, "W"), N, K, _dev(x, torch.float32, "x"),
                               x.shape[-1], B, _dev(y, torch.float32, "y"), y.shape[-1],
                               _dev(residual, torch.float32, "residual"),
@@ -164,7 +173,7 @@ def q4_0_gemv_fused(W0: torch.Tensor, W1: torch.Tensor | None, N: int, K: int, x
         raise ValueError("x must have >= K columns and y >= N")
     need = q4_0_gemv_workspace(B, K) if K % 32 == 0 else 0
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _scratch(need, x.device, stream)
     st = lib.gem_q4_0_gemv_fused(_dev(W0, torch.uint8, "W0"), _dev(W1, torch.uint8, "W1"), N, K,
                                  _dev(x, torch.float32, "x"), x.shape[-1], B,
                                  _dev(gamma, torch.float32, "gamma"), eps, act,
@@ -194,7 +203,7 @@ def q4_0_gemm(W0: torch.Tensor, W1: torch.Tensor | None, N: int, K: int, x: torc
         raise ValueError("x must have >= K columns and y >= N")
     need = q4_0_gemm_workspace(M, K) if K % 32 == 0 else 0
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = _scratch(need, x.device, stream)
     st = lib.gem_q4_0_gemm(_dev(W0, torch.uint8, "W0"), _dev(W1, torch.uint8, "W1"), N, K,
                            _dev(x, torch.float32, "x"), x.shape[-1], M,
                            _dev(gamma, torch.float32, "gamma"), eps, act,
@@ -233,7 +242,7 @@ def argmax(y: torch.Tensor, idx: torch.Tensor, workspace: torch.Tensor | None = 
         raise ValueError("idx must hold B indices")
     need = argmax_workspace(B, N)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=y.device)
+        workspace = _scratch(max(need, 1), y.device, stream)
     st = lib.gem_argmax(_dev(y, torch.float32, "y"), N, B, N, _dev(idx, torch.int32, "idx"),
                         _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream))
     _check(st, "gem_argmax")
@@ -252,7 +261,7 @@ def topk(y: torch.Tensor, k: int, idx: torch.Tensor, val: torch.Tensor,
     N = y.shape[-1]
     need = topk_workspace(B, N, k)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=y.device)
+        workspace = _scratch(need, y.device, stream)
     st = lib.gem_topk(_dev(y, torch.float32, "y"), N, B, N, k, _dev(idx, torch.int32, "idx"),
                       _dev(val, torch.float32, "val"), _dev(workspace, torch.uint8, "workspace"),
                       workspace.numel() if workspace is not None else 0, _stream(stream))
@@ -526,10 +535,7 @@ def kv4_attn(q: torch.Tensor, n_q: int, n_kv: int, d: int, cu_tokens: torch.Tens
     if rows != T:
         raise ValueError("out must have T=%d rows, got %d" % (T, rows))
     if workspace is None:
-        need = lib.gem_kv4_attn_workspace(T, B, n_q, n_kv, d)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        if stream is not None and need:
-            workspace.record_stream(stream)   # it is given back here, before that stream has used it
+        workspace = _scratch(lib.gem_kv4_attn_workspace(T, B, n_q, n_kv, d), q.device, stream)
     ws_bytes = workspace.shape[0]
     st = lib.gem_kv4_attn(qp, ldq, T, _here(cu_tokens, torch.int32, "cu_tokens", (B + 1,), dev),
                           _here(kv_len, torch.int32, "kv_len", (B,), dev), B, n_q, n_kv, d,
