@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 
 from parity import assert_close
-from test_gpu_kv4 import _attn_case, _attn_run, _attn_want, env  # noqa: F401
+from test_gpu_kv4 import ATTN, _attn_case, _attn_run, _attn_want, env  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +41,48 @@ def test_units_that_a_failed_wait_cuts_short_are_not_written(env, heads):
     status.zero_()
     assert_close(_attn_run(g, t, *args, status=status, workspace=ws), want, "the call after")
     assert int(status) == 0
+
+
+def _form(T, B, G, d):
+    """The rule by which the library chooses a kernel: 0 up to 4 query rows a request on average, 1 up to 8
+    (any more at d 256 and 512), 2 beyond.  T counts the rows of q, those behind the last request too."""
+    rows = max(1, -(-T // B)) * G
+    return 0 if rows <= 4 else 1 if rows <= 8 or d >= 256 else 2
+
+
+# (kv lengths, new tokens, n_q, n_kv, d, page, window): single tokens at every number of query heads to a KV head,
+# windows among them, and several tokens that leave rows of a unit empty
+ROWS_OF_A_UNIT = [
+    ([1, 700, 63], [1] * 3, G * 2, 2, d, 16, w) for G in (1, 2, 3, 4, 5, 6, 7, 8) for d in (64, 128) for w in (0, 100)
+] + [
+    ([400, 33], [1] * 2, G, 1, d, 32, w) for G in (1, 3, 4, 5, 8) for d in (256, 512) for w in (0, 45)
+] + [
+    ([150, 40, 500], [2, 1, 3], 6, 2, 64, 16, 0), ([150, 40, 500], [2, 1, 1], 2, 2, 128, 32, 60),
+    ([90, 200], [3, 2], 3, 1, 128, 16, 0), ([90, 200], [7, 3], 5, 1, 128, 16, 33), ([77], [4], 7, 1, 64, 32, 0),
+    ([77, 300], [5, 4], 3, 1, 256, 16, 20), ([200], [3], 5, 1, 512, 64, 0), ([45] * 34, [1] * 34, 3, 1, 128, 16, 0),
+]
+EXACT = [c for c in ATTN if sum(c[1])] + ROWS_OF_A_UNIT
+
+
+def test_every_form_of_the_kernel_is_among_the_cases():
+    seen = {(c[4], _form(sum(c[1]), len(c[1]), c[2] // c[3], c[4])) for c in EXACT}
+    assert seen == {(d, f) for d in (64, 128, 256, 512) for f in range(3 if d < 256 else 2)}
+    windows = {(c[4], _form(sum(c[1]), len(c[1]), c[2] // c[3], c[4])) for c in EXACT if c[6]}
+    assert windows == seen
+
+
+@pytest.mark.parametrize("spare", [0, 40], ids=["exact", "spare_rows"])
+@pytest.mark.parametrize("case", EXACT, ids=lambda c: "kv%d_new%d_G%d_d%d_p%d_w%d_B%d" % (
+    max(c[0]), max(c[1]), c[2] // c[3], c[4], c[5], c[6], len(c[0])))
+def test_attention_with_rows_for_the_tokens_alone_and_with_room_to_spare(env, case, spare):
+    """The rows of q choose the kernel, so both a call that has as many rows as tokens and one of a step that was
+    captured with room for more are compared; rows behind the last request stay as they were."""
+    g, t = env
+    kv_len, fresh, n_q, n_kv, d, page, window = case
+    r = np.random.RandomState(sum(kv_len) + d + n_q)
+    pool, table, cu, q = _attn_case(r, t, kv_len, fresh, n_q, n_kv, d, page, spare_rows=spare)
+    args = (pool, table, cu, q, kv_len, n_q, n_kv, d, page, window, d ** -0.5)
+    got = _attn_run(g, t, *args)
+    assert np.all(got[cu[-1]:] == 4.0), "rows behind the last request were written"
+    assert_close(got[:cu[-1]], _attn_want(*args), "attention")
+    assert g.device_status(reset=True) == 0
