@@ -501,7 +501,9 @@ GEM_API gem_status gem_kv4_gather(const void *pool, int64_t n_pages, int page, i
  *   of 0 .. p), which the pool must already hold:
  *     out[t][h*d + e] = sum_j softmax_j(scale * q_h . K[j]) * V[j][e],  KV head h / (n_q / n_kv).
  *   q      [T][ldq] fp32, 16-byte aligned, ldq % 4 == 0;  out [T][ldo] fp32, which must not
- *          overlap q.  Rows from cu_tokens[B] on are neither read nor written.
+ *          overlap q.  Rows from cu_tokens[B] on are neither read nor written.  T, the rows that q has,
+ *          chooses the kernel by its mean over the requests: a step of single tokens is fastest with
+ *          T = B (with rows to spare it may take twice as long), the results are right with any.
  *   table  [B][max_pages] int32; entries from ceil(kv_len / page) on are not read, nor those that
  *          lie before every row's window.
  *   d 64, 128, 256 or 512; n_q % n_kv == 0, n_q / n_kv <= 8; B in 0..4096; T * n_kv < 2^31.

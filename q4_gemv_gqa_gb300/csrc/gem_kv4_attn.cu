@@ -18,9 +18,10 @@
 // instruction, more rows take two.  Each row has a power for every block of 32 dims, of q once a unit, of p sV in
 // each step: one for all blocks loses the bits of the small ones (blocks 2^24 apart were 1e-4 off for q, 2e-2
 // for V).
-// The wide tcgen05 path wants both operands in binary16 or fp8 tiles in shared memory: here one operand
-// is 4-bit codes and would first be written out four times as large, for eight columns of output, so
-// the unpacking, not the multiply rate, would bound it just the same.
+// The wide tcgen05 path wants both operands in binary16 or fp8 tiles in shared memory.  In decoding one
+// operand is 4-bit codes and would first be written out four times as large, for eight columns of output, so
+// the unpacking, not the multiply rate, would bound it just the same.  (That does not hold for chunks: 32 new
+// tokens of four heads are the 128 rows of a tile.  They run here too, in units of 16 rows.)
 //
 // Schedule.  The work is (request, KV head, group of query rows) units of steps of 32 positions.  Their
 // number is known on the device only, so a fixed grid of warps takes equal contiguous shares of all
@@ -146,7 +147,9 @@ __device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// Word of 8 codes, nibbles n0 .. n7 from the low end -> (n0, n4), (n1, n5), (n2, n6), (n3, n7), less 8 each.
+// Word of 8 codes, nibbles n0 .. n7 from the low end -> (n0, n4), (n1, n5), (n2, n6), (n3, n7), less 8 each.  (Integers
+// put into the mantissa of a power of two are an old way to convert them; for 4-bit weights and binary16 it is
+// described by Kim, Henry, Fahim and Awadalla, "Who Says Elephants Can't Run", 2022.)
 struct Codes {
     uint32_t v[4];
 };
@@ -236,10 +239,11 @@ struct Cfg {
 
 // ---- the kernel ------------------------------------------------------------------------------------
 //
-// What bounds it: the warp instructions, about 770 a step of 32 positions at d 128 and four rows, of
-// which unpacking the codes is 290 and splitting p times V's scale 100, and their latency, with three
-// warps a scheduler issuing in 58 % of the cycles.  8 requests of up to 32,768 positions (32 / 8 heads,
-// d 128, 257 MB): 68 us, 3.8 TB/s, 56 % of the measured copy rate.  Short batches are latency: 1 x 4097 positions take 9 us.
+// What bounds it: the warp instructions, about 850 a step of 32 positions at d 128 and four rows, of
+// which unpacking the codes is 290 and splitting p times V's scale, with its powers of two, 180, and their
+// latency, with three warps a scheduler issuing in 57 % of the cycles.  8 requests of up to 32,768 positions
+// (32 / 8 heads, d 128, 257 MB): 75 us, 3.4 TB/s, 50 % of the measured copy rate (68 us with one power of two for all
+// blocks, which loses bits).  Short batches are latency: 1 x 4097 positions take 9.3 us.
 // One CTA of 12 warps an SM has 168 registers a thread for the sums, q and the operands under way; two of
 // 8 have 128, spill, and took 71 us there against 66.7 at that point, 15.1 against 12.9 for 8 requests of up
 // to 2049 positions; 10 warps took 76 and 12.1.
@@ -1033,12 +1037,15 @@ Variant variant() {
             Part<D, C::kRows>::kFloats, C::smem};
 }
 
-// Query rows a unit has: one token's heads, or as many tokens as the batch brings on average while
+// Query rows a unit has: one token's heads, or as many tokens as the batch has rows for on average while
 // the sums of a warp stay in registers.  (Any batch is right with any of them: a request's tokens are cut
-// into units.)  Measured: 8 rows of d 128 take 8 warps of 255 registers (4 x 32 new tokens: 62 us with 16
-// rows when these were compared, 65 now; 12 warps spill, 104; 32 rows in warps of 64 dims, 77); so do 8 rows at d 256 and 512, with 256
-// dims a warp (1 x 32,769, d 512: 36 us then, 38 now; 128 dims a warp: 37 with 12 warps, 52 with 16).  Up to four rows
-// take 128 dims a warp.
+// into units.)  The host knows the rows of q, not the tokens that are there: a decoding step with rows to spare
+// is run like one with more tokens, and the largest request of a mixed batch does not count alone.  8 x 32,768
+// positions, four heads to a KV head: 75 us with 8 rows, 149 with 170; 8 x 2049: 13.4 and 21.9; at d 256, 16 k: 168 and
+// 172.  Measured when these were compared: 8 rows of d 128 take 8 warps of 255 registers (4 x 32 new tokens: 62 us
+// with 16 rows, 73 now; 12 warps spill, 104; 32 rows in warps of 64 dims, 77); so do 8 rows at d 256 and 512, with
+// 256 dims a warp (1 x 32,769, d 512: 36 us then, 42 now; 128 dims a warp: 37 with 12 warps, 52 with 16).  Up to four
+// rows take 128 dims a warp.
 Variant pick(int64_t T, int B, int G, int d) {
     const int64_t tokens = std::max<int64_t>(1, (T + B - 1) / std::max(B, 1));
     const int64_t want = tokens * G;

@@ -54,9 +54,9 @@ __device__ __forceinline__ int row_state(const MropeParams& P, int64_t t) {
 // (32 for D = 512) hold a head: a lane four neighbouring pairs (i, i + R/2) (past the rotated dims, pairs of
 // kept ones), the same for every head, so that the angles are taken once for all heads of a warp and a
 // head is two 16-byte loads, one reduction and two stores a lane.  A warp takes `heads` heads of one
-// token, the loads of the next under way while one is rotated.  Bound by HBM: 167.7 MB (read once, written
-// once) in 34.4 us are 4.9 TB/s, 72 % of the measured copy rate; a plain contiguous copy of the same bytes
-// takes 28.7 us here.
+// token, the loads of the next under way while one is rotated.  167.7 MB (read once, written once) take
+// 34.5 us, 4.9 TB/s, 72 % of the measured copy rate, bound by the loads in flight (one head a warp ahead, 4093
+// warps in all); a plain contiguous copy of the same bytes takes 28.7 us here.
 template <int D>
 __global__ void __launch_bounds__(256, D < 512 ? 4 : 2) mrope_rows_kernel(const MropeParams P, const __grid_constant__ MropeFreq F, int heads,
                                                          int chunks) {
@@ -154,7 +154,8 @@ __global__ void __launch_bounds__(256, D < 512 ? 4 : 2) mrope_rows_kernel(const 
     }
 }
 
-// Any even d and R: one warp per (token, head), the head in shared memory (96 us on the rows above).
+// Any even d and R: one warp per (token, head), the head in shared memory and the angles taken for each head
+// (96 us on the rows above: scalar loads, and as many sines as values).
 __global__ void __launch_bounds__(128) mrope_kernel(const MropeParams P, const __grid_constant__ MropeFreq F) {
     __shared__ float buf[4][kMaxHeadDim];
     pdl_wait_trigger();
@@ -195,8 +196,9 @@ __global__ void __launch_bounds__(128) mrope_kernel(const MropeParams P, const _
     for (int e = P.R + lane; e < P.d; e += 32) out[e] = sb[e];
 }
 
-// The frequencies are a function of these alone; a thread keeps the last ones it computed (a model's
-// layers ask for the same), since their powers cost more than the launch.
+// The frequencies are a function of these alone; a thread keeps the last ones it computed, since their powers
+// cost more than the launch and layers of one kind ask for the same.  (Between kinds of layers with bases or
+// sections of their own they are computed again.)
 struct FreqKey {
     float theta;
     int n_axes, interleaved;
