@@ -1,8 +1,9 @@
-"""Paged 4-bit attention: what is left where a wait runs out, the stream of its scratch, and every form of the
-kernel at the row counts that choose it."""
+"""Paged 4-bit cache: what is left where a wait runs out, every form of the attention kernel at the row counts that
+choose it, and offsets past 32 bits."""
 import numpy as np
 import pytest
 
+from oracle import kv4
 from parity import assert_close
 from test_gpu_kv4 import ATTN, _attn_case, _attn_run, _attn_want, env  # noqa: F401
 
@@ -86,3 +87,50 @@ def test_attention_with_rows_for_the_tokens_alone_and_with_room_to_spare(env, ca
     assert np.all(got[cu[-1]:] == 4.0), "rows behind the last request were written"
     assert_close(got[:cu[-1]], _attn_want(*args), "attention")
     assert g.device_status(reset=True) == 0
+
+
+def test_offsets_past_32_bits(env):
+    """A pool of more than 4 GiB and rows of more than 2^31 values: the last pages and rows are the ones in use."""
+    g, t = env
+    n_q, n_kv, d, page, n = 8, 2, 128, 64, 70
+    size = g.kv4_page_bytes(n_kv, d, page)
+    n_pages = (5 << 30) // size
+    pool = t.empty((n_pages, size), dtype=t.uint8, device="cuda")
+    cols = (n_q + 2 * n_kv) * d
+    T = (1 << 31) // cols + 5000
+    qkv = t.empty((T, cols), device="cuda")
+    r = np.random.RandomState(90)
+    x = r.randn(n, cols).astype(np.float32)
+    qkv[T - n:] = t.from_numpy(x).cuda()
+    i32 = dict(dtype=t.int32, device="cuda")
+    pos, slot = t.full((1, T), -1, **i32), t.full((T,), -1, **i32)
+    pages = [n_pages - 1, n_pages - 3]
+    where = np.array([pages[j // page] * page + j % page for j in range(n)], np.int32)
+    pos[0, T - n:] = t.arange(n, **i32)
+    slot[T - n:] = t.from_numpy(where).cuda()
+    g.qknorm_mrope(qkv, n_q, n_kv, d, None, None, 1e-6, pos, [d // 2], 1e4, qkv)
+    rows = qkv[T - n:].cpu().numpy()
+    want = kv4.qknorm_mrope(x, n_q, n_kv, d, None, None, 1e-6, np.arange(n)[None], [d // 2], 1e4)
+    assert_close(rows[:, :want.shape[1]], want, "rope", max_abs=2e-6 * np.abs(want).max(), rel_l2=1e-6)
+    k, v = qkv[:, n_q * d:(n_q + n_kv) * d], qkv[:, (n_q + n_kv) * d:]
+    g.kv4_append(k, v, n_kv, d, slot, pool, page)
+    K, V = (kv4.values(*kv4.quantise(rows[:, at:at + n_kv * d].reshape(n, n_kv, d))).reshape(n, -1)
+            for at in (n_q * d, (n_q + n_kv) * d))
+    out = t.zeros((2, T, n_kv * d), device="cuda")
+    g.kv4_gather(pool, page, n_kv, d, slot, out[0], out[1])
+    assert np.array_equal(out[:, T - n:].cpu().numpy(), np.stack([K, V]).astype(np.float32))
+    del out
+    att = t.zeros((T, n_q * d), device="cuda")
+    g.kv4_attn(qkv, n_q, n_kv, d, t.tensor([T - n, T], **i32), t.tensor([n], **i32), t.tensor([pages], **i32), pool, page, 0,
+               d ** -0.5, att)
+    ref = kv4.attention(rows[:, :n_q * d].reshape(n, n_q, d), K.reshape(n, n_kv, d), V.reshape(n, n_kv, d), n, 0, d ** -0.5)
+    assert_close(att[T - n:].cpu().numpy(), ref.reshape(n, -1), "attention")
+    assert g.device_status(reset=True) == 0
+
+
+def test_a_workspace_is_asked_for_wherever_there_is_work(env):
+    g, _ = env
+    for d in (64, 128, 256, 512):
+        for G in range(1, 9):
+            for T, B in ((1, 1), (4, 4), (64, 3), (4096, 4096)):
+                assert g.kv4_attn_workspace(T, B, 2 * G, 2, d) > 0
