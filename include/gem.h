@@ -533,6 +533,95 @@ GEM_API gem_status gem_kv4_attn(const float *q, int64_t ldq, int64_t T, const in
                                 void *stream);
 
 /*
+ * The 8-bit floating-point path: gem_rmsnorm_fp8, gem_quant_fp8 and gem_fp8_gemm.  The pages have no
+ * counterpart of these calls; they are the form of [GELO] 06's block topology (pre-norm, projection,
+ * gated activation, projection) for prompts and batches of any number of rows, with weights held in
+ * e4m3 (1 sign, 4 exponent and 3 mantissa bits, up to +-448; 0x7f and 0xff are NaN).
+ *
+ * A row of H values in 8 bits: codes [H] and scales [ceil(H / 128)] fp32, value = code * scale of its
+ * block of 128 (the last block may be shorter).  For a block with largest magnitude m
+ *     scale = the smallest power of two with m <= 448 * scale,   code = e4m3(value / scale),
+ * rounded to nearest even; dividing by a power of two rounds nothing, so a code depends on the value
+ * alone.  m < 2^-100: scale 0, codes 0.  m not finite: scale NaN, codes 0.
+ * A layer on T rows: gem_rmsnorm_fp8, gem_fp8_gemm (QKV), attention, gem_quant_fp8, gem_fp8_gemm (O);
+ * gem_rmsnorm_fp8, gem_fp8_gemm (gate and up as one matrix), gem_quant_fp8, gem_fp8_gemm (down).
+ */
+
+/*
+ * Residual addition, RMSNorm and its output in 8 bits.
+ *   h[t] = x[t] + residual[t]  (fp32; residual NULL: x[t]);   out[t] = h[t]  (out NULL: not kept)
+ *   y[t][i] = h[t][i] / sqrt(mean_i h[t][i]^2 + eps) * gamma[i]  (gamma NULL: 1), in 8 bits as above.
+ *   x [T][ldx], residual [T][ldr], out [T][ldo] fp32, 16-byte aligned, strides multiples of 4 values;
+ *          out may be x or residual with the same stride, else must not overlap them.
+ *   gamma  [H] fp32, 16-byte aligned.
+ *   codes  [T][ldc] bytes, 16-byte aligned, ldc a multiple of 16;  scales [T][lds] fp32, lds >= ceil(H / 128).
+ *   H a multiple of 16, at most 32768 (GEM_ERR_UNSUPPORTED_SHAPE otherwise); T < 2^31.
+ *   The mean square is summed to about 2^-40 and a value next to a border of two codes is decided in
+ *   fp64, so the codes are those of the exact y (for squares above 2^-100).  A row whose sum of squares
+ *   is not finite in fp32 gets NaN scales.
+ */
+GEM_API gem_status gem_rmsnorm_fp8(const float *x, int64_t ldx, const float *residual, int64_t ldr,
+                                   float *out, int64_t ldo, int64_t T, int64_t H, const float *gamma,
+                                   float eps, uint8_t *codes, int64_t ldc, float *scales, int64_t lds,
+                                   void *stream);
+
+/*
+ * Rows in 8 bits: of the gated activation (up set) or of x itself (up NULL).
+ *   y[t][i] = up ? act(x[t][i]) * up[t][i] : x[t][i], in 8 bits as above; act as gem_swiglu, taken as
+ *   x / (1 + e^-z) with z = x (silu) or 2 sqrt(2/pi) (x + 0.044715 x^3) (gelu_tanh); 0 where z < -83.
+ *   x [T][ldx], up [T][ldu] fp32, 16-byte aligned, strides multiples of 4 values (the two halves of a
+ *   merged projection's rows will do).  codes, scales, H, T as gem_rmsnorm_fp8, H of any size.
+ *   Codes are those of the exact y: next to a border they are decided in fp64.
+ */
+GEM_API gem_status gem_quant_fp8(const float *x, int64_t ldx, const float *up, int64_t ldu, int64_t T,
+                                 int64_t H, int act, uint8_t *codes, int64_t ldc, float *scales,
+                                 int64_t lds, void *stream);
+
+/*
+ * Product of 8-bit rows with 8-bit weights that have a scale for each block of 128 x 128.
+ *   y[m][n] = sum_b xs[m][b] * ws[n / 128][b] * (sum_{k in block b} x[m][k] * W[n][k])  (+ residual[m][n])
+ *   W   [N][K] e4m3, rows contiguous;   ws [ceil(N / 128)][ceil(K / 128)] fp32, any values.
+ *   x   [M][ldx] e4m3, ldx >= K;  xs [M][ldxs] fp32, ldxs >= ceil(K / 128), any values.
+ *   y   [M][ldy] fp32, ldy >= N;  residual nullable, [M][ldy], may be y.  y must not overlap the rest.
+ *   W and x 16-byte aligned, ldx a multiple of 16 (GEM_ERR_MISALIGNED); K a multiple of 16
+ *   (GEM_ERR_UNSUPPORTED_SHAPE); M, N, K < 2^31.  Rows of y whose base and stride are multiples of 16
+ *   bytes are written fastest.
+ *   The products of a block are summed on the tensor cores (tcgen05, fp32 accumulation), the blocks in
+ *   fp32 in order of k, so a result does not depend on M.  A NaN code or scale makes NaN of the results
+ *   that it takes part in.  A wait that runs out sets GEM_DEVFLAG_TIMEOUT in *status (nullable: the
+ *   library's word); y is then unspecified.  No workspace.  Deterministic.
+ */
+GEM_API gem_status gem_fp8_gemm(const void *W, const float *ws, int64_t N, int64_t K, const void *x,
+                                int64_t ldx, const float *xs, int64_t ldxs, int64_t M, float *y,
+                                int64_t ldy, const float *residual, int32_t *status, void *stream);
+
+/*
+ * Log probabilities of given tokens, their ranks, the entropy and the top alternatives of logit rows:
+ * what scoring a prompt and showing a sampled token's alternatives need.  The pages have no counterpart;
+ * it stands beside gem_argmax and gem_topk.
+ *   l = scale * y[t][0..N);   logp[t] = l[tokens[t]] - lse,   lse = log sum_n e^l[n]
+ *   rank[t]    1 + the entries above tokens[t] in gem_topk's order of y (larger first, equal ones by
+ *              lowest index); nullable.
+ *   entropy[t] = -sum_n p[n] log p[n], p = e^(l - lse), where p[n] = 0 counts 0; nullable.
+ *   idx[t][r], val[t][r], r < k: gem_topk's indices and their log probabilities l[idx] - lse; k in
+ *              0..64, k <= N (k 0: both may be NULL).
+ *   y [T][ldy] fp32, ldy >= N, 1 <= N < 2^31; T * ceil(N / 2048) < 2^31; scale > 0 and finite.
+ *   tokens     [T] int32; nullable with logp and rank.  -1: none given, logp 0 and rank 0.  Any other value
+ *              outside [0, N) sets GEM_DEVFLAG_POS_RANGE, logp NaN and rank 0.
+ *   -inf logits (banned tokens) have probability 0.  A row with a NaN or +inf, or of -inf alone: logp,
+ *   entropy and val are NaN, rank and idx as stated (NaN after every number; a NaN token's rank counts
+ *   the numbers and the NaNs of lower index).
+ *   workspace  gem_logprobs_workspace(T, N, k) bytes (may be 0), 256-byte aligned, no initialisation;
+ *              calls that can run at the same time need one each.
+ *   Sums are fp32; one pass over y.  Deterministic.
+ */
+GEM_API size_t gem_logprobs_workspace(int64_t T, int64_t N, int k);
+GEM_API gem_status gem_logprobs(const float *y, int64_t ldy, int64_t T, int64_t N, float scale,
+                                const int32_t *tokens, float *logp, int32_t *rank, float *entropy,
+                                int k, int32_t *idx, float *val, void *workspace, size_t ws_bytes,
+                                int32_t *status, void *stream);
+
+/*
  * Gated FFN activation  [GELO] 04/05 (Qwen3 SwiGLU; Gemma gelu_pytorch_tanh).
  *   out = act(gate) * up,  act 0: silu(g) = g / (1 + e^-g);
  *                          act 1: 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))).

@@ -27,7 +27,7 @@ DEVFLAG_NO_ROOM = 8
 __all__ = ["GemError", "q4_0_gemv", "q4_0_gemv_workspace", "q4_0_gemv_fused", "q8_0_gemv", "argmax", "argmax_workspace", "rmsnorm", "rmsnorm_qknorm_rope", "gqa_decode_attn",
            "gqa_decode_attn_workspace", "gqa_decode_attn_fused", "swiglu", "decode_layer", "decode_layer_workspace",
            "kv4_page_bytes", "kv_block_tables", "qknorm_mrope", "kv4_append", "kv4_gather", "kv4_attn",
-           "kv4_attn_workspace", "DeviceLayer", "device_status", "status_from_flags", "set_wait_limit",
+           "kv4_attn_workspace", "rmsnorm_fp8", "quant_fp8", "fp8_gemm", "logprobs", "logprobs_workspace", "DeviceLayer", "device_status", "status_from_flags", "set_wait_limit",
            "set_test_injection", "LayerDesc"]
 
 
@@ -415,7 +415,7 @@ def _rows(t: torch.Tensor, cols: int, name: str, device: int):
             name, cols, t.dtype, tuple(t.shape), t.device))
     rows, have = t.shape
     ld, step = t.stride()
-    if have < cols or (step != 1 and have > 1):
+    if have < cols or (step != 1 and have > 1 and rows):
         raise ValueError("%s must be fp32 [rows, >= %d] with contiguous rows, got %s strides %s" % (
             name, cols, tuple(t.shape), t.stride()))
     return t.data_ptr(), (ld if rows > 1 else (have + 3) // 4 * 4), rows
@@ -544,6 +544,119 @@ def kv4_attn(q: torch.Tensor, n_q: int, n_kv: int, d: int, cu_tokens: torch.Tens
                           _status(status, dev), _stream_on(stream, dev))
     _check(st, "gem_kv4_attn")
     return out
+
+
+# ---- 8-bit floating point, scores -----------------------------------------------------------
+
+
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)   # e4m3 codes
+
+
+def _codes(t: torch.Tensor, cols: int, name: str, device: int):
+    """(pointer, row stride, rows) of e4m3 codes [rows, >= cols] (uint8 or float8_e4m3fn) whose rows are contiguous."""
+    if t.dim() != 2 or t.dtype not in _E4M3 or t.get_device() != device:
+        raise ValueError("%s must be uint8 or float8_e4m3fn [rows, >= %d] on the current CUDA device, got %s %s on %s" % (
+            name, cols, t.dtype, tuple(t.shape), t.device))
+    rows, have = t.shape
+    ld, step = t.stride()
+    if have < cols or (step != 1 and have > 1 and rows):
+        raise ValueError("%s must be [rows, >= %d] with contiguous rows, got %s strides %s" % (
+            name, cols, tuple(t.shape), t.stride()))
+    return t.data_ptr(), (ld if rows > 1 else (have + 15) // 16 * 16), rows
+
+
+def _same_rows(rows: int, **others: int) -> None:
+    for name, n in others.items():
+        if n != rows:
+            raise ValueError("%s must have %d rows, got %d" % (name, rows, n))
+
+
+def rmsnorm_fp8(x: torch.Tensor, gamma: torch.Tensor | None, eps: float, codes: torch.Tensor, scales: torch.Tensor,
+                residual: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None):
+    """RMSNorm of x (+ residual) in 8 bits: x fp32 [T, H], codes uint8 or float8_e4m3fn [T, >= H], scales fp32
+    [T, >= ceil(H / 128)].  out (may be x or residual) receives x + residual."""
+    dev = torch.cuda.current_device()
+    H = x.shape[-1]
+    xp, ldx, T = _rows(x, H, "x", dev)
+    rp, ldr, r_rows = (None, 0, T) if residual is None else _rows(residual, H, "residual", dev)
+    op, ldo, o_rows = (None, 0, T) if out is None else _rows(out, H, "out", dev)
+    cp, ldc, c_rows = _codes(codes, H, "codes", dev)
+    sp, lds, s_rows = _rows(scales, -(-H // 128), "scales", dev)
+    _same_rows(T, residual=r_rows, out=o_rows, codes=c_rows, scales=s_rows)
+    st = lib.gem_rmsnorm_fp8(xp, ldx, rp, ldr, op, ldo, T, H, None if gamma is None else _here(gamma, torch.float32, "gamma", (H,), dev),
+                             eps, cp, ldc, sp, lds, _stream_on(stream, dev))
+    _check(st, "gem_rmsnorm_fp8")
+    return codes, scales
+
+
+def quant_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, up: torch.Tensor | None = None,
+              act: int = ACT_SILU, stream=None):
+    """act(x) * up, or x itself (up None), in 8 bits; x, up fp32 [T, H] (column ranges of a wider tensor will
+    do), codes and scales as rmsnorm_fp8."""
+    dev = torch.cuda.current_device()
+    H = x.shape[-1]
+    xp, ldx, T = _rows(x, H, "x", dev)
+    up_p, ldu, u_rows = (None, 0, T) if up is None else _rows(up, H, "up", dev)
+    cp, ldc, c_rows = _codes(codes, H, "codes", dev)
+    sp, lds, s_rows = _rows(scales, -(-H // 128), "scales", dev)
+    _same_rows(T, up=u_rows, codes=c_rows, scales=s_rows)
+    st = lib.gem_quant_fp8(xp, ldx, up_p, ldu, T, H, act, cp, ldc, sp, lds, _stream_on(stream, dev))
+    _check(st, "gem_quant_fp8")
+    return codes, scales
+
+
+def fp8_gemm(W: torch.Tensor, w_scales: torch.Tensor, x: torch.Tensor, x_scales: torch.Tensor, y: torch.Tensor,
+             residual: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y = x @ W.T (+ residual) of 8-bit rows: W [N, K] e4m3 (uint8 or float8_e4m3fn) with w_scales fp32
+    [ceil(N / 128), ceil(K / 128)], x [M, >= K] with x_scales fp32 [M, >= ceil(K / 128)], y and residual (which
+    may be y) fp32 [M, >= N] of the same row stride."""
+    dev = torch.cuda.current_device()
+    if W.dim() != 2 or not W.is_contiguous():
+        raise ValueError("W must be contiguous [N, K], got %s strides %s" % (tuple(W.shape), W.stride()))
+    N, K = W.shape
+    wp, _, _ = _codes(W, K, "W", dev)
+    xp, ldx, M = _codes(x, K, "x", dev)
+    sp, lds, s_rows = _rows(x_scales, -(-K // 128), "x_scales", dev)
+    yp, ldy, y_rows = _rows(y, N, "y", dev)
+    rp, ldr, r_rows = (None, ldy, M) if residual is None else _rows(residual, N, "residual", dev)
+    _same_rows(M, x_scales=s_rows, y=y_rows, residual=r_rows)
+    if ldr != ldy and M > 1:
+        raise ValueError("residual must have y's row stride %d, got %d" % (ldy, ldr))
+    st = lib.gem_fp8_gemm(wp, _here(w_scales, torch.float32, "w_scales", (-(-N // 128), -(-K // 128)), dev), N, K, xp, ldx,
+                          sp, lds, M, yp, ldy, rp, _status(status, dev), _stream_on(stream, dev))
+    _check(st, "gem_fp8_gemm")
+    return y
+
+
+def logprobs_workspace(T: int, N: int, k: int) -> int:
+    return int(lib.gem_logprobs_workspace(T, N, k))
+
+
+def logprobs(y: torch.Tensor, tokens: torch.Tensor | None, logp: torch.Tensor | None, entropy: torch.Tensor | None = None,
+             rank: torch.Tensor | None = None, idx: torch.Tensor | None = None, val: torch.Tensor | None = None,
+             scale: float = 1.0, workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
+             stream=None) -> None:
+    """Scores of the logit rows y (fp32 [T, N]): logp, entropy fp32 and rank int32 [T] of the tokens int32 [T]
+    (-1: none), and the k alternatives idx int32, val fp32 [T, k] with their log probabilities.  Outputs that are
+    None are not computed.  workspace: uint8, at least logprobs_workspace(T, N, k) bytes (allocated when not given)."""
+    dev = torch.cuda.current_device()
+    N = y.shape[-1]
+    yp, ldy, T = _rows(y, N, "y", dev)
+    f32, i32 = torch.float32, torch.int32
+    here = lambda t, dtype, name: None if t is None else _here(t, dtype, name, (T,), dev)  # noqa: E731
+    if (idx is None) != (val is None):
+        raise ValueError("idx and val come together")
+    k = 0 if idx is None else idx.shape[-1]
+    if workspace is None:
+        need = lib.gem_logprobs_workspace(T, N, k)
+        workspace = _scratch(need, y.device, stream) if need else None
+    ws_bytes = 0 if workspace is None else workspace.shape[0]
+    st = lib.gem_logprobs(yp, ldy, T, N, scale, here(tokens, i32, "tokens"), here(logp, f32, "logp"), here(rank, i32, "rank"),
+                          here(entropy, f32, "entropy"), k, _here(idx, i32, "idx", (T, k), dev) if k else None,
+                          _here(val, f32, "val", (T, k), dev) if k else None,
+                          None if workspace is None else _here(workspace, torch.uint8, "workspace", (ws_bytes,), dev), ws_bytes,
+                          _status(status, dev), _stream_on(stream, dev))
+    _check(st, "gem_logprobs")
 
 
 class DeviceLayer:
