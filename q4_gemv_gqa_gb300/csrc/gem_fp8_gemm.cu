@@ -1,58 +1,285 @@
-// gem_fp8_gemm.cu — product of rows in 8-bit floating point with weights scaled by blocks of 128 x 128.
-#include <cuda_fp8.h>
+// gem_fp8_gemm.cu — product of rows in 8-bit floating point with weights scaled by blocks of 128 x 128
+// (gem_fp8_gemm), on tcgen05.
+//
+// y[m][n] = sum_b xs[m][b] ws[n / 128][b] d_b[m][n],  d_b = the product over the 128 values of block b.
+// The tensor cores sum d_b in tensor memory (four instructions of 32 values, the first of which overwrites);
+// other warps read it back, scale it and add it to sums in registers while the next block's product runs in
+// another part of tensor memory.  So the scales may have any values and the long sums are plain fp32.
+//
+// fp8_rows_kernel (up to 128 rows of x): the weights are what the call reads, and the rows of W take the
+// 128-row side of the product, the rows of x its 16..128 columns.
+#include "gem_tcgen05.cuh"
 
-#include "gem_device.cuh"
+#include <map>
+#include <mutex>
+#include <utility>
 
 namespace gem {
 namespace {
 
 struct GemmParams {
-    const uint8_t* W;
     const float* ws;
-    int N, K, M, kb;
-    const uint8_t* x; int64_t ldx;
-    const float* xs; int64_t ldxs;
-    float* y; int64_t ldy;
+    const float* xs;
+    int64_t ldxs;
     const float* res;
+    float* y;
+    int64_t ldy;
+    int N, M, kb;
+    int rows, tiles;        // rows of W a tile, tiles
+    int split;              // CTAs of a cluster that share a tile's blocks
+    int stages, wbytes;     // ring stages, bytes of W in one
+    int chunk;              // blocks whose x scales are held at a time
     int* status;
 };
 
-__device__ __forceinline__ float e4m3(uint8_t c) {
-    __nv_fp8_e4m3 v;
-    v.__x = c;
-    return static_cast<float>(v);
+// ---- few rows of x -----------------------------------------------------------------------------
+// Warps 0..3 scale and add (lane = row of W), warp 4 loads, warp 5 issues the products.
+constexpr int kRowsThreads = 192;
+constexpr int kMaxStages = 48;
+constexpr int kScaleBytes = 24 << 10;
+
+template <int NT>
+constexpr int kRowsBuffers = NT >= 128 ? 4 : 8;   // of NT columns in tensor memory, at most 512
+
+struct RowsBarriers {
+    uint64_t full[kMaxStages], empty[kMaxStages], dfull[8], dempty[8];
+    uint32_t tmem;
+    int dead;
+};
+
+template <int NT>
+__global__ void __launch_bounds__(kRowsThreads) fp8_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const GemmParams p) {
+    constexpr int NB = kRowsBuffers<NT>;
+    extern __shared__ uint8_t raw[];
+    __shared__ RowsBarriers bar;
+    // the ring, 1024-byte aligned: W's rows, then x's rows; behind it the x scales and the cluster's sums
+    uint8_t* ring = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    const int stage_bytes = p.wbytes + NT * 128;
+    const int tail = 16384 - p.wbytes;   // the last stage's product reads 128 rows of W, of which p.rows are its own
+    float* xs_sh = reinterpret_cast<float*>(ring + p.stages * stage_bytes + max(0, tail - NT * 128));
+    float* part = xs_sh + p.chunk * NT;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = static_cast<int>(blockIdx.x) % p.split, first = static_cast<int>(blockIdx.x) / p.split, step = static_cast<int>(gridDim.x) / p.split;
+    const int b0 = static_cast<int>(static_cast<int64_t>(p.kb) * rank / p.split), b1 = static_cast<int>(static_cast<int64_t>(p.kb) * (rank + 1) / p.split);
+    volatile int* dead = &bar.dead;
+
+    if (tid == 0) {
+        bar.dead = 0;
+        for (int i = 0; i < p.stages; ++i) {
+            mbar_init(&bar.full[i], 1);
+            mbar_init(&bar.empty[i], 1);
+        }
+        for (int i = 0; i < NB; ++i) {
+            mbar_init(&bar.dfull[i], 1);
+            mbar_init(&bar.dempty[i], 4);
+        }
+        fence_mbar_init();
+        prefetch_tensormap(&tmW);
+        prefetch_tensormap(&tmX);
+    }
+    if (warp == 5) tmem_alloc<1>(&bar.tmem, NB * NT);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bar.tmem;
+    const int ntile = first < p.tiles ? (p.tiles - first + step - 1) / step : 0, per = b1 - b0;
+    const int total = ntile * per;   // blocks of this CTA, in the order of all its warps
+    int issued = 0;                  // of them, by the loading thread
+
+    if (warp == 4) {
+        if (lane == 0) {
+            const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_last();
+            const uint32_t bytes = static_cast<uint32_t>(p.rows * 128 + NT * 128);
+            const uint32_t extra = blockIdx.x == 0 && (test_inject() & GEM_INJECT_RING_SHORTFALL) ? 16u : 0u;
+            auto load_w = [&](int i) {
+                const int s = i % p.stages, t = first + i / per * step, b = b0 + i % per;
+                mbar_arrive_expect_tx(&bar.full[s], bytes + (i == 0 ? extra : 0u));
+                tma_load_2d(ring + s * stage_bytes, &tmW, b * 128, t * p.rows, &bar.full[s], once);
+            };
+            auto load_x = [&](int i) {
+                const int s = i % p.stages;
+                tma_load_2d(ring + s * stage_bytes + p.wbytes, &tmX, (b0 + i % per) * 128, 0, &bar.full[s], keep);
+            };
+            // the first ring's weights before the wait (no launch writes weights), its rows of x behind it
+            const int ahead = min(total, p.stages);
+            for (int i = 0; i < ahead; ++i) load_w(i);
+            pdl_wait_trigger();
+            for (int i = 0; i < ahead; ++i) load_x(i);
+            for (issued = ahead; issued < total; ++issued) {
+                if (!mbar_wait(&bar.empty[issued % p.stages], static_cast<uint32_t>((issued / p.stages - 1) & 1), p.status) || *dead) break;
+                load_w(issued);
+                load_x(issued);
+            }
+            if (issued < total) *dead = 1;
+        }
+    } else if (warp == 5) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = umma_idesc_e4m3(128, NT);
+            int i = 0;
+            for (; i < total; ++i) {
+                const int s = i % p.stages, d = i % NB;
+                if (i >= NB && !mbar_wait(&bar.dempty[d], static_cast<uint32_t>((i / NB - 1) & 1), p.status)) break;
+                if (!mbar_wait(&bar.full[s], static_cast<uint32_t>((i / p.stages) & 1), p.status) || *dead) break;
+                tc_fence_after();
+                const uint32_t a = smem_u32(ring + s * stage_bytes);
+                const uint64_t da = umma_desc(a), db = umma_desc(a + p.wbytes);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) umma_e4m3<1>(tmem + d * NT, da + 2 * k, db + 2 * k, idesc, k > 0);
+                umma_commit<1>(&bar.empty[s]);
+                umma_commit<1>(&bar.dfull[d]);
+            }
+            if (i < total) {
+                *dead = 1;
+                // what was issued ends before the tensor memory is given back
+                if (i > 0) (void)mbar_wait(&bar.dfull[(i - 1) % NB], static_cast<uint32_t>(((i - 1) / NB) & 1), nullptr);
+            }
+        }
+        __syncwarp();
+    } else {
+        const int row = warp * 32 + lane;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        pdl_wait_trigger();
+        int i = 0;
+        bool ok = true;
+        for (int t = first; t < p.tiles; t += step) {
+            const int n = t * p.rows + row;
+            const bool mine = row < p.rows && n < p.N;
+            const float* wrow = p.ws + static_cast<int64_t>(min(n, p.N - 1) >> 7) * p.kb;
+            float acc[NT];
+#pragma unroll
+            for (int m = 0; m < NT; ++m) acc[m] = 0.f;
+            float w_next = per > 0 ? __ldg(wrow + b0) : 0.f;
+            for (int b = b0; b < b1; ++b, ++i) {
+                const int c = (b - b0) % p.chunk;
+                if (c == 0 && (per > p.chunk || t == first)) {   // the next blocks' x scales, turned to [block][row]
+                    const int nblk = min(p.chunk, b1 - b);
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    for (int e = tid; e < NT * nblk; e += 128) {
+                        const int m = e / nblk, q = e - m * nblk;
+                        xs_sh[q * NT + m] = m < p.M ? __ldg(p.xs + m * p.ldxs + b + q) : 0.f;
+                    }
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                }
+                const float w = w_next;
+                if (b + 1 < b1) w_next = __ldg(wrow + b + 1);
+                const int d = i % NB;
+                if (ok && (!mbar_wait(&bar.dfull[d], static_cast<uint32_t>((i / NB) & 1), p.status) || *dead)) {
+                    *dead = 1;
+                    ok = false;
+                }
+                ok = __all_sync(~0u, ok);
+                if (!ok) continue;   // keeps to the barriers above
+                tc_fence_after();
+                const float4* sx = reinterpret_cast<const float4*>(xs_sh + c * NT);
+#pragma unroll
+                for (int g = 0; g < NT; g += 16) {
+                    float v[16];
+                    tmem_ld16(v, lanes + d * NT + g);
+                    tmem_wait_ld();
+                    if (g + 16 == NT) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar.dempty[d]);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float4 x4 = sx[g / 4 + q];
+                        acc[g + 4 * q + 0] = fmaf(v[4 * q + 0], x4.x * w, acc[g + 4 * q + 0]);
+                        acc[g + 4 * q + 1] = fmaf(v[4 * q + 1], x4.y * w, acc[g + 4 * q + 1]);
+                        acc[g + 4 * q + 2] = fmaf(v[4 * q + 2], x4.z * w, acc[g + 4 * q + 2]);
+                        acc[g + 4 * q + 3] = fmaf(v[4 * q + 3], x4.w * w, acc[g + 4 * q + 3]);
+                    }
+                }
+            }
+            if (p.split > 1) {
+#pragma unroll
+                for (int m = 0; m < NT; ++m)
+                    if (m < p.M) part[m * 128 + row] = acc[m];
+            } else if (mine && ok) {
+#pragma unroll
+                for (int m = 0; m < NT; ++m)
+                    if (m < p.M) {
+                        const int64_t at = m * p.ldy + n;
+                        p.y[at] = p.res ? acc[m] + p.res[at] : acc[m];
+                    }
+            }
+        }
+    }
+    __syncwarp();
+    if (p.split > 1) {
+        // the cluster's CTAs hold one tile's sums; each adds up a share of the rows of x, in order of k
+        cluster_sync();
+        if (warp < 4) {
+            const int row = warp * 32 + lane, n = first * p.rows + row;
+            if (row < p.rows && n < p.N)
+                for (int m = rank; m < p.M; m += p.split) {
+                    float v = 0.f;
+                    for (int r = 0; r < p.split; ++r) v += ld_peer(peer_addr(&part[m * 128 + row], r));
+                    const int64_t at = m * p.ldy + n;
+                    p.y[at] = p.res ? v + p.res[at] : v;
+                }
+        }
+        __syncwarp();
+        cluster_sync();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (*dead && tid == 128) drain_stages(bar.full, p.stages, max(0, issued - p.stages), issued - 1);
+    if (warp == 5) {
+        tc_fence_after();
+        tmem_free<1>(tmem, NB * NT);
+    }
 }
 
-// 64 x 64 results a CTA, 4 x 4 a thread; 16 of K at a time through shared memory.
-__global__ void __launch_bounds__(256) fp8_gemm_kernel(const GemmParams p) {
-    __shared__ float a[16][65], b[16][65];
-    pdl_wait_trigger();
-    const int m0 = blockIdx.y * 64, n0 = blockIdx.x * 64, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {}, part[4][4] = {};
-    for (int k0 = 0; k0 < p.K; k0 += 16) {
-        for (int i = threadIdx.x; i < 1024; i += 256) {
-            const int r = i >> 4, k = i & 15;
-            a[k][r] = m0 + r < p.M ? e4m3(p.x[(m0 + r) * p.ldx + k0 + k]) : 0.f;
-            b[k][r] = n0 + r < p.N ? e4m3(p.W[static_cast<int64_t>(n0 + r) * p.K + k0 + k]) : 0.f;
+gem_status ensure_smem(const void* fn, int device, size_t bytes) {
+    static std::mutex mu;
+    static std::map<std::pair<int, const void*>, size_t> done;
+    std::lock_guard<std::mutex> lk(mu);
+    size_t& have = done[{device, fn}];
+    if (have >= bytes) return GEM_OK;
+    GEM_CUDA_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)));
+    have = bytes;
+    return GEM_OK;
+}
+
+template <int NT>
+gem_status launch_rows(GemmParams p, const void* W, int64_t K, const void* x, int64_t ldx, const DeviceInfo& di, cudaStream_t stream) {
+    gem_status st;
+    // Rows a tile and CTAs a tile: the fewest block-rows on the busiest SM.
+    p.split = 1;
+    p.rows = 128;
+    double best = 1e30;
+    for (int s : {1, 2, 4}) {
+        if (s > 1 && p.kb < 4 * s) break;
+        for (int r = 128; r >= 8; r -= 8) {
+            const int64_t tiles = (p.N + r - 1) / r;
+            if (s > 1 && tiles * s > di.num_sms / 4 * 4 - 8) continue;   // one round of clusters
+            const int64_t rounds = (tiles * s + di.num_sms - 1) / di.num_sms;
+            const double cost = static_cast<double>(rounds) * ((p.kb + s - 1) / s) * std::max(r, 40) + (s > 1 ? 200.0 : 0.0);
+            if (cost < best * 0.999) {
+                best = cost;
+                p.rows = r;
+                p.split = s;
+            }
         }
-        __syncthreads();
-        for (int k = 0; k < 16; ++k)
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) part[i][j] = fmaf(a[k][ty + 16 * i], b[k][tx + 16 * j], part[i][j]);
-        __syncthreads();
-        if ((k0 + 16) % 128 == 0 || k0 + 16 == p.K)
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) {
-                    const int m = min(m0 + ty + 16 * i, p.M - 1), n = min(n0 + tx + 16 * j, p.N - 1);
-                    acc[i][j] = fmaf(part[i][j], p.xs[m * p.ldxs + k0 / 128] * p.ws[static_cast<int64_t>(n / 128) * p.kb + k0 / 128], acc[i][j]);
-                    part[i][j] = 0.f;
-                }
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-            if (m < p.M && n < p.N) p.y[m * p.ldy + n] = acc[i][j] + (p.res ? p.res[m * p.ldy + n] : 0.f);
-        }
+    p.tiles = (p.N + p.rows - 1) / p.rows;
+    p.wbytes = (p.rows * 128 + 1023) / 1024 * 1024;
+    const int per = (p.kb + p.split - 1) / p.split;
+    p.chunk = std::min(per, kScaleBytes / (NT * 4));
+    const int stage = p.wbytes + NT * 128, after = std::max(0, 16384 - stage);
+    const int fixed = 1024 + after + p.chunk * NT * 4 + (p.split > 1 ? NT * 512 : 0) + static_cast<int>(sizeof(RowsBarriers)) + 1024;
+    const int64_t grid = p.split > 1 ? int64_t(p.tiles) * p.split : std::min<int64_t>(p.tiles, di.num_sms);
+    const int64_t blocks = per * ((int64_t(p.tiles) * p.split + grid - 1) / grid);   // of the busiest CTA
+    p.stages = static_cast<int>(std::min<int64_t>(std::min<int64_t>(kMaxStages, blocks), (static_cast<int64_t>(di.smem_optin) - fixed) / stage));
+    const size_t smem = static_cast<size_t>(1024 + p.stages * stage + after + p.chunk * NT * 4 + (p.split > 1 ? NT * 512 : 0));
+    CUtensorMap tmW, tmX;
+    if ((st = make_tensor_map_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, W, K, p.N, K, 128, p.rows, CU_TENSOR_MAP_SWIZZLE_128B)) != GEM_OK) return st;
+    if ((st = make_tensor_map_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, K, p.M, ldx, 128, NT, CU_TENSOR_MAP_SWIZZLE_128B)) != GEM_OK) return st;
+    const void* fn = reinterpret_cast<const void*>(fp8_rows_kernel<NT>);
+    if ((st = ensure_smem(fn, di.device, smem)) != GEM_OK) return st;
+    void* args[] = {&tmW, &tmX, &p};
+    return launch_pdl_cluster(fn, dim3(static_cast<unsigned>(grid)), dim3(kRowsThreads), smem, stream, args, p.split);
 }
 
 }  // namespace
@@ -62,7 +289,7 @@ extern "C" {
 
 gem_status gem_fp8_gemm(const void* W, const float* ws, int64_t N, int64_t K, const void* x, int64_t ldx,
                         const float* xs, int64_t ldxs, int64_t M, float* y, int64_t ldy, const float* residual,
-                        int32_t* status, void* stream) {
+                        int32_t* status, void* stream_v) {
     using namespace gem;
     if (M < 0 || N < 0 || K < 0) return GEM_ERR_INVALID_ARG;
     constexpr int64_t lim = (int64_t(1) << 31) - 512;
@@ -78,24 +305,26 @@ gem_status gem_fp8_gemm(const void* W, const float* ws, int64_t N, int64_t K, co
     gem_status st;
     if ((st = device_info(&di)) != GEM_OK) return st;
     GemmParams p{};
-    p.W = static_cast<const uint8_t*>(W);
     p.ws = ws;
     p.N = static_cast<int>(N);
-    p.K = static_cast<int>(K);
-    p.M = static_cast<int>(M);
     p.kb = static_cast<int>((K + 127) / 128);
-    p.x = static_cast<const uint8_t*>(x);
-    p.ldx = ldx;
-    p.xs = xs;
     p.ldxs = ldxs;
-    p.y = y;
     p.ldy = ldy;
-    p.res = residual;
     p.status = status ? status : di.status_word;
-    void* args[] = {&p};
-    return launch_pdl(reinterpret_cast<const void*>(fp8_gemm_kernel),
-                      dim3(static_cast<unsigned>((N + 63) / 64), static_cast<unsigned>((M + 63) / 64)), dim3(256), 0,
-                      static_cast<cudaStream_t>(stream), args);
+    cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
+    for (int64_t m = 0; m < M; m += 128) {
+        p.M = static_cast<int>(std::min<int64_t>(128, M - m));
+        p.xs = xs + m * ldxs;
+        p.y = y + m * ldy;
+        p.res = residual ? residual + m * ldy : nullptr;
+        const uint8_t* xm = static_cast<const uint8_t*>(x) + m * ldx;
+        if (p.M <= 16) st = launch_rows<16>(p, W, K, xm, ldx, di, stream);
+        else if (p.M <= 32) st = launch_rows<32>(p, W, K, xm, ldx, di, stream);
+        else if (p.M <= 64) st = launch_rows<64>(p, W, K, xm, ldx, di, stream);
+        else st = launch_rows<128>(p, W, K, xm, ldx, di, stream);
+        if (st != GEM_OK) return st;
+    }
+    return GEM_OK;
 }
 
 }  // extern "C"
