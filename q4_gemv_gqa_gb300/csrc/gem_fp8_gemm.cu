@@ -35,28 +35,32 @@ struct GemmParams {
 // ---- few rows of x -----------------------------------------------------------------------------
 // Warps 0..3 scale and add (lane = row of W), warp 4 loads, warp 5 issues the products.
 constexpr int kRowsThreads = 192;
-constexpr int kMaxStages = 48;
+constexpr int kMaxStages = 24;
 constexpr int kScaleBytes = 24 << 10;
 
+// Blocks a ring stage and a tensor-memory buffer hold, and such buffers (of kGroup * NT columns, at most 512
+// together): the waits and the read-back latency of a step are paid once for kGroup blocks.
 template <int NT>
-constexpr int kRowsBuffers = NT >= 128 ? 4 : 8;   // of NT columns in tensor memory, at most 512
+constexpr int kGroup = NT <= 32 ? 4 : NT == 64 ? 2 : 1;
+template <int NT>
+constexpr int kBuffers = 4;
 
 struct RowsBarriers {
-    uint64_t full[kMaxStages], empty[kMaxStages], dfull[8], dempty[8];
+    uint64_t full[kMaxStages], empty[kMaxStages], dfull[4], dempty[4];
     uint32_t tmem;
     int dead;
 };
 
 template <int NT>
 __global__ void __launch_bounds__(kRowsThreads) fp8_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const GemmParams p) {
-    constexpr int NB = kRowsBuffers<NT>;
+    constexpr int NB = kBuffers<NT>, J = kGroup<NT>, COLS = NB * J * NT;
     extern __shared__ uint8_t raw[];
     __shared__ RowsBarriers bar;
-    // the ring, 1024-byte aligned: W's rows, then x's rows; behind it the x scales and the cluster's sums
+    // the ring, 1024-byte aligned: for each block W's rows, then x's; behind it the x scales and the cluster's sums
     uint8_t* ring = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-    const int stage_bytes = p.wbytes + NT * 128;
-    const int tail = 16384 - p.wbytes;   // the last stage's product reads 128 rows of W, of which p.rows are its own
-    float* xs_sh = reinterpret_cast<float*>(ring + p.stages * stage_bytes + max(0, tail - NT * 128));
+    const int block_bytes = p.wbytes + NT * 128, stage_bytes = J * block_bytes;
+    // the last block's product reads 128 rows of W, of which p.rows are its own: the ring is followed by that much
+    float* xs_sh = reinterpret_cast<float*>(ring + p.stages * stage_bytes + max(0, 16384 - block_bytes));
     float* part = xs_sh + p.chunk * NT;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = static_cast<int>(blockIdx.x) % p.split, first = static_cast<int>(blockIdx.x) / p.split, step = static_cast<int>(gridDim.x) / p.split;
@@ -77,56 +81,70 @@ __global__ void __launch_bounds__(kRowsThreads) fp8_rows_kernel(const __grid_con
         prefetch_tensormap(&tmW);
         prefetch_tensormap(&tmX);
     }
-    if (warp == 5) tmem_alloc<1>(&bar.tmem, NB * NT);
+    if (warp == 5) tmem_alloc<1>(&bar.tmem, COLS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bar.tmem;
-    const int ntile = first < p.tiles ? (p.tiles - first + step - 1) / step : 0, per = b1 - b0;
-    const int total = ntile * per;   // blocks of this CTA, in the order of all its warps
-    int issued = 0;                  // of them, by the loading thread
+    // steps of up to J blocks of a tile, in the same order in all warps
+    const int ntile = first < p.tiles ? (p.tiles - first + step - 1) / step : 0;
+    const int total = ntile * ((b1 - b0 + J - 1) / J);
+    int issued = 0;   // by the loading thread
 
     if (warp == 4) {
         if (lane == 0) {
             const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_last();
-            const uint32_t bytes = static_cast<uint32_t>(p.rows * 128 + NT * 128);
             const uint32_t extra = blockIdx.x == 0 && (test_inject() & GEM_INJECT_RING_SHORTFALL) ? 16u : 0u;
-            auto load_w = [&](int i) {
-                const int s = i % p.stages, t = first + i / per * step, b = b0 + i % per;
-                mbar_arrive_expect_tx(&bar.full[s], bytes + (i == 0 ? extra : 0u));
-                tma_load_2d(ring + s * stage_bytes, &tmW, b * 128, t * p.rows, &bar.full[s], once);
+            // stage, row of W and block of the next load, counted up (a division would cost more than the load)
+            int ws = 0, wb = b0, wn = first * p.rows, xs = 0, xb = b0;
+            uint32_t phase = 1;
+            auto load_w = [&](uint32_t more) {
+                const int nj = min(J, b1 - wb);
+                mbar_arrive_expect_tx(&bar.full[ws], static_cast<uint32_t>(nj * (p.rows * 128 + NT * 128)) + more);
+                uint8_t* to = ring + ws * stage_bytes;
+                for (int j = 0; j < nj; ++j) tma_load_2d(to + j * block_bytes, &tmW, (wb + j) * 128, wn, &bar.full[ws], once);
+                if (++ws == p.stages) ws = 0, phase ^= 1;
+                if ((wb += J) >= b1) wb = b0, wn += step * p.rows;
             };
-            auto load_x = [&](int i) {
-                const int s = i % p.stages;
-                tma_load_2d(ring + s * stage_bytes + p.wbytes, &tmX, (b0 + i % per) * 128, 0, &bar.full[s], keep);
+            auto load_x = [&]() {
+                const int nj = min(J, b1 - xb);
+                uint8_t* to = ring + xs * stage_bytes + p.wbytes;
+                for (int j = 0; j < nj; ++j) tma_load_2d(to + j * block_bytes, &tmX, (xb + j) * 128, 0, &bar.full[xs], keep);
+                if (++xs == p.stages) xs = 0;
+                if ((xb += J) >= b1) xb = b0;
             };
             // the first ring's weights before the wait (no launch writes weights), its rows of x behind it
             const int ahead = min(total, p.stages);
-            for (int i = 0; i < ahead; ++i) load_w(i);
+            for (int i = 0; i < ahead; ++i) load_w(i == 0 ? extra : 0u);
             pdl_wait_trigger();
-            for (int i = 0; i < ahead; ++i) load_x(i);
+            for (int i = 0; i < ahead; ++i) load_x();
             for (issued = ahead; issued < total; ++issued) {
-                if (!mbar_wait(&bar.empty[issued % p.stages], static_cast<uint32_t>((issued / p.stages - 1) & 1), p.status) || *dead) break;
-                load_w(issued);
-                load_x(issued);
+                if (!mbar_wait(&bar.empty[ws], phase, p.status) || *dead) break;
+                load_w(0u);
+                load_x();
             }
             if (issued < total) *dead = 1;
         }
     } else if (warp == 5) {
         if (lane == 0) {
             constexpr uint32_t idesc = umma_idesc_e4m3(128, NT);
-            int i = 0;
+            int i = 0, s = 0, b = b0;
+            uint32_t phase = 0;
             for (; i < total; ++i) {
-                const int s = i % p.stages, d = i % NB;
+                const int d = i % NB, nj = min(J, b1 - b);
                 if (i >= NB && !mbar_wait(&bar.dempty[d], static_cast<uint32_t>((i / NB - 1) & 1), p.status)) break;
-                if (!mbar_wait(&bar.full[s], static_cast<uint32_t>((i / p.stages) & 1), p.status) || *dead) break;
+                if (!mbar_wait(&bar.full[s], phase, p.status) || *dead) break;
                 tc_fence_after();
-                const uint32_t a = smem_u32(ring + s * stage_bytes);
-                const uint64_t da = umma_desc(a), db = umma_desc(a + p.wbytes);
+                uint32_t a = smem_u32(ring + s * stage_bytes);
+                for (int j = 0; j < nj; ++j, a += block_bytes) {
+                    const uint64_t da = umma_desc(a), db = umma_desc(a + p.wbytes);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) umma_e4m3<1>(tmem + d * NT, da + 2 * k, db + 2 * k, idesc, k > 0);
+                    for (int k = 0; k < 4; ++k) umma_e4m3<1>(tmem + (d * J + j) * NT, da + 2 * k, db + 2 * k, idesc, k > 0);
+                }
                 umma_commit<1>(&bar.empty[s]);
                 umma_commit<1>(&bar.dfull[d]);
+                if (++s == p.stages) s = 0, phase ^= 1;
+                if ((b += J) >= b1) b = b0;
             }
             if (i < total) {
                 *dead = 1;
@@ -134,7 +152,6 @@ __global__ void __launch_bounds__(kRowsThreads) fp8_rows_kernel(const __grid_con
                 if (i > 0) (void)mbar_wait(&bar.dfull[(i - 1) % NB], static_cast<uint32_t>(((i - 1) / NB) & 1), nullptr);
             }
         }
-        __syncwarp();
     } else {
         const int row = warp * 32 + lane;
         const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
@@ -148,10 +165,13 @@ __global__ void __launch_bounds__(kRowsThreads) fp8_rows_kernel(const __grid_con
             float acc[NT];
 #pragma unroll
             for (int m = 0; m < NT; ++m) acc[m] = 0.f;
-            float w_next = per > 0 ? __ldg(wrow + b0) : 0.f;
-            for (int b = b0; b < b1; ++b, ++i) {
-                const int c = (b - b0) % p.chunk;
-                if (c == 0 && (per > p.chunk || t == first)) {   // the next blocks' x scales, turned to [block][row]
+            float w_next[J];
+#pragma unroll
+            for (int j = 0; j < J; ++j) w_next[j] = __ldg(wrow + min(b0 + j, p.kb - 1));
+            int c = p.chunk - J;
+            for (int b = b0; b < b1; b += J, ++i) {
+                if ((c += J) == p.chunk) c = 0;
+                if (c == 0 && (b1 - b0 > p.chunk || t == first)) {   // the next blocks' x scales, turned to [block][row]
                     const int nblk = min(p.chunk, b1 - b);
                     asm volatile("bar.sync 1, 128;" ::: "memory");
                     for (int e = tid; e < NT * nblk; e += 128) {
@@ -160,9 +180,13 @@ __global__ void __launch_bounds__(kRowsThreads) fp8_rows_kernel(const __grid_con
                     }
                     asm volatile("bar.sync 1, 128;" ::: "memory");
                 }
-                const float w = w_next;
-                if (b + 1 < b1) w_next = __ldg(wrow + b + 1);
-                const int d = i % NB;
+                float w[J];
+#pragma unroll
+                for (int j = 0; j < J; ++j) {
+                    w[j] = w_next[j];
+                    w_next[j] = __ldg(wrow + min(b + J + j, p.kb - 1));
+                }
+                const int d = i % NB, nj = min(J, b1 - b);
                 if (ok && (!mbar_wait(&bar.dfull[d], static_cast<uint32_t>((i / NB) & 1), p.status) || *dead)) {
                     *dead = 1;
                     ok = false;
@@ -170,24 +194,33 @@ __global__ void __launch_bounds__(kRowsThreads) fp8_rows_kernel(const __grid_con
                 ok = __all_sync(~0u, ok);
                 if (!ok) continue;   // keeps to the barriers above
                 tc_fence_after();
-                const float4* sx = reinterpret_cast<const float4*>(xs_sh + c * NT);
+                // 64 columns at a time: of one block, or of several (those that the step does not have are not used)
+                constexpr int C = J * NT < 64 ? J * NT : 64;
 #pragma unroll
-                for (int g = 0; g < NT; g += 16) {
-                    float v[16];
-                    tmem_ld16(v, lanes + d * NT + g);
+                for (int g = 0; g < J * NT; g += C) {
+                    float v[C / 16][16];
+#pragma unroll
+                    for (int u = 0; u < C / 16; ++u) tmem_ld16(v[u], lanes + d * J * NT + g + 16 * u);
                     tmem_wait_ld();
-                    if (g + 16 == NT) {
+                    if (g + C == J * NT) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&bar.dempty[d]);
                     }
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float4 x4 = sx[g / 4 + q];
-                        acc[g + 4 * q + 0] = fmaf(v[4 * q + 0], x4.x * w, acc[g + 4 * q + 0]);
-                        acc[g + 4 * q + 1] = fmaf(v[4 * q + 1], x4.y * w, acc[g + 4 * q + 1]);
-                        acc[g + 4 * q + 2] = fmaf(v[4 * q + 2], x4.z * w, acc[g + 4 * q + 2]);
-                        acc[g + 4 * q + 3] = fmaf(v[4 * q + 3], x4.w * w, acc[g + 4 * q + 3]);
+                    for (int u = 0; u < C / 16; ++u) {
+                        const int j = (g + 16 * u) / NT, m = (g + 16 * u) % NT;
+                        if (j < nj) {
+                            const float4* sx = reinterpret_cast<const float4*>(xs_sh + (c + j) * NT + m);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const float4 x4 = sx[q];
+                                acc[m + 4 * q + 0] = fmaf(v[u][4 * q + 0], x4.x * w[j], acc[m + 4 * q + 0]);
+                                acc[m + 4 * q + 1] = fmaf(v[u][4 * q + 1], x4.y * w[j], acc[m + 4 * q + 1]);
+                                acc[m + 4 * q + 2] = fmaf(v[u][4 * q + 2], x4.z * w[j], acc[m + 4 * q + 2]);
+                                acc[m + 4 * q + 3] = fmaf(v[u][4 * q + 3], x4.w * w[j], acc[m + 4 * q + 3]);
+                            }
+                        }
                     }
                 }
             }
@@ -227,7 +260,7 @@ __global__ void __launch_bounds__(kRowsThreads) fp8_rows_kernel(const __grid_con
     if (*dead && tid == 128) drain_stages(bar.full, p.stages, max(0, issued - p.stages), issued - 1);
     if (warp == 5) {
         tc_fence_after();
-        tmem_free<1>(tmem, NB * NT);
+        tmem_free<1>(tmem, COLS);
     }
 }
 
@@ -266,13 +299,15 @@ gem_status launch_rows(GemmParams p, const void* W, int64_t K, const void* x, in
     p.tiles = (p.N + p.rows - 1) / p.rows;
     p.wbytes = (p.rows * 128 + 1023) / 1024 * 1024;
     const int per = (p.kb + p.split - 1) / p.split;
-    p.chunk = std::min(per, kScaleBytes / (NT * 4));
-    const int stage = p.wbytes + NT * 128, after = std::max(0, 16384 - stage);
-    const int fixed = 1024 + after + p.chunk * NT * 4 + (p.split > 1 ? NT * 512 : 0) + static_cast<int>(sizeof(RowsBarriers)) + 1024;
+    constexpr int J = kGroup<NT>;
+    p.chunk = std::min((per + J - 1) / J * J, kScaleBytes / (NT * 4));   // a multiple of J
+    const int block = p.wbytes + NT * 128, after = std::max(0, 16384 - block);
+    const int fixed = 1024 + after + p.chunk * NT * 4 + (p.split > 1 ? NT * 512 : 0);
     const int64_t grid = p.split > 1 ? int64_t(p.tiles) * p.split : std::min<int64_t>(p.tiles, di.num_sms);
-    const int64_t blocks = per * ((int64_t(p.tiles) * p.split + grid - 1) / grid);   // of the busiest CTA
-    p.stages = static_cast<int>(std::min<int64_t>(std::min<int64_t>(kMaxStages, blocks), (static_cast<int64_t>(di.smem_optin) - fixed) / stage));
-    const size_t smem = static_cast<size_t>(1024 + p.stages * stage + after + p.chunk * NT * 4 + (p.split > 1 ? NT * 512 : 0));
+    const int64_t steps = (per + J - 1) / J * ((int64_t(p.tiles) * p.split + grid - 1) / grid);   // of the busiest CTA
+    p.stages = static_cast<int>(std::min(std::min<int64_t>(kMaxStages, steps),
+                                         (static_cast<int64_t>(di.smem_optin) - fixed - static_cast<int>(sizeof(RowsBarriers)) - 512) / (J * block)));
+    const size_t smem = static_cast<size_t>(fixed + p.stages * J * block);
     CUtensorMap tmW, tmX;
     if ((st = make_tensor_map_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, W, K, p.N, K, 128, p.rows, CU_TENSOR_MAP_SWIZZLE_128B)) != GEM_OK) return st;
     if ((st = make_tensor_map_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, K, p.M, ldx, 128, NT, CU_TENSOR_MAP_SWIZZLE_128B)) != GEM_OK) return st;
