@@ -33,16 +33,17 @@ struct GemmParams {
 };
 
 // ---- few rows of x -----------------------------------------------------------------------------
-// Warps 0..3 scale and add (lane = row of W), warp 4 loads, warp 5 issues the products.
-constexpr int kRowsThreads = 192;
+// The last two warps load and issue the products; the others scale and add.  Of these, four times kWarps<NT>,
+// warp w has the rows of W of lane quarter w % 4 and columns w / 4 * NT / kWarps<NT> and on.
 constexpr int kMaxStages = 24;
 constexpr int kScaleBytes = 24 << 10;
 
-// Blocks a ring stage and a tensor-memory buffer hold, and such buffers (of kGroup * NT columns, at most 512
-// together): the waits and the read-back latency of a step are paid once for kGroup blocks.
+// Blocks a ring stage and a tensor-memory buffer hold, of four such buffers (kGroup * NT columns each, 512
+// together at most): the waits and the read-back latency of a step are paid once for kGroup blocks.
 template <int NT>
 constexpr int kGroup = NT <= 32 ? 4 : NT == 64 ? 2 : 1;
 template <int NT>
+constexpr int kWarps = NT <= 32 ? 2 : 4;
 constexpr int kBuffers = 4;
 
 struct RowsBarriers {
@@ -52,8 +53,8 @@ struct RowsBarriers {
 };
 
 template <int NT>
-__global__ void __launch_bounds__(kRowsThreads) fp8_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const GemmParams p) {
-    constexpr int NB = kBuffers<NT>, J = kGroup<NT>, COLS = NB * J * NT;
+__global__ void __launch_bounds__(kWarps<NT> * 128 + 64) fp8_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const GemmParams p) {
+    constexpr int NB = kBuffers, J = kGroup<NT>, COLS = NB * J * NT, Q = kWarps<NT>, CW = NT / Q;
     extern __shared__ uint8_t raw[];
     __shared__ RowsBarriers bar;
     // the ring, 1024-byte aligned: for each block W's rows, then x's; behind it the x scales and the cluster's sums
@@ -75,13 +76,13 @@ __global__ void __launch_bounds__(kRowsThreads) fp8_rows_kernel(const __grid_con
         }
         for (int i = 0; i < NB; ++i) {
             mbar_init(&bar.dfull[i], 1);
-            mbar_init(&bar.dempty[i], 4);
+            mbar_init(&bar.dempty[i], 4 * Q);
         }
         fence_mbar_init();
         prefetch_tensormap(&tmW);
         prefetch_tensormap(&tmX);
     }
-    if (warp == 5) tmem_alloc<1>(&bar.tmem, COLS);
+    if (warp == 4 * Q + 1) tmem_alloc<1>(&bar.tmem, COLS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -89,72 +90,70 @@ __global__ void __launch_bounds__(kRowsThreads) fp8_rows_kernel(const __grid_con
     // steps of up to J blocks of a tile, in the same order in all warps
     const int ntile = first < p.tiles ? (p.tiles - first + step - 1) / step : 0;
     const int total = ntile * ((b1 - b0 + J - 1) / J);
-    int issued = 0;   // by the loading thread
+    int issued = 0;   // by the loading warp
 
-    if (warp == 4) {
-        if (lane == 0) {
-            const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_last();
-            const uint32_t extra = blockIdx.x == 0 && (test_inject() & GEM_INJECT_RING_SHORTFALL) ? 16u : 0u;
-            // stage, row of W and block of the next load, counted up (a division would cost more than the load)
-            int ws = 0, wb = b0, wn = first * p.rows, xs = 0, xb = b0;
-            uint32_t phase = 1;
-            auto load_w = [&](uint32_t more) {
-                const int nj = min(J, b1 - wb);
-                mbar_arrive_expect_tx(&bar.full[ws], static_cast<uint32_t>(nj * (p.rows * 128 + NT * 128)) + more);
-                uint8_t* to = ring + ws * stage_bytes;
-                for (int j = 0; j < nj; ++j) tma_load_2d(to + j * block_bytes, &tmW, (wb + j) * 128, wn, &bar.full[ws], once);
-                if (++ws == p.stages) ws = 0, phase ^= 1;
-                if ((wb += J) >= b1) wb = b0, wn += step * p.rows;
-            };
-            auto load_x = [&]() {
-                const int nj = min(J, b1 - xb);
-                uint8_t* to = ring + xs * stage_bytes + p.wbytes;
-                for (int j = 0; j < nj; ++j) tma_load_2d(to + j * block_bytes, &tmX, (xb + j) * 128, 0, &bar.full[xs], keep);
-                if (++xs == p.stages) xs = 0;
-                if ((xb += J) >= b1) xb = b0;
-            };
-            // the first ring's weights before the wait (no launch writes weights), its rows of x behind it
-            const int ahead = min(total, p.stages);
-            for (int i = 0; i < ahead; ++i) load_w(i == 0 ? extra : 0u);
-            pdl_wait_trigger();
-            for (int i = 0; i < ahead; ++i) load_x();
-            for (issued = ahead; issued < total; ++issued) {
-                if (!mbar_wait(&bar.empty[ws], phase, p.status) || *dead) break;
-                load_w(0u);
-                load_x();
-            }
-            if (issued < total) *dead = 1;
+    if (warp == 4 * Q) {
+        const uint64_t once = l2_policy_evict_first(), keep = l2_policy_evict_last();
+        const uint32_t extra = blockIdx.x == 0 && (test_inject() & GEM_INJECT_RING_SHORTFALL) ? 16u : 0u;
+        const uint32_t base = smem_u32(ring);
+        // stage, row of W and block of the next load, counted up (a division would cost more than the load)
+        int ws = 0, wb = b0, wn = first * p.rows, xs = 0, xb = b0;
+        uint32_t phase = 1;
+        auto load_w = [&](uint32_t more) {
+            const int nj = min(J, b1 - wb);
+            warp_expect_tx(&bar.full[ws], static_cast<uint32_t>(nj * (p.rows * 128 + NT * 128)) + more);
+            const uint32_t to = base + ws * stage_bytes;
+            for (int j = 0; j < nj; ++j) warp_tma_2d(to + j * block_bytes, &tmW, (wb + j) * 128, wn, &bar.full[ws], once);
+            if (++ws == p.stages) ws = 0, phase ^= 1;
+            if ((wb += J) >= b1) wb = b0, wn += step * p.rows;
+        };
+        auto load_x = [&]() {
+            const int nj = min(J, b1 - xb);
+            const uint32_t to = base + xs * stage_bytes + p.wbytes;
+            for (int j = 0; j < nj; ++j) warp_tma_2d(to + j * block_bytes, &tmX, (xb + j) * 128, 0, &bar.full[xs], keep);
+            if (++xs == p.stages) xs = 0;
+            if ((xb += J) >= b1) xb = b0;
+        };
+        // the first ring's weights before the wait (no launch writes weights), its rows of x behind it
+        const int ahead = min(total, p.stages);
+        for (int i = 0; i < ahead; ++i) load_w(i == 0 ? extra : 0u);
+        pdl_wait_trigger();
+        for (int i = 0; i < ahead; ++i) load_x();
+        for (issued = ahead; issued < total; ++issued) {
+            if (!warp_wait(&bar.empty[ws], phase, p.status, dead)) break;
+            load_w(0u);
+            load_x();
         }
-    } else if (warp == 5) {
-        if (lane == 0) {
-            constexpr uint32_t idesc = umma_idesc_e4m3(128, NT);
-            int i = 0, s = 0, b = b0;
-            uint32_t phase = 0;
-            for (; i < total; ++i) {
-                const int d = i % NB, nj = min(J, b1 - b);
-                if (i >= NB && !mbar_wait(&bar.dempty[d], static_cast<uint32_t>((i / NB - 1) & 1), p.status)) break;
-                if (!mbar_wait(&bar.full[s], phase, p.status) || *dead) break;
-                tc_fence_after();
-                uint32_t a = smem_u32(ring + s * stage_bytes);
-                for (int j = 0; j < nj; ++j, a += block_bytes) {
-                    const uint64_t da = umma_desc(a), db = umma_desc(a + p.wbytes);
+        if (issued < total) *dead = 1;
+    } else if (warp == 4 * Q + 1) {
+        constexpr uint32_t idesc = umma_idesc_e4m3(128, NT);
+        const uint32_t base = smem_u32(ring);
+        int i = 0, s = 0, b = b0;
+        uint32_t phase = 0;
+        for (; i < total; ++i) {
+            const int d = i % NB, nj = min(J, b1 - b);
+            if (i >= NB && !warp_wait(&bar.dempty[d], static_cast<uint32_t>((i / NB - 1) & 1), p.status, dead)) break;
+            if (!warp_wait(&bar.full[s], phase, p.status, dead)) break;
+            tc_fence_after();
+            uint32_t a = base + s * stage_bytes;
+            for (int j = 0; j < nj; ++j, a += block_bytes) {
+                const uint64_t da = umma_desc(a), db = umma_desc(a + p.wbytes);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) umma_e4m3<1>(tmem + (d * J + j) * NT, da + 2 * k, db + 2 * k, idesc, k > 0);
-                }
-                umma_commit<1>(&bar.empty[s]);
-                umma_commit<1>(&bar.dfull[d]);
-                if (++s == p.stages) s = 0, phase ^= 1;
-                if ((b += J) >= b1) b = b0;
+                for (int k = 0; k < 4; ++k) umma_e4m3<1>(tmem + (d * J + j) * NT, da + 2 * k, db + 2 * k, idesc, k > 0);
             }
-            if (i < total) {
-                *dead = 1;
-                // what was issued ends before the tensor memory is given back
-                if (i > 0) (void)mbar_wait(&bar.dfull[(i - 1) % NB], static_cast<uint32_t>(((i - 1) / NB) & 1), nullptr);
-            }
+            umma_commit<1>(&bar.empty[s]);
+            umma_commit<1>(&bar.dfull[d]);
+            if (++s == p.stages) s = 0, phase ^= 1;
+            if ((b += J) >= b1) b = b0;
+        }
+        if (i < total) {
+            *dead = 1;
+            // what was issued ends before the tensor memory is given back
+            if (i > 0) (void)mbar_wait(&bar.dfull[(i - 1) % NB], static_cast<uint32_t>(((i - 1) / NB) & 1), nullptr);
         }
     } else {
-        const int row = warp * 32 + lane;
-        const uint32_t lanes = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        const int row = (warp & 3) * 32 + lane, col = (warp >> 2) * CW;
+        const uint32_t from = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + col;
         pdl_wait_trigger();
         int i = 0;
         bool ok = true;
@@ -162,9 +161,9 @@ __global__ void __launch_bounds__(kRowsThreads) fp8_rows_kernel(const __grid_con
             const int n = t * p.rows + row;
             const bool mine = row < p.rows && n < p.N;
             const float* wrow = p.ws + static_cast<int64_t>(min(n, p.N - 1) >> 7) * p.kb;
-            float acc[NT];
+            float acc[CW];
 #pragma unroll
-            for (int m = 0; m < NT; ++m) acc[m] = 0.f;
+            for (int m = 0; m < CW; ++m) acc[m] = 0.f;
             float w_next[J];
 #pragma unroll
             for (int j = 0; j < J; ++j) w_next[j] = __ldg(wrow + min(b0 + j, p.kb - 1));
@@ -173,12 +172,12 @@ __global__ void __launch_bounds__(kRowsThreads) fp8_rows_kernel(const __grid_con
                 if ((c += J) == p.chunk) c = 0;
                 if (c == 0 && (b1 - b0 > p.chunk || t == first)) {   // the next blocks' x scales, turned to [block][row]
                     const int nblk = min(p.chunk, b1 - b);
-                    asm volatile("bar.sync 1, 128;" ::: "memory");
-                    for (int e = tid; e < NT * nblk; e += 128) {
+                    asm volatile("bar.sync 1, %0;" ::"n"(Q * 128) : "memory");
+                    for (int e = tid; e < NT * nblk; e += Q * 128) {
                         const int m = e / nblk, q = e - m * nblk;
                         xs_sh[q * NT + m] = m < p.M ? __ldg(p.xs + m * p.ldxs + b + q) : 0.f;
                     }
-                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                    asm volatile("bar.sync 1, %0;" ::"n"(Q * 128) : "memory");
                 }
                 float w[J];
 #pragma unroll
@@ -187,52 +186,43 @@ __global__ void __launch_bounds__(kRowsThreads) fp8_rows_kernel(const __grid_con
                     w_next[j] = __ldg(wrow + min(b + J + j, p.kb - 1));
                 }
                 const int d = i % NB, nj = min(J, b1 - b);
-                if (ok && (!mbar_wait(&bar.dfull[d], static_cast<uint32_t>((i / NB) & 1), p.status) || *dead)) {
+                if (ok && !warp_wait(&bar.dfull[d], static_cast<uint32_t>((i / NB) & 1), p.status, dead)) {
                     *dead = 1;
                     ok = false;
                 }
-                ok = __all_sync(~0u, ok);
                 if (!ok) continue;   // keeps to the barriers above
                 tc_fence_after();
-                // 64 columns at a time: of one block, or of several (those that the step does not have are not used)
-                constexpr int C = J * NT < 64 ? J * NT : 64;
+                // columns of blocks that the step does not have are read and not used
+                float v[J][CW];
 #pragma unroll
-                for (int g = 0; g < J * NT; g += C) {
-                    float v[C / 16][16];
+                for (int j = 0; j < J; ++j) tmem_ld<CW>(v[j], from + (d * J + j) * NT);
+                tmem_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.dempty[d]);
 #pragma unroll
-                    for (int u = 0; u < C / 16; ++u) tmem_ld16(v[u], lanes + d * J * NT + g + 16 * u);
-                    tmem_wait_ld();
-                    if (g + C == J * NT) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar.dempty[d]);
-                    }
+                for (int j = 0; j < J; ++j)
+                    if (j < nj) {
+                        const float4* sx = reinterpret_cast<const float4*>(xs_sh + (c + j) * NT + col);
 #pragma unroll
-                    for (int u = 0; u < C / 16; ++u) {
-                        const int j = (g + 16 * u) / NT, m = (g + 16 * u) % NT;
-                        if (j < nj) {
-                            const float4* sx = reinterpret_cast<const float4*>(xs_sh + (c + j) * NT + m);
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const float4 x4 = sx[q];
-                                acc[m + 4 * q + 0] = fmaf(v[u][4 * q + 0], x4.x * w[j], acc[m + 4 * q + 0]);
-                                acc[m + 4 * q + 1] = fmaf(v[u][4 * q + 1], x4.y * w[j], acc[m + 4 * q + 1]);
-                                acc[m + 4 * q + 2] = fmaf(v[u][4 * q + 2], x4.z * w[j], acc[m + 4 * q + 2]);
-                                acc[m + 4 * q + 3] = fmaf(v[u][4 * q + 3], x4.w * w[j], acc[m + 4 * q + 3]);
-                            }
+                        for (int q = 0; q < CW / 4; ++q) {
+                            const float4 x4 = sx[q];
+                            acc[4 * q + 0] = fmaf(v[j][4 * q + 0], x4.x * w[j], acc[4 * q + 0]);
+                            acc[4 * q + 1] = fmaf(v[j][4 * q + 1], x4.y * w[j], acc[4 * q + 1]);
+                            acc[4 * q + 2] = fmaf(v[j][4 * q + 2], x4.z * w[j], acc[4 * q + 2]);
+                            acc[4 * q + 3] = fmaf(v[j][4 * q + 3], x4.w * w[j], acc[4 * q + 3]);
                         }
                     }
-                }
             }
             if (p.split > 1) {
 #pragma unroll
-                for (int m = 0; m < NT; ++m)
-                    if (m < p.M) part[m * 128 + row] = acc[m];
+                for (int m = 0; m < CW; ++m)
+                    if (col + m < p.M) part[(col + m) * 128 + row] = acc[m];
             } else if (mine && ok) {
 #pragma unroll
-                for (int m = 0; m < NT; ++m)
-                    if (m < p.M) {
-                        const int64_t at = m * p.ldy + n;
+                for (int m = 0; m < CW; ++m)
+                    if (col + m < p.M) {
+                        const int64_t at = (col + m) * p.ldy + n;
                         p.y[at] = p.res ? acc[m] + p.res[at] : acc[m];
                     }
             }
@@ -242,10 +232,10 @@ __global__ void __launch_bounds__(kRowsThreads) fp8_rows_kernel(const __grid_con
     if (p.split > 1) {
         // the cluster's CTAs hold one tile's sums; each adds up a share of the rows of x, in order of k
         cluster_sync();
-        if (warp < 4) {
-            const int row = warp * 32 + lane, n = first * p.rows + row;
+        if (warp < 4 * Q) {
+            const int row = (warp & 3) * 32 + lane, n = first * p.rows + row;
             if (row < p.rows && n < p.N)
-                for (int m = rank; m < p.M; m += p.split) {
+                for (int m = rank + p.split * (warp >> 2); m < p.M; m += p.split * Q) {
                     float v = 0.f;
                     for (int r = 0; r < p.split; ++r) v += ld_peer(peer_addr(&part[m * 128 + row], r));
                     const int64_t at = m * p.ldy + n;
@@ -257,8 +247,8 @@ __global__ void __launch_bounds__(kRowsThreads) fp8_rows_kernel(const __grid_con
     }
     tc_fence_before();
     __syncthreads();
-    if (*dead && tid == 128) drain_stages(bar.full, p.stages, max(0, issued - p.stages), issued - 1);
-    if (warp == 5) {
+    if (*dead && warp == 4 * Q && lane == 0) drain_stages(bar.full, p.stages, max(0, issued - p.stages), issued - 1);
+    if (warp == 4 * Q + 1) {
         tc_fence_after();
         tmem_free<1>(tmem, COLS);
     }
@@ -314,7 +304,7 @@ gem_status launch_rows(GemmParams p, const void* W, int64_t K, const void* x, in
     const void* fn = reinterpret_cast<const void*>(fp8_rows_kernel<NT>);
     if ((st = ensure_smem(fn, di.device, smem)) != GEM_OK) return st;
     void* args[] = {&tmW, &tmX, &p};
-    return launch_pdl_cluster(fn, dim3(static_cast<unsigned>(grid)), dim3(kRowsThreads), smem, stream, args, p.split);
+    return launch_pdl_cluster(fn, dim3(static_cast<unsigned>(grid)), dim3(kWarps<NT> * 128 + 64), smem, stream, args, p.split);
 }
 
 }  // namespace
