@@ -27,7 +27,8 @@ struct GemmParams {
     int N, M, kb;
     int rows, tiles;        // rows of W a tile, tiles
     int split;              // CTAs of a cluster that share a tile's blocks
-    int stages, wbytes;     // ring stages, bytes of W in one
+    int stages;             // of the ring
+    int whole;              // K is a multiple of 128: one copy brings a step's blocks
     int chunk;              // blocks whose x scales are held at a time
     int* status;
 };
@@ -45,6 +46,8 @@ constexpr int kGroup = NT <= 32 ? 4 : NT == 64 ? 2 : 1;
 template <int NT>
 constexpr int kWarps = NT <= 32 ? 2 : 4;
 constexpr int kBuffers = 4;
+template <int NT>
+constexpr int kPitch = NT + 4;   // of the x scales of a block: spreads a column's stores over the banks
 
 struct RowsBarriers {
     uint64_t full[kMaxStages], empty[kMaxStages], dfull[4], dempty[4];
@@ -54,18 +57,19 @@ struct RowsBarriers {
 
 template <int NT>
 __global__ void __launch_bounds__(kWarps<NT> * 128 + 64) fp8_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const GemmParams p) {
-    constexpr int NB = kBuffers, J = kGroup<NT>, COLS = NB * J * NT, Q = kWarps<NT>, CW = NT / Q;
+    constexpr int NB = kBuffers, J = kGroup<NT>, COLS = NB * J * NT, Q = kWarps<NT>, CW = NT / Q, XP = kPitch<NT>;
     extern __shared__ uint8_t raw[];
     __shared__ RowsBarriers bar;
-    // the ring, 1024-byte aligned: for each block W's rows, then x's; behind it the x scales and the cluster's sums
+    // the ring, 1024-byte aligned: a stage's blocks of W, then those of x; behind it the x scales and the cluster's sums
     uint8_t* ring = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-    const int block_bytes = p.wbytes + NT * 128, stage_bytes = J * block_bytes;
-    // the last block's product reads 128 rows of W, of which p.rows are its own: the ring is followed by that much
-    float* xs_sh = reinterpret_cast<float*>(ring + p.stages * stage_bytes + max(0, 16384 - block_bytes));
-    float* part = xs_sh + p.chunk * NT;
+    const int wbytes = p.rows * 128, stage_bytes = J * (wbytes + NT * 128);
+    // a product reads 128 rows of W, of which p.rows are its own: the ring is followed by what that may be past its end
+    float* xs_sh = reinterpret_cast<float*>(ring + p.stages * stage_bytes + max(0, 16384 - wbytes - J * NT * 128));
+    float* part = xs_sh + p.chunk * XP;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = static_cast<int>(blockIdx.x) % p.split, first = static_cast<int>(blockIdx.x) / p.split, step = static_cast<int>(gridDim.x) / p.split;
-    const int b0 = static_cast<int>(static_cast<int64_t>(p.kb) * rank / p.split), b1 = static_cast<int>(static_cast<int64_t>(p.kb) * (rank + 1) / p.split);
+    const int groups = (p.kb + J - 1) / J;
+    const int b0 = groups * rank / p.split * J, b1 = min(p.kb, groups * (rank + 1) / p.split * J);   // this CTA's blocks
     volatile int* dead = &bar.dead;
 
     if (tid == 0) {
@@ -100,17 +104,23 @@ __global__ void __launch_bounds__(kWarps<NT> * 128 + 64) fp8_rows_kernel(const _
         int ws = 0, wb = b0, wn = first * p.rows, xs = 0, xb = b0;
         uint32_t phase = 1;
         auto load_w = [&](uint32_t more) {
-            const int nj = min(J, b1 - wb);
-            warp_expect_tx(&bar.full[ws], static_cast<uint32_t>(nj * (p.rows * 128 + NT * 128)) + more);
+            const int nj = p.whole ? J : min(J, b1 - wb);
             const uint32_t to = base + ws * stage_bytes;
-            for (int j = 0; j < nj; ++j) warp_tma_2d(to + j * block_bytes, &tmW, (wb + j) * 128, wn, &bar.full[ws], once);
+            warp_expect_tx(&bar.full[ws], static_cast<uint32_t>(nj * (p.rows + NT) * 128) + more);
+            if (p.whole)
+                warp_tma_3d(to, &tmW, 0, wn, wb, &bar.full[ws], once);
+            else
+                for (int j = 0; j < nj; ++j) warp_tma_2d(to + j * wbytes, &tmW, (wb + j) * 128, wn, &bar.full[ws], once);
             if (++ws == p.stages) ws = 0, phase ^= 1;
             if ((wb += J) >= b1) wb = b0, wn += step * p.rows;
         };
         auto load_x = [&]() {
             const int nj = min(J, b1 - xb);
-            const uint32_t to = base + xs * stage_bytes + p.wbytes;
-            for (int j = 0; j < nj; ++j) warp_tma_2d(to + j * block_bytes, &tmX, (xb + j) * 128, 0, &bar.full[xs], keep);
+            const uint32_t to = base + xs * stage_bytes + J * wbytes;
+            if (p.whole)
+                warp_tma_3d(to, &tmX, 0, 0, xb, &bar.full[xs], keep);
+            else
+                for (int j = 0; j < nj; ++j) warp_tma_2d(to + j * NT * 128, &tmX, (xb + j) * 128, 0, &bar.full[xs], keep);
             if (++xs == p.stages) xs = 0;
             if ((xb += J) >= b1) xb = b0;
         };
@@ -127,7 +137,8 @@ __global__ void __launch_bounds__(kWarps<NT> * 128 + 64) fp8_rows_kernel(const _
         if (issued < total) *dead = 1;
     } else if (warp == 4 * Q + 1) {
         constexpr uint32_t idesc = umma_idesc_e4m3(128, NT);
-        const uint32_t base = smem_u32(ring);
+        const uint64_t da0 = umma_desc(smem_u32(ring)), db0 = umma_desc(smem_u32(ring) + J * wbytes);
+        uint64_t da = da0, db = db0;
         int i = 0, s = 0, b = b0;
         uint32_t phase = 0;
         for (; i < total; ++i) {
@@ -135,15 +146,13 @@ __global__ void __launch_bounds__(kWarps<NT> * 128 + 64) fp8_rows_kernel(const _
             if (i >= NB && !warp_wait(&bar.dempty[d], static_cast<uint32_t>((i / NB - 1) & 1), p.status, dead)) break;
             if (!warp_wait(&bar.full[s], phase, p.status, dead)) break;
             tc_fence_after();
-            uint32_t a = base + s * stage_bytes;
-            for (int j = 0; j < nj; ++j, a += block_bytes) {
-                const uint64_t da = umma_desc(a), db = umma_desc(a + p.wbytes);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) umma_e4m3<1>(tmem + (d * J + j) * NT, da + 2 * k, db + 2 * k, idesc, k > 0);
-            }
+            for (int j = 0; j < J; ++j)
+                if (j < nj) umma_e4m3<1>(tmem + (d * J + j) * NT, da + j * (wbytes >> 4), db + j * NT * 8, idesc);
             umma_commit<1>(&bar.empty[s]);
             umma_commit<1>(&bar.dfull[d]);
-            if (++s == p.stages) s = 0, phase ^= 1;
+            da += stage_bytes >> 4, db += stage_bytes >> 4;
+            if (++s == p.stages) s = 0, phase ^= 1, da = da0, db = db0;
             if ((b += J) >= b1) b = b0;
         }
         if (i < total) {
@@ -161,9 +170,9 @@ __global__ void __launch_bounds__(kWarps<NT> * 128 + 64) fp8_rows_kernel(const _
             const int n = t * p.rows + row;
             const bool mine = row < p.rows && n < p.N;
             const float* wrow = p.ws + static_cast<int64_t>(min(n, p.N - 1) >> 7) * p.kb;
-            float acc[CW];
+            float2 acc[CW / 2];
 #pragma unroll
-            for (int m = 0; m < CW; ++m) acc[m] = 0.f;
+            for (int m = 0; m < CW / 2; ++m) acc[m] = make_float2(0.f, 0.f);
             float w_next[J];
 #pragma unroll
             for (int j = 0; j < J; ++j) w_next[j] = __ldg(wrow + min(b0 + j, p.kb - 1));
@@ -173,9 +182,11 @@ __global__ void __launch_bounds__(kWarps<NT> * 128 + 64) fp8_rows_kernel(const _
                 if (c == 0 && (b1 - b0 > p.chunk || t == first)) {   // the next blocks' x scales, turned to [block][row]
                     const int nblk = min(p.chunk, b1 - b);
                     asm volatile("bar.sync 1, %0;" ::"n"(Q * 128) : "memory");
-                    for (int e = tid; e < NT * nblk; e += Q * 128) {
-                        const int m = e / nblk, q = e - m * nblk;
-                        xs_sh[q * NT + m] = m < p.M ? __ldg(p.xs + m * p.ldxs + b + q) : 0.f;
+#pragma unroll
+                    for (int u = 0; u < CW / 4; ++u) {   // a warp takes the rows warp, warp + 4 Q, ..
+                        const int m = warp + 4 * Q * u;
+                        const float* src = p.xs + m * p.ldxs + b;
+                        for (int q = lane; q < nblk; q += 32) xs_sh[q * XP + m] = m < p.M ? __ldg(src + q) : 0.f;
                     }
                     asm volatile("bar.sync 1, %0;" ::"n"(Q * 128) : "memory");
                 }
@@ -203,27 +214,27 @@ __global__ void __launch_bounds__(kWarps<NT> * 128 + 64) fp8_rows_kernel(const _
 #pragma unroll
                 for (int j = 0; j < J; ++j)
                     if (j < nj) {
-                        const float4* sx = reinterpret_cast<const float4*>(xs_sh + (c + j) * NT + col);
+                        const float4* sx = reinterpret_cast<const float4*>(xs_sh + (c + j) * XP + col);
 #pragma unroll
                         for (int q = 0; q < CW / 4; ++q) {
                             const float4 x4 = sx[q];
-                            acc[4 * q + 0] = fmaf(v[j][4 * q + 0], x4.x * w[j], acc[4 * q + 0]);
-                            acc[4 * q + 1] = fmaf(v[j][4 * q + 1], x4.y * w[j], acc[4 * q + 1]);
-                            acc[4 * q + 2] = fmaf(v[j][4 * q + 2], x4.z * w[j], acc[4 * q + 2]);
-                            acc[4 * q + 3] = fmaf(v[j][4 * q + 3], x4.w * w[j], acc[4 * q + 3]);
+                            const float2 w2 = make_float2(w[j], w[j]);
+                            acc[2 * q] = ffma2(make_float2(v[j][4 * q], v[j][4 * q + 1]), fmul2(make_float2(x4.x, x4.y), w2), acc[2 * q]);
+                            acc[2 * q + 1] = ffma2(make_float2(v[j][4 * q + 2], v[j][4 * q + 3]), fmul2(make_float2(x4.z, x4.w), w2), acc[2 * q + 1]);
                         }
                     }
             }
             if (p.split > 1) {
 #pragma unroll
                 for (int m = 0; m < CW; ++m)
-                    if (col + m < p.M) part[(col + m) * 128 + row] = acc[m];
+                    if (col + m < p.M) part[(col + m) * 128 + row] = m & 1 ? acc[m / 2].y : acc[m / 2].x;
             } else if (mine && ok) {
 #pragma unroll
                 for (int m = 0; m < CW; ++m)
                     if (col + m < p.M) {
                         const int64_t at = (col + m) * p.ldy + n;
-                        p.y[at] = p.res ? acc[m] + p.res[at] : acc[m];
+                        const float v = m & 1 ? acc[m / 2].y : acc[m / 2].x;
+                        p.y[at] = p.res ? v + p.res[at] : v;
                     }
             }
         }
@@ -268,17 +279,20 @@ gem_status ensure_smem(const void* fn, int device, size_t bytes) {
 template <int NT>
 gem_status launch_rows(GemmParams p, const void* W, int64_t K, const void* x, int64_t ldx, const DeviceInfo& di, cudaStream_t stream) {
     gem_status st;
-    // Rows a tile and CTAs a tile: the fewest block-rows on the busiest SM.
+    // Rows of W a tile and CTAs that share a tile's blocks: the shortest time of the busiest SM.  A block costs its
+    // bytes, or its products where it has fewer than 64 rows (they take the same time for any number of rows);
+    // a cluster costs its joining.  Clusters only where one round of them does it: 4 CTAs of one GPC fit 36 times.
     p.split = 1;
     p.rows = 128;
     double best = 1e30;
     for (int s : {1, 2, 4}) {
-        if (s > 1 && p.kb < 4 * s) break;
+        const int room = s == 1 ? di.num_sms : s == 2 ? di.num_sms / 2 * 2 : di.num_sms / 4 * 4 - 8;
+        if (s > 1 && p.kb < 8 * s) break;
         for (int r = 128; r >= 8; r -= 8) {
-            const int64_t tiles = (p.N + r - 1) / r;
-            if (s > 1 && tiles * s > di.num_sms / 4 * 4 - 8) continue;   // one round of clusters
-            const int64_t rounds = (tiles * s + di.num_sms - 1) / di.num_sms;
-            const double cost = static_cast<double>(rounds) * ((p.kb + s - 1) / s) * std::max(r, 40) + (s > 1 ? 200.0 : 0.0);
+            const int64_t ctas = int64_t(s) * ((p.N + r - 1) / r);
+            if (s > 1 && ctas > room) continue;
+            const int64_t rounds = (ctas + di.num_sms - 1) / di.num_sms;
+            const double cost = static_cast<double>(rounds) * ((p.kb + s - 1) / s) * std::max(r, 64) + (s > 1 ? 300.0 : 0.0);
             if (cost < best * 0.999) {
                 best = cost;
                 p.rows = r;
@@ -287,20 +301,29 @@ gem_status launch_rows(GemmParams p, const void* W, int64_t K, const void* x, in
         }
     }
     p.tiles = (p.N + p.rows - 1) / p.rows;
-    p.wbytes = (p.rows * 128 + 1023) / 1024 * 1024;
-    const int per = (p.kb + p.split - 1) / p.split;
     constexpr int J = kGroup<NT>;
-    p.chunk = std::min((per + J - 1) / J * J, kScaleBytes / (NT * 4));   // a multiple of J
-    const int block = p.wbytes + NT * 128, after = std::max(0, 16384 - block);
-    const int fixed = 1024 + after + p.chunk * NT * 4 + (p.split > 1 ? NT * 512 : 0);
+    const int groups = (p.kb + J - 1) / J, per = (groups + p.split - 1) / p.split;
+    p.chunk = std::min(per * J, kScaleBytes / (kPitch<NT> * 4) / J * J);
+    const int stage = J * (p.rows + NT) * 128, after = std::max(0, 16384 - p.rows * 128 - J * NT * 128);
+    const int fixed = 1024 + after + p.chunk * kPitch<NT> * 4 + (p.split > 1 ? NT * 512 : 0);
     const int64_t grid = p.split > 1 ? int64_t(p.tiles) * p.split : std::min<int64_t>(p.tiles, di.num_sms);
-    const int64_t steps = (per + J - 1) / J * ((int64_t(p.tiles) * p.split + grid - 1) / grid);   // of the busiest CTA
+    const int64_t steps = per * ((int64_t(p.tiles) * p.split + grid - 1) / grid);   // of the busiest CTA
     p.stages = static_cast<int>(std::min(std::min<int64_t>(kMaxStages, steps),
-                                         (static_cast<int64_t>(di.smem_optin) - fixed - static_cast<int>(sizeof(RowsBarriers)) - 512) / (J * block)));
-    const size_t smem = static_cast<size_t>(fixed + p.stages * J * block);
+                                         (static_cast<int64_t>(di.smem_optin) - fixed - static_cast<int>(sizeof(RowsBarriers)) - 512) / stage));
+    const size_t smem = static_cast<size_t>(fixed + p.stages * stage);
+    p.whole = K % 128 == 0;
     CUtensorMap tmW, tmX;
-    if ((st = make_tensor_map_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, W, K, p.N, K, 128, p.rows, CU_TENSOR_MAP_SWIZZLE_128B)) != GEM_OK) return st;
-    if ((st = make_tensor_map_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, K, p.M, ldx, 128, NT, CU_TENSOR_MAP_SWIZZLE_128B)) != GEM_OK) return st;
+    const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const auto swz = CU_TENSOR_MAP_SWIZZLE_128B;
+    const uint64_t uK = K, uN = p.N, uM = p.M, blocks = p.kb;
+    const uint32_t rows = p.rows;
+    if (p.whole) {
+        if ((st = make_tensor_map_3d(&tmW, u8, W, {128, uN, blocks}, uK, 128, {128, rows, J}, swz)) != GEM_OK) return st;
+        if ((st = make_tensor_map_3d(&tmX, u8, x, {128, uM, blocks}, ldx, 128, {128, NT, J}, swz)) != GEM_OK) return st;
+    } else {
+        if ((st = make_tensor_map_2d(&tmW, u8, W, uK, uN, uK, 128, rows, swz)) != GEM_OK) return st;
+        if ((st = make_tensor_map_2d(&tmX, u8, x, uK, uM, ldx, 128, NT, swz)) != GEM_OK) return st;
+    }
     const void* fn = reinterpret_cast<const void*>(fp8_rows_kernel<NT>);
     if ((st = ensure_smem(fn, di.device, smem)) != GEM_OK) return st;
     void* args[] = {&tmW, &tmX, &p};

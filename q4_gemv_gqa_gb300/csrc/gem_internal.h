@@ -41,6 +41,11 @@ gem_status make_tensor_map_2d(CUtensorMap* tm, CUtensorMapDataType dtype, const 
                               uint64_t dim0, uint64_t dim1, uint64_t stride1_bytes,
                               uint32_t box0, uint32_t box1, CUtensorMapSwizzle swizzle);
 
+// 3-D form: strides of the second and third dimension in bytes.
+gem_status make_tensor_map_3d(CUtensorMap* tm, CUtensorMapDataType dtype, const void* base, const uint64_t (&dim)[3],
+                              uint64_t stride1_bytes, uint64_t stride2_bytes, const uint32_t (&box)[3],
+                              CUtensorMapSwizzle swizzle);
+
 // Launch with programmatic stream serialization enabled.
 gem_status launch_pdl(const void* kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                       void** args);

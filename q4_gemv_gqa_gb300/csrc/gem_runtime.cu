@@ -73,9 +73,9 @@ gem_status device_info(DeviceInfo* out) {
     return GEM_OK;
 }
 
-gem_status make_tensor_map_2d(CUtensorMap* tm, CUtensorMapDataType dtype, const void* base, uint64_t dim0,
-                              uint64_t dim1, uint64_t stride1_bytes, uint32_t box0, uint32_t box1,
-                              CUtensorMapSwizzle swizzle) {
+static gem_status make_tensor_map(CUtensorMap* tm, CUtensorMapDataType dtype, int rank, const void* base,
+                                  const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box,
+                                  CUtensorMapSwizzle swizzle) {
     std::call_once(g_encode_once, [] {
         void* fn = nullptr;
         cudaDriverEntryPointQueryResult q{};
@@ -86,15 +86,28 @@ gem_status make_tensor_map_2d(CUtensorMap* tm, CUtensorMapDataType dtype, const 
         g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     });
     if (g_encode_err != cudaSuccess || !g_encode) return cuda_fail(g_encode_err);
-    cuuint64_t dims[2] = {dim0, dim1};
-    cuuint64_t strides[1] = {stride1_bytes};
-    cuuint32_t box[2] = {box0, box1};
-    cuuint32_t estr[2] = {1, 1};
-    CUresult r = g_encode(tm, dtype, 2, const_cast<void*>(base), dims, strides, box, estr,
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = g_encode(tm, dtype, static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides, box, estr,
                           CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return cuda_fail(cudaErrorInvalidValue);
     return GEM_OK;
+}
+
+gem_status make_tensor_map_2d(CUtensorMap* tm, CUtensorMapDataType dtype, const void* base, uint64_t dim0,
+                              uint64_t dim1, uint64_t stride1_bytes, uint32_t box0, uint32_t box1,
+                              CUtensorMapSwizzle swizzle) {
+    const cuuint64_t dims[2] = {dim0, dim1}, strides[1] = {stride1_bytes};
+    const cuuint32_t box[2] = {box0, box1};
+    return make_tensor_map(tm, dtype, 2, base, dims, strides, box, swizzle);
+}
+
+gem_status make_tensor_map_3d(CUtensorMap* tm, CUtensorMapDataType dtype, const void* base, const uint64_t (&dim)[3],
+                              uint64_t stride1_bytes, uint64_t stride2_bytes, const uint32_t (&box)[3],
+                              CUtensorMapSwizzle swizzle) {
+    const cuuint64_t dims[3] = {dim[0], dim[1], dim[2]}, strides[2] = {stride1_bytes, stride2_bytes};
+    const cuuint32_t b[3] = {box[0], box[1], box[2]};
+    return make_tensor_map(tm, dtype, 3, base, dims, strides, b, swizzle);
 }
 
 gem_status launch_pdl(const void* kernel, dim3 grid, dim3 block, size_t smem, cudaStream_t stream,

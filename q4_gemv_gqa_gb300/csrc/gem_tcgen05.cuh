@@ -67,19 +67,26 @@ __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.
 // ---- products ----------------------------------------------------------------------------
 // The calls below are made by a whole warp, whose elected lane acts: addresses and descriptors then stay in
 // uniform registers (from one lane of a diverged warp a product took 70 cycles to issue and a copy 107).
+// d = a x b over 128 bytes of K (four products of 32, the first of which overwrites d)
 template <int G>
-__device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
     if constexpr (G == 1)
         asm volatile(
-            "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.u32 p, %4, 0;\n"
-            " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+            "{\n .reg .pred e;\n .reg .b64 x, y;\n elect.sync _|e, 0xffffffff;\n"
+            " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, 0;\n"
+            " add.s64 x, %1, 2;\n add.s64 y, %2, 2;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, 1;\n"
+            " add.s64 x, %1, 4;\n add.s64 y, %2, 4;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, 1;\n"
+            " add.s64 x, %1, 6;\n add.s64 y, %2, 6;\n @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], x, y, %3, 1;\n}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc)
             : "memory");
     else
         asm volatile(
-            "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.u32 p, %4, 0;\n"
-            " @e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+            "{\n .reg .pred e;\n .reg .b64 x, y;\n elect.sync _|e, 0xffffffff;\n"
+            " @e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, 0;\n"
+            " add.s64 x, %1, 2;\n add.s64 y, %2, 2;\n @e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], x, y, %3, 1;\n"
+            " add.s64 x, %1, 4;\n add.s64 y, %2, 4;\n @e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], x, y, %3, 1;\n"
+            " add.s64 x, %1, 6;\n add.s64 y, %2, 6;\n @e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], x, y, %3, 1;\n}\n" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc)
             : "memory");
 }
 // One arrival on `bar` (G 2: on both CTAs' barrier at that place) when the products issued so far are done.
@@ -113,9 +120,33 @@ __device__ __forceinline__ void warp_tma_2d(uint32_t dst, const CUtensorMap* tm,
         "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(smem_u32(bar)), "l"(policy)
         : "memory");
 }
-// mbar_wait of a whole warp, which stays converged: false where a lane's wait ran out or another warp's did.
+__device__ __forceinline__ void warp_tma_3d(uint32_t dst, const CUtensorMap* tm, int32_t c0, int32_t c1, int32_t c2, uint64_t* bar,
+                                            uint64_t policy) {
+    asm volatile(
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+        " @e cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;\n}\n" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)), "l"(policy)
+        : "memory");
+}
+// mbar_wait of a whole warp, which stays converged: false where the wait ran out, or where another warp's did
+// (looked at only while this one has to wait: a phase that is done costs one test).
+static __device__ __noinline__ bool warp_wait_slow(uint64_t* bar, uint32_t parity, int* status, volatile int* dead) {
+    bool ok = false;
+    const uint64_t t0 = globaltimer_ns(), limit = wait_limit_ns();
+    while (true) {
+        for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(bar, parity);
+        if (ok || *dead) break;
+        if (globaltimer_ns() - t0 > limit) {
+            if (status) atomicOr(status, GEM_DEVFLAG_TIMEOUT);
+            break;
+        }
+    }
+    return __all_sync(~0u, ok);
+}
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status, volatile int* dead) {
-    return __all_sync(~0u, mbar_wait(bar, parity, status) && !*dead);
+    if (__all_sync(~0u, mbar_try_wait(bar, parity))) return true;
+    return warp_wait_slow(bar, parity, status, dead);
 }
 
 // ---- clusters ------------------------------------------------------------------------------
