@@ -265,6 +265,225 @@ __global__ void __launch_bounds__(kWarps<NT> * 128 + 64) fp8_rows_kernel(const _
     }
 }
 
+// ---- many rows of x ------------------------------------------------------------------------------
+// Two CTAs work on one tile of 256 rows of x (128 a CTA) and BN rows of W (half of them loaded by each; the
+// tensor cores of both read all of them): a product of 256 x BN halves what an SM loads for its share of the
+// results, which would otherwise bound it.  Warps 0..15 scale and add (warp w: lane quarter w % 4, columns
+// w / 4 * BN / 4 and on; a thread has one row of x, so a block's scale is one number), warp 16 loads, warp 17
+// of the first CTA issues the products of both.
+constexpr int kTileStages = 5;
+constexpr int kTileThreads = 18 * 32;
+
+struct TileParams {
+    const float* ws;
+    const float* xs;
+    int64_t ldxs;
+    const float* res;
+    float* y;
+    int64_t ldy;
+    int N, M, kb;
+    int mtiles, tiles;
+    int wide;               // y's rows (and the residual's) start on 16 bytes
+    int* status;
+};
+
+struct TileBarriers {
+    uint64_t full[kTileStages], empty[kTileStages], dfull[2], dempty[2];
+    uint32_t tmem;
+    int dead;
+};
+
+template <int BN>
+constexpr int kTileStage = 16384 + BN * 64;
+template <int BN>
+constexpr int kTileSmem = 1024 + kTileStages * kTileStage<BN> + 16 * 4096;
+
+template <int BN>
+__global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const TileParams p) {
+    constexpr int CW = BN / 4, STAGE = kTileStage<BN>;
+    extern __shared__ uint8_t raw[];
+    __shared__ TileBarriers bar;
+    uint8_t* ring = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = cluster_rank();
+    const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
+    volatile int* dead = &bar.dead;
+
+    if (tid == 0) {
+        bar.dead = 0;
+        for (int i = 0; i < kTileStages; ++i) {
+            mbar_init(&bar.full[i], 1);
+            mbar_init(&bar.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.dfull[i], 1);
+            mbar_init(&bar.dempty[i], 32);
+        }
+        fence_mbar_init();
+        prefetch_tensormap(&tmW);
+        prefetch_tensormap(&tmX);
+    }
+    if (warp == 17) tmem_alloc<2>(&bar.tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = bar.tmem;
+    const int ntile = pair < p.tiles ? (p.tiles - pair + pairs - 1) / pairs : 0;
+    int issued = 0;   // stages, by the loading warp
+
+    if (warp == 16) {
+        pdl_wait_trigger();
+        const uint64_t keep = l2_policy_evict_last();
+        const uint32_t extra = blockIdx.x == 0 && (test_inject() & GEM_INJECT_RING_SHORTFALL) ? 16u : 0u;
+        const uint32_t base = smem_u32(ring), full0 = peer_addr(&bar.full[0], 0);
+        int s = 0;
+        uint32_t phase = 1;
+        bool ok = true;
+        for (int i = 0; i < ntile && ok; ++i) {
+            const int t = pair + i * pairs, mt = t % p.mtiles, nt = t / p.mtiles;
+            const int m0 = mt * 256 + static_cast<int>(rank) * 128, n0 = nt * BN + static_cast<int>(rank) * (BN / 2);
+            for (int b = 0; b < p.kb; ++b) {
+                if (issued >= kTileStages && !warp_wait(&bar.empty[s], phase, p.status, dead)) {
+                    ok = false;
+                    break;
+                }
+                if (rank == 0) warp_expect_tx(&bar.full[s], 2 * STAGE + (issued == 0 ? extra : 0u));
+                warp_tma_2d_pair(base + s * STAGE, &tmX, b * 128, m0, full0 + 8 * s, keep);
+                warp_tma_2d_pair(base + s * STAGE + 16384, &tmW, b * 128, n0, full0 + 8 * s, keep);
+                ++issued;
+                if (++s == kTileStages) s = 0, phase ^= 1;
+            }
+        }
+        if (!ok) *dead = 1;
+    } else if (warp == 17) {
+        if (rank == 0) {
+            constexpr uint32_t idesc = umma_idesc_e4m3(256, BN);
+            const uint64_t da0 = umma_desc(smem_u32(ring)), db0 = umma_desc(smem_u32(ring) + 16384);
+            const int total = ntile * p.kb;
+            uint64_t da = da0, db = db0;
+            int i = 0, s = 0;
+            uint32_t phase = 0;
+            for (; i < total; ++i) {
+                const int d = i & 1;
+                if (i >= 2 && !warp_wait(&bar.dempty[d], static_cast<uint32_t>((i / 2 - 1) & 1), p.status, dead)) break;
+                if (!warp_wait(&bar.full[s], phase, p.status, dead)) break;
+                tc_fence_after();
+                umma_e4m3<2>(tmem + d * 256, da, db, idesc);
+                umma_commit<2>(&bar.empty[s]);
+                umma_commit<2>(&bar.dfull[d]);
+                da += STAGE >> 4, db += STAGE >> 4;
+                if (++s == kTileStages) s = 0, phase ^= 1, da = da0, db = db0;
+            }
+            if (i < total) {
+                *dead = 1;
+                // what was issued ends before the tensor memory is given back
+                if (i > 0) (void)mbar_wait(&bar.dfull[(i - 1) & 1], static_cast<uint32_t>(((i - 1) / 2) & 1), nullptr);
+            }
+        }
+    } else {
+        const int row = (warp & 3) * 32 + lane, col = (warp >> 2) * CW;
+        const uint32_t from = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + col;
+        const uint32_t empty0 = peer_addr(&bar.dempty[0], 0);
+        float* stage = reinterpret_cast<float*>(ring + kTileStages * STAGE + warp * 4096);
+        pdl_wait_trigger();
+        int i = 0;
+        bool ok = true;
+        for (int it = 0; it < ntile && ok; ++it) {
+            const int t = pair + it * pairs, mt = t % p.mtiles, nt = t / p.mtiles;
+            const int mw = mt * 256 + static_cast<int>(rank) * 128 + (warp & 3) * 32, n0 = nt * BN + col;   // the warp's first row and column
+            const float* xrow = p.xs + static_cast<int64_t>(min(mw + lane, p.M - 1)) * p.ldxs;
+            // the warp's columns lie in one or two blocks of 128 rows of W
+            const int nb = n0 >> 7, last = (p.N - 1) >> 7;
+            const float* w0row = p.ws + static_cast<int64_t>(min(nb, last)) * p.kb;
+            const float* w1row = p.ws + static_cast<int64_t>(min(nb + 1, last)) * p.kb;
+            float2 acc[CW / 2];
+#pragma unroll
+            for (int m = 0; m < CW / 2; ++m) acc[m] = make_float2(0.f, 0.f);
+            // scales are requested two blocks ahead
+            float x0 = __ldg(xrow), x1 = __ldg(xrow + min(1, p.kb - 1)), wa0 = __ldg(w0row), wa1 = __ldg(w0row + min(1, p.kb - 1));
+            float wb0 = 0.f, wb1 = 0.f;
+            if (128 % CW) wb0 = __ldg(w1row), wb1 = __ldg(w1row + min(1, p.kb - 1));
+            for (int b = 0; b < p.kb; ++b, ++i) {
+                const float sa = x0 * wa0, sb = 128 % CW ? x0 * wb0 : sa;
+                const int ahead = min(b + 2, p.kb - 1);
+                x0 = x1, wa0 = wa1, wb0 = wb1;
+                x1 = __ldg(xrow + ahead);
+                wa1 = __ldg(w0row + ahead);
+                if (128 % CW) wb1 = __ldg(w1row + ahead);
+                const int d = i & 1;
+                if (!warp_wait(&bar.dfull[d], static_cast<uint32_t>((i / 2) & 1), p.status, dead)) {
+                    *dead = 1;
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int u = 0; u < CW / 16; ++u) {
+                    float v[16];
+                    tmem_ld<16>(v, from + d * 256 + 16 * u);
+                    tmem_wait_ld();
+                    if (u + 1 == CW / 16) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_peer(empty0 + 8 * d);
+                    }
+                    const float sc = (n0 + 16 * u) >> 7 == nb ? sa : sb;
+                    const float2 s2 = make_float2(sc, sc);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) acc[8 * u + q] = ffma2(make_float2(v[2 * q], v[2 * q + 1]), s2, acc[8 * u + q]);
+                }
+            }
+            if (!ok) break;
+            // out through the warp's piece of shared memory, 32 (or 16) columns at a time: rows of 128 bytes, whose
+            // 16-byte pieces are turned by the row, so that neither side meets itself in a bank
+#pragma unroll
+            for (int c0 = 0; c0 < CW; c0 += 32) {
+                constexpr int kAll = 32;
+                const int cols = CW - c0 < kAll ? CW - c0 : kAll;
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    if (4 * q < cols)
+                        reinterpret_cast<float4*>(stage)[lane * 8 + (q ^ (lane & 7))] =
+                            make_float4(acc[(c0 + 4 * q) / 2].x, acc[(c0 + 4 * q) / 2].y, acc[(c0 + 4 * q) / 2 + 1].x, acc[(c0 + 4 * q) / 2 + 1].y);
+                __syncwarp();
+                const int q = lane & 7;
+#pragma unroll
+                for (int r0 = 0; r0 < 32; r0 += 4) {
+                    const int r = r0 + (lane >> 3), m = mw + r, n = n0 + c0 + 4 * q;
+                    if (4 * q < cols && m < p.M && n < p.N) {
+                        float4 v = reinterpret_cast<const float4*>(stage)[r * 8 + (q ^ (r & 7))];
+                        float* to = p.y + m * p.ldy + n;
+                        const float* add = p.res ? p.res + m * p.ldy + n : nullptr;
+                        if (p.wide && n + 4 <= p.N) {
+                            if (add) {
+                                const float4 a = *reinterpret_cast<const float4*>(add);
+                                v.x += a.x, v.y += a.y, v.z += a.z, v.w += a.w;
+                            }
+                            *reinterpret_cast<float4*>(to) = v;
+                        } else {
+                            const float e[4] = {v.x, v.y, v.z, v.w};
+                            for (int j = 0; j < 4 && n + j < p.N; ++j) to[j] = add ? e[j] + add[j] : e[j];
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    // the copies of both CTAs are counted on the first one's barriers
+    if (*dead && rank == 0 && warp == 16 && lane == 0) drain_stages(bar.full, kTileStages, max(0, issued - kTileStages), issued - 1);
+    __syncwarp();
+    cluster_sync();
+    if (warp == 17) {
+        tc_fence_after();
+        tmem_free<2>(tmem, 512);
+    }
+}
+
 gem_status ensure_smem(const void* fn, int device, size_t bytes) {
     static std::mutex mu;
     static std::map<std::pair<int, const void*>, size_t> done;
@@ -330,6 +549,24 @@ gem_status launch_rows(GemmParams p, const void* W, int64_t K, const void* x, in
     return launch_pdl_cluster(fn, dim3(static_cast<unsigned>(grid)), dim3(kWarps<NT> * 128 + 64), smem, stream, args, p.split);
 }
 
+template <int BN>
+gem_status launch_tile(const GemmParams& g, const void* W, int64_t K, const void* x, int64_t ldx, const DeviceInfo& di, cudaStream_t stream) {
+    TileParams p{};
+    p.ws = g.ws, p.xs = g.xs, p.ldxs = g.ldxs, p.res = g.res, p.y = g.y, p.ldy = g.ldy, p.N = g.N, p.M = g.M, p.kb = g.kb, p.status = g.status;
+    p.mtiles = (p.M + 255) / 256;
+    p.tiles = p.mtiles * ((p.N + BN - 1) / BN);
+    p.wide = !(((reinterpret_cast<uintptr_t>(p.y) | reinterpret_cast<uintptr_t>(p.res)) & 15) || p.ldy % 4);
+    gem_status st;
+    CUtensorMap tmW, tmX;
+    if ((st = make_tensor_map_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, W, K, p.N, K, 128, BN / 2, CU_TENSOR_MAP_SWIZZLE_128B)) != GEM_OK) return st;
+    if ((st = make_tensor_map_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, K, p.M, ldx, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B)) != GEM_OK) return st;
+    const void* fn = reinterpret_cast<const void*>(fp8_tile_kernel<BN>);
+    if ((st = ensure_smem(fn, di.device, kTileSmem<BN>)) != GEM_OK) return st;
+    const int pairs = std::min(p.tiles, di.num_sms / 2);
+    void* args[] = {&tmW, &tmX, &p};
+    return launch_pdl_cluster(fn, dim3(static_cast<unsigned>(2 * pairs)), dim3(kTileThreads), kTileSmem<BN>, stream, args, 2);
+}
+
 }  // namespace
 }  // namespace gem
 
@@ -341,7 +578,7 @@ gem_status gem_fp8_gemm(const void* W, const float* ws, int64_t N, int64_t K, co
     using namespace gem;
     if (M < 0 || N < 0 || K < 0) return GEM_ERR_INVALID_ARG;
     constexpr int64_t lim = (int64_t(1) << 31) - 512;
-    if (K % 16 || M > lim || N > lim || K > lim) return GEM_ERR_UNSUPPORTED_SHAPE;
+    if (K % 16 || M > lim || N > lim || K > lim || ((M + 255) / 256) * ((N + 127) / 128) > lim) return GEM_ERR_UNSUPPORTED_SHAPE;
     if (M == 0 || N == 0) return GEM_OK;
     if (K == 0 || !W || !ws || !x || !xs || !y) return GEM_ERR_INVALID_ARG;
     if (ldx < K || ldxs < (K + 127) / 128 || ldy < N) return GEM_ERR_INVALID_ARG;
@@ -360,19 +597,15 @@ gem_status gem_fp8_gemm(const void* W, const float* ws, int64_t N, int64_t K, co
     p.ldy = ldy;
     p.status = status ? status : di.status_word;
     cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
-    for (int64_t m = 0; m < M; m += 128) {
-        p.M = static_cast<int>(std::min<int64_t>(128, M - m));
-        p.xs = xs + m * ldxs;
-        p.y = y + m * ldy;
-        p.res = residual ? residual + m * ldy : nullptr;
-        const uint8_t* xm = static_cast<const uint8_t*>(x) + m * ldx;
-        if (p.M <= 16) st = launch_rows<16>(p, W, K, xm, ldx, di, stream);
-        else if (p.M <= 32) st = launch_rows<32>(p, W, K, xm, ldx, di, stream);
-        else if (p.M <= 64) st = launch_rows<64>(p, W, K, xm, ldx, di, stream);
-        else st = launch_rows<128>(p, W, K, xm, ldx, di, stream);
-        if (st != GEM_OK) return st;
-    }
-    return GEM_OK;
+    p.M = static_cast<int>(M);
+    p.xs = xs;
+    p.y = y;
+    p.res = residual;
+    if (M <= 16) return launch_rows<16>(p, W, K, x, ldx, di, stream);
+    if (M <= 32) return launch_rows<32>(p, W, K, x, ldx, di, stream);
+    if (M <= 64) return launch_rows<64>(p, W, K, x, ldx, di, stream);
+    if (M <= 128) return launch_rows<128>(p, W, K, x, ldx, di, stream);
+    return launch_tile<256>(p, W, K, x, ldx, di, stream);
 }
 
 }  // extern "C"
