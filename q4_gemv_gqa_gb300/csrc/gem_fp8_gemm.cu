@@ -268,11 +268,16 @@ __global__ void __launch_bounds__(kWarps<NT> * 128 + 64) fp8_rows_kernel(const _
 // ---- many rows of x ------------------------------------------------------------------------------
 // Two CTAs work on one tile of 256 rows of x (128 a CTA) and BN rows of W (half of them loaded by each; the
 // tensor cores of both read all of them): a product of 256 x BN halves what an SM loads for its share of the
-// results, which would otherwise bound it.  Warps 0..15 scale and add (warp w: lane quarter w % 4, columns
-// w / 4 * BN / 4 and on; a thread has one row of x, so a block's scale is one number), warp 16 loads, warp 17
-// of the first CTA issues the products of both.
+// results, which would otherwise bound it.  Warps 0..7 scale and add (warp w: lane quarter w % 4, columns
+// w / 4 * BN / 2 and on; a thread has one row of x, so a block's scale is one number), warp 8 loads, warp 9 of
+// the first CTA issues the products of both; the last warpgroup gives its registers to the first two.
 constexpr int kTileStages = 5;
-constexpr int kTileThreads = 18 * 32;
+constexpr int kTileChunk = 8;             // blocks whose x scales a warp holds at a time, twice
+constexpr int kTilePitch = 33;            // of a block's 32 scales: spreads the copies over the banks
+constexpr int kTileScales = 2 * kTileChunk * kTilePitch * 4;
+constexpr int kTileWarps = 8;             // that scale and add
+constexpr int kTileThreads = (kTileWarps + 4) * 32;
+constexpr int kTileRegs = 232, kTileRegsLeft = 40;   // 256 * 232 + 128 * 40 = 384 * 168, what the block starts with
 
 struct TileParams {
     const float* ws;
@@ -284,6 +289,7 @@ struct TileParams {
     int N, M, kb;
     int mtiles, tiles;
     int wide;               // y's rows (and the residual's) start on 16 bytes
+    int copy;               // results leave by asynchronous copies: such rows, and no residual
     int* status;
 };
 
@@ -296,11 +302,11 @@ struct TileBarriers {
 template <int BN>
 constexpr int kTileStage = 16384 + BN * 64;
 template <int BN>
-constexpr int kTileSmem = 1024 + kTileStages * kTileStage<BN> + 16 * 4096;
+constexpr int kTileSmem = 1024 + kTileStages * kTileStage<BN> + kTileWarps * (4096 + kTileScales);
 
 template <int BN>
-__global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const TileParams p) {
-    constexpr int CW = BN / 4, STAGE = kTileStage<BN>;
+__global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmY, const TileParams p) {
+    constexpr int CW = BN / (kTileWarps / 4), STAGE = kTileStage<BN>;
     extern __shared__ uint8_t raw[];
     __shared__ TileBarriers bar;
     uint8_t* ring = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -317,13 +323,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.dfull[i], 1);
-            mbar_init(&bar.dempty[i], 32);
+            mbar_init(&bar.dempty[i], 2 * kTileWarps);
         }
         fence_mbar_init();
         prefetch_tensormap(&tmW);
         prefetch_tensormap(&tmX);
     }
-    if (warp == 17) tmem_alloc<2>(&bar.tmem, 512);
+    if (warp == kTileWarps + 1) tmem_alloc<2>(&bar.tmem, 512);
     tc_fence_before();
     __syncthreads();
     cluster_sync();
@@ -332,7 +338,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
     const int ntile = pair < p.tiles ? (p.tiles - pair + pairs - 1) / pairs : 0;
     int issued = 0;   // stages, by the loading warp
 
-    if (warp == 16) {
+    if (warp >= kTileWarps) regs_give<kTileRegsLeft>();
+    if (warp >= kTileWarps + 2) {
+    } else if (warp == kTileWarps) {
         pdl_wait_trigger();
         const uint64_t keep = l2_policy_evict_last();
         const uint32_t extra = blockIdx.x == 0 && (test_inject() & GEM_INJECT_RING_SHORTFALL) ? 16u : 0u;
@@ -356,7 +364,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
             }
         }
         if (!ok) *dead = 1;
-    } else if (warp == 17) {
+    } else if (warp == kTileWarps + 1) {
         if (rank == 0) {
             constexpr uint32_t idesc = umma_idesc_e4m3(256, BN);
             const uint64_t da0 = umma_desc(smem_u32(ring)), db0 = umma_desc(smem_u32(ring) + 16384);
@@ -382,35 +390,55 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
             }
         }
     } else {
-        const int row = (warp & 3) * 32 + lane, col = (warp >> 2) * CW;
+        regs_take<kTileRegs>();
+        const int col = (warp >> 2) * CW;
         const uint32_t from = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + col;
         const uint32_t empty0 = peer_addr(&bar.dempty[0], 0);
         float* stage = reinterpret_cast<float*>(ring + kTileStages * STAGE + warp * 4096);
+        float* xs_sh = reinterpret_cast<float*>(ring + kTileStages * STAGE + kTileWarps * 4096 + warp * kTileScales);
         pdl_wait_trigger();
         int i = 0;
         bool ok = true;
         for (int it = 0; it < ntile && ok; ++it) {
             const int t = pair + it * pairs, mt = t % p.mtiles, nt = t / p.mtiles;
             const int mw = mt * 256 + static_cast<int>(rank) * 128 + (warp & 3) * 32, n0 = nt * BN + col;   // the warp's first row and column
-            const float* xrow = p.xs + static_cast<int64_t>(min(mw + lane, p.M - 1)) * p.ldxs;
-            // the warp's columns lie in one or two blocks of 128 rows of W
+            // x scales of the next blocks, 8 of a row side by side, into [block][row]
+            auto request = [&](int b, int half) {
+                const int q = b + (lane & 7);
+                const uint32_t to = smem_u32(xs_sh) + ((half * kTileChunk + (lane & 7)) * kTilePitch + (lane >> 3)) * 4;
+                if (q < p.kb) {
+                    const float* src = p.xs + q;
+#pragma unroll
+                    for (int r = 0; r < 32; r += 4) cp_async_4(to + 4 * r, src + min(mw + r + (lane >> 3), p.M - 1) * p.ldxs);
+                }
+                cp_async_commit();
+            };
+            request(0, 0);
+            request(kTileChunk, 1);
+            // the warp's columns lie in one or two blocks of 128 rows of W, whose scales are requested two blocks ahead
             const int nb = n0 >> 7, last = (p.N - 1) >> 7;
             const float* w0row = p.ws + static_cast<int64_t>(min(nb, last)) * p.kb;
-            const float* w1row = p.ws + static_cast<int64_t>(min(nb + 1, last)) * p.kb;
-            float2 acc[CW / 2];
+            const int to_b = nb < last ? p.kb : 0;
+            uint64_t acc[CW / 2];
 #pragma unroll
-            for (int m = 0; m < CW / 2; ++m) acc[m] = make_float2(0.f, 0.f);
-            // scales are requested two blocks ahead
-            float x0 = __ldg(xrow), x1 = __ldg(xrow + min(1, p.kb - 1)), wa0 = __ldg(w0row), wa1 = __ldg(w0row + min(1, p.kb - 1));
-            float wb0 = 0.f, wb1 = 0.f;
-            if (128 % CW) wb0 = __ldg(w1row), wb1 = __ldg(w1row + min(1, p.kb - 1));
+            for (int m = 0; m < CW / 2; ++m) acc[m] = 0;
+            float wa0 = __ldg(w0row), wa1 = __ldg(w0row + min(1, p.kb - 1)), wb0 = 0.f, wb1 = 0.f;
+            if (128 % CW) wb0 = __ldg(w0row + to_b), wb1 = __ldg(w0row + to_b + min(1, p.kb - 1));
             for (int b = 0; b < p.kb; ++b, ++i) {
-                const float sa = x0 * wa0, sb = 128 % CW ? x0 * wb0 : sa;
+                const int c = b & (2 * kTileChunk - 1);
+                if ((b & (kTileChunk - 1)) == 0) {
+                    if (b > 0) {   // the half that is behind takes the blocks after the next ones
+                        __syncwarp();
+                        request(b + kTileChunk, (c / kTileChunk) ^ 1);
+                    }
+                    cp_async_wait<1>();
+                    __syncwarp();
+                }
+                const float x0 = xs_sh[c * kTilePitch + lane], sa = x0 * wa0, sb = 128 % CW ? x0 * wb0 : sa;
                 const int ahead = min(b + 2, p.kb - 1);
-                x0 = x1, wa0 = wa1, wb0 = wb1;
-                x1 = __ldg(xrow + ahead);
+                wa0 = wa1, wb0 = wb1;
                 wa1 = __ldg(w0row + ahead);
-                if (128 % CW) wb1 = __ldg(w1row + ahead);
+                if (128 % CW) wb1 = __ldg(w0row + to_b + ahead);
                 const int d = i & 1;
                 if (!warp_wait(&bar.dfull[d], static_cast<uint32_t>((i / 2) & 1), p.status, dead)) {
                     *dead = 1;
@@ -418,40 +446,54 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
                     break;
                 }
                 tc_fence_after();
+                // CH columns at a time, the next ones requested before these are added
+                constexpr int CH = 16;
+                float v[2][CH];
+                tmem_ld<CH>(v[0], from + d * 256);
 #pragma unroll
-                for (int u = 0; u < CW / 16; ++u) {
-                    float v[16];
-                    tmem_ld<16>(v, from + d * 256 + 16 * u);
+                for (int u = 0; u < CW / CH; ++u) {
                     tmem_wait_ld();
-                    if (u + 1 == CW / 16) {
+                    if (u + 1 < CW / CH) {
+                        tmem_ld<CH>(v[(u + 1) & 1], from + d * 256 + CH * (u + 1));
+                    } else {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_peer(empty0 + 8 * d);
                     }
-                    const float sc = (n0 + 16 * u) >> 7 == nb ? sa : sb;
-                    const float2 s2 = make_float2(sc, sc);
+                    const float sc = (n0 + CH * u) >> 7 == nb ? sa : sb;
+                    const uint64_t s2 = pair_of(sc);
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) acc[8 * u + q] = ffma2(make_float2(v[2 * q], v[2 * q + 1]), s2, acc[8 * u + q]);
+                    for (int q = 0; q < CH / 2; ++q)
+                        pair_fma(acc[CH / 2 * u + q], v[u & 1][2 * q], v[u & 1][2 * q + 1], s2);
                 }
             }
+            cp_async_wait<0>();
             if (!ok) break;
-            // out through the warp's piece of shared memory, 32 (or 16) columns at a time: rows of 128 bytes, whose
+            // out through the warp's piece of shared memory, 32 columns at a time: rows of 128 bytes, whose
             // 16-byte pieces are turned by the row, so that neither side meets itself in a bank
 #pragma unroll
             for (int c0 = 0; c0 < CW; c0 += 32) {
-                constexpr int kAll = 32;
-                const int cols = CW - c0 < kAll ? CW - c0 : kAll;
+                tma_store_wait_read<0>();   // the elected lane's copies of what stood here before
+                __syncwarp();
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
-                    if (4 * q < cols)
-                        reinterpret_cast<float4*>(stage)[lane * 8 + (q ^ (lane & 7))] =
-                            make_float4(acc[(c0 + 4 * q) / 2].x, acc[(c0 + 4 * q) / 2].y, acc[(c0 + 4 * q) / 2 + 1].x, acc[(c0 + 4 * q) / 2 + 1].y);
+                    {
+                        const float2 lo = pair_get(acc[(c0 + 4 * q) / 2]), hi = pair_get(acc[(c0 + 4 * q) / 2 + 1]);
+                        reinterpret_cast<float4*>(stage)[lane * 8 + (q ^ (lane & 7))] = make_float4(lo.x, lo.y, hi.x, hi.y);
+                    }
+                if (p.copy) {
+                    // rows and columns past the end of y are left out by the copy
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (n0 + c0 < p.N && mw < p.M) warp_tma_store_2d(&tmY, n0 + c0, mw, smem_u32(stage));
+                    continue;
+                }
                 __syncwarp();
                 const int q = lane & 7;
-#pragma unroll
+#pragma unroll 1
                 for (int r0 = 0; r0 < 32; r0 += 4) {
                     const int r = r0 + (lane >> 3), m = mw + r, n = n0 + c0 + 4 * q;
-                    if (4 * q < cols && m < p.M && n < p.N) {
+                    if (m < p.M && n < p.N) {
                         float4 v = reinterpret_cast<const float4*>(stage)[r * 8 + (q ^ (r & 7))];
                         float* to = p.y + m * p.ldy + n;
                         const float* add = p.res ? p.res + m * p.ldy + n : nullptr;
@@ -470,15 +512,16 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
                 __syncwarp();
             }
         }
+        tma_store_wait_read<0>();
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
     // the copies of both CTAs are counted on the first one's barriers
-    if (*dead && rank == 0 && warp == 16 && lane == 0) drain_stages(bar.full, kTileStages, max(0, issued - kTileStages), issued - 1);
+    if (*dead && rank == 0 && warp == kTileWarps && lane == 0) drain_stages(bar.full, kTileStages, max(0, issued - kTileStages), issued - 1);
     __syncwarp();
     cluster_sync();
-    if (warp == 17) {
+    if (warp == kTileWarps + 1) {
         tc_fence_after();
         tmem_free<2>(tmem, 512);
     }
@@ -560,10 +603,13 @@ gem_status launch_tile(const GemmParams& g, const void* W, int64_t K, const void
     CUtensorMap tmW, tmX;
     if ((st = make_tensor_map_2d(&tmW, CU_TENSOR_MAP_DATA_TYPE_UINT8, W, K, p.N, K, 128, BN / 2, CU_TENSOR_MAP_SWIZZLE_128B)) != GEM_OK) return st;
     if ((st = make_tensor_map_2d(&tmX, CU_TENSOR_MAP_DATA_TYPE_UINT8, x, K, p.M, ldx, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B)) != GEM_OK) return st;
+    CUtensorMap tmY = tmX;
+    p.copy = p.wide && !p.res;
+    if (p.copy && (st = make_tensor_map_2d(&tmY, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.y, p.N, p.M, p.ldy * 4, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B)) != GEM_OK) return st;
     const void* fn = reinterpret_cast<const void*>(fp8_tile_kernel<BN>);
     if ((st = ensure_smem(fn, di.device, kTileSmem<BN>)) != GEM_OK) return st;
     const int pairs = std::min(p.tiles, di.num_sms / 2);
-    void* args[] = {&tmW, &tmX, &p};
+    void* args[] = {&tmW, &tmX, &tmY, &p};
     return launch_pdl_cluster(fn, dim3(static_cast<unsigned>(2 * pairs)), dim3(kTileThreads), kTileSmem<BN>, stream, args, 2);
 }
 

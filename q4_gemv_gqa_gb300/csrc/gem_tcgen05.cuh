@@ -129,9 +129,31 @@ __device__ __forceinline__ void warp_tma_3d(uint32_t dst, const CUtensorMap* tm,
         "l"(reinterpret_cast<uint64_t>(tm)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)), "l"(policy)
         : "memory");
 }
+// Registers of the executing warpgroup (all of its warps): of the block's own at launch.
+template <int N>
+__device__ __forceinline__ void regs_take() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_give() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+// Shared memory to global memory; the source may be written again when at most `left` later groups are being read.
+__device__ __forceinline__ void warp_tma_store_2d(const CUtensorMap* tm, int32_t c0, int32_t c1, uint32_t src) {
+    asm volatile(
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+        " @e cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n @e cp.async.bulk.commit_group;\n}\n" ::"l"(
+            reinterpret_cast<uint64_t>(tm)),
+        "r"(c0), "r"(c1), "r"(src)
+        : "memory");
+}
+template <int LEFT>
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(LEFT) : "memory"); }
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
 // mbar_wait of a whole warp, which stays converged: false where the wait ran out, or where another warp's did
 // (looked at only while this one has to wait: a phase that is done costs one test).
-static __device__ __noinline__ bool warp_wait_slow(uint64_t* bar, uint32_t parity, int* status, volatile int* dead) {
+__device__ __forceinline__ bool warp_wait_slow(uint64_t* bar, uint32_t parity, int* status, volatile int* dead) {
     bool ok = false;
     const uint64_t t0 = globaltimer_ns(), limit = wait_limit_ns();
     while (true) {
@@ -147,6 +169,21 @@ static __device__ __noinline__ bool warp_wait_slow(uint64_t* bar, uint32_t parit
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status, volatile int* dead) {
     if (__all_sync(~0u, mbar_try_wait(bar, parity))) return true;
     return warp_wait_slow(bar, parity, status, dead);
+}
+
+// Two sums in one register pair: (lo, hi) += (a, b) * (s, s), s given twice by pair_of.
+__device__ __forceinline__ uint64_t pair_of(float v) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ void pair_fma(uint64_t& acc, float a, float b, uint64_t s) {
+    asm("{\n .reg .b64 t;\n mov.b64 t, {%1, %2};\n fma.rn.f32x2 %0, t, %3, %0;\n}\n" : "+l"(acc) : "f"(a), "f"(b), "l"(s));
+}
+__device__ __forceinline__ float2 pair_get(uint64_t acc) {
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(acc));
+    return v;
 }
 
 // ---- clusters ------------------------------------------------------------------------------
@@ -173,7 +210,7 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 // Into this CTA's shared memory, its bytes counted on a barrier of either CTA of the pair.
 __device__ __forceinline__ void warp_tma_2d_pair(uint32_t dst, const CUtensorMap* tm, int32_t c0, int32_t c1, uint32_t bar, uint64_t policy) {
