@@ -294,7 +294,7 @@ struct TileParams {
 };
 
 struct TileBarriers {
-    uint64_t full[kTileStages], empty[kTileStages], dfull[2], dempty[2];
+    uint64_t full[kTileStages], empty[kTileStages], dfull[2], dempty[2], done;
     uint32_t tmem;
     int dead;
 };
@@ -325,6 +325,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
             mbar_init(&bar.dfull[i], 1);
             mbar_init(&bar.dempty[i], 2 * kTileWarps);
         }
+        mbar_init(&bar.done, 1);
         fence_mbar_init();
         prefetch_tensormap(&tmW);
         prefetch_tensormap(&tmX);
@@ -386,7 +387,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
             if (i < total) {
                 *dead = 1;
                 // what was issued ends before the tensor memory is given back
-                if (i > 0) (void)mbar_wait(&bar.dfull[(i - 1) & 1], static_cast<uint32_t>(((i - 1) / 2) & 1), nullptr);
+                umma_commit<2>(&bar.done);
+                (void)mbar_wait(&bar.done, 0, nullptr);
             }
         }
     } else {
@@ -446,25 +448,20 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
                     break;
                 }
                 tc_fence_after();
-                // CH columns at a time, the next ones requested before these are added
-                constexpr int CH = 16;
-                float v[2][CH];
-                tmem_ld<CH>(v[0], from + d * 256);
+                // 16 columns at a time: more would not leave registers for the sums
 #pragma unroll
-                for (int u = 0; u < CW / CH; ++u) {
+                for (int u = 0; u < CW / 16; ++u) {
+                    float v[16];
+                    tmem_ld<16>(v, from + d * 256 + 16 * u);
                     tmem_wait_ld();
-                    if (u + 1 < CW / CH) {
-                        tmem_ld<CH>(v[(u + 1) & 1], from + d * 256 + CH * (u + 1));
-                    } else {
+                    if (u + 1 == CW / 16) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_peer(empty0 + 8 * d);
                     }
-                    const float sc = (n0 + CH * u) >> 7 == nb ? sa : sb;
-                    const uint64_t s2 = pair_of(sc);
+                    const uint64_t s2 = pair_of((n0 + 16 * u) >> 7 == nb ? sa : sb);
 #pragma unroll
-                    for (int q = 0; q < CH / 2; ++q)
-                        pair_fma(acc[CH / 2 * u + q], v[u & 1][2 * q], v[u & 1][2 * q + 1], s2);
+                    for (int q = 0; q < 8; ++q) pair_fma(acc[8 * u + q], v[2 * q], v[2 * q + 1], s2);
                 }
             }
             cp_async_wait<0>();
