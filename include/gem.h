@@ -605,21 +605,17 @@ GEM_API gem_status gem_fp8_gemm(const void *W, const float *ws, int64_t N, int64
  *   entropy[t] = -sum_n p[n] log p[n], p = e^(l - lse), where p[n] = 0 counts 0; nullable.
  *   idx[t][r], val[t][r], r < k: gem_topk's indices and their log probabilities l[idx] - lse; k in
  *              0..64, k <= N (k 0: both may be NULL).
- *   y [T][ldy] fp32, ldy >= N, 1 <= N < 2^31; T * ceil(N / 2048) < 2^31; scale > 0 and finite.
+ *   y [T][ldy] fp32, ldy >= N, 1 <= N < 2^31; T < 2^28; scale > 0 and finite.
  *   tokens     [T] int32; nullable with logp and rank.  -1: none given, logp 0 and rank 0.  Any other value
  *              outside [0, N) sets GEM_DEVFLAG_POS_RANGE, logp NaN and rank 0.
  *   -inf logits (banned tokens) have probability 0.  A row with a NaN or +inf, or of -inf alone: logp,
  *   entropy and val are NaN, rank and idx as stated (NaN after every number; a NaN token's rank counts
  *   the numbers and the NaNs of lower index).
- *   workspace  gem_logprobs_workspace(T, N, k) bytes (may be 0), 256-byte aligned, no initialisation;
- *              calls that can run at the same time need one each.
- *   Sums are fp32; one pass over y.  Deterministic.
+ *   No output may overlap y.  Sums are fp32; one pass over y, no workspace.  Deterministic.
  */
-GEM_API size_t gem_logprobs_workspace(int64_t T, int64_t N, int k);
 GEM_API gem_status gem_logprobs(const float *y, int64_t ldy, int64_t T, int64_t N, float scale,
                                 const int32_t *tokens, float *logp, int32_t *rank, float *entropy,
-                                int k, int32_t *idx, float *val, void *workspace, size_t ws_bytes,
-                                int32_t *status, void *stream);
+                                int k, int32_t *idx, float *val, int32_t *status, void *stream);
 
 /*
  * Gated FFN activation  [GELO] 04/05 (Qwen3 SwiGLU; Gemma gelu_pytorch_tanh).

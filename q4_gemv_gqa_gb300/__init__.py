@@ -27,7 +27,7 @@ DEVFLAG_NO_ROOM = 8
 __all__ = ["GemError", "q4_0_gemv", "q4_0_gemv_workspace", "q4_0_gemv_fused", "q8_0_gemv", "argmax", "argmax_workspace", "rmsnorm", "rmsnorm_qknorm_rope", "gqa_decode_attn",
            "gqa_decode_attn_workspace", "gqa_decode_attn_fused", "swiglu", "decode_layer", "decode_layer_workspace",
            "kv4_page_bytes", "kv_block_tables", "qknorm_mrope", "kv4_append", "kv4_gather", "kv4_attn",
-           "kv4_attn_workspace", "rmsnorm_fp8", "quant_fp8", "fp8_gemm", "logprobs", "logprobs_workspace", "DeviceLayer", "device_status", "status_from_flags", "set_wait_limit",
+           "kv4_attn_workspace", "rmsnorm_fp8", "quant_fp8", "fp8_gemm", "logprobs", "DeviceLayer", "device_status", "status_from_flags", "set_wait_limit",
            "set_test_injection", "LayerDesc"]
 
 
@@ -628,17 +628,12 @@ def fp8_gemm(W: torch.Tensor, w_scales: torch.Tensor, x: torch.Tensor, x_scales:
     return y
 
 
-def logprobs_workspace(T: int, N: int, k: int) -> int:
-    return int(lib.gem_logprobs_workspace(T, N, k))
-
-
 def logprobs(y: torch.Tensor, tokens: torch.Tensor | None, logp: torch.Tensor | None, entropy: torch.Tensor | None = None,
              rank: torch.Tensor | None = None, idx: torch.Tensor | None = None, val: torch.Tensor | None = None,
-             scale: float = 1.0, workspace: torch.Tensor | None = None, status: torch.Tensor | None = None,
-             stream=None) -> None:
+             scale: float = 1.0, status: torch.Tensor | None = None, stream=None) -> None:
     """Scores of the logit rows y (fp32 [T, N]): logp, entropy fp32 and rank int32 [T] of the tokens int32 [T]
     (-1: none), and the k alternatives idx int32, val fp32 [T, k] with their log probabilities.  Outputs that are
-    None are not computed.  workspace: uint8, at least logprobs_workspace(T, N, k) bytes (allocated when not given)."""
+    None are not computed."""
     dev = torch.cuda.current_device()
     N = y.shape[-1]
     yp, ldy, T = _rows(y, N, "y", dev)
@@ -647,15 +642,9 @@ def logprobs(y: torch.Tensor, tokens: torch.Tensor | None, logp: torch.Tensor | 
     if (idx is None) != (val is None):
         raise ValueError("idx and val come together")
     k = 0 if idx is None else idx.shape[-1]
-    if workspace is None:
-        need = lib.gem_logprobs_workspace(T, N, k)
-        workspace = _scratch(need, y.device, stream) if need else None
-    ws_bytes = 0 if workspace is None else workspace.shape[0]
     st = lib.gem_logprobs(yp, ldy, T, N, scale, here(tokens, i32, "tokens"), here(logp, f32, "logp"), here(rank, i32, "rank"),
                           here(entropy, f32, "entropy"), k, _here(idx, i32, "idx", (T, k), dev) if k else None,
-                          _here(val, f32, "val", (T, k), dev) if k else None,
-                          None if workspace is None else _here(workspace, torch.uint8, "workspace", (ws_bytes,), dev), ws_bytes,
-                          _status(status, dev), _stream_on(stream, dev))
+                          _here(val, f32, "val", (T, k), dev) if k else None, _status(status, dev), _stream_on(stream, dev))
     _check(st, "gem_logprobs")
 
 

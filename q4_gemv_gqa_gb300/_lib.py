@@ -72,8 +72,7 @@ PROTOTYPES = {
     "gem_rmsnorm_fp8": (i32, [p, i64, p, i64, p, i64, i64, i64, p, C.c_float, p, i64, p, i64, p]),
     "gem_quant_fp8": (i32, [p, i64, p, i64, i64, i64, i32, p, i64, p, i64, p]),
     "gem_fp8_gemm": (i32, [p, p, i64, i64, p, i64, p, i64, i64, p, i64, p, p, p]),
-    "gem_logprobs_workspace": (C.c_size_t, [i64, i64, i32]),
-    "gem_logprobs": (i32, [p, i64, i64, i64, C.c_float, p, p, p, p, i32, p, p, p, C.c_size_t, p, p]),
+    "gem_logprobs": (i32, [p, i64, i64, i64, C.c_float, p, p, p, p, i32, p, p, p, p]),
     "gem_swiglu": (i32, [p, p, i32, i64, i32, p, p]),
     "gem_decode_layer_workspace": (C.c_size_t, [C.POINTER(LayerDesc), i32, i64]),
     "gem_decode_layer": (i32, [C.POINTER(LayerDesc), i32, p, p, p, i64, p, p, C.c_size_t, p, p]),

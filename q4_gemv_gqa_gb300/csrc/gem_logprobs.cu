@@ -1,12 +1,26 @@
 // gem_logprobs.cu — log probabilities of given tokens, their ranks, the entropy and the top alternatives of
-// logit rows.
-#include "gem_device.cuh"
+// logit rows (gem_logprobs), in one pass over the logits.
+//
+// A thread keeps the largest logit m that it has seen, s = sum e^(l - m) and e = sum (l - m) e^(l - m), brings
+// them to a new m where one comes, and after the pass they are joined the same way:
+//     lse = m + log s,   entropy = log s - e / s.
+// Both terms of the entropy are positive, so nothing cancels; l - m is formed before it is scaled, so that its
+// error is relative.  The list of the k largest needs no second pass either: what can be in it is at least as
+// large as the k-th largest of the first piece's warp maxima, and after that as the k-th in the list so far, so
+// that a piece of 32 values a thread is looked at again only where its maximum passes that (a few of 10^5
+// values do).  The rank counts values only in pieces whose maximum reaches the given token's logit.
+//
+// Bound by the read of the logits.  A row is one CTA's, or a cluster's, whose CTAs join their sums and lists
+// through shared memory: no workspace, no counters, and an order that depends on the sizes alone.
+#include "gem_tcgen05.cuh"
 
 namespace gem {
 namespace {
 
-constexpr int kThreads = 512;
 constexpr int kMaxTop = 64;
+constexpr int kVec = 8;              // 16-byte loads of a thread in a piece
+constexpr int kHeld = 2048;          // keys that may wait to be sorted
+constexpr float kLowest = -3.402823466e38f;
 
 struct ScoreParams {
     const float* y; int64_t ldy;
@@ -16,80 +30,292 @@ struct ScoreParams {
     float* logp;
     int32_t* rank;
     float* entropy;
-    int k;
+    int k, split;
     int32_t* idx;
     float* val;
     int* status;
 };
 
-// 64-bit keys in the order of the list: larger values first (NaN after every number), then lower indices
-__device__ __forceinline__ uint64_t key_of(float v, int64_t i) {
+// Order of the list as an integer: larger values first (NaN after every number), then, in a key's low word, lower indices.
+__device__ __forceinline__ uint32_t order_of(float v) {
     v = v == 0.f ? 0.f : v;   // -0 and 0 are equal
-    uint32_t u = __float_as_uint(v);
-    u = v != v ? 0u : (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-    return static_cast<uint64_t>(u) << 32 | static_cast<uint32_t>(~static_cast<uint32_t>(i));
+    const uint32_t u = __float_as_uint(v);
+    return v != v ? 0u : (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+    return o == 0 ? __int_as_float(0x7fffffff) : __uint_as_float((o & 0x80000000u) ? o & 0x7fffffffu : ~o);
+}
+__device__ __forceinline__ uint64_t key_of(float v, int64_t i) {
+    return static_cast<uint64_t>(order_of(v)) << 32 | static_cast<uint32_t>(~static_cast<uint32_t>(i));
 }
 
-template <class T, class F>
-__device__ T cta_reduce(T v, T* red, F f) {
-    for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(~0u, v, o));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = red[0];
-    for (int i = 1; i < kThreads / 32; ++i) v = f(v, red[i]);
-    return v;
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(const ScoreParams p) {
-    __shared__ unsigned long long red64[kThreads / 32];
-    __shared__ float red32[kThreads / 32];
-    pdl_wait_trigger();
-    const int64_t t = blockIdx.x;
+struct Sums {
+    float m, s, e;   // e in powers of two: sum of w * log2 w
+};
+// c = scale * log2 e: e^(scale (a - b)) = 2^(c (a - b))
+__device__ __forceinline__ void raise(Sums& a, float m, float c) {
+    const float d = fmaxf((a.m - m) * c, -1e30f), f = exp2_fast(d);
+    a.e = f * fmaf(a.s, d, a.e);
+    a.s *= f;
+    a.m = m;
+}
+__device__ __forceinline__ Sums join(Sums a, Sums b, float c) {
+    const float m = fmaxf(a.m, b.m);
+    raise(a, m, c);
+    raise(b, m, c);
+    return {m, a.s + b.s, a.e + b.e};
+}
+__device__ __forceinline__ Sums shfl_xor(Sums a, int o) {
+    return {__shfl_xor_sync(~0u, a.m, o), __shfl_xor_sync(~0u, a.s, o), __shfl_xor_sync(~0u, a.e, o)};
+}
+
+template <int THREADS>
+struct ScoreShared {
+    unsigned long long held[kHeld];
+    unsigned long long top[kMaxTop];
+    Sums sums[THREADS / 32], all;
+    uint32_t largest[THREADS / 32];
+    int above[THREADS / 32], total;
+    int n;
+};
+
+// The k largest of the first n held keys, in order, into sh.top (0 where there are fewer) and to the front of
+// sh.held.  A key's place is the number of larger ones, counted by 1 to 32 lanes.
+template <int THREADS>
+__device__ void sort_held(ScoreShared<THREADS>& sh, int n, int k) {
+    const int tid = threadIdx.x;
+    __syncthreads();
+    if (tid < kMaxTop) sh.top[tid] = 0;
+    __syncthreads();
+    int lanes = 32;
+    while (lanes > 1 && n * lanes > THREADS) lanes >>= 1;
+    const int part = tid & (lanes - 1), end = (n * lanes + 31) / 32 * 32;
+    for (int at = tid; at < end; at += THREADS) {
+        const int i = at / lanes;
+        const unsigned long long mine = i < n ? sh.held[i] : 0;
+        int place = 0;
+        for (int j = part; j < n; j += lanes) place += sh.held[j] > mine;
+        for (int o = lanes >> 1; o > 0; o >>= 1) place += __shfl_xor_sync(~0u, place, o);
+        if (part == 0 && mine && place < k) sh.top[place] = mine;
+    }
+    __syncthreads();
+    if (tid < k) sh.held[tid] = sh.top[tid];
+    __syncthreads();
+}
+
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const ScoreParams p) {
+    __shared__ ScoreShared<THREADS> sh;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int W = THREADS / 32;
+    const int64_t t = blockIdx.x / p.split;
+    const int part = static_cast<int>(blockIdx.x % p.split);
     const float* row = p.y + t * p.ldy;
-    auto larger = [](float a, float b) { return a > b || a != a ? a : b; };   // keeps a NaN
-    auto sum = [](float a, float b) { return a + b; };
-    float m = -INFINITY;
-    for (int64_t i = threadIdx.x; i < p.N; i += kThreads) m = larger(row[i], m);
-    m = cta_reduce(m, red32, larger);
-    float s = 0.f, e = 0.f;
-    for (int64_t i = threadIdx.x; i < p.N; i += kThreads) {
-        const float d = p.scale * (row[i] - m), w = expf(d);
-        s += w;
-        if (w != 0.f) e = fmaf(w, d, e);
+    // 16-byte pieces from the first aligned entry on; the entries before and after them are the first CTA's
+    const int head = static_cast<int>(min(static_cast<int64_t>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) / 4 & 3), p.N));
+    const int64_t nv = (p.N - head) / 4;
+    const int rest = static_cast<int>(p.N - head - 4 * nv);
+    const int64_t per = (nv + p.split - 1) / p.split, v0 = min(nv, per * part), v1 = min(nv, v0 + per);
+    const float c = p.scale * 1.4426950408889634f;
+    const int k = p.k;
+    pdl_wait_trigger();
+
+    const int tok = p.tokens ? p.tokens[t] : -1;
+    const bool given = tok >= 0 && tok < p.N, count = given && p.rank;
+    const float target = given ? row[tok] : 0.f;
+    const float least = target == target ? target : -INFINITY;   // every piece may hold entries above a NaN
+    auto is_above = [&](float v, int64_t i) {
+        if (target != target) return v == v || i < tok;
+        return v > target || (v == target && i < tok);
+    };
+
+    Sums sum{kLowest, 0.f, 0.f};
+    int above = 0;
+    unsigned long long least_key = 0;   // the list's least key; what is not above it is not looked at
+    if (tid == 0) sh.n = 0;
+    __syncthreads();
+    if (part == 0 && tid < head + rest) {
+        const int64_t i = tid < head ? tid : 4 * nv + tid;
+        const float v = row[i], m = fmaxf(v, kLowest), d = (v - m) * c, w = exp2_fast(d);
+        sum = {m, w, fmaxf(d, -200.f) * (d < -200.f ? 0.f : w)};
+        above += count && is_above(v, i);
+        if (k) sh.held[atomicAdd(&sh.n, 1)] = key_of(v, i);
     }
-    s = cta_reduce(s, red32, sum);
-    e = cta_reduce(e, red32, sum);
-    const float log_s = logf(s);
-    if (p.entropy && threadIdx.x == 0) p.entropy[t] = log_s - e / s;
-    if (p.tokens) {
-        const int tok = p.tokens[t];
-        const bool given = tok >= 0 && tok < p.N;
-        unsigned long long above = 0;
-        if (given && p.rank) {
-            const uint64_t mine = key_of(row[tok], tok);
-            for (int64_t i = threadIdx.x; i < p.N; i += kThreads) above += key_of(row[i], i) > mine;
-            above = cta_reduce(above, red64, [](unsigned long long a, unsigned long long b) { return a + b; });
+    bool first = true;
+    for (int64_t at = v0; at < v1; at += THREADS * kVec) {
+        float x[4 * kVec];
+        const int64_t mine = at + tid;
+#pragma unroll
+        for (int u = 0; u < kVec; ++u) {
+            float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            if (mine + u * THREADS < v1) v = __ldcs(reinterpret_cast<const float4*>(row + head) + mine + u * THREADS);
+            x[4 * u] = v.x, x[4 * u + 1] = v.y, x[4 * u + 2] = v.z, x[4 * u + 3] = v.w;
         }
-        if (threadIdx.x == 0) {
+        const int have = mine >= v1 ? 0 : static_cast<int>(min((v1 - mine + THREADS - 1) / THREADS, static_cast<int64_t>(kVec)));   // loads that are there
+        float most = x[0];
+#pragma unroll
+        for (int j = 1; j < 4 * kVec; ++j) most = fmaxf(most, x[j]);
+        if (most > sum.m) raise(sum, most, c);
+        float s[4] = {}, e[4] = {};
+#pragma unroll
+        for (int j = 0; j < 4 * kVec; ++j) {
+            const float d = (x[j] - sum.m) * c, w = exp2_fast(d);
+            s[j & 3] += w;
+            e[j & 3] = fmaf(fmaxf(d, -200.f), w, e[j & 3]);   // w is 0 there; a NaN is in s
+        }
+        sum.s += (s[0] + s[1]) + (s[2] + s[3]);
+        sum.e += (e[0] + e[1]) + (e[2] + e[3]);
+        auto index = [&](int j) { return head + 4 * (mine + (j >> 2) * THREADS) + (j & 3); };
+        if (count && !(most < least)) {
+#pragma unroll
+            for (int j = 0; j < 4 * kVec; ++j) above += (j >> 2) < have && is_above(x[j], index(j));
+        }
+        if (k == 0) continue;
+        uint32_t bar = static_cast<uint32_t>(least_key >> 32);
+        if (first) {
+            // At least k entries of the piece reach the k-th largest of the warps' maxima, or, with a longer list than
+            // warps, the least of the warps' q-th largest lane maxima, q = ceil(k / warps).
+            uint32_t o = most > -INFINITY ? order_of(most) : 0u, w = 0;   // -inf may stand for a NaN, or for no entry
+            for (int q = (k + W - 1) / W; q > 0; --q) {
+                w = __reduce_max_sync(~0u, o);
+                if (o == w) o = 0;
+            }
+            if (lane == 0) sh.largest[warp] = w;
+            __syncthreads();
+            const uint32_t b = lane < W ? sh.largest[lane] : 0u;
+            if (k > W) {
+                bar = __reduce_min_sync(~0u, lane < W ? b : ~0u);
+            } else {
+                int larger = 0;
+                for (int q = 0; q < W; ++q) {
+                    const uint32_t other = __shfl_sync(~0u, b, q);
+                    larger += other > b || (other == b && q < lane);
+                }
+                bar = __reduce_max_sync(~0u, lane < W && larger == k - 1 ? b : 0u);
+            }
+            least_key = bar ? (static_cast<unsigned long long>(bar) << 32) - 1 : 0ull;
+            bar = static_cast<uint32_t>((least_key + 1) >> 32);
+        }
+        const bool all = bar == 0;   // NaN and -inf may be listed
+        const float floor_v = all ? 0.f : value_of(bar);
+        const bool look = have && (all || !(most < floor_v));
+        if (__syncthreads_or(look)) {
+            uint32_t mask = 0;
+            if (look)
+#pragma unroll
+                for (int j = 0; j < 4 * kVec; ++j) mask |= ((j >> 2) < have && (all || x[j] >= floor_v)) ? 1u << j : 0u;
+            const int before = sh.n;
+            __syncthreads();
+            int pos = mask ? atomicAdd(&sh.n, __popc(mask)) : 0;
+            __syncthreads();
+            int n = sh.n;
+            if (n <= kHeld) {
+                while (mask) {
+                    const int j = __ffs(mask) - 1;
+                    mask &= mask - 1;
+                    const int64_t i = index(j);
+                    const unsigned long long key = key_of(__ldg(row + i), i);
+                    sh.held[pos++] = key > least_key ? key : 0ull;
+                }
+            } else {
+                // more than fit (equal or rising values): one entry a thread at a time, sorted as often as need be
+                n = before;
+                for (int j = 0; j < 4 * kVec; ++j) {
+                    if (n + THREADS > kHeld) {
+                        sort_held(sh, n, k);
+                        n = min(n, k);
+                        least_key = n == k ? sh.top[k - 1] : 0ull;
+                    }
+                    __syncthreads();
+                    if (tid == 0) sh.n = n;
+                    __syncthreads();
+                    if (mask >> j & 1) {
+                        const int64_t i = index(j);
+                        const unsigned long long key = key_of(__ldg(row + i), i);
+                        if (key > least_key) sh.held[atomicAdd(&sh.n, 1)] = key;
+                    }
+                    __syncthreads();
+                    n = sh.n;
+                }
+            }
+            // the list so far raises the bar: after the first piece, and when many have come together
+            if ((first || n > kHeld / 4) && n >= k) {
+                sort_held(sh, n, k);
+                if (tid == 0) sh.n = k;
+                least_key = sh.top[k - 1];
+            }
+            __syncthreads();
+        }
+        first = false;
+    }
+
+    for (int o = 16; o > 0; o >>= 1) {
+        sum = join(sum, shfl_xor(sum, o), c);
+        above += __shfl_xor_sync(~0u, above, o);
+    }
+    if (lane == 0) sh.sums[warp] = sum, sh.above[warp] = above;
+    __syncthreads();
+    if (k) sort_held(sh, sh.n, k);
+    if (warp == 0) {
+        sum = lane < W ? sh.sums[lane] : Sums{kLowest, 0.f, 0.f};
+        above = lane < W ? sh.above[lane] : 0;
+        for (int o = 16; o > 0; o >>= 1) {
+            sum = join(sum, shfl_xor(sum, o), c);
+            above += __shfl_xor_sync(~0u, above, o);
+        }
+        if (lane == 0) sh.all = sum, sh.total = above;
+    }
+    __syncthreads();
+    if (p.split > 1) {
+        cluster_sync();
+        if (part == 0) {
+            if (warp == 0) {
+                sum = {kLowest, 0.f, 0.f};
+                above = 0;
+                if (lane < p.split) {
+                    const uint32_t a = peer_addr(&sh.all, lane);
+                    sum = {ld_peer(a), ld_peer(a + 4), ld_peer(a + 8)};
+                    above = __float_as_int(ld_peer(peer_addr(&sh.total, lane)));
+                }
+                for (int o = 16; o > 0; o >>= 1) {
+                    sum = join(sum, shfl_xor(sum, o), c);
+                    above += __shfl_xor_sync(~0u, above, o);
+                }
+            }
+            for (int i = tid; i < p.split * k; i += THREADS) {
+                const uint32_t a = peer_addr(&sh.top[i % k], i / k);
+                sh.held[i] = static_cast<unsigned long long>(__float_as_uint(ld_peer(a + 4))) << 32 | __float_as_uint(ld_peer(a));
+            }
+            __syncthreads();
+            if (tid == 0) sh.all = sum, sh.total = above;
+        }
+        // the lists of the others are read before the first CTA's is overwritten by the sort, and before they leave
+        cluster_sync();
+        if (part != 0) return;
+        if (k) sort_held(sh, p.split * k, k);
+        __syncthreads();
+    }
+    sum = sh.all;
+    // no finite logit, or one that is not a number
+    const float log_s = sum.s > 0.f ? logf(sum.s) : __int_as_float(0x7fffffff);
+    if (tid == 0) {
+        if (p.entropy) p.entropy[t] = log_s - 0.6931471805599453f * (sum.e / sum.s);
+        if (p.tokens) {
             if (!given && tok != -1) atomicOr(p.status, GEM_DEVFLAG_POS_RANGE);
-            if (p.logp) p.logp[t] = given ? p.scale * (row[tok] - m) - log_s : tok == -1 ? 0.f : __int_as_float(0x7fffffff);
-            if (p.rank) p.rank[t] = given ? static_cast<int>(above) + 1 : 0;
+            if (p.logp) p.logp[t] = given ? p.scale * (target - sum.m) - log_s : tok == -1 ? 0.f : __int_as_float(0x7fffffff);
+            if (p.rank) p.rank[t] = given ? sh.total + 1 : 0;
         }
     }
-    unsigned long long last = ~0ull;
-    for (int r = 0; r < p.k; ++r) {
-        unsigned long long best = 0;
-        for (int64_t i = threadIdx.x; i < p.N; i += kThreads) {
-            const unsigned long long q = key_of(row[i], i);
-            if (q < last && q > best) best = q;
-        }
-        last = cta_reduce(best, red64, [](unsigned long long a, unsigned long long b) { return a > b ? a : b; });
-        if (threadIdx.x == 0) {
-            const int i = static_cast<int>(~static_cast<uint32_t>(last));
-            p.idx[t * p.k + r] = i;
-            p.val[t * p.k + r] = p.scale * (row[i] - m) - log_s;
-        }
+    if (tid < k) {
+        const unsigned long long key = sh.top[tid];
+        p.idx[t * k + tid] = static_cast<int>(~static_cast<uint32_t>(key));
+        p.val[t * k + tid] = p.scale * (value_of(static_cast<uint32_t>(key >> 32)) - sum.m) - log_s;
     }
 }
 
@@ -98,23 +324,14 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(const ScoreParams p)
 
 extern "C" {
 
-size_t gem_logprobs_workspace(int64_t T, int64_t N, int k) {
-    (void)T, (void)N, (void)k;
-    return 0;
-}
-
 gem_status gem_logprobs(const float* y, int64_t ldy, int64_t T, int64_t N, float scale, const int32_t* tokens,
-                        float* logp, int32_t* rank, float* entropy, int k, int32_t* idx, float* val, void* workspace,
-                        size_t ws_bytes, int32_t* status, void* stream) {
+                        float* logp, int32_t* rank, float* entropy, int k, int32_t* idx, float* val, int32_t* status,
+                        void* stream) {
     using namespace gem;
     if (T < 0 || N < 1 || k < 0 || k > N || !(scale > 0.f) || !(scale <= 3.402823466e38f)) return GEM_ERR_INVALID_ARG;
-    if (k > kMaxTop || N >= (int64_t(1) << 31) || T > ((int64_t(1) << 31) - 1) / ((N + 2047) / 2048))
-        return GEM_ERR_UNSUPPORTED_SHAPE;
+    if (k > kMaxTop || N >= (int64_t(1) << 31) || T >= (int64_t(1) << 28)) return GEM_ERR_UNSUPPORTED_SHAPE;
     if (T == 0) return GEM_OK;
     if (!y || ldy < N || (k && (!idx || !val)) || ((logp || rank) && !tokens)) return GEM_ERR_INVALID_ARG;
-    const size_t need = gem_logprobs_workspace(T, N, k);
-    if (need && (!workspace || ws_bytes < need)) return GEM_ERR_WORKSPACE;
-    if (need && (reinterpret_cast<uintptr_t>(workspace) & 255)) return GEM_ERR_MISALIGNED;
     if ((reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(tokens) | reinterpret_cast<uintptr_t>(logp) |
          reinterpret_cast<uintptr_t>(rank) | reinterpret_cast<uintptr_t>(entropy) | reinterpret_cast<uintptr_t>(idx) |
          reinterpret_cast<uintptr_t>(val) | reinterpret_cast<uintptr_t>(status)) & 3)
@@ -122,10 +339,29 @@ gem_status gem_logprobs(const float* y, int64_t ldy, int64_t T, int64_t N, float
     DeviceInfo di;
     gem_status st;
     if ((st = device_info(&di)) != GEM_OK) return st;
-    ScoreParams p{y, ldy, N, scale, tokens, logp, rank, entropy, k, idx, val, status ? status : di.status_word};
+    ScoreParams p{y, ldy, N, scale, tokens, logp, rank, entropy, k, 1, idx, val, status ? status : di.status_word};
+    // Few rows: 1024 threads, 8 CTAs a row, each with all of its part in flight.  Else 256 threads, and as many CTAs
+    // a row as give the fewest rounds of the four that an SM holds (a further one costs about as much as a piece).
+    const bool few = T * 8 <= di.num_sms;
+    const int threads = few ? 1024 : 256;
+    const int64_t pieces = (N / 4 + threads * kVec - 1) / (threads * kVec);
+    if (few) {
+        while (p.split < 8 && p.split < pieces) p.split *= 2;
+    } else {
+        const int64_t slots = int64_t(di.num_sms) * 4;
+        double best = 1e30;
+        for (int s : {1, 2, 4, 8}) {
+            if (s > 1 && s > pieces) break;
+            const double cost = static_cast<double>((T * s + slots - 1) / slots) * (static_cast<double>((pieces + s - 1) / s) + 1.0);
+            if (cost < best) {
+                best = cost;
+                p.split = s;
+            }
+        }
+    }
     void* args[] = {&p};
-    return launch_pdl(reinterpret_cast<const void*>(logprobs_kernel), dim3(static_cast<unsigned>(T)), dim3(kThreads), 0,
-                      static_cast<cudaStream_t>(stream), args);
+    const void* fn = few ? reinterpret_cast<const void*>(logprobs_kernel<1024>) : reinterpret_cast<const void*>(logprobs_kernel<256>);
+    return launch_pdl_cluster(fn, dim3(static_cast<unsigned>(T * p.split)), dim3(threads), 0, static_cast<cudaStream_t>(stream), args, p.split);
 }
 
 }  // extern "C"

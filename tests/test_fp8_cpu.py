@@ -151,20 +151,16 @@ def test_gemm_refusals(lib):
 
 
 def test_logprobs_refusals(lib):
-    need = lib.gem_logprobs_workspace(4, 1000, 5)
-
-    def f(y=D, ldy=1000, T=4, N=1000, scale=1.0, tok=D, logp=D, rank=D, ent=D, k=5, idx=D, val=D, ws=D, size=need, status=None):
-        return lib.gem_logprobs(y, ldy, T, N, scale, tok, logp, rank, ent, k, idx, val, ws, size, status, None)
+    def f(y=D, ldy=1000, T=4, N=1000, scale=1.0, tok=D, logp=D, rank=D, ent=D, k=5, idx=D, val=D, status=None):
+        return lib.gem_logprobs(y, ldy, T, N, scale, tok, logp, rank, ent, k, idx, val, status, None)
 
     assert f(T=0) == OK
     assert f(T=-1) == INVALID and f(N=0) == INVALID and f(k=-1) == INVALID and f(N=4, k=5) == INVALID
     assert f(scale=0.0) == INVALID and f(scale=-1.0) == INVALID and f(scale=math.nan) == INVALID and f(scale=math.inf) == INVALID
     assert f(y=None) == INVALID and f(ldy=999) == INVALID and f(idx=None) == INVALID and f(val=None) == INVALID and f(tok=None) == INVALID
-    assert f(k=65) == UNSUPPORTED and f(N=1 << 31, ldy=1 << 31) == UNSUPPORTED and f(T=1 << 31) == UNSUPPORTED
+    assert f(k=65) == UNSUPPORTED and f(N=1 << 31, ldy=1 << 31) == UNSUPPORTED and f(T=1 << 28) == UNSUPPORTED
     assert f(y=BAD) == MISALIGNED and f(tok=BAD) == MISALIGNED and f(logp=BAD) == MISALIGNED and f(val=BAD) == MISALIGNED
-    if need:
-        assert f(ws=None) == WORKSPACE and f(size=need - 1) == WORKSPACE and f(ws=ODD) == MISALIGNED
-    assert need % 256 == 0
+    assert f(rank=BAD) == MISALIGNED and f(ent=BAD) == MISALIGNED and f(idx=BAD) == MISALIGNED and f(status=BAD) == MISALIGNED
 
 
 def test_binding_refuses_other_devices_and_shapes(lib):

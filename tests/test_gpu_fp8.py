@@ -388,8 +388,7 @@ def _mlp(gem, t, T, H, F, V, seed=0):
              gu=t.empty(T, 2 * F, device="cuda"), c2=t.empty(T, F, dtype=f8, device="cuda"), s2=t.empty(T, -(-F // 128), device="cuda"),
              h2=t.empty(T, H, device="cuda"), c3=t.empty(T, H, dtype=f8, device="cuda"), s3=t.empty(T, -(-H // 128), device="cuda"),
              lg=t.empty(T, V, device="cuda"), logp=t.empty(T, device="cuda"), ent=t.empty(T, device="cuda"), rank=t.empty(T, dtype=t.int32, device="cuda"),
-             idx=t.empty(T, 5, dtype=t.int32, device="cuda"), val=t.empty(T, 5, device="cuda"),
-             ws=t.empty(max(1, gem.logprobs_workspace(T, V, 5)), dtype=t.uint8, device="cuda"))
+             idx=t.empty(T, 5, dtype=t.int32, device="cuda"), val=t.empty(T, 5, device="cuda"))
 
     def step(stream=None):
         F_ = d["gu"].shape[1] // 2
@@ -399,7 +398,7 @@ def _mlp(gem, t, T, H, F, V, seed=0):
         gem.fp8_gemm(d["down"], d["down_s"], d["c2"], d["s2"], d["h2"], residual=d["h"], stream=stream)
         gem.rmsnorm_fp8(d["h2"], d["g2"], 1e-6, d["c3"], d["s3"], stream=stream)
         gem.fp8_gemm(d["logits"], d["logits_s"], d["c3"], d["s3"], d["lg"], stream=stream)
-        gem.logprobs(d["lg"], d["tokens"], d["logp"], d["ent"], d["rank"], d["idx"], d["val"], workspace=d["ws"], stream=stream)
+        gem.logprobs(d["lg"], d["tokens"], d["logp"], d["ent"], d["rank"], d["idx"], d["val"], stream=stream)
 
     return d, step
 

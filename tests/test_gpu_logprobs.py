@@ -195,18 +195,12 @@ def test_many_rows(env):
     _check(_run(env, y, tokens, 3), y, tokens, 3)
 
 
-def test_workspace_and_no_rows(env):
+def test_no_rows(env):
     gem, t = env
-    y = _logits(1, 200000, 9)
-    need = gem.logprobs_workspace(1, 200000, 20)
-    ws = t.full((need + 256,), 0xFF, dtype=t.uint8, device="cuda")     # no initialisation is asked for
-    for _ in range(2):
-        _check(_run(env, y, [77], 20, workspace=ws), y, [77], 20)
-    assert (ws[need:] == 0xFF).all()
-    if need:
-        with pytest.raises(gem.GemError):
-            _run(env, y, [77], 20, workspace=ws[:need - 1])
     _run(env, np.zeros((0, 10), np.float32), np.zeros(0, np.int32), 2)
+    y = _logits(3, 50, 1)
+    got = _run(env, y, [1, 2, 3], 50)                    # the list is the whole row
+    _check(got, y, [1, 2, 3], 50)
 
 
 def test_agrees_with_top_k_and_argmax(env):
