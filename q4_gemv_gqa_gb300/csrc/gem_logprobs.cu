@@ -12,13 +12,16 @@
 //
 // Bound by the read of the logits.  A row is one CTA's, or a cluster's, whose CTAs join their sums and lists
 // through shared memory: no workspace, no counters, and an order that depends on the sizes alone.
+#include <mutex>
+#include <set>
+
 #include "gem_tcgen05.cuh"
 
 namespace gem {
 namespace {
 
 constexpr int kMaxTop = 64;
-constexpr int kVec = 8;              // 16-byte loads of a thread in a piece
+constexpr int kVec = 4;              // 16-byte loads of a thread in a piece of 16 values
 constexpr int kHeld = 2048;          // keys that may wait to be sorted
 constexpr float kLowest = -3.402823466e38f;
 
@@ -85,28 +88,67 @@ struct ScoreShared {
     int n;
 };
 
-// The k largest of the first n held keys, in order, into sh.top (0 where there are fewer) and to the front of
-// sh.held.  A key's place is the number of larger ones, counted by 1 to 32 lanes.
+// x[j], without a place in memory for x
+__device__ __forceinline__ float pick(const float (&x)[16], int j) {
+    float a[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a[i] = j & 8 ? x[i + 8] : x[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = j & 4 ? a[i + 4] : a[i];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) a[i] = j & 2 ? a[i + 2] : a[i];
+    return j & 1 ? a[1] : a[0];
+}
+
+// The k largest of the first n held keys (all different), in order, into sh.top and to the front of sh.held; sh.n
+// becomes their number.  A key's place is the number of larger ones, counted by 1 to 32 lanes.  The keys have been
+// written before a barrier; the result may be used at once.
 template <int THREADS>
 __device__ void sort_held(ScoreShared<THREADS>& sh, int n, int k) {
     const int tid = threadIdx.x;
-    __syncthreads();
-    if (tid < kMaxTop) sh.top[tid] = 0;
-    __syncthreads();
-    int lanes = 32;
-    while (lanes > 1 && n * lanes > THREADS) lanes >>= 1;
-    const int part = tid & (lanes - 1), end = (n * lanes + 31) / 32 * 32;
+    int shift = 5;
+    while (shift > 0 && (n << shift) > THREADS) --shift;
+    const int lanes = 1 << shift, part = tid & (lanes - 1), end = ((n << shift) + 31) & ~31;
     for (int at = tid; at < end; at += THREADS) {
-        const int i = at / lanes;
-        const unsigned long long mine = i < n ? sh.held[i] : 0;
+        const int i = at >> shift;
+        const unsigned long long mine = i < n ? sh.held[i] : ~0ull;
         int place = 0;
         for (int j = part; j < n; j += lanes) place += sh.held[j] > mine;
         for (int o = lanes >> 1; o > 0; o >>= 1) place += __shfl_xor_sync(~0u, place, o);
-        if (part == 0 && mine && place < k) sh.top[place] = mine;
+        if (part == 0 && i < n && place < k) sh.top[place] = mine;
     }
     __syncthreads();
-    if (tid < k) sh.held[tid] = sh.top[tid];
+    if (tid < min(n, k)) sh.held[tid] = sh.top[tid];
+    if (tid == 0) sh.n = min(n, k);
     __syncthreads();
+}
+
+// The list of entries v0 .. v1 (16-byte pieces behind `head`) and of `more` single ones, where more came together
+// than can wait (rising or equal values): one entry a thread at a time, sorted as often as need be.
+template <int THREADS>
+__device__ __noinline__ void list_slowly(ScoreShared<THREADS>& sh, const float* row, int head, int64_t v0, int64_t v1, int64_t nv, int more, int k) {
+    const int tid = threadIdx.x;
+    unsigned long long least_key = 0;
+    int n = 0;
+    for (int64_t at = 4 * v0 - (more + 3) / 4 * 4; at < 4 * v1; at += THREADS) {
+        __syncthreads();
+        if (n + THREADS > kHeld) {
+            sort_held(sh, n, k);
+            n = min(n, k);
+            least_key = n == k ? sh.top[k - 1] : 0ull;
+        }
+        if (tid == 0) sh.n = n;
+        __syncthreads();
+        const int64_t j = at + tid;   // below 4 v0: the single entries
+        const int single = static_cast<int>(4 * v0 - j) - 1;
+        if (j < 4 * v1 && (j >= 4 * v0 || single < more)) {
+            const int64_t i = j >= 4 * v0 ? head + j : single < head ? single : 4 * nv + single;
+            const unsigned long long key = key_of(row[i], i);
+            if (key > least_key) sh.held[atomicAdd(&sh.n, 1)] = key;
+        }
+        __syncthreads();
+        n = sh.n;
+    }
 }
 
 template <int THREADS>
@@ -120,16 +162,31 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     // 16-byte pieces from the first aligned entry on; the entries before and after them are the first CTA's
     const int head = static_cast<int>(min(static_cast<int64_t>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) / 4 & 3), p.N));
     const int64_t nv = (p.N - head) / 4;
-    const int rest = static_cast<int>(p.N - head - 4 * nv);
+    const int more = part == 0 ? head + static_cast<int>(p.N - head - 4 * nv) : 0;
     const int64_t per = (nv + p.split - 1) / p.split, v0 = min(nv, per * part), v1 = min(nv, v0 + per);
     const float c = p.scale * 1.4426950408889634f;
     const int k = p.k;
     pdl_wait_trigger();
 
+    // This thread's 16-byte pieces are first, first + THREADS, .. of the CTA's `len`; the next ones are on their way
+    // while it works on the last (through shared memory, two or three deep, they came no faster).
+    const float4* from = reinterpret_cast<const float4*>(row + head) + v0 + tid;
+    const int len = static_cast<int>(v1 - v0);
+    float4 next[kVec];
+    auto request = [&](int at) {
+        if (at + THREADS * kVec <= len) {
+#pragma unroll
+            for (int u = 0; u < kVec; ++u) next[u] = __ldcs(from + at + u * THREADS);
+        } else {
+#pragma unroll
+            for (int u = 0; u < kVec; ++u)
+                next[u] = at + u * THREADS + tid < len ? __ldcs(from + at + u * THREADS) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        }
+    };
+    request(0);
     const int tok = p.tokens ? p.tokens[t] : -1;
     const bool given = tok >= 0 && tok < p.N, count = given && p.rank;
     const float target = given ? row[tok] : 0.f;
-    const float least = target == target ? target : -INFINITY;   // every piece may hold entries above a NaN
     auto is_above = [&](float v, int64_t i) {
         if (target != target) return v == v || i < tok;
         return v > target || (v == target && i < tok);
@@ -138,47 +195,60 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     Sums sum{kLowest, 0.f, 0.f};
     int above = 0;
     unsigned long long least_key = 0;   // the list's least key; what is not above it is not looked at
+    float floor_v = 0.f;                // its value;
+    bool all = true;                    // or none yet: NaN and -inf may be listed
     if (tid == 0) sh.n = 0;
     __syncthreads();
-    if (part == 0 && tid < head + rest) {
+    if (tid < more) {
         const int64_t i = tid < head ? tid : 4 * nv + tid;
         const float v = row[i], m = fmaxf(v, kLowest), d = (v - m) * c, w = exp2_fast(d);
         sum = {m, w, fmaxf(d, -200.f) * (d < -200.f ? 0.f : w)};
         above += count && is_above(v, i);
         if (k) sh.held[atomicAdd(&sh.n, 1)] = key_of(v, i);
     }
-    bool first = true;
-    for (int64_t at = v0; at < v1; at += THREADS * kVec) {
+    // of entries before the given token equal ones are above it too
+    const float bound_before = target, bound_after = nextafterf(target, INFINITY);
+    int turn = 0, look_at = k == 0 ? 1 << 30 : k > W ? 0 : 1;
+    for (int at = 0; at < len; at += THREADS * kVec, ++turn) {
         float x[4 * kVec];
-        const int64_t mine = at + tid;
 #pragma unroll
-        for (int u = 0; u < kVec; ++u) {
-            float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-            if (mine + u * THREADS < v1) v = __ldcs(reinterpret_cast<const float4*>(row + head) + mine + u * THREADS);
-            x[4 * u] = v.x, x[4 * u + 1] = v.y, x[4 * u + 2] = v.z, x[4 * u + 3] = v.w;
-        }
-        const int have = mine >= v1 ? 0 : static_cast<int>(min((v1 - mine + THREADS - 1) / THREADS, static_cast<int64_t>(kVec)));   // loads that are there
+        for (int u = 0; u < kVec; ++u) x[4 * u] = next[u].x, x[4 * u + 1] = next[u].y, x[4 * u + 2] = next[u].z, x[4 * u + 3] = next[u].w;
+        request(at + THREADS * kVec);
         float most = x[0];
 #pragma unroll
         for (int j = 1; j < 4 * kVec; ++j) most = fmaxf(most, x[j]);
         if (most > sum.m) raise(sum, most, c);
-        float s[4] = {}, e[4] = {};
+        float2 s2 = make_float2(0.f, 0.f), e2 = s2;
+        const float2 m2 = make_float2(-sum.m, -sum.m), c2 = make_float2(c, c);
 #pragma unroll
-        for (int j = 0; j < 4 * kVec; ++j) {
-            const float d = (x[j] - sum.m) * c, w = exp2_fast(d);
-            s[j & 3] += w;
-            e[j & 3] = fmaf(fmaxf(d, -200.f), w, e[j & 3]);   // w is 0 there; a NaN is in s
+        for (int j = 0; j < 4 * kVec; j += 2) {
+            const float2 d = fmul2(fadd2(make_float2(x[j], x[j + 1]), m2), c2), w = make_float2(exp2_fast(d.x), exp2_fast(d.y));
+            s2 = fadd2(s2, w);
+            e2 = ffma2(make_float2(fmaxf(d.x, -200.f), fmaxf(d.y, -200.f)), w, e2);   // w is 0 there; a NaN is in s
         }
-        sum.s += (s[0] + s[1]) + (s[2] + s[3]);
-        sum.e += (e[0] + e[1]) + (e[2] + e[3]);
-        auto index = [&](int j) { return head + 4 * (mine + (j >> 2) * THREADS) + (j & 3); };
-        if (count && !(most < least)) {
+        sum.s += s2.x + s2.y;
+        sum.e += e2.x + e2.y;
+        // bit j: entry j is there
+        const int left = len - at - tid;
+        const uint32_t valid = left <= 0 ? 0u : left > (kVec - 1) * THREADS ? 0xffffu : (1u << 4 * ((left + THREADS - 1) / THREADS)) - 1;
+        auto index = [&](int j) { return head + 4 * (v0 + at + (j >> 2) * THREADS + tid) + (j & 3); };
+        auto at_least = [&](float bound) {
+            uint32_t m = 0;
 #pragma unroll
-            for (int j = 0; j < 4 * kVec; ++j) above += (j >> 2) < have && is_above(x[j], index(j));
+            for (int j = 0; j < 4 * kVec; ++j) m |= x[j] >= bound ? 1u << j : 0u;
+            return m;
+        };
+        if (count) {
+            const int64_t low = head + 4 * (v0 + at), high = low + 4 * THREADS * kVec;
+            if (target != target || (tok >= low && tok < high)) {   // one by one: here an entry's place counts
+                for (int j = 0; j < 4 * kVec; ++j) above += (valid >> j & 1) && is_above(pick(x, j), index(j));
+            } else {
+                const float bound = tok >= high ? bound_before : bound_after;
+                if (!(most < bound)) above += __popc(at_least(bound) & valid);
+            }
         }
         if (k == 0) continue;
-        uint32_t bar = static_cast<uint32_t>(least_key >> 32);
-        if (first) {
+        if (turn == 0) {
             // At least k entries of the piece reach the k-th largest of the warps' maxima, or, with a longer list than
             // warps, the least of the warps' q-th largest lane maxima, q = ceil(k / warps).
             uint32_t o = most > -INFINITY ? order_of(most) : 0u, w = 0;   // -inf may stand for a NaN, or for no entry
@@ -189,6 +259,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
             if (lane == 0) sh.largest[warp] = w;
             __syncthreads();
             const uint32_t b = lane < W ? sh.largest[lane] : 0u;
+            uint32_t bar;
             if (k > W) {
                 bar = __reduce_min_sync(~0u, lane < W ? b : ~0u);
             } else {
@@ -200,59 +271,33 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
                 bar = __reduce_max_sync(~0u, lane < W && larger == k - 1 ? b : 0u);
             }
             least_key = bar ? (static_cast<unsigned long long>(bar) << 32) - 1 : 0ull;
-            bar = static_cast<uint32_t>((least_key + 1) >> 32);
+            all = bar == 0;
+            floor_v = all ? 0.f : value_of(bar);
         }
-        const bool all = bar == 0;   // NaN and -inf may be listed
-        const float floor_v = all ? 0.f : value_of(bar);
-        const bool look = have && (all || !(most < floor_v));
-        if (__syncthreads_or(look)) {
-            uint32_t mask = 0;
-            if (look)
-#pragma unroll
-                for (int j = 0; j < 4 * kVec; ++j) mask |= ((j >> 2) < have && (all || x[j] >= floor_v)) ? 1u << j : 0u;
-            const int before = sh.n;
-            __syncthreads();
-            int pos = mask ? atomicAdd(&sh.n, __popc(mask)) : 0;
-            __syncthreads();
-            int n = sh.n;
-            if (n <= kHeld) {
-                while (mask) {
-                    const int j = __ffs(mask) - 1;
-                    mask &= mask - 1;
-                    const int64_t i = index(j);
-                    const unsigned long long key = key_of(__ldg(row + i), i);
-                    sh.held[pos++] = key > least_key ? key : 0ull;
-                }
-            } else {
-                // more than fit (equal or rising values): one entry a thread at a time, sorted as often as need be
-                n = before;
-                for (int j = 0; j < 4 * kVec; ++j) {
-                    if (n + THREADS > kHeld) {
-                        sort_held(sh, n, k);
-                        n = min(n, k);
-                        least_key = n == k ? sh.top[k - 1] : 0ull;
-                    }
-                    __syncthreads();
-                    if (tid == 0) sh.n = n;
-                    __syncthreads();
-                    if (mask >> j & 1) {
-                        const int64_t i = index(j);
-                        const unsigned long long key = key_of(__ldg(row + i), i);
-                        if (key > least_key) sh.held[atomicAdd(&sh.n, 1)] = key;
-                    }
-                    __syncthreads();
-                    n = sh.n;
+        if (all || most >= floor_v) {
+            for (uint32_t mask = (all ? ~0u : at_least(floor_v)) & valid; mask; mask &= mask - 1) {
+                const int j = __ffs(mask) - 1;
+                const unsigned long long key = key_of(pick(x, j), index(j));
+                if (key > least_key) {
+                    const int pos = atomicAdd(&sh.n, 1);
+                    if (pos < kHeld) sh.held[pos] = key;   // else all is listed again, below
                 }
             }
-            // the list so far raises the bar: after the first piece, and when many have come together
-            if ((first || n > kHeld / 4) && n >= k) {
+        }
+        // The list so far raises the bar, after 1 (2), 4, 8, 16, .. pieces: then about k entries pass it in as many again.
+        if (turn == look_at) {
+            look_at = 2 * turn + 1;
+            __syncthreads();
+            const int n = sh.n;
+            if (n <= kHeld && n > k) {
                 sort_held(sh, n, k);
-                if (tid == 0) sh.n = k;
                 least_key = sh.top[k - 1];
+                const uint32_t bar = static_cast<uint32_t>(least_key >> 32);
+                all = bar == 0;
+                floor_v = all ? 0.f : value_of(bar);
             }
             __syncthreads();
         }
-        first = false;
     }
 
     for (int o = 16; o > 0; o >>= 1) {
@@ -261,7 +306,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     }
     if (lane == 0) sh.sums[warp] = sum, sh.above[warp] = above;
     __syncthreads();
-    if (k) sort_held(sh, sh.n, k);
+    if (k) {
+        if (sh.n > kHeld) list_slowly(sh, row, head, v0, v1, nv, more, k);
+        // a part of a row hands on a short list as it is
+        if (p.split == 1 || sh.n > max(2 * k, 16)) sort_held(sh, sh.n, k);
+    }
     if (warp == 0) {
         sum = lane < W ? sh.sums[lane] : Sums{kLowest, 0.f, 0.f};
         above = lane < W ? sh.above[lane] : 0;
@@ -273,6 +322,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     }
     __syncthreads();
     if (p.split > 1) {
+        int listed = 0;
         cluster_sync();
         if (part == 0) {
             if (warp == 0) {
@@ -288,18 +338,28 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
                     above += __shfl_xor_sync(~0u, above, o);
                 }
             }
-            for (int i = tid; i < p.split * k; i += THREADS) {
-                const uint32_t a = peer_addr(&sh.top[i % k], i / k);
-                sh.held[i] = static_cast<unsigned long long>(__float_as_uint(ld_peer(a + 4))) << 32 | __float_as_uint(ld_peer(a));
+            // the parts' lists one behind the other (this one's is in its place); a warp fetches every W-th
+            const int m = lane < p.split ? __float_as_int(ld_peer(peer_addr(&sh.n, lane))) : 0;
+            int n = m;   // up to and with part `lane`
+            for (int o = 1; o < 32; o <<= 1) {
+                const int other = __shfl_up_sync(~0u, n, o);
+                n += lane >= o ? other : 0;
             }
+            for (int r = 1 + warp; r < p.split; r += W) {
+                const int size = __shfl_sync(~0u, m, r), to = __shfl_sync(~0u, n, r - 1);
+                for (int i = lane; i < size; i += 32) {
+                    const uint32_t a = peer_addr(&sh.held[i], r);
+                    sh.held[to + i] = static_cast<unsigned long long>(__float_as_uint(ld_peer(a + 4))) << 32 | __float_as_uint(ld_peer(a));
+                }
+            }
+            n = __shfl_sync(~0u, n, 31);
+            listed = n;
             __syncthreads();
             if (tid == 0) sh.all = sum, sh.total = above;
         }
-        // the lists of the others are read before the first CTA's is overwritten by the sort, and before they leave
-        cluster_sync();
+        cluster_sync();   // what the others hold has been read
         if (part != 0) return;
-        if (k) sort_held(sh, p.split * k, k);
-        __syncthreads();
+        if (k) sort_held(sh, listed, k);
     }
     sum = sh.all;
     // no finite logit, or one that is not a number
@@ -340,19 +400,25 @@ gem_status gem_logprobs(const float* y, int64_t ldy, int64_t T, int64_t N, float
     gem_status st;
     if ((st = device_info(&di)) != GEM_OK) return st;
     ScoreParams p{y, ldy, N, scale, tokens, logp, rank, entropy, k, 1, idx, val, status ? status : di.status_word};
-    // Few rows: 1024 threads, 8 CTAs a row, each with all of its part in flight.  Else 256 threads, and as many CTAs
-    // a row as give the fewest rounds of the four that an SM holds (a further one costs about as much as a piece).
-    const bool few = T * 8 <= di.num_sms;
-    const int threads = few ? 1024 : 256;
+    // Few rows: 16 CTAs of 512 threads a row (a cluster of that size wants the kernel's consent).  Else 256 threads, and
+    // as many CTAs a row as give the fewest rounds of the four that an SM holds; beginning and joining cost a CTA about
+    // as much as 12 pieces.
+    const bool few = T <= 4;
+    const int threads = few ? 512 : 256;
     const int64_t pieces = (N / 4 + threads * kVec - 1) / (threads * kVec);
+    const void* fn = few ? reinterpret_cast<const void*>(logprobs_kernel<512>) : reinterpret_cast<const void*>(logprobs_kernel<256>);
     if (few) {
-        while (p.split < 8 && p.split < pieces) p.split *= 2;
+        while (p.split < 16 && p.split < pieces) p.split *= 2;
+        static std::mutex mu;
+        static std::set<int> done;
+        std::lock_guard<std::mutex> lk(mu);
+        if (done.insert(di.device).second) GEM_CUDA_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
     } else {
         const int64_t slots = int64_t(di.num_sms) * 4;
         double best = 1e30;
         for (int s : {1, 2, 4, 8}) {
             if (s > 1 && s > pieces) break;
-            const double cost = static_cast<double>((T * s + slots - 1) / slots) * (static_cast<double>((pieces + s - 1) / s) + 1.0);
+            const double cost = static_cast<double>((T * s + slots - 1) / slots) * (static_cast<double>((pieces + s - 1) / s) + 12.0);
             if (cost < best) {
                 best = cost;
                 p.split = s;
@@ -360,7 +426,6 @@ gem_status gem_logprobs(const float* y, int64_t ldy, int64_t T, int64_t N, float
         }
     }
     void* args[] = {&p};
-    const void* fn = few ? reinterpret_cast<const void*>(logprobs_kernel<1024>) : reinterpret_cast<const void*>(logprobs_kernel<256>);
     return launch_pdl_cluster(fn, dim3(static_cast<unsigned>(T * p.split)), dim3(threads), 0, static_cast<cudaStream_t>(stream), args, p.split);
 }
 
