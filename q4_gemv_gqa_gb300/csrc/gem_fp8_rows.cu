@@ -58,10 +58,25 @@ __device__ __forceinline__ uint32_t decide_x4(uint32_t lo, uint32_t hi, const do
     return out;
 }
 
-__device__ __forceinline__ uint32_t abs_bits(float4 v) {
-    return max(max(__float_as_uint(fabsf(v.x)), __float_as_uint(fabsf(v.y))),
-               max(__float_as_uint(fabsf(v.z)), __float_as_uint(fabsf(v.w))));
+// Four values as two packed pairs: an instruction does two of them.
+struct Four {
+    float2 a, b;
+};
+__device__ __forceinline__ Four four(float4 v) { return {make_float2(v.x, v.y), make_float2(v.z, v.w)}; }
+__device__ __forceinline__ Four four(float v) { return {make_float2(v, v), make_float2(v, v)}; }
+__device__ __forceinline__ float4 flat(Four v) { return make_float4(v.a.x, v.a.y, v.b.x, v.b.y); }
+__device__ __forceinline__ Four operator+(Four x, Four y) { return {fadd2(x.a, y.a), fadd2(x.b, y.b)}; }
+__device__ __forceinline__ Four operator*(Four x, Four y) { return {fmul2(x.a, y.a), fmul2(x.b, y.b)}; }
+__device__ __forceinline__ Four fma4(Four x, Four y, Four z) { return {ffma2(x.a, y.a, z.a), ffma2(x.b, y.b, z.b)}; }
+__device__ __forceinline__ uint32_t e4m3x4(Four v) { return e4m3x4(v.a.x, v.a.y, v.b.x, v.b.y); }
+
+// bits of the largest magnitude; a NaN is larger than any
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
+    return r;
 }
+__device__ __forceinline__ uint32_t abs_bits(Four v) { return __float_as_uint(max_nan(max_nan(v.a.x, v.a.y), max_nan(v.b.x, v.b.y))); }
 
 // ---- sums to twice the precision (Dekker's and Knuth's error-free sums and products) ----------
 struct Pair {
@@ -71,22 +86,25 @@ __device__ __forceinline__ Pair two_sum(float a, float b) {
     const float s = a + b, t = s - a;
     return {s, (a - (s - t)) + (b - t)};
 }
-__device__ __forceinline__ Pair add(Pair a, Pair b) {
+__device__ __forceinline__ Pair add(Pair a, Pair b) {   // the low part is not kept small against the high one
     const Pair s = two_sum(a.hi, b.hi);
-    const float lo = s.lo + (a.lo + b.lo), hi = s.hi + lo;
-    return {hi, lo - (hi - s.hi)};
+    return {s.hi, s.lo + (a.lo + b.lo)};
 }
-__device__ __forceinline__ void add_square(Pair& s, float v) {
-    const float p = v * v;
-    const Pair t = two_sum(s.hi, p);
-    s.hi = t.hi;
-    s.lo += t.lo + fmaf(v, v, -p);
+// four sums at once, of the squares of v
+struct Pairs {
+    Four hi, lo;
+};
+__device__ __forceinline__ void add_squares(Pairs& s, Four v) {
+    const Four minus = four(-1.f), p = v * v, e = fma4(v, v, p * minus);   // v^2 = p + e
+    const Four t = s.hi + p, u = fma4(s.hi, minus, t), w = fma4(u, minus, t);
+    // the sum's error: (hi - (t - u)) + (p - u)
+    s.lo = s.lo + (fma4(w, minus, s.hi) + fma4(u, minus, p)) + e;
+    s.hi = t;
 }
 
-// 1 / sqrt(s / H + eps) to about 2^-43
-__device__ __forceinline__ Pair inv_rms(Pair s, float H, float eps) {
-    const float q0 = __fdiv_rn(s.hi, H);
-    const float q1 = __fdiv_rn(fmaf(-q0, H, s.hi) + s.lo, H);
+// 1 / sqrt(s / H + eps) to about 2^-43; 1 / H as a pair
+__device__ __forceinline__ Pair inv_rms(Pair s, Pair one_h, float eps) {
+    const float q0 = s.hi * one_h.hi, q1 = fmaf(s.hi, one_h.hi, -q0) + fmaf(s.hi, one_h.lo, s.lo * one_h.hi);
     Pair q = two_sum(q0, eps);
     q.lo += q1;
     const float r = rsqrtf(q.hi), a = r * r, b = fmaf(r, r, -a);
@@ -103,6 +121,8 @@ struct NormParams {
     int64_t T; int H;
     const float* gamma;
     float eps;
+    Pair one_h;             // 1 / H
+    int fold;               // half of the power of two that the warps of a row fit in
     uint8_t* codes; int64_t ldc;
     float* scales; int64_t lds;
 };
@@ -120,97 +140,89 @@ __device__ __noinline__ uint32_t norm64_codes(uint32_t lo, uint32_t hi, float4 h
     return decide_x4(lo, hi, y, k);
 }
 
-// One CTA of ceil(blocks / NB) warps a row, rows dealt out round robin; a lane holds NB pieces of four
-// values.  PIPE: it also holds gamma for all rows, and the next row's loads are in flight while it sums
-// this one's (rows too long for the registers of that are read when their turn comes).
-template <int NB, bool PIPE, int THREADS>
-__global__ void __launch_bounds__(THREADS) rmsnorm_fp8_kernel(const NormParams p) {
-    __shared__ Pair part[2][32];
+// One CTA of ceil(blocks / NB) warps a row; a lane holds NB pieces of four values.  What concerns a block and not its
+// values (scale, bounds) is done for the warp's NB blocks at once, a lane each.
+template <int NB, int THREADS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS) rmsnorm_fp8_kernel(const NormParams p) {
+    __shared__ Pair part[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     auto col = [&](int i) { return (warp + i * nw) * 128 + lane * 4; };
-    const float4 zero4 = make_float4(0.f, 0.f, 0.f, 0.f);
     auto gamma = [&](int i) {
-        return p.gamma && col(i) < p.H ? __ldg(reinterpret_cast<const float4*>(p.gamma + col(i))) : make_float4(1.f, 1.f, 1.f, 1.f);
+        return p.gamma && col(i) < p.H ? four(__ldg(reinterpret_cast<const float4*>(p.gamma + col(i)))) : four(1.f);
     };
-    float4 gs[PIPE ? NB : 1], nx[NB], nr[NB];
-    auto request = [&](int64_t t) {
-#pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            nx[i] = nr[i] = zero4;
-            if (col(i) < p.H) {
-                nx[i] = __ldcs(reinterpret_cast<const float4*>(p.x + t * p.ldx + col(i)));
-                if (p.res) nr[i] = __ldcs(reinterpret_cast<const float4*>(p.res + t * p.ldr + col(i)));
-            }
-        }
-    };
+    const int64_t t = blockIdx.x;
     pdl_wait_trigger();
-    if (PIPE) {
+    Four h[NB], res[NB];
 #pragma unroll
-        for (int i = 0; i < NB; ++i) gs[i] = gamma(i);
-        request(blockIdx.x);
-    }
-    int turn = 0;
-    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, turn ^= 1) {
-        if (!PIPE) request(t);
-        float4 h[NB];
-        Pair s{0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            h[i] = make_float4(nx[i].x + nr[i].x, nx[i].y + nr[i].y, nx[i].z + nr[i].z, nx[i].w + nr[i].w);
-            if (p.out && col(i) < p.H) *reinterpret_cast<float4*>(p.out + t * p.ldo + col(i)) = h[i];
-            add_square(s, h[i].x);
-            add_square(s, h[i].y);
-            add_square(s, h[i].z);
-            add_square(s, h[i].w);
+    for (int i = 0; i < NB; ++i) {   // all loads before their use
+        h[i] = res[i] = four(0.f);
+        if (col(i) < p.H) {
+            h[i] = four(__ldcs(reinterpret_cast<const float4*>(p.x + t * p.ldx + col(i))));
+            if (p.res) res[i] = four(__ldcs(reinterpret_cast<const float4*>(p.res + t * p.ldr + col(i))));
         }
-        if (PIPE && t + gridDim.x < p.T) request(t + gridDim.x);
+    }
+    Pairs sum{four(0.f), four(0.f)};
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
+    for (int i = 0; i < NB; ++i) {
+        h[i] = h[i] + res[i];
+        if (p.out && col(i) < p.H) *reinterpret_cast<float4*>(p.out + t * p.ldo + col(i)) = flat(h[i]);
+        add_squares(sum, h[i]);
+    }
+    Pair s = add(add({sum.hi.a.x, sum.lo.a.x}, {sum.hi.a.y, sum.lo.a.y}), add({sum.hi.b.x, sum.lo.b.x}, {sum.hi.b.y, sum.lo.b.y}));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        s = add(s, {__shfl_xor_sync(~0u, s.hi, o), __shfl_xor_sync(~0u, s.lo, o)});
+    if (nw > 1) {
+        if (lane == 0) part[warp] = s;
+        __syncthreads();
+        s = lane < nw ? part[lane] : Pair{0.f, 0.f};
+        for (int o = p.fold; o > 0; o >>= 1)
             s = add(s, {__shfl_xor_sync(~0u, s.hi, o), __shfl_xor_sync(~0u, s.lo, o)});
-        if (nw > 1) {
-            // two buffers in turn: a warp writes one again only behind the next row's barrier
-            if (lane == 0) part[turn][warp] = s;
-            __syncthreads();
-            s = lane < nw ? part[turn][lane] : Pair{0.f, 0.f};
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                s = add(s, {__shfl_xor_sync(~0u, s.hi, o), __shfl_xor_sync(~0u, s.lo, o)});
-        }
-        const Pair r = inv_rms(s, static_cast<float>(p.H), p.eps);
-        const bool finite = s.hi < __int_as_float(kInfBits);   // false for NaN too
-#pragma unroll
-        for (int i = 0; i < NB; ++i) {
-            const int c = col(i);
-            if (c - lane * 4 >= p.H) break;   // no such block (the same for the warp)
-            const float4 g = PIPE ? gs[i] : gamma(i);
-            float4 v = make_float4(h[i].x * g.x, h[i].y * g.y, h[i].z * g.z, h[i].w * g.w);
-            if (c >= p.H) v = zero4;
-            const uint32_t mb = __reduce_max_sync(~0u, abs_bits(v));
-            const float m = __uint_as_float(mb) * r.hi, m0 = m * (1.f - kNormErr), m1 = m * (1.f + kNormErr);
-            uint32_t code = 0;
-            float scale = 0.f;
-            if (!finite || mb >= kInfBits || !(m1 < __int_as_float(kInfBits))) {
-                scale = __int_as_float(0x7fffffff);
-            } else if (m1 >= kTiny) {
-                int k = scale_exp(fmaxf(m0, kTiny));
-                bool zero = false;
-                if (k != scale_exp(m1) || m0 < kTiny) {   // next to a border
-                    const double top = c < p.H ? norm64_top(h[i], g, r) : 0.0;
-                    zero = !__any_sync(~0u, top >= static_cast<double>(kTiny));
-                    if (__any_sync(~0u, top > static_cast<double>(kMaxCode) * static_cast<double>(pow2f(k)))) ++k;
-                }
-                if (!zero) {
-                    scale = pow2f(k);
-                    const float f = r.hi * pow2f(-k), f0 = f * (1.f - kNormErr), f1 = f * (1.f + kNormErr);
-                    const uint32_t lo = e4m3x4(v.x * f0, v.y * f0, v.z * f0, v.w * f0);
-                    code = e4m3x4(v.x * f1, v.y * f1, v.z * f1, v.w * f1);
-                    if (lo != code) code = norm64_codes(lo, code, h[i], g, r, k);
-                }
-            }
-            if (c < p.H) *reinterpret_cast<uint32_t*>(p.codes + t * p.ldc + c) = code;
-            if (lane == 0) p.scales[t * p.lds + (c >> 7)] = scale;
-        }
+        s = {__shfl_sync(~0u, s.hi, 0), __shfl_sync(~0u, s.lo, 0)};
     }
+    const Pair r = inv_rms(s, p.one_h, p.eps);
+    const bool finite = s.hi < __int_as_float(kInfBits);   // false for NaN too
+
+    // (gamma is read from the caches where it is used, twice a row: registers for more rows at once count for more)
+    uint32_t mb = 0;   // lane i: the largest of block i
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+        const uint32_t most = __reduce_max_sync(~0u, col(i) < p.H ? abs_bits(h[i] * gamma(i)) : 0u);
+        if (lane == i) mb = most;
+    }
+    const float m = __uint_as_float(mb) * r.hi, m0 = m * (1.f - kNormErr), m1 = m * (1.f + kNormErr);
+    const bool bad = !finite || !(m1 < __int_as_float(kInfBits)), some = !bad && m1 >= kTiny;
+    int k = some ? scale_exp(fmaxf(m0, kTiny)) : 0;
+    float scale = bad ? __int_as_float(0x7fffffff) : some ? pow2f(k) : 0.f;
+    unsigned near = __ballot_sync(~0u, some && (k != scale_exp(m1) || m0 < kTiny));   // blocks next to a border of the scale
+    while (near) {
+        const int b = __ffs(near) - 1;
+        near &= near - 1;
+        double top = 0.0;
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+            if (i == b && col(i) < p.H) top = norm64_top(flat(h[i]), flat(gamma(i)), r);
+        const int kb = __shfl_sync(~0u, k, b);
+        const bool zero = !__any_sync(~0u, top >= static_cast<double>(kTiny));
+        const bool over = __any_sync(~0u, top > static_cast<double>(kMaxCode) * static_cast<double>(pow2f(kb)));
+        if (lane == b) k += over, scale = zero ? 0.f : pow2f(k);
+    }
+    const float f = scale > 0.f ? r.hi * pow2f(-k) : 0.f;   // 0: codes 0 (a NaN scale is not above 0)
+#pragma unroll
+    for (int i = 0; i < NB; ++i) {
+        const int c = col(i);
+        const float fi = __shfl_sync(~0u, f, i);
+        const Four g = gamma(i), v = h[i] * g;
+        const uint32_t lo = e4m3x4(v * four(fi * (1.f - kNormErr)));
+        uint32_t code = e4m3x4(v * four(fi * (1.f + kNormErr)));
+        if (__any_sync(~0u, lo != code)) {
+            const int ki = __shfl_sync(~0u, k, i);
+            if (lo != code) code = norm64_codes(lo, code, flat(h[i]), flat(g), r, ki);
+        }
+        if (c < p.H) *reinterpret_cast<uint32_t*>(p.codes + t * p.ldc + c) = fi > 0.f ? code : 0u;
+    }
+    const int block = warp + lane * nw;
+    if (lane < NB && block * 128 < p.H) p.scales[t * p.lds + block] = scale;
 }
 
 // ---- the gated activation, or a plain row --------------------------------------------------------
@@ -227,20 +239,39 @@ constexpr float kGateLow = -83.f;    // the gate is 0 below it (e^83 is still fi
 constexpr double kGelu1 = 1.5957691216057308;                  // 2 sqrt(2 / pi)
 constexpr double kGelu3 = kGelu1 * 0.044715;
 
-// act(x) * u and a bound of its relative error.  e^-z is 2^(a + b), a + b = -z log2(e) as a pair, so that
-// its error stays 2^-22 for any z; then a reciprocal and two products.  GELU's z itself is off by 2^-22 |z|.
+// act(x) * u of four values, and a bound of their relative error: 9.5e-7, and for GELU, whose z is itself off by 2^-22
+// of it, 2.4e-7 max(-z, 1/2) more (above 0 the gate's own flatness holds z's error down).  e^-z is 2^(a + b), a + b = -z log2(e) as a pair, so that its error stays
+// 2^-22 for any z; then a reciprocal and two products.
 template <int ACT>
-__device__ __forceinline__ float gated(float x, float u, float& err) {
-    const float g = ACT == 1 ? x * fmaf(x * x, static_cast<float>(kGelu3), static_cast<float>(kGelu1)) : x;
-    const float z = fminf(fmaxf(g, -100.f), 100.f);   // beyond them the gate is 0 or 1 all the same
-    err = ACT == 1 ? fmaf(fabsf(z), 2.4e-7f, 9.5e-7f) : 9.5e-7f;
-    const float l2e = 1.4426950408889634f, a = -z * l2e;
-    const float b = fmaf(-z, l2e, -a) - z * 1.925963033500947e-8f;
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(a));
-    e = fmaf(e, b * 0.6931471805599453f, e);
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-    return x * (z < kGateLow ? 0.f : x == x ? r : x) * u;
+__device__ __forceinline__ Four gated(Four x, Four u, float& err) {
+    Four z = x;
+    if (ACT == 1) z = x * fma4(x * x, four(static_cast<float>(kGelu3)), four(static_cast<float>(kGelu1)));
+    // beyond these the gate is 0 or 1 all the same (and so for a NaN, which the product with x keeps)
+    auto held = [](float v) { return v >= kGateLow ? fminf(v, 100.f) : -200.f; };
+    z = {make_float2(held(z.a.x), held(z.a.y)), make_float2(held(z.b.x), held(z.b.y))};
+    err = 9.5e-7f;
+    if (ACT == 1) {
+        auto depth = [](float v) { return v > -150.f ? -v : 0.f; };   // a gate of 0 is exact
+        err = fmaf(fmaxf(fmaxf(fmaxf(depth(z.a.x), depth(z.a.y)), fmaxf(depth(z.b.x), depth(z.b.y))), 0.5f), 2.4e-7f, err);
+    }
+    const float l2e = 1.4426950408889634f;
+    const Four a = z * four(-l2e);
+    const Four b = fma4(z, four(-1.925963033500947e-8f), fma4(z, four(-l2e), a * four(-1.f)));
+    auto exp2_of = [](float v) {
+        float e;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v));
+        return e;
+    };
+    auto inverse = [](float v) {
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+        return r;
+    };
+    Four e{make_float2(exp2_of(a.a.x), exp2_of(a.a.y)), make_float2(exp2_of(a.b.x), exp2_of(a.b.y))};
+    // e (1 + b ln 2) + 1; at z = -200 e is infinite and b tiny, and its inverse 0
+    e = fma4(e, fma4(b, four(0.6931471805599453f), four(1.f)), four(1.f));
+    const Four r{make_float2(inverse(e.a.x), inverse(e.a.y)), make_float2(inverse(e.b.x), inverse(e.b.y))};
+    return x * r * u;
 }
 template <int ACT>
 __device__ __noinline__ double gated64(float x, float u) {
@@ -266,27 +297,23 @@ __global__ void __launch_bounds__(256) quant_fp8_kernel(const QuantParams p) {
     const int first = (blockIdx.y * (blockDim.x >> 5) + warp) * U * 128;
     pdl_wait_trigger();
     if (first >= p.H) return;
-    float4 x[U], u[U];
+    Four x[U], u[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
         const int c = first + i * 128 + lane * 4;
-        x[i] = u[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        x[i] = u[i] = four(0.f);
         if (c < p.H) {
-            x[i] = __ldcs(reinterpret_cast<const float4*>(p.x + t * p.ldx + c));
-            if (ACT != kPlain) u[i] = __ldcs(reinterpret_cast<const float4*>(p.up + t * p.ldu + c));
+            x[i] = four(__ldcs(reinterpret_cast<const float4*>(p.x + t * p.ldx + c)));
+            if (ACT != kPlain) u[i] = four(__ldcs(reinterpret_cast<const float4*>(p.up + t * p.ldu + c)));
         }
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
         const int c = first + i * 128 + lane * 4;
         if (first + i * 128 >= p.H) break;
-        float4 v = x[i], err = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (ACT != kPlain) {
-            v.x = gated<ACT>(x[i].x, u[i].x, err.x);
-            v.y = gated<ACT>(x[i].y, u[i].y, err.y);
-            v.z = gated<ACT>(x[i].z, u[i].z, err.z);
-            v.w = gated<ACT>(x[i].w, u[i].w, err.w);
-        }
+        Four v = x[i];
+        float err = 0.f;
+        if (ACT != kPlain) v = gated<ACT>(x[i], u[i], err);
         const uint32_t mb = __reduce_max_sync(~0u, abs_bits(v));
         const float m = __uint_as_float(mb);
         uint32_t code = 0;
@@ -296,28 +323,23 @@ __global__ void __launch_bounds__(256) quant_fp8_kernel(const QuantParams p) {
         } else if (ACT == kPlain) {
             if (m >= kTiny) {
                 const int k = scale_exp(m);
-                const float f = pow2f(-k);
                 scale = pow2f(k);
-                code = e4m3x4(v.x * f, v.y * f, v.z * f, v.w * f);
+                code = e4m3x4(v * four(pow2f(-k)));
             }
         } else if (m * 1.0001f >= kTiny) {
-            // the largest error of the lanes' bounds stands for the block's
-            const float worst = __uint_as_float(__reduce_max_sync(
-                ~0u, __float_as_uint(fmaxf(fmaxf(err.x, err.y), fmaxf(err.z, err.w)))));
+            const float worst = ACT == 1 ? __uint_as_float(__reduce_max_sync(~0u, __float_as_uint(err))) : err;   // for the block
             int k = scale_exp(fmaxf(m * (1.f - worst), kTiny));
             bool zero = false;
             if (k != scale_exp(fmaxf(m * (1.f + worst), kTiny)) || m * (1.f - worst) < kTiny) {
-                const double top = gated64_top<ACT>(x[i], u[i]);
+                const double top = gated64_top<ACT>(flat(x[i]), flat(u[i]));
                 zero = !__any_sync(~0u, top >= static_cast<double>(kTiny));
                 if (__any_sync(~0u, top > static_cast<double>(kMaxCode) * static_cast<double>(pow2f(k)))) ++k;
             }
             if (!zero) {
                 scale = pow2f(k);
-                const float f = pow2f(-k);
-                v.x *= f, v.y *= f, v.z *= f, v.w *= f;
-                const uint32_t lo = e4m3x4(fmaf(-v.x, err.x, v.x), fmaf(-v.y, err.y, v.y), fmaf(-v.z, err.z, v.z), fmaf(-v.w, err.w, v.w));
-                code = e4m3x4(fmaf(v.x, err.x, v.x), fmaf(v.y, err.y, v.y), fmaf(v.z, err.z, v.z), fmaf(v.w, err.w, v.w));
-                if (lo != code) code = gated64_codes<ACT>(lo, code, x[i], u[i], k);
+                const uint32_t lo = e4m3x4(v * four(pow2f(-k) * (1.f - err)));
+                code = e4m3x4(v * four(pow2f(-k) * (1.f + err)));
+                if (lo != code) code = gated64_codes<ACT>(lo, code, flat(x[i]), flat(u[i]), k);
             }
         }
         if (c < p.H) *reinterpret_cast<uint32_t*>(p.codes + t * p.ldc + c) = code;
@@ -333,12 +355,13 @@ gem_status check_out(const uint8_t* codes, int64_t ldc, const float* scales, int
     return GEM_OK;
 }
 
-template <int NB, bool PIPE, int THREADS>
-gem_status launch_norm(NormParams p, int blocks, int ctas, cudaStream_t stream) {
+template <int NB, int THREADS, int CTAS>
+gem_status launch_norm(NormParams p, int blocks, cudaStream_t stream) {
     const int warps = (blocks + NB - 1) / NB;
+    while (2 * p.fold < warps) p.fold = p.fold ? 2 * p.fold : 1;
     void* args[] = {&p};
-    return launch_pdl(reinterpret_cast<const void*>(rmsnorm_fp8_kernel<NB, PIPE, THREADS>),
-                      dim3(static_cast<unsigned>(std::min<int64_t>(p.T, ctas))), dim3(warps * 32), 0, stream, args);
+    return launch_pdl(reinterpret_cast<const void*>(rmsnorm_fp8_kernel<NB, THREADS, CTAS>), dim3(static_cast<unsigned>(p.T)),
+                      dim3(warps * 32), 0, stream, args);
 }
 
 }  // namespace
@@ -361,13 +384,18 @@ gem_status gem_rmsnorm_fp8(const float* x, int64_t ldx, const float* residual, i
         return GEM_ERR_MISALIGNED;
     DeviceInfo di;
     if ((st = device_info(&di)) != GEM_OK) return st;
-    NormParams p{x, ldx, residual, ldr, out, ldo, T, static_cast<int>(H), gamma, eps, codes, ldc, scales, lds};
+    const double one_h = 1.0 / static_cast<double>(H);
+    const float one_h_hi = static_cast<float>(one_h);
+    NormParams p{x, ldx, residual, ldr, out, ldo, T, static_cast<int>(H), gamma, eps,
+                 {one_h_hi, static_cast<float>(one_h - static_cast<double>(one_h_hi))}, 0, codes, ldc, scales, lds};
     const int blocks = static_cast<int>((H + 127) / 128);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // few rows: a block a warp, the shortest chain; else four, with as many CTAs as stay resident
-    if (blocks <= 32 && T <= di.num_sms) return launch_norm<1, true, 1024>(p, blocks, di.num_sms, s);
-    if (blocks <= 64) return launch_norm<4, true, 512>(p, blocks, di.num_sms * std::max(1, 20 / ((blocks + 3) / 4)), s);
-    return launch_norm<8, false, 1024>(p, blocks, di.num_sms * 4, s);
+    // few rows: a block a warp, the shortest chain; else four, in so few registers that three rows are in work on an SM
+    // (4096 x 5376: 68 us; two rows 81; one, with the next row's loads ahead in 122 registers, 76)
+    if (blocks <= 32 && T <= di.num_sms) return launch_norm<1, 1024, 1>(p, blocks, s);
+    if (blocks <= 48) return launch_norm<4, 384, 3>(p, blocks, s);
+    if (blocks <= 128) return launch_norm<4, 1024, 1>(p, blocks, s);
+    return launch_norm<8, 1024, 1>(p, blocks, s);
 }
 
 gem_status gem_quant_fp8(const float* x, int64_t ldx, const float* up, int64_t ldu, int64_t T, int64_t H, int act,
