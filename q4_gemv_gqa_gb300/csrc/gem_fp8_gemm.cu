@@ -271,7 +271,6 @@ __global__ void __launch_bounds__(kWarps<NT> * 128 + 64) fp8_rows_kernel(const _
 // results, which would otherwise bound it.  Warps 0..7 scale and add (warp w: lane quarter w % 4, columns
 // w / 4 * BN / 2 and on; a thread has one row of x, so a block's scale is one number), warp 8 loads, warp 9 of
 // the first CTA issues the products of both; the last warpgroup gives its registers to the first two.
-constexpr int kTileStages = 5;
 constexpr int kTileChunk = 8;             // blocks whose x scales a warp holds at a time, twice
 constexpr int kTilePitch = 33;            // of a block's 32 scales: spreads the copies over the banks
 constexpr int kTileScales = 2 * kTileChunk * kTilePitch * 4;
@@ -294,19 +293,23 @@ struct TileParams {
 };
 
 struct TileBarriers {
-    uint64_t full[kTileStages], empty[kTileStages], dfull[2], dempty[2], done;
+    uint64_t full[8], empty[8], dfull[4], dempty[4], done;
     uint32_t tmem;
     int dead;
 };
 
 template <int BN>
 constexpr int kTileStage = 16384 + BN * 64;
+// Ring stages: what shared memory holds.  Small tiles need them, or they wait for the memory's latency (with 5 instead
+// of 8 a step of 64 columns takes 0.24 us).
 template <int BN>
-constexpr int kTileSmem = 1024 + kTileStages * kTileStage<BN> + kTileWarps * (4096 + kTileScales);
+constexpr int kTileStages = BN > 128 ? 5 : BN > 64 ? 7 : 8;
+template <int BN>
+constexpr int kTileSmem = 1024 + kTileStages<BN> * kTileStage<BN> + kTileWarps * (4096 + kTileScales);
 
 template <int BN>
 __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmY, const TileParams p) {
-    constexpr int CW = BN / (kTileWarps / 4), STAGE = kTileStage<BN>;
+    constexpr int CW = BN / (kTileWarps / 4), STAGE = kTileStage<BN>, STAGES = kTileStages<BN>, NB = BN > 128 ? 2 : 4;   // buffers of BN columns of tensor memory
     extern __shared__ uint8_t raw[];
     __shared__ TileBarriers bar;
     uint8_t* ring = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -317,11 +320,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
 
     if (tid == 0) {
         bar.dead = 0;
-        for (int i = 0; i < kTileStages; ++i) {
+        for (int i = 0; i < STAGES; ++i) {
             mbar_init(&bar.full[i], 1);
             mbar_init(&bar.empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < NB; ++i) {
             mbar_init(&bar.dfull[i], 1);
             mbar_init(&bar.dempty[i], 2 * kTileWarps);
         }
@@ -353,7 +356,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
             const int t = pair + i * pairs, mt = t % p.mtiles, nt = t / p.mtiles;
             const int m0 = mt * 256 + static_cast<int>(rank) * 128, n0 = nt * BN + static_cast<int>(rank) * (BN / 2);
             for (int b = 0; b < p.kb; ++b) {
-                if (issued >= kTileStages && !warp_wait(&bar.empty[s], phase, p.status, dead)) {
+                if (issued >= STAGES && !warp_wait(&bar.empty[s], phase, p.status, dead)) {
                     ok = false;
                     break;
                 }
@@ -361,7 +364,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
                 warp_tma_2d_pair(base + s * STAGE, &tmX, b * 128, m0, full0 + 8 * s, keep);
                 warp_tma_2d_pair(base + s * STAGE + 16384, &tmW, b * 128, n0, full0 + 8 * s, keep);
                 ++issued;
-                if (++s == kTileStages) s = 0, phase ^= 1;
+                if (++s == STAGES) s = 0, phase ^= 1;
             }
         }
         if (!ok) *dead = 1;
@@ -374,15 +377,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
             int i = 0, s = 0;
             uint32_t phase = 0;
             for (; i < total; ++i) {
-                const int d = i & 1;
-                if (i >= 2 && !warp_wait(&bar.dempty[d], static_cast<uint32_t>((i / 2 - 1) & 1), p.status, dead)) break;
+                const int d = i & (NB - 1);
+                if (i >= NB && !warp_wait(&bar.dempty[d], static_cast<uint32_t>((i / NB - 1) & 1), p.status, dead)) break;
                 if (!warp_wait(&bar.full[s], phase, p.status, dead)) break;
                 tc_fence_after();
-                umma_e4m3<2>(tmem + d * 256, da, db, idesc);
+                umma_e4m3<2>(tmem + d * BN, da, db, idesc);
                 umma_commit<2>(&bar.empty[s]);
                 umma_commit<2>(&bar.dfull[d]);
                 da += STAGE >> 4, db += STAGE >> 4;
-                if (++s == kTileStages) s = 0, phase ^= 1, da = da0, db = db0;
+                if (++s == STAGES) s = 0, phase ^= 1, da = da0, db = db0;
             }
             if (i < total) {
                 *dead = 1;
@@ -396,8 +399,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
         const int col = (warp >> 2) * CW;
         const uint32_t from = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + col;
         const uint32_t empty0 = peer_addr(&bar.dempty[0], 0);
-        float* stage = reinterpret_cast<float*>(ring + kTileStages * STAGE + warp * 4096);
-        float* xs_sh = reinterpret_cast<float*>(ring + kTileStages * STAGE + kTileWarps * 4096 + warp * kTileScales);
+        float* stage = reinterpret_cast<float*>(ring + STAGES * STAGE + warp * 4096);
+        float* xs_sh = reinterpret_cast<float*>(ring + STAGES * STAGE + kTileWarps * 4096 + warp * kTileScales);
         pdl_wait_trigger();
         int i = 0;
         bool ok = true;
@@ -441,8 +444,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
                 wa0 = wa1, wb0 = wb1;
                 wa1 = __ldg(w0row + ahead);
                 if (128 % CW) wb1 = __ldg(w0row + to_b + ahead);
-                const int d = i & 1;
-                if (!warp_wait(&bar.dfull[d], static_cast<uint32_t>((i / 2) & 1), p.status, dead)) {
+                const int d = i & (NB - 1);
+                if (!warp_wait(&bar.dfull[d], static_cast<uint32_t>((i / NB) & 1), p.status, dead)) {
                     *dead = 1;
                     ok = false;
                     break;
@@ -452,7 +455,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
 #pragma unroll
                 for (int u = 0; u < CW / 16; ++u) {
                     float v[16];
-                    tmem_ld<16>(v, from + d * 256 + 16 * u);
+                    tmem_ld<16>(v, from + d * BN + 16 * u);
                     tmem_wait_ld();
                     if (u + 1 == CW / 16) {
                         tc_fence_before();
@@ -515,7 +518,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
     tc_fence_before();
     __syncthreads();
     // the copies of both CTAs are counted on the first one's barriers
-    if (*dead && rank == 0 && warp == kTileWarps && lane == 0) drain_stages(bar.full, kTileStages, max(0, issued - kTileStages), issued - 1);
+    if (*dead && rank == 0 && warp == kTileWarps && lane == 0) drain_stages(bar.full, STAGES, max(0, issued - STAGES), issued - 1);
     __syncwarp();
     cluster_sync();
     if (warp == kTileWarps + 1) {
@@ -535,12 +538,11 @@ gem_status ensure_smem(const void* fn, int device, size_t bytes) {
     return GEM_OK;
 }
 
-template <int NT>
-gem_status launch_rows(GemmParams p, const void* W, int64_t K, const void* x, int64_t ldx, const DeviceInfo& di, cudaStream_t stream) {
-    gem_status st;
-    // Rows of W a tile and CTAs that share a tile's blocks: the shortest time of the busiest SM.  A block costs its
-    // bytes, or its products where it has fewer than 64 rows (they take the same time for any number of rows);
-    // a cluster costs its joining.  Clusters only where one round of them does it: 4 CTAs of one GPC fit 36 times.
+// Rows of W a tile and CTAs that share a tile's blocks: the shortest time of the busiest SM.  A block costs its bytes,
+// or its products where it has fewer than 64 rows (they take the same time for any number of rows); a cluster costs
+// its joining.  Clusters only where one round of them does it: 4 CTAs of one GPC fit 36 times.
+void plan_rows(GemmParams* g, const DeviceInfo& di) {
+    GemmParams& p = *g;
     p.split = 1;
     p.rows = 128;
     double best = 1e30;
@@ -560,6 +562,12 @@ gem_status launch_rows(GemmParams p, const void* W, int64_t K, const void* x, in
         }
     }
     p.tiles = (p.N + p.rows - 1) / p.rows;
+}
+
+template <int NT>
+gem_status launch_rows(GemmParams p, const void* W, int64_t K, const void* x, int64_t ldx, const DeviceInfo& di, cudaStream_t stream) {
+    gem_status st;
+    plan_rows(&p, di);
     constexpr int J = kGroup<NT>;
     const int groups = (p.kb + J - 1) / J, per = (groups + p.split - 1) / p.split;
     p.chunk = std::min(per * J, kScaleBytes / (kPitch<NT> * 4) / J * J);
@@ -647,8 +655,21 @@ gem_status gem_fp8_gemm(const void* W, const float* ws, int64_t N, int64_t K, co
     if (M <= 16) return launch_rows<16>(p, W, K, x, ldx, di, stream);
     if (M <= 32) return launch_rows<32>(p, W, K, x, ldx, di, stream);
     if (M <= 64) return launch_rows<64>(p, W, K, x, ldx, di, stream);
-    if (M <= 128) return launch_rows<128>(p, W, K, x, ldx, di, stream);
-    return launch_tile<256>(p, W, K, x, ldx, di, stream);
+    // More rows: tiles of 256, 128 or 64 columns by their time, rounds of 76 pairs x blocks x 0.47, 0.32 or 0.24 us (a
+    // smaller tile costs more for its size and less where there are few); up to 128 rows the kernel above where it
+    // takes less: 0.46 us a block and 5 to begin and end, 3 more for a cluster (128 x 2048 x 4096: 13.2 and 7.7 us,
+    // 128 x 5376 x 21504: 43 and 47).
+    const int64_t mt = (M + 255) / 256, pairs = di.num_sms / 2;
+    auto tile_us = [&](int bn, double step) { return 4.0 + static_cast<double>((mt * ((N + bn - 1) / bn) + pairs - 1) / pairs) * p.kb * step; };
+    const double us256 = tile_us(256, 0.5), us128 = tile_us(128, 0.32), us64 = tile_us(64, 0.24), best = std::min(us256, std::min(us128, us64));
+    if (M <= 128) {
+        plan_rows(&p, di);
+        const double rounds = static_cast<double>((int64_t(p.tiles) * p.split + di.num_sms - 1) / di.num_sms);
+        if (rounds * ((p.kb + p.split - 1) / p.split) * 0.46 + (p.split > 1 ? 8.0 : 5.0) <= best) return launch_rows<128>(p, W, K, x, ldx, di, stream);
+    }
+    if (us256 <= best) return launch_tile<256>(p, W, K, x, ldx, di, stream);
+    if (us128 <= best) return launch_tile<128>(p, W, K, x, ldx, di, stream);
+    return launch_tile<64>(p, W, K, x, ldx, di, stream);
 }
 
 }  // extern "C"
