@@ -39,13 +39,14 @@ struct GemmParams {
 constexpr int kMaxStages = 24;
 constexpr int kScaleBytes = 24 << 10;
 
-// Blocks a ring stage and a tensor-memory buffer hold, of four such buffers (kGroup * NT columns each, 512
+// Blocks a ring stage and a tensor-memory buffer hold, of kBuffers such buffers (kGroup * NT columns each, 512
 // together at most): the waits and the read-back latency of a step are paid once for kGroup blocks.
 template <int NT>
-constexpr int kGroup = NT <= 32 ? 4 : NT == 64 ? 2 : 1;
+constexpr int kGroup = NT <= 64 ? 4 : 2;
+template <int NT>
+constexpr int kBuffers = NT >= 64 ? 2 : 4;
 template <int NT>
 constexpr int kWarps = NT <= 32 ? 2 : 4;
-constexpr int kBuffers = 4;
 template <int NT>
 constexpr int kPitch = NT + 4;   // of the x scales of a block: spreads a column's stores over the banks
 
@@ -57,7 +58,7 @@ struct RowsBarriers {
 
 template <int NT>
 __global__ void __launch_bounds__(kWarps<NT> * 128 + 64) fp8_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const GemmParams p) {
-    constexpr int NB = kBuffers, J = kGroup<NT>, COLS = NB * J * NT, Q = kWarps<NT>, CW = NT / Q, XP = kPitch<NT>;
+    constexpr int NB = kBuffers<NT>, J = kGroup<NT>, COLS = NB * J * NT, Q = kWarps<NT>, CW = NT / Q, XP = kPitch<NT>;
     extern __shared__ uint8_t raw[];
     __shared__ RowsBarriers bar;
     // the ring, 1024-byte aligned: a stage's blocks of W, then those of x; behind it the x scales and the cluster's sums
@@ -80,7 +81,7 @@ __global__ void __launch_bounds__(kWarps<NT> * 128 + 64) fp8_rows_kernel(const _
         }
         for (int i = 0; i < NB; ++i) {
             mbar_init(&bar.dfull[i], 1);
-            mbar_init(&bar.dempty[i], 4 * Q);
+            mbar_init(&bar.dempty[i], Q * ((p.rows + 31) / 32));   // the warps whose rows the tile has
         }
         fence_mbar_init();
         prefetch_tensormap(&tmW);
@@ -190,6 +191,7 @@ __global__ void __launch_bounds__(kWarps<NT> * 128 + 64) fp8_rows_kernel(const _
                     }
                     asm volatile("bar.sync 1, %0;" ::"n"(Q * 128) : "memory");
                 }
+                if ((warp & 3) * 32 >= p.rows) continue;
                 float w[J];
 #pragma unroll
                 for (int j = 0; j < J; ++j) {
@@ -203,26 +205,32 @@ __global__ void __launch_bounds__(kWarps<NT> * 128 + 64) fp8_rows_kernel(const _
                 }
                 if (!ok) continue;   // keeps to the barriers above
                 tc_fence_after();
-                // columns of blocks that the step does not have are read and not used
-                float v[J][CW];
+                // JB blocks at a time (what the registers hold); columns of blocks that the step lacks are read and not used
+                constexpr int JB = J * CW > 32 && NT > 32 ? 32 / CW : J;
 #pragma unroll
-                for (int j = 0; j < J; ++j) tmem_ld<CW>(v[j], from + (d * J + j) * NT);
-                tmem_wait_ld();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.dempty[d]);
+                for (int g = 0; g < J; g += JB) {
+                    float v[JB][CW];
 #pragma unroll
-                for (int j = 0; j < J; ++j)
-                    if (j < nj) {
-                        const float4* sx = reinterpret_cast<const float4*>(xs_sh + (c + j) * XP + col);
-#pragma unroll
-                        for (int q = 0; q < CW / 4; ++q) {
-                            const float4 x4 = sx[q];
-                            const float2 w2 = make_float2(w[j], w[j]);
-                            acc[2 * q] = ffma2(make_float2(v[j][4 * q], v[j][4 * q + 1]), fmul2(make_float2(x4.x, x4.y), w2), acc[2 * q]);
-                            acc[2 * q + 1] = ffma2(make_float2(v[j][4 * q + 2], v[j][4 * q + 3]), fmul2(make_float2(x4.z, x4.w), w2), acc[2 * q + 1]);
-                        }
+                    for (int j = 0; j < JB; ++j) tmem_ld<CW>(v[j], from + (d * J + g + j) * NT);
+                    tmem_wait_ld();
+                    if (g + JB == J) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar.dempty[d]);
                     }
+#pragma unroll
+                    for (int j = 0; j < JB; ++j)
+                        if (g + j < nj) {
+                            const float4* sx = reinterpret_cast<const float4*>(xs_sh + (c + g + j) * XP + col);
+                            const float2 w2 = make_float2(w[g + j], w[g + j]);
+#pragma unroll
+                            for (int q = 0; q < CW / 4; ++q) {
+                                const float4 x4 = sx[q];
+                                acc[2 * q] = ffma2(make_float2(v[j][4 * q], v[j][4 * q + 1]), fmul2(make_float2(x4.x, x4.y), w2), acc[2 * q]);
+                                acc[2 * q + 1] = ffma2(make_float2(v[j][4 * q + 2], v[j][4 * q + 3]), fmul2(make_float2(x4.z, x4.w), w2), acc[2 * q + 1]);
+                            }
+                        }
+                }
             }
             if (p.split > 1) {
 #pragma unroll
@@ -657,15 +665,15 @@ gem_status gem_fp8_gemm(const void* W, const float* ws, int64_t N, int64_t K, co
     if (M <= 64) return launch_rows<64>(p, W, K, x, ldx, di, stream);
     // More rows: tiles of 256, 128 or 64 columns by their time, rounds of 76 pairs x blocks x 0.47, 0.32 or 0.24 us (a
     // smaller tile costs more for its size and less where there are few); up to 128 rows the kernel above where it
-    // takes less: 0.46 us a block and 5 to begin and end, 3 more for a cluster (128 x 2048 x 4096: 13.2 and 7.7 us,
-    // 128 x 5376 x 21504: 43 and 47).
+    // takes less: 0.41 us a block and 5 to begin and end, 3 more for a cluster (128 x 2048 x 4096: 13.2 and 7.7 us,
+    // 128 x 5376 x 21504: 40 and 47).
     const int64_t mt = (M + 255) / 256, pairs = di.num_sms / 2;
     auto tile_us = [&](int bn, double step) { return 4.0 + static_cast<double>((mt * ((N + bn - 1) / bn) + pairs - 1) / pairs) * p.kb * step; };
     const double us256 = tile_us(256, 0.5), us128 = tile_us(128, 0.32), us64 = tile_us(64, 0.24), best = std::min(us256, std::min(us128, us64));
     if (M <= 128) {
         plan_rows(&p, di);
         const double rounds = static_cast<double>((int64_t(p.tiles) * p.split + di.num_sms - 1) / di.num_sms);
-        if (rounds * ((p.kb + p.split - 1) / p.split) * 0.46 + (p.split > 1 ? 8.0 : 5.0) <= best) return launch_rows<128>(p, W, K, x, ldx, di, stream);
+        if (rounds * ((p.kb + p.split - 1) / p.split) * 0.41 + (p.split > 1 ? 8.0 : 5.0) <= best) return launch_rows<128>(p, W, K, x, ldx, di, stream);
     }
     if (us256 <= best) return launch_tile<256>(p, W, K, x, ldx, di, stream);
     if (us128 <= best) return launch_tile<128>(p, W, K, x, ldx, di, stream);

@@ -468,3 +468,30 @@ def test_layer_in_graphs_and_on_two_streams(env):
     t.cuda.synchronize()
     for (d, _step), w in zip(sets, want):
         assert all(t.equal(d[k], w[k]) for k in _OUT)
+
+
+# ---- waits that run out ---------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("M,K,N", [(4, 256, 64), (8, 2048, 384), (40, 1024, 700), (3, 4096, 640), (100, 2560, 19456), (300, 512, 512), (600, 1008, 1201)])
+def test_gemm_wait_that_runs_out_is_reported(env, M, K, N):
+    """The first stage of CTA 0 expects 16 bytes more than it gets: every wait behind it gives up after the limit, the
+    call ends and says so, and the next one is right."""
+    gem, t = env
+    W, ws, x, xs = _operands(M, K, N, 6)
+    d = [_dev(t, a) for a in (W, ws, x, xs)]
+    y, status = t.full((M, N), -7.0, device="cuda"), t.zeros(1, dtype=t.int32, device="cuda")
+    t.cuda.synchronize()
+    gem.set_wait_limit(1_000_000)
+    gem.set_test_injection(gem.INJECT_RING_SHORTFALL)
+    try:
+        gem.fp8_gemm(*d, y, status=status)
+        t.cuda.synchronize()
+    finally:
+        gem.set_test_injection(0)
+        gem.set_wait_limit(0)
+    assert gem.status_from_flags(int(status)) == 6 and gem.device_status() == 0
+    status.zero_()
+    gem.fp8_gemm(*d, y, status=status)
+    want, most = fp8.gemm(W, ws, x, xs)
+    assert np.all(np.abs(y.cpu().numpy() - want) <= _tol(K, most)) and int(status) == 0
