@@ -575,14 +575,15 @@ def rmsnorm_fp8(x: torch.Tensor, gamma: torch.Tensor | None, eps: float, codes: 
                 residual: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None):
     """RMSNorm of x (+ residual) in 8 bits: x fp32 [T, H], codes uint8 or float8_e4m3fn [T, >= H], scales fp32
     [T, >= ceil(H / 128)].  out (may be x or residual) receives x + residual."""
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()
     H = x.shape[-1]
     xp, ldx, T = _rows(x, H, "x", dev)
     rp, ldr, r_rows = (None, 0, T) if residual is None else _rows(residual, H, "residual", dev)
     op, ldo, o_rows = (None, 0, T) if out is None else _rows(out, H, "out", dev)
     cp, ldc, c_rows = _codes(codes, H, "codes", dev)
     sp, lds, s_rows = _rows(scales, -(-H // 128), "scales", dev)
-    _same_rows(T, residual=r_rows, out=o_rows, codes=c_rows, scales=s_rows)
+    if not T == r_rows == o_rows == c_rows == s_rows:
+        _same_rows(T, residual=r_rows, out=o_rows, codes=c_rows, scales=s_rows)
     st = lib.gem_rmsnorm_fp8(xp, ldx, rp, ldr, op, ldo, T, H, None if gamma is None else _here(gamma, torch.float32, "gamma", (H,), dev),
                              eps, cp, ldc, sp, lds, _stream_on(stream, dev))
     _check(st, "gem_rmsnorm_fp8")
@@ -593,13 +594,14 @@ def quant_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, up: to
               act: int = ACT_SILU, stream=None):
     """act(x) * up, or x itself (up None), in 8 bits; x, up fp32 [T, H] (column ranges of a wider tensor will
     do), codes and scales as rmsnorm_fp8."""
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()
     H = x.shape[-1]
     xp, ldx, T = _rows(x, H, "x", dev)
     up_p, ldu, u_rows = (None, 0, T) if up is None else _rows(up, H, "up", dev)
     cp, ldc, c_rows = _codes(codes, H, "codes", dev)
     sp, lds, s_rows = _rows(scales, -(-H // 128), "scales", dev)
-    _same_rows(T, up=u_rows, codes=c_rows, scales=s_rows)
+    if not T == u_rows == c_rows == s_rows:
+        _same_rows(T, up=u_rows, codes=c_rows, scales=s_rows)
     st = lib.gem_quant_fp8(xp, ldx, up_p, ldu, T, H, act, cp, ldc, sp, lds, _stream_on(stream, dev))
     _check(st, "gem_quant_fp8")
     return codes, scales
@@ -610,7 +612,7 @@ def fp8_gemm(W: torch.Tensor, w_scales: torch.Tensor, x: torch.Tensor, x_scales:
     """y = x @ W.T (+ residual) of 8-bit rows: W [N, K] e4m3 (uint8 or float8_e4m3fn) with w_scales fp32
     [ceil(N / 128), ceil(K / 128)], x [M, >= K] with x_scales fp32 [M, >= ceil(K / 128)], y and residual (which
     may be y) fp32 [M, >= N] of the same row stride."""
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()
     if W.dim() != 2 or not W.is_contiguous():
         raise ValueError("W must be contiguous [N, K], got %s strides %s" % (tuple(W.shape), W.stride()))
     N, K = W.shape
@@ -619,7 +621,8 @@ def fp8_gemm(W: torch.Tensor, w_scales: torch.Tensor, x: torch.Tensor, x_scales:
     sp, lds, s_rows = _rows(x_scales, -(-K // 128), "x_scales", dev)
     yp, ldy, y_rows = _rows(y, N, "y", dev)
     rp, ldr, r_rows = (None, ldy, M) if residual is None else _rows(residual, N, "residual", dev)
-    _same_rows(M, x_scales=s_rows, y=y_rows, residual=r_rows)
+    if not M == s_rows == y_rows == r_rows:
+        _same_rows(M, x_scales=s_rows, y=y_rows, residual=r_rows)
     if ldr != ldy and M > 1:
         raise ValueError("residual must have y's row stride %d, got %d" % (ldy, ldr))
     st = lib.gem_fp8_gemm(wp, _here(w_scales, torch.float32, "w_scales", (-(-N // 128), -(-K // 128)), dev), N, K, xp, ldx,
@@ -634,16 +637,16 @@ def logprobs(y: torch.Tensor, tokens: torch.Tensor | None, logp: torch.Tensor | 
     """Scores of the logit rows y (fp32 [T, N]): logp, entropy fp32 and rank int32 [T] of the tokens int32 [T]
     (-1: none), and the k alternatives idx int32, val fp32 [T, k] with their log probabilities.  Outputs that are
     None are not computed."""
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()
     N = y.shape[-1]
     yp, ldy, T = _rows(y, N, "y", dev)
     f32, i32 = torch.float32, torch.int32
-    here = lambda t, dtype, name: None if t is None else _here(t, dtype, name, (T,), dev)  # noqa: E731
     if (idx is None) != (val is None):
         raise ValueError("idx and val come together")
     k = 0 if idx is None else idx.shape[-1]
-    st = lib.gem_logprobs(yp, ldy, T, N, scale, here(tokens, i32, "tokens"), here(logp, f32, "logp"), here(rank, i32, "rank"),
-                          here(entropy, f32, "entropy"), k, _here(idx, i32, "idx", (T, k), dev) if k else None,
+    st = lib.gem_logprobs(yp, ldy, T, N, scale, None if tokens is None else _here(tokens, i32, "tokens", (T,), dev),
+                          None if logp is None else _here(logp, f32, "logp", (T,), dev), None if rank is None else _here(rank, i32, "rank", (T,), dev),
+                          None if entropy is None else _here(entropy, f32, "entropy", (T,), dev), k, _here(idx, i32, "idx", (T, k), dev) if k else None,
                           _here(val, f32, "val", (T, k), dev) if k else None, _status(status, dev), _stream_on(stream, dev))
     _check(st, "gem_logprobs")
 

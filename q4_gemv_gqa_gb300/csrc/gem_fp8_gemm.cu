@@ -459,20 +459,25 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
                     break;
                 }
                 tc_fence_after();
-                // 16 columns at a time: more would not leave registers for the sums
+                // 32 columns at a time, as two reads of 16 (one of 32, which wants its registers in a row, spills)
+                constexpr int G = CW < 32 ? 1 : 2;
 #pragma unroll
-                for (int u = 0; u < CW / 16; ++u) {
-                    float v[16];
-                    tmem_ld<16>(v, from + d * BN + 16 * u);
+                for (int u = 0; u < CW / 16; u += G) {
+                    float v[G][16];
+#pragma unroll
+                    for (int g = 0; g < G; ++g) tmem_ld<16>(v[g], from + d * BN + 16 * (u + g));
                     tmem_wait_ld();
-                    if (u + 1 == CW / 16) {
+                    if (u + G == CW / 16) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_peer(empty0 + 8 * d);
                     }
-                    const uint64_t s2 = pair_of((n0 + 16 * u) >> 7 == nb ? sa : sb);
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) pair_fma(acc[8 * u + q], v[2 * q], v[2 * q + 1], s2);
+                    for (int g = 0; g < G; ++g) {
+                        const uint64_t s2 = pair_of((n0 + 16 * (u + g)) >> 7 == nb ? sa : sb);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) pair_fma(acc[8 * (u + g) + q], v[g][2 * q], v[g][2 * q + 1], s2);
+                    }
                 }
             }
             cp_async_wait<0>();

@@ -179,14 +179,15 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* s
     return warp_wait_slow(bar, parity, status, dead);
 }
 
-// Two sums in one register pair: (lo, hi) += (a, b) * (s, s), s given twice by pair_of.
+// Two sums in one register pair: (lo, hi) += (a, b) * (s, s), s given twice by pair_of.  Volatile, so that the adds
+// stay between the reads of tensor memory that they stand between.
 __device__ __forceinline__ uint64_t pair_of(float v) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(v));
     return r;
 }
 __device__ __forceinline__ void pair_fma(uint64_t& acc, float a, float b, uint64_t s) {
-    asm("{\n .reg .b64 t;\n mov.b64 t, {%1, %2};\n fma.rn.f32x2 %0, t, %3, %0;\n}\n" : "+l"(acc) : "f"(a), "f"(b), "l"(s));
+    asm volatile("{\n .reg .b64 t;\n mov.b64 t, {%1, %2};\n fma.rn.f32x2 %0, t, %3, %0;\n}\n" : "+l"(acc) : "f"(a), "f"(b), "l"(s));
 }
 __device__ __forceinline__ float2 pair_get(uint64_t acc) {
     float2 v;
