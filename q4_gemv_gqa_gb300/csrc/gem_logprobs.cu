@@ -7,10 +7,14 @@
 // Both terms of the entropy are positive, so nothing cancels; l - m is formed before it is scaled, so that its
 // error is relative.  The list of the k largest needs no second pass either: what can be in it is at least as
 // large as the k-th largest of the first piece's warp maxima, and after that as the k-th in the list so far, so
-// that a piece of 32 values a thread is looked at again only where its maximum passes that (a few of 10^5
-// values do).  The rank counts values only in pieces whose maximum reaches the given token's logit.
+// that a piece of 16 values a thread is looked at again only where its maximum passes that (a few of 10^5
+// values do).  Banned entries (-inf) take part only where fewer than k others are left, and then the first k entries
+// hold enough of them; a row whose numbers run out before that (NaN) is listed again, slowly.  The rank counts values
+// only in pieces whose maximum reaches the given token's logit.
 //
-// Bound by the read of the logits.  A row is one CTA's, or a cluster's, whose CTAs join their sums and lists
+// Bound by the read of the logits where there are many: 1021 x 262144 takes 199 us (1.07 GB, 79 % of the copy rate; 192
+// without a list).  61 x 151669 with 20 alternatives takes 26 us, 14 of them without a list: five pieces a CTA, so
+// beginning and joining count; 1 x 262144 9.6 us.  A row is one CTA's, or a cluster's, whose CTAs join their sums and lists
 // through shared memory: no workspace, no counters, and an order that depends on the sizes alone.
 #include <mutex>
 #include <set>
@@ -124,7 +128,7 @@ __device__ void sort_held(ScoreShared<THREADS>& sh, int n, int k) {
 }
 
 // The list of entries v0 .. v1 (16-byte pieces behind `head`) and of `more` single ones, where more came together
-// than can wait (rising or equal values): one entry a thread at a time, sorted as often as need be.
+// than can wait (rising values), or too few (NaN): one entry a thread at a time, sorted as often as need be.
 template <int THREADS>
 __device__ __noinline__ void list_slowly(ScoreShared<THREADS>& sh, const float* row, int head, int64_t v0, int64_t v1, int64_t nv, int more, int k) {
     const int tid = threadIdx.x;
@@ -195,8 +199,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     Sums sum{kLowest, 0.f, 0.f};
     int above = 0;
     unsigned long long least_key = 0;   // the list's least key; what is not above it is not looked at
-    float floor_v = 0.f;                // its value;
-    bool all = true;                    // or none yet: NaN and -inf may be listed
+    float floor_v = kLowest;            // its value, or the least finite one
     if (tid == 0) sh.n = 0;
     __syncthreads();
     if (tid < more) {
@@ -204,7 +207,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
         const float v = row[i], m = fmaxf(v, kLowest), d = (v - m) * c, w = exp2_fast(d);
         sum = {m, w, fmaxf(d, -200.f) * (d < -200.f ? 0.f : w)};
         above += count && is_above(v, i);
-        if (k) sh.held[atomicAdd(&sh.n, 1)] = key_of(v, i);
+        if (k && (v > -INFINITY || (v == v && tid < head))) sh.held[atomicAdd(&sh.n, 1)] = key_of(v, i);
     }
     // of entries before the given token equal ones are above it too
     const float bound_before = target, bound_after = nextafterf(target, INFINITY);
@@ -271,11 +274,15 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
                 bar = __reduce_max_sync(~0u, lane < W && larger == k - 1 ? b : 0u);
             }
             least_key = bar ? (static_cast<unsigned long long>(bar) << 32) - 1 : 0ull;
-            all = bar == 0;
-            floor_v = all ? 0.f : value_of(bar);
+            floor_v = bar ? value_of(bar) : kLowest;
         }
-        if (all || most >= floor_v) {
-            for (uint32_t mask = (all ? ~0u : at_least(floor_v)) & valid; mask; mask &= mask - 1) {
+        const bool banned = turn == 0 && 4 * tid < k;   // among the first k entries
+        if (most >= floor_v || banned) {
+            uint32_t mask = at_least(floor_v);
+            if (banned)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) mask |= x[j] == -INFINITY && 4 * tid + j < k ? 1u << j : 0u;
+            for (mask &= valid; mask; mask &= mask - 1) {
                 const int j = __ffs(mask) - 1;
                 const unsigned long long key = key_of(pick(x, j), index(j));
                 if (key > least_key) {
@@ -292,9 +299,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
             if (n <= kHeld && n > k) {
                 sort_held(sh, n, k);
                 least_key = sh.top[k - 1];
-                const uint32_t bar = static_cast<uint32_t>(least_key >> 32);
-                all = bar == 0;
-                floor_v = all ? 0.f : value_of(bar);
+                floor_v = fmaxf(value_of(static_cast<uint32_t>(least_key >> 32)), kLowest);
             }
             __syncthreads();
         }
@@ -307,7 +312,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     if (lane == 0) sh.sums[warp] = sum, sh.above[warp] = above;
     __syncthreads();
     if (k) {
-        if (sh.n > kHeld) list_slowly(sh, row, head, v0, v1, nv, more, k);
+        if (sh.n > kHeld || sh.n < min(static_cast<int64_t>(k), 4 * (v1 - v0) + more)) list_slowly(sh, row, head, v0, v1, nv, more, k);
         // a part of a row hands on a short list as it is
         if (p.split == 1 || sh.n > max(2 * k, 16)) sort_held(sh, sh.n, k);
     }

@@ -82,6 +82,23 @@ def test_masked_rows_and_ties(env, N):
     _check(_run(env, y, tokens, 33), y, tokens, 33)
 
 
+@pytest.mark.parametrize("left", [1, 3, 19, 20, 21, 200])
+@pytest.mark.parametrize("N", [300, 4099, 151669])
+def test_few_entries_that_are_not_banned(env, left, N):
+    """Grammars leave a handful of tokens: the list goes on with banned ones, by index."""
+    r = np.random.RandomState(left)
+    y = np.full((70, N), -np.inf, np.float32)
+    tokens = np.zeros(70, np.int64)
+    for t in range(70):
+        at = r.choice(N, min(left, N), replace=False) if t % 3 else np.arange(N - min(left, N), N)
+        y[t, at] = r.randn(at.size).round(1)
+        tokens[t] = at[0] if t % 2 else r.randint(N)
+    y[5, ::2] = np.nan                                   # and NaN behind them
+    y[6, 1:70] = np.nan
+    for k in (1, 20, 64):
+        _check(_run(env, y, tokens, k), y, tokens, k)
+
+
 def test_sorted_rows(env):
     """The list's order in the row: the largest first, last, or in the threads' own strides."""
     N = 70000
