@@ -1,7 +1,8 @@
 /*
  * gem.h — C ABI of the GB300 (sm_103a) decoder-step library: Q4_0 dequantise-and-matvec,
  * RMSNorm / per-head QK-norm / RoPE / KV append, grouped-query split-K decode attention,
- * gated FFN activation, one whole decoder layer step, and a paged 4-bit KV cache.
+ * gated FFN activation, one whole decoder layer step, a paged 4-bit KV cache, 8-bit floating-point
+ * rows and products for prompts and batches, and log probabilities of what a model answers with.
  *
  * Sources, cited by page title and section:
  *   [GEM]  "gem" engine research record (Gemma 4 native engine), sections "Verified model
@@ -32,7 +33,7 @@
  *   - The fast path needs K % 256 == 0 and a 16-byte aligned matrix; other matrices with
  *     K % 32 == 0 go through a slower general kernel.  K % 32 != 0 is rejected.
  *   - Batch B is 0..8 (0 = nothing to do).  Larger batches are GEM_ERR_UNSUPPORTED_SHAPE.  (The
- *     paged cache's calls have limits of their own.)
+ *     calls of the paged cache, of the 8-bit path and gem_logprobs have limits of their own.)
  *   - Arguments are checked on the host before anything is enqueued; a rejected call has
  *     no effect.  Values only the device can see (positions) are checked by the kernels,
  *     which then skip the offending sequence and OR a GEM_DEVFLAG_* bit into *status
@@ -106,7 +107,7 @@ GEM_API gem_status gem_status_from_flags(int32_t flags);
  *           GEM_INJECT_RING_SHORTFALL  the one-row Q4_0 GEMV (B = 1, K % 256 == 0) makes
  *             CTA 0 expect 16 bytes more than its last ring stage receives, so that stage's
  *             wait runs out after the wait limit (every copy still lands); gem_kv4_attn's first
- *             warp does the same with its first stage;
+ *             warp and gem_fp8_gemm's CTA 0 do the same with their first stage;
  *           GEM_INJECT_GRID_ARRIVAL  gem_decode_step makes CTA 0 leave out its arrival at
  *             the step's first grid barrier, so every CTA's barrier wait runs out and the
  *             step is aborted (the plan must then be destroyed and created again).
@@ -557,8 +558,8 @@ GEM_API gem_status gem_kv4_attn(const float *q, int64_t ldq, int64_t T, const in
  *   codes  [T][ldc] bytes, 16-byte aligned, ldc a multiple of 16;  scales [T][lds] fp32, lds >= ceil(H / 128).
  *   H a multiple of 16, at most 32768 (GEM_ERR_UNSUPPORTED_SHAPE otherwise); T < 2^31.
  *   The mean square is summed to about 2^-40 and a value next to a border of two codes is decided in
- *   fp64, so the codes are those of the exact y (for squares above 2^-100).  A row whose sum of squares
- *   is not finite in fp32 gets NaN scales.
+ *   fp64, so the codes are those of the exact y (for squares, and products with gamma, above 2^-100).  A
+ *   row whose sum of squares is not finite in fp32 gets NaN scales.
  */
 GEM_API gem_status gem_rmsnorm_fp8(const float *x, int64_t ldx, const float *residual, int64_t ldr,
                                    float *out, int64_t ldo, int64_t T, int64_t H, const float *gamma,
@@ -570,7 +571,8 @@ GEM_API gem_status gem_rmsnorm_fp8(const float *x, int64_t ldx, const float *res
  *   y[t][i] = up ? act(x[t][i]) * up[t][i] : x[t][i], in 8 bits as above; act as gem_swiglu, taken as
  *   x / (1 + e^-z) with z = x (silu) or 2 sqrt(2/pi) (x + 0.044715 x^3) (gelu_tanh); 0 where z < -83.
  *   x [T][ldx], up [T][ldu] fp32, 16-byte aligned, strides multiples of 4 values (the two halves of a
- *   merged projection's rows will do).  codes, scales, H, T as gem_rmsnorm_fp8, H of any size.
+ *   merged projection's rows will do).  codes, scales, T as gem_rmsnorm_fp8; H a multiple of 16,
+ *   at most 2^24.  codes and scales must not overlap x or up.
  *   Codes are those of the exact y: next to a border they are decided in fp64.
  */
 GEM_API gem_status gem_quant_fp8(const float *x, int64_t ldx, const float *up, int64_t ldu, int64_t T,
@@ -586,10 +588,13 @@ GEM_API gem_status gem_quant_fp8(const float *x, int64_t ldx, const float *up, i
  *   W and x 16-byte aligned, ldx a multiple of 16 (GEM_ERR_MISALIGNED); K a multiple of 16
  *   (GEM_ERR_UNSUPPORTED_SHAPE); M, N, K < 2^31.  Rows of y whose base and stride are multiples of 16
  *   bytes are written fastest.
- *   The products of a block are summed on the tensor cores (tcgen05, fp32 accumulation), the blocks in
- *   fp32 in order of k, so a result does not depend on M.  A NaN code or scale makes NaN of the results
- *   that it takes part in.  A wait that runs out sets GEM_DEVFLAG_TIMEOUT in *status (nullable: the
- *   library's word); y is then unspecified.  No workspace.  Deterministic.
+ *   The products of a block are summed on the tensor cores (tcgen05, fp32 accumulation); the blocks' sums
+ *   are scaled and added in fp32 in order of k (where few rows of x share out K over a cluster, its parts
+ *   in order).  A NaN code or scale makes NaN of the results that it takes part in.
+ *   W, like every weight of the library, is read ahead of the call before: the library call that directly
+ *   precedes this one on the stream must not be the one that writes W.
+ *   A wait that runs out sets GEM_DEVFLAG_TIMEOUT in *status (nullable: the library's word); y is then
+ *   unspecified.  No workspace.  Deterministic.
  */
 GEM_API gem_status gem_fp8_gemm(const void *W, const float *ws, int64_t N, int64_t K, const void *x,
                                 int64_t ldx, const float *xs, int64_t ldxs, int64_t M, float *y,
