@@ -53,8 +53,18 @@ constexpr int kScaleBytes = 24 << 10;
 // together at most): the waits and the read-back latency of a step are paid once for kGroup blocks.
 template <int NT>
 constexpr int kGroup = NT <= 64 ? 4 : 2;
+// A cluster's CTAs hold their columns until all of them are done, and an allocation waits for as long as it has to: were
+// two clusters on the same SMs, each with the columns that the other's second CTA wants, both would wait for ever (two
+// streams are enough).  So what fits an SM in shared memory of such CTAs, which have two stages or more of 64 rows of W
+// or more, fits in tensor memory too: two of 256 columns.  Other launches hold columns only while they work.
 template <int NT>
-constexpr int kBuffers = NT >= 64 ? 2 : 4;
+constexpr int kBuffers = NT >= 32 ? 2 : 4;
+template <int NT>
+constexpr int kColumns = kBuffers<NT> * kGroup<NT> * NT;
+template <int NT>
+constexpr int kClusterSmem = 2 * kGroup<NT> * (64 + NT) * 128 + NT * 512;
+static_assert(kColumns<16> <= 256 && kColumns<32> <= 256 && 3 * kClusterSmem<16> > (228 << 10));
+static_assert(kClusterSmem<64> + kClusterSmem<16> > (228 << 10) && kClusterSmem<128> + kClusterSmem<16> > (228 << 10));
 template <int NT>
 constexpr int kWarps = NT <= 32 ? 2 : 4;
 template <int NT>
@@ -68,7 +78,7 @@ struct RowsBarriers {
 
 template <int NT>
 __global__ void __launch_bounds__(kWarps<NT> * 128 + 64) fp8_rows_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const GemmParams p) {
-    constexpr int NB = kBuffers<NT>, J = kGroup<NT>, COLS = NB * J * NT, Q = kWarps<NT>, CW = NT / Q, XP = kPitch<NT>;
+    constexpr int NB = kBuffers<NT>, J = kGroup<NT>, COLS = kColumns<NT>, Q = kWarps<NT>, CW = NT / Q, XP = kPitch<NT>;
     extern __shared__ uint8_t raw[];
     __shared__ RowsBarriers bar;
     // the ring, 1024-byte aligned: a stage's blocks of W, then those of x; behind it the x scales and the cluster's sums
@@ -385,6 +395,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
                 if (++s == STAGES) s = 0, phase ^= 1;
             }
         }
+        // the last products' arrivals come from the other CTA's side: this one stays until they are here
+        for (int i = 0; i < STAGES && ok; ++i) {   // (a stage without any passes at once)
+            ok = warp_wait(&bar.empty[s], phase, p.status, dead);
+            if (++s == STAGES) s = 0, phase ^= 1;
+        }
         if (!ok) *dead = 1;
     } else if (warp == kTileWarps + 1) {
         if (rank == 0) {
@@ -651,7 +666,7 @@ gem_status gem_fp8_gemm(const void* W, const float* ws, int64_t N, int64_t K, co
                         int32_t* status, void* stream_v) {
     using namespace gem;
     if (M < 0 || N < 0 || K < 0) return GEM_ERR_INVALID_ARG;
-    constexpr int64_t lim = (int64_t(1) << 31) - 512;
+    constexpr int64_t lim = (int64_t(1) << 31) - 512;   // tiles at the edge end in 32 bits
     if (K % 16 || M > lim || N > lim || K > lim || ((M + 255) / 256) * ((N + 127) / 128) > lim) return GEM_ERR_UNSUPPORTED_SHAPE;
     if (M == 0 || N == 0) return GEM_OK;
     if (K == 0 || !W || !ws || !x || !xs || !y) return GEM_ERR_INVALID_ARG;

@@ -495,3 +495,47 @@ def test_gemm_wait_that_runs_out_is_reported(env, M, K, N):
     gem.fp8_gemm(*d, y, status=status)
     want, most = fp8.gemm(W, ws, x, xs)
     assert np.all(np.abs(y.cpu().numpy() - want) <= _tol(K, most)) and int(status) == 0
+
+
+def test_gemm_clusters_on_three_streams(env):
+    """Calls whose clusters share out K, of different widths, at once: none keeps another's tensor memory from it."""
+    gem, t = env
+    calls = []
+    for i, (M, K, N) in enumerate([(8, 4096, 640), (24, 4096, 1100), (50, 2048, 384)]):
+        W, ws, x, xs = _operands(M, K, N, i)
+        want, most = fp8.gemm(W, ws, x, xs)
+        calls.append((want, _tol(K, most), [_dev(t, a) for a in (W, ws, x, xs)], t.zeros(40, M, N, device="cuda"), t.cuda.Stream()))
+    t.cuda.synchronize()
+    for r in range(40):
+        for _, _, (W, ws, x, xs), y, s in calls:
+            gem.fp8_gemm(W, ws, x, xs, y[r], stream=s)
+    t.cuda.synchronize()
+    for want, tol, _, y, _ in calls:
+        got = y.cpu().numpy()
+        assert (got == got[:1]).all()
+        assert (np.abs(got[0] - want) <= tol).all()
+    assert gem.device_status() == 0
+
+
+@pytest.mark.parametrize("call", ["gem.rmsnorm_fp8(x, None, 1e-6, c, s)", "gem.quant_fp8(x, c, s)", "gem.fp8_gemm(c, s[:1], c, s, y)",
+                                  "gem.fp8_gemm(c, s[:1], c.repeat(3, 1), s.repeat(3, 1), y.repeat(3, 1))", "gem.logprobs(x, None, None, x.new_empty(100))"])
+def test_first_call_of_a_process_may_be_captured(call):
+    """Whatever a call sets up in its process, it sets up without the stream."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, q4_gemv_gqa_gb300 as gem
+x = torch.ones(100, 128, device="cuda"); c = torch.zeros(100, 128, device="cuda", dtype=torch.uint8)
+s = torch.ones(100, 1, device="cuda"); y = torch.ones(100, 100, device="cuda")
+def run(): %s
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    run()
+g.replay(); torch.cuda.synchronize()
+assert gem.device_status() == 0
+""" % call
+    done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=240,
+                          cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert done.returncode == 0, done.stderr[-2000:]
