@@ -556,7 +556,8 @@ GEM_API gem_status gem_kv4_attn(const float *q, int64_t ldq, int64_t T, const in
  *          out may be x or residual with the same stride, else must not overlap them.
  *   gamma  [H] fp32, 16-byte aligned.
  *   codes  [T][ldc] bytes, 16-byte aligned, ldc a multiple of 16;  scales [T][lds] fp32, lds >= ceil(H / 128).
- *   H a multiple of 16, at most 32768 (GEM_ERR_UNSUPPORTED_SHAPE otherwise); T < 2^31.
+ *          They must not overlap x, residual or out.
+ *   eps finite and >= 0.  H a multiple of 16, at most 32768 (GEM_ERR_UNSUPPORTED_SHAPE otherwise); T < 2^31.
  *   The mean square is summed to about 2^-40 and a value next to a border of two codes is decided in
  *   fp64, so the codes are those of the exact y (for squares, and products with gamma, above 2^-100).  A
  *   row whose sum of squares is not finite in fp32 gets NaN scales.
@@ -583,7 +584,8 @@ GEM_API gem_status gem_quant_fp8(const float *x, int64_t ldx, const float *up, i
  * Product of 8-bit rows with 8-bit weights that have a scale for each block of 128 x 128.
  *   y[m][n] = sum_b xs[m][b] * ws[n / 128][b] * (sum_{k in block b} x[m][k] * W[n][k])  (+ residual[m][n])
  *   W   [N][K] e4m3, rows contiguous;   ws [ceil(N / 128)][ceil(K / 128)] fp32, any values.
- *   x   [M][ldx] e4m3, ldx >= K;  xs [M][ldxs] fp32, ldxs >= ceil(K / 128), any values.
+ *   x   [M][ldx] e4m3, ldx >= K;  xs [M][ldxs] fp32, ldxs >= ceil(K / 128), any values
+ *          (xs * ws is rounded to fp32 before it scales the sum: it loses bits below 2^-126).
  *   y   [M][ldy] fp32, ldy >= N;  residual nullable, [M][ldy], may be y.  y must not overlap the rest.
  *   W and x 16-byte aligned, ldx a multiple of 16 (GEM_ERR_MISALIGNED); K a multiple of 16
  *   (GEM_ERR_UNSUPPORTED_SHAPE); M, N, K < 2^31.  Rows of y whose base and stride are multiples of 16

@@ -116,7 +116,7 @@ def test_norm_refusals(lib):
         return lib.gem_rmsnorm_fp8(x, ldx, res, ldr, out, ldo, T, H, gamma, eps, codes, ldc, scales, lds, None)
 
     assert f(T=0) == OK and f(H=0, ldx=0) == OK
-    assert f(T=-1) == INVALID and f(H=-16) == INVALID and f(eps=-1.0) == INVALID and f(eps=math.nan) == INVALID
+    assert f(T=-1) == INVALID and f(H=-16) == INVALID and f(eps=-1.0) == INVALID and f(eps=math.nan) == INVALID and f(eps=math.inf) == INVALID
     assert f(x=None) == INVALID and f(codes=None) == INVALID and f(scales=None) == INVALID
     assert f(ldx=252) == INVALID and f(res=D, ldr=252) == INVALID and f(out=D, ldo=252) == INVALID and f(ldc=240) == INVALID and f(lds=1) == INVALID
     assert f(out=D, ldo=512) == INVALID                       # out is x, with another stride
