@@ -593,8 +593,9 @@ GEM_API gem_status gem_quant_fp8(const float *x, int64_t ldx, const float *up, i
  *   The products of a block are summed on the tensor cores (tcgen05, fp32 accumulation); the blocks' sums
  *   are scaled and added in fp32 in order of k (where few rows of x share out K over a cluster, its parts
  *   in order).  A NaN code or scale makes NaN of the results that it takes part in.
- *   W, like every weight of the library, is read ahead of the call before: the library call that directly
- *   precedes this one on the stream must not be the one that writes W.
+ *   W, like every weight of the library, may be read while the kernel before this one on the stream ends:
+ *   that kernel must not be the one that writes W (an event, a synchronisation or another launch between
+ *   them will do).
  *   A wait that runs out sets GEM_DEVFLAG_TIMEOUT in *status (nullable: the library's word); y is then
  *   unspecified.  No workspace.  Deterministic.
  */
