@@ -13,9 +13,10 @@
 // only in pieces whose maximum reaches the given token's logit.
 //
 // Bound by the read of the logits where there are many: 1021 x 262144 takes 199 us (1.07 GB, 79 % of the copy rate; 192
-// without a list).  61 x 151669 with 20 alternatives takes 26 us, 14 of them without a list: five pieces a CTA, so
-// beginning and joining count; 1 x 262144 9.6 us.  A row is one CTA's, or a cluster's, whose CTAs join their sums and lists
+// without a list).  61 x 151669 with 20 alternatives takes 24 us, 14 of them without a list: ten pieces a CTA, so
+// beginning, listing and joining count; 1 x 262144 9.6 us.  A row is one CTA's, or a cluster's, whose CTAs join their sums and lists
 // through shared memory: no workspace, no counters, and an order that depends on the sizes alone.
+#include <cmath>
 #include <mutex>
 #include <set>
 
@@ -406,8 +407,9 @@ gem_status gem_logprobs(const float* y, int64_t ldy, int64_t T, int64_t N, float
     if ((st = device_info(&di)) != GEM_OK) return st;
     ScoreParams p{y, ldy, N, scale, tokens, logp, rank, entropy, k, 1, idx, val, status ? status : di.status_word};
     // Few rows: 16 CTAs of 512 threads a row (a cluster of that size wants the kernel's consent).  Else 256 threads, and
-    // as many CTAs a row as give the fewest rounds of the four that an SM holds; beginning and joining cost a CTA about
-    // as much as 12 pieces.
+    // as many CTAs a row as take the shortest time.  A piece takes 0.5 us where an SM has one or two CTAs and 1.1 us where
+    // it has the four that it holds; beginning, listing and joining take as long as 32 pieces; of clusters fewer fit.
+    // (61 x 151669, list of 20: 4 CTAs a row 23 us, 2 28, 8 25; 150 rows: 2 CTAs 27 us, 4 35.)
     const bool few = T <= 4;
     const int threads = few ? 512 : 256;
     const int64_t pieces = (N / 4 + threads * kVec - 1) / (threads * kVec);
@@ -419,11 +421,13 @@ gem_status gem_logprobs(const float* y, int64_t ldy, int64_t T, int64_t N, float
         std::lock_guard<std::mutex> lk(mu);
         if (done.insert(di.device).second) GEM_CUDA_TRY(cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
     } else {
-        const int64_t slots = int64_t(di.num_sms) * 4;
         double best = 1e30;
         for (int s : {1, 2, 4, 8}) {
             if (s > 1 && s > pieces) break;
-            const double cost = static_cast<double>((T * s + slots - 1) / slots) * (static_cast<double>((pieces + s - 1) / s) + 12.0);
+            const int64_t ctas = T * s, an_sm = (ctas + di.num_sms - 1) / di.num_sms;
+            const double slots = di.num_sms * (s > 1 ? 3.7 : 4.0), rounds = std::ceil(static_cast<double>(ctas) / slots);
+            const double piece = an_sm <= 2 ? 1.0 : an_sm == 3 ? 1.5 : 2.2;
+            const double cost = rounds * (static_cast<double>((pieces + s - 1) / s) * piece + 32.0);
             if (cost < best) {
                 best = cost;
                 p.split = s;
