@@ -203,12 +203,15 @@ __global__ void __launch_bounds__(kWarps<NT> * 128 + 64) fp8_rows_kernel(const _
                 if (c == 0 && (b1 - b0 > p.chunk || t == first)) {   // the next blocks' x scales, turned to [block][row]
                     const int nblk = min(p.chunk, b1 - b);
                     asm volatile("bar.sync 1, %0;" ::"n"(Q * 128) : "memory");
-#pragma unroll
-                    for (int u = 0; u < CW / 4; ++u) {   // a warp takes the rows warp, warp + 4 Q, ..
-                        const int m = warp + 4 * Q * u;
+                    for (int m = warp; m < NT; m += 4 * Q) {   // all on their way at once
                         const float* src = p.xs + m * p.ldxs + b;
-                        for (int q = lane; q < nblk; q += 32) xs_sh[q * XP + m] = m < p.M ? __ldg(src + q) : 0.f;
+                        for (int q = lane; q < nblk; q += 32) {
+                            if (m < p.M) cp_async_4(smem_u32(xs_sh + q * XP + m), src + q);
+                            else xs_sh[q * XP + m] = 0.f;
+                        }
                     }
+                    cp_async_commit();
+                    cp_async_wait<0>();
                     asm volatile("bar.sync 1, %0;" ::"n"(Q * 128) : "memory");
                 }
                 if ((warp & 3) * 32 >= p.rows) continue;
@@ -274,11 +277,22 @@ __global__ void __launch_bounds__(kWarps<NT> * 128 + 64) fp8_rows_kernel(const _
         if (warp < 4 * Q) {
             const int row = (warp & 3) * 32 + lane, n = first * p.rows + row;
             if (row < p.rows && n < p.N)
-                for (int m = rank + p.split * (warp >> 2); m < p.M; m += p.split * Q) {
-                    float v = 0.f;
-                    for (int r = 0; r < p.split; ++r) v += ld_peer(peer_addr(&part[m * 128 + row], r));
-                    const int64_t at = m * p.ldy + n;
-                    p.y[at] = p.res ? v + p.res[at] : v;
+                for (int m0 = rank + p.split * (warp >> 2); m0 < p.M; m0 += 4 * p.split * Q) {   // four rows' reads at once
+                    float v[4][4], add[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int m = min(m0 + i * p.split * Q, p.M - 1);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) v[i][r] = r < p.split ? ld_peer(peer_addr(&part[m * 128 + row], r)) : 0.f;
+                        add[i] = p.res ? p.res[m * p.ldy + n] : 0.f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int m = m0 + i * p.split * Q;
+                        float sum = v[i][0];
+                        for (int r = 1; r < 4; ++r) sum = r < p.split ? sum + v[i][r] : sum;
+                        if (m < p.M) p.y[m * p.ldy + n] = p.res ? sum + add[i] : sum;
+                    }
                 }
         }
         __syncwarp();
