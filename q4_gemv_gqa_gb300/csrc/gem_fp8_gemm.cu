@@ -10,16 +10,20 @@
 // of the product, the rows of x its 16..128 columns.  The tensor cores read W straight from shared memory, so nothing
 // is unpacked, and a tile may have any multiple of 8 rows of W (the rest of the 128 is whatever lies there, and not
 // used): the height is chosen so that all SMs get the same share.  8 x 5376 x 21504: 19.7 us, 5.9 TB/s of W, 87 % of the
-// copy rate, where it streams; 61 x 21504 x 5376: 26.9 us, bound by the warps that scale and add; 1 x 2048 x 4096: 4.6 us.
+// copy rate, where it streams; 61 x 21504 x 5376: 23.4 us, of which 17 stream (three CTAs on 128 rows of W; shared memory's
+// bandwidth, for loads, products and scales, is as busy as the copy); 1 x 2048 x 4096: 4.6 us.
 //
 // fp8_tile_kernel (more rows): pairs of CTAs, 256 rows of x by up to 256 of W.  4096 x 5376 x 21504: 388 us,
 // 2.44 PFLOP/s, tensor cores 52 % active.  Without the adds it takes 321 us, without the products 340 to 354, without
 // both 234: reading back and adding 128 x 256 sums for each 128 of K takes as long as their product, and two buffers of
 // tensor memory do not hide all of one behind the other.  Tried and not kept: halves of 128 columns with four buffers
-// (420 us: x is read twice from shared memory), 160 columns with three (407, bound by the L2), 16 adding warps (403), the
+// (420 us: x is read twice from shared memory), 160 columns with three (407, bound by the L2), W on the 256-row side and 320 columns of x in three buffers (300 rows of x 30 us
+// against 27, 4096 686: smaller buffers wait longer for one another), the next read-back on its way while one is added
+// (no change), 16 adding warps (403), the
 // scales made by warps of their own (445, registers spill), reads of 32 or 64 columns in one (450 to 530, likewise).
 #include "gem_tcgen05.cuh"
 
+#include <array>
 #include <map>
 #include <mutex>
 #include <utility>
@@ -47,24 +51,26 @@ struct GemmParams {
 // The last two warps load and issue the products; the others scale and add.  Of these, four times kWarps<NT>,
 // warp w has the rows of W of lane quarter w % 4 and columns w / 4 * NT / kWarps<NT> and on.
 constexpr int kMaxStages = 24;
+constexpr int kMaxSplit = 8;
 constexpr int kScaleBytes = 24 << 10;
 
 // Blocks a ring stage and a tensor-memory buffer hold, of kBuffers such buffers (kGroup * NT columns each, 512
 // together at most): the waits and the read-back latency of a step are paid once for kGroup blocks.
 template <int NT>
 constexpr int kGroup = NT <= 64 ? 4 : 2;
-// A cluster's CTAs hold their columns until all of them are done, and an allocation waits for as long as it has to: were
-// two clusters on the same SMs, each with the columns that the other's second CTA wants, both would wait for ever (two
-// streams are enough).  So what fits an SM in shared memory of such CTAs, which have two stages or more of 64 rows of W
-// or more, fits in tensor memory too: two of 256 columns.  Other launches hold columns only while they work.
 template <int NT>
-constexpr int kBuffers = NT >= 32 ? 2 : 4;
+constexpr int kBuffers = NT >= 64 ? 2 : 4;
 template <int NT>
 constexpr int kColumns = kBuffers<NT> * kGroup<NT> * NT;
+// A cluster's CTAs hold their columns until all of them are done, and an allocation waits for as long as it has to: were
+// two clusters on the same SMs, each with the columns that the other's second CTA wants, both would wait for ever (two
+// streams are enough).  So the CTAs of a cluster take at least so much shared memory that those which fit an SM fit in
+// tensor memory too: two of up to 16 rows of x (256 columns), which have two stages or more of 64 rows of W or more, or
+// a wider one alone.  Other launches hold columns only while they work.
+constexpr int kSmSmem = 228 << 10;
 template <int NT>
-constexpr int kClusterSmem = 2 * kGroup<NT> * (64 + NT) * 128 + NT * 512;
-static_assert(kColumns<16> <= 256 && kColumns<32> <= 256 && 3 * kClusterSmem<16> > (228 << 10));
-static_assert(kClusterSmem<64> + kClusterSmem<16> > (228 << 10) && kClusterSmem<128> + kClusterSmem<16> > (228 << 10));
+constexpr int kClusterSmem = NT <= 16 ? 2 * kGroup<NT> * (64 + NT) * 128 : 149 << 10;
+static_assert(2 * kColumns<16> <= 512 && 3 * kClusterSmem<16> > kSmSmem && kClusterSmem<16> + kClusterSmem<32> > kSmSmem);
 template <int NT>
 constexpr int kWarps = NT <= 32 ? 2 : 4;
 template <int NT>
@@ -81,12 +87,12 @@ __global__ void __launch_bounds__(kWarps<NT> * 128 + 64) fp8_rows_kernel(const _
     constexpr int NB = kBuffers<NT>, J = kGroup<NT>, COLS = kColumns<NT>, Q = kWarps<NT>, CW = NT / Q, XP = kPitch<NT>;
     extern __shared__ uint8_t raw[];
     __shared__ RowsBarriers bar;
-    // the ring, 1024-byte aligned: a stage's blocks of W, then those of x; behind it the x scales and the cluster's sums
+    // the ring, 1024-byte aligned: a stage's blocks of W, then those of x; behind it the x scales
     uint8_t* ring = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     const int wbytes = p.rows * 128, stage_bytes = J * (wbytes + NT * 128);
     // a product reads 128 rows of W, of which p.rows are its own: the ring is followed by what that may be past its end
     float* xs_sh = reinterpret_cast<float*>(ring + p.stages * stage_bytes + max(0, 16384 - wbytes - J * NT * 128));
-    float* part = xs_sh + p.chunk * XP;
+    float* part = reinterpret_cast<float*>(ring);   // [row of x][128], when all products are done
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = static_cast<int>(blockIdx.x) % p.split, first = static_cast<int>(blockIdx.x) / p.split, step = static_cast<int>(gridDim.x) / p.split;
     const int groups = (p.kb + J - 1) / J;
@@ -255,10 +261,10 @@ __global__ void __launch_bounds__(kWarps<NT> * 128 + 64) fp8_rows_kernel(const _
                         }
                 }
             }
-            if (p.split > 1) {
+            if (p.split > 1) {   // (a warp without rows has waited for nothing: the ring may still be in use)
 #pragma unroll
                 for (int m = 0; m < CW; ++m)
-                    if (col + m < p.M) part[(col + m) * 128 + row] = m & 1 ? acc[m / 2].y : acc[m / 2].x;
+                    if (row < p.rows && col + m < p.M) part[(col + m) * 128 + row] = m & 1 ? acc[m / 2].y : acc[m / 2].x;
             } else if (mine && ok) {
 #pragma unroll
                 for (int m = 0; m < CW; ++m)
@@ -278,19 +284,20 @@ __global__ void __launch_bounds__(kWarps<NT> * 128 + 64) fp8_rows_kernel(const _
             const int row = (warp & 3) * 32 + lane, n = first * p.rows + row;
             if (row < p.rows && n < p.N)
                 for (int m0 = rank + p.split * (warp >> 2); m0 < p.M; m0 += 4 * p.split * Q) {   // four rows' reads at once
-                    float v[4][4], add[4];
+                    float v[4][kMaxSplit], add[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int m = min(m0 + i * p.split * Q, p.M - 1);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) v[i][r] = r < p.split ? ld_peer(peer_addr(&part[m * 128 + row], r)) : 0.f;
+                        for (int r = 0; r < kMaxSplit; ++r) v[i][r] = r < p.split ? ld_peer(peer_addr(&part[m * 128 + row], r)) : 0.f;
                         add[i] = p.res ? p.res[m * p.ldy + n] : 0.f;
                     }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int m = m0 + i * p.split * Q;
                         float sum = v[i][0];
-                        for (int r = 1; r < 4; ++r) sum = r < p.split ? sum + v[i][r] : sum;
+#pragma unroll
+                        for (int r = 1; r < kMaxSplit; ++r) sum = r < p.split ? sum + v[i][r] : sum;
                         if (m < p.M) p.y[m * p.ldy + n] = p.res ? sum + add[i] : sum;
                     }
                 }
@@ -590,46 +597,81 @@ gem_status ensure_smem(const void* fn, int device, size_t bytes) {
     return GEM_OK;
 }
 
-// Rows of W a tile and CTAs that share a tile's blocks: the shortest time of the busiest SM.  A block costs its bytes,
-// or its products where it has fewer than 64 rows (they take the same time for any number of rows); a cluster costs
-// its joining.  Clusters only where one round of them does it: 4 CTAs of one GPC fit 36 times.
-void plan_rows(GemmParams* g, const DeviceInfo& di) {
+// CTAs of clusters of s that run at once, one an SM (a cluster lies in one GPC, so not all SMs can be used).
+int cluster_room(const void* fn, int threads, int s, int device) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim = {static_cast<unsigned>(s), 1, 1};
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(s);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = kSmSmem / 2;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (ensure_smem(fn, device, kSmSmem / 2) == GEM_OK && cudaOccupancyMaxActiveClusters(&n, fn, &cfg) == cudaSuccess) return n * s;
+    (void)cudaGetLastError();   // none then
+    return 0;
+}
+
+// The same for all sizes and a kernel, asked once a device.
+template <int NT>
+std::array<int, kMaxSplit + 1> cluster_rooms(int device) {
+    static std::mutex mu;
+    static std::map<int, std::array<int, kMaxSplit + 1>> known;
+    std::lock_guard<std::mutex> lk(mu);
+    auto [it, fresh] = known.try_emplace(device);
+    if (fresh)
+        for (int s = 2; s <= kMaxSplit; ++s) it->second[s] = cluster_room(reinterpret_cast<const void*>(fp8_rows_kernel<NT>), kWarps<NT> * 128 + 64, s, device);
+    return it->second;
+}
+
+// Rows of W a tile and CTAs that share a tile's blocks by their time (returned in us, without beginning and end): the
+// blocks' products and adds, whatever the rows of W, or the read of W but for the first blocks, which are on their way
+// before the call begins.  A cluster costs its joining; of clusters there is one round.  (61 x 21504 x 5376: 3 CTAs on 128 rows 23.7 us, 2 on 72 24.9, 1 on 72 37.9;
+// 16 x 9728 x 2560: 4 on 128 6.8, 3 on 64 8.1, 2 on 64 9.1, 1 on 64 12.6.)
+template <int NT>
+double plan_rows(GemmParams* g, const DeviceInfo& di) {
     GemmParams& p = *g;
-    p.split = 1;
-    p.rows = 128;
+    constexpr int J = kGroup<NT>;
+    constexpr double block = NT <= 16 ? 0.12 : NT <= 32 ? 0.16 : NT <= 64 ? 0.27 : 0.42;
+    const int groups = (p.kb + J - 1) / J;
+    const auto rooms = cluster_rooms<NT>(di.device);
     double best = 1e30;
-    for (int s : {1, 2, 4}) {
-        const int room = s == 1 ? di.num_sms : s == 2 ? di.num_sms / 2 * 2 : di.num_sms / 4 * 4 - 8;
-        if (s > 1 && p.kb < 8 * s) break;
-        for (int r = 128; r >= 8; r -= 8) {
-            const int64_t ctas = int64_t(s) * ((p.N + r - 1) / r);
-            if (s > 1 && ctas > room) continue;
-            const int64_t rounds = (ctas + di.num_sms - 1) / di.num_sms;
-            const double cost = static_cast<double>(rounds) * ((p.kb + s - 1) / s) * std::max(r, 64) + (s > 1 ? 300.0 : 0.0);
-            if (cost < best * 0.999) {
-                best = cost;
+    for (int r = 128; r >= 8; r -= 8) {
+        const int tiles = (p.N + r - 1) / r;
+        for (int s = 1; s <= kMaxSplit && s <= groups; ++s) {
+            if (s > 1 && int64_t(tiles) * s > rooms[s]) continue;
+            const int blocks = std::min(p.kb, (groups + s - 1) / s * J), rounds = s > 1 ? 1 : (tiles + di.num_sms - 1) / di.num_sms;
+            const double total = static_cast<double>(rounds) * blocks;   // of the busiest SM
+            // its share of the read, which fewer SMs do not draw at the whole rate
+            const double read = std::max(static_cast<double>(std::min<int64_t>(int64_t(tiles) * s, di.num_sms)), 140.0) * r * (128.0 / 5.9e6);
+            const double us = std::max(total * block, std::max(0.0, total - 8.0) * read) + (s > 1 ? 1.2 + 0.04 * p.M : 0.0);
+            if (us < best * 0.999) {
+                best = us;
                 p.rows = r;
                 p.split = s;
             }
         }
     }
     p.tiles = (p.N + p.rows - 1) / p.rows;
+    return best;
 }
 
 template <int NT>
 gem_status launch_rows(GemmParams p, const void* W, int64_t K, const void* x, int64_t ldx, const DeviceInfo& di, cudaStream_t stream) {
     gem_status st;
-    plan_rows(&p, di);
+    plan_rows<NT>(&p, di);
     constexpr int J = kGroup<NT>;
     const int groups = (p.kb + J - 1) / J, per = (groups + p.split - 1) / p.split;
     p.chunk = std::min(per * J, kScaleBytes / (kPitch<NT> * 4) / J * J);
     const int stage = J * (p.rows + NT) * 128, after = std::max(0, 16384 - p.rows * 128 - J * NT * 128);
-    const int fixed = 1024 + after + p.chunk * kPitch<NT> * 4 + (p.split > 1 ? NT * 512 : 0);
+    const int fixed = 1024 + after + p.chunk * kPitch<NT> * 4;
     const int64_t grid = p.split > 1 ? int64_t(p.tiles) * p.split : std::min<int64_t>(p.tiles, di.num_sms);
     const int64_t steps = per * ((int64_t(p.tiles) * p.split + grid - 1) / grid);   // of the busiest CTA
     p.stages = static_cast<int>(std::min(std::min<int64_t>(kMaxStages, steps),
                                          (static_cast<int64_t>(di.smem_optin) - fixed - static_cast<int>(sizeof(RowsBarriers)) - 512) / stage));
-    const size_t smem = static_cast<size_t>(fixed + p.stages * stage);
+    const size_t smem = std::max(static_cast<size_t>(fixed + p.stages * stage), static_cast<size_t>(p.split > 1 ? kClusterSmem<NT> : 0));
     p.whole = K % 128 == 0;
     CUtensorMap tmW, tmX;
     const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
@@ -709,15 +751,12 @@ gem_status gem_fp8_gemm(const void* W, const float* ws, int64_t N, int64_t K, co
     if (M <= 64) return launch_rows<64>(p, W, K, x, ldx, di, stream);
     // More rows: tiles of 256, 128 or 64 columns by their time, rounds of 76 pairs x blocks x 0.47, 0.32 or 0.24 us (a
     // smaller tile costs more for its size and less where there are few); up to 128 rows the kernel above where it
-    // takes less: 0.41 us a block and 5 to begin and end, 3 more for a cluster (128 x 2048 x 4096: 13.2 and 7.7 us,
-    // 128 x 5376 x 21504: 40 and 47).
+    // takes less (128 x 21504 x 5376: 31 us and 48, 128 x 5376 x 21504: 38 and 47; 128 x 2048 x 4096: 13 and 7.7).
     const int64_t mt = (M + 255) / 256, pairs = di.num_sms / 2;
     auto tile_us = [&](int bn, double step) { return 4.0 + static_cast<double>((mt * ((N + bn - 1) / bn) + pairs - 1) / pairs) * p.kb * step; };
     const double us256 = tile_us(256, 0.5), us128 = tile_us(128, 0.32), us64 = tile_us(64, 0.24), best = std::min(us256, std::min(us128, us64));
     if (M <= 128) {
-        plan_rows(&p, di);
-        const double rounds = static_cast<double>((int64_t(p.tiles) * p.split + di.num_sms - 1) / di.num_sms);
-        if (rounds * ((p.kb + p.split - 1) / p.split) * 0.41 + (p.split > 1 ? 8.0 : 5.0) <= best) return launch_rows<128>(p, W, K, x, ldx, di, stream);
+        if (plan_rows<128>(&p, di) + 4.5 <= best) return launch_rows<128>(p, W, K, x, ldx, di, stream);
     }
     if (us256 <= best) return launch_tile<256>(p, W, K, x, ldx, di, stream);
     if (us128 <= best) return launch_tile<128>(p, W, K, x, ldx, di, stream);

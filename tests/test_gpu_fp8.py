@@ -291,6 +291,18 @@ def test_gemm_shows_every_product(env):
     assert np.array_equal(y.cpu().numpy().astype(np.float64), fp8.gemm(W, ws, x, xs)[0])
 
 
+@pytest.mark.parametrize("K", [640, 1024, 1536, 2560, 3200, 5376, 9728])
+@pytest.mark.parametrize("M", [1, 16, 31, 64, 127])
+def test_gemm_clusters_of_every_size(env, M, K):
+    """Few rows of W and long ones: clusters of one to eight CTAs, whose parts lie where their operands were."""
+    for N in (40, 200, 2560):
+        W, ws, x, xs = _operands(M, K, N, M + K)
+        want, most = fp8.gemm(W, ws, x, xs)
+        got = [_product(env, W, ws, x, xs).cpu().numpy() for _ in range(3)]
+        assert np.all(np.abs(got[0] - want) <= _tol(K, most))
+        assert all(np.array_equal(g, got[0]) for g in got)
+
+
 @pytest.mark.parametrize("M", [3, 50, 100, 260])
 def test_gemm_strides_and_residual_in_place(env, M):
     gem, t = env
@@ -497,11 +509,11 @@ def test_gemm_wait_that_runs_out_is_reported(env, M, K, N):
     assert np.all(np.abs(y.cpu().numpy() - want) <= _tol(K, most)) and int(status) == 0
 
 
-def test_gemm_clusters_on_three_streams(env):
+def test_gemm_clusters_on_several_streams(env):
     """Calls whose clusters share out K, of different widths, at once: none keeps another's tensor memory from it."""
     gem, t = env
     calls = []
-    for i, (M, K, N) in enumerate([(8, 4096, 640), (24, 4096, 1100), (50, 2048, 384)]):
+    for i, (M, K, N) in enumerate([(8, 4096, 640), (24, 4096, 1100), (50, 2048, 384), (16, 1024, 2048), (100, 8192, 256)]):
         W, ws, x, xs = _operands(M, K, N, i)
         want, most = fp8.gemm(W, ws, x, xs)
         calls.append((want, _tol(K, most), [_dev(t, a) for a in (W, ws, x, xs)], t.zeros(40, M, N, device="cuda"), t.cuda.Stream()))
@@ -518,7 +530,8 @@ def test_gemm_clusters_on_three_streams(env):
 
 
 @pytest.mark.parametrize("call", ["gem.rmsnorm_fp8(x, None, 1e-6, c, s)", "gem.quant_fp8(x, c, s)", "gem.fp8_gemm(c, s[:1], c, s, y)",
-                                  "gem.fp8_gemm(c, s[:1], c.repeat(3, 1), s.repeat(3, 1), y.repeat(3, 1))", "gem.logprobs(x, None, None, x.new_empty(100))"])
+                                  "gem.fp8_gemm(c, s[:1], c.repeat(3, 1), s.repeat(3, 1), y.repeat(3, 1))", "gem.logprobs(x, None, None, x.new_empty(100))",
+                                  "gem.fp8_gemm(c.new_zeros(64, 2048), x.new_ones(1, 16), c.new_zeros(8, 2048), x.new_ones(8, 16), x.new_zeros(8, 64))"])
 def test_first_call_of_a_process_may_be_captured(call):
     """Whatever a call sets up in its process, it sets up without the stream."""
     import os
