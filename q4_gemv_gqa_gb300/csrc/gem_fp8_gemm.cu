@@ -9,18 +9,18 @@
 // fp8_rows_kernel (up to 128 rows of x): the weights are what the call reads, and the rows of W take the 128-row side
 // of the product, the rows of x its 16..128 columns.  The tensor cores read W straight from shared memory, so nothing
 // is unpacked, and a tile may have any multiple of 8 rows of W (the rest of the 128 is whatever lies there, and not
-// used): the height is chosen so that all SMs get the same share.  8 x 5376 x 21504: 19.7 us, 5.9 TB/s of W, 87 % of the
-// copy rate, where it streams; 61 x 21504 x 5376: 23.4 us, of which 17 stream (three CTAs on 128 rows of W; shared memory's
-// bandwidth, for loads, products and scales, is as busy as the copy); 1 x 2048 x 4096: 4.6 us.
+// used): height and CTAs a tile are chosen so that the busiest SM is done first.  8 x 5376 x 21504: 19.7 us, 5.9 TB/s
+// of W, 87 % of the copy rate; 61 x 21504 x 5376: 23.4 us, of which 17 stream (three CTAs on 128 rows of W; loads,
+// products and scales keep shared memory as busy as the copy keeps HBM); 1 x 2048 x 4096: 4.6 us.
 //
 // fp8_tile_kernel (more rows): pairs of CTAs, 256 rows of x by up to 256 of W.  4096 x 5376 x 21504: 388 us,
 // 2.44 PFLOP/s, tensor cores 52 % active.  Without the adds it takes 321 us, without the products 340 to 354, without
 // both 234: reading back and adding 128 x 256 sums for each 128 of K takes as long as their product, and two buffers of
 // tensor memory do not hide all of one behind the other.  Tried and not kept: halves of 128 columns with four buffers
-// (420 us: x is read twice from shared memory), 160 columns with three (407, bound by the L2), W on the 256-row side and 320 columns of x in three buffers (300 rows of x 30 us
-// against 27, 4096 686: smaller buffers wait longer for one another), the next read-back on its way while one is added
-// (no change), 16 adding warps (403), the
-// scales made by warps of their own (445, registers spill), reads of 32 or 64 columns in one (450 to 530, likewise).
+// (420 us: x is read twice from shared memory); 160 columns with three (407, bound by the L2); W on the 256-row side and
+// 320 columns of x in three buffers (686, and 30 us against 27 for 300 rows of x: smaller buffers wait longer for one
+// another); the next read-back on its way while one is added (no change); 16 adding warps (403); the scales made by
+// warps of their own (445, registers spill); reads of 32 or 64 columns in one (450 to 530, likewise).
 #include "gem_tcgen05.cuh"
 
 #include <array>
