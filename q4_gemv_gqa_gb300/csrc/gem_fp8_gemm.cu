@@ -319,10 +319,13 @@ __global__ void __launch_bounds__(kWarps<NT> * 128 + 64) fp8_rows_kernel(const _
 // tensor cores of both read all of them): a product of 256 x BN halves what an SM loads for its share of the
 // results, which would otherwise bound it.  Warps 0..7 scale and add (warp w: lane quarter w % 4, columns
 // w / 4 * BN / 2 and on; a thread has one row of x, so a block's scale is one number), warp 8 loads, warp 9 of
-// the first CTA issues the products of both; the last warpgroup gives its registers to the first two.
+// the first CTA issues the products of both; the last warpgroup gives its registers to the first two.  SPLIT: the two to
+// four pairs of a cluster share the blocks of its one tile (130 x 21504 x 5376: 39 us, 56 by single pairs;
+// 500 x 9728 x 2560: 23 and 28); a kernel of its own, for the other's registers are all in use.
 constexpr int kTileChunk = 8;             // blocks whose x scales a warp holds at a time, twice
 constexpr int kTilePitch = 33;            // of a block's 32 scales: spreads the copies over the banks
 constexpr int kTileScales = 2 * kTileChunk * kTilePitch * 4;
+constexpr int kTileSplit = 4;             // pairs of a cluster at most
 constexpr int kTileWarps = 8;             // that scale and add
 constexpr int kTileThreads = (kTileWarps + 4) * 32;
 constexpr int kTileRegs = 232, kTileRegsLeft = 40;   // 256 * 232 + 128 * 40 = 384 * 168, what the block starts with
@@ -336,6 +339,7 @@ struct TileParams {
     int64_t ldy;
     int N, M, kb;
     int mtiles, tiles;
+    int split;              // pairs of a cluster that share a tile's blocks
     int wide;               // y's rows (and the residual's) start on 16 bytes
     int copy;               // results leave by asynchronous copies: such rows, and no residual
     int* status;
@@ -356,15 +360,17 @@ constexpr int kTileStages = BN > 128 ? 5 : BN > 64 ? 7 : 8;
 template <int BN>
 constexpr int kTileSmem = 1024 + kTileStages<BN> * kTileStage<BN> + kTileWarps * (4096 + kTileScales);
 
-template <int BN>
+template <int BN, bool SPLIT>
 __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmY, const TileParams p) {
     constexpr int CW = BN / (kTileWarps / 4), STAGE = kTileStage<BN>, STAGES = kTileStages<BN>, NB = BN > 128 ? 2 : 4;   // buffers of BN columns of tensor memory
     extern __shared__ uint8_t raw[];
     __shared__ TileBarriers bar;
     uint8_t* ring = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t rank = cluster_rank();
-    const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
+    const uint32_t crank = cluster_rank(), rank = SPLIT ? crank & 1 : crank, lead = SPLIT ? crank & ~1u : 0u;   // the pair's first
+    const int split = SPLIT ? p.split : 1, part = SPLIT ? static_cast<int>(crank >> 1) : 0;
+    const int b0 = SPLIT ? p.kb * part / split : 0, b1 = SPLIT ? p.kb * (part + 1) / split : p.kb;   // the pair's blocks
+    const int pair = static_cast<int>(blockIdx.x) / (2 * split), pairs = static_cast<int>(gridDim.x) / (2 * split);
     volatile int* dead = &bar.dead;
 
     if (tid == 0) {
@@ -397,14 +403,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
         pdl_wait_trigger();
         const uint64_t keep = l2_policy_evict_last();
         const uint32_t extra = blockIdx.x == 0 && (test_inject() & GEM_INJECT_RING_SHORTFALL) ? 16u : 0u;
-        const uint32_t base = smem_u32(ring), full0 = peer_addr(&bar.full[0], 0);
+        const uint32_t base = smem_u32(ring), full0 = peer_addr(&bar.full[0], lead);
         int s = 0;
         uint32_t phase = 1;
         bool ok = true;
         for (int i = 0; i < ntile && ok; ++i) {
             const int t = pair + i * pairs, mt = t % p.mtiles, nt = t / p.mtiles;
             const int m0 = mt * 256 + static_cast<int>(rank) * 128, n0 = nt * BN + static_cast<int>(rank) * (BN / 2);
-            for (int b = 0; b < p.kb; ++b) {
+            for (int b = b0; b < b1; ++b) {
                 if (issued >= STAGES && !warp_wait(&bar.empty[s], phase, p.status, dead)) {
                     ok = false;
                     break;
@@ -426,7 +432,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
         if (rank == 0) {
             constexpr uint32_t idesc = umma_idesc_e4m3(256, BN);
             const uint64_t da0 = umma_desc(smem_u32(ring)), db0 = umma_desc(smem_u32(ring) + 16384);
-            const int total = ntile * p.kb;
+            const int total = ntile * (b1 - b0);
             uint64_t da = da0, db = db0;
             int i = 0, s = 0;
             uint32_t phase = 0;
@@ -436,15 +442,15 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
                 if (!warp_wait(&bar.full[s], phase, p.status, dead)) break;
                 tc_fence_after();
                 umma_e4m3<2>(tmem + d * BN, da, db, idesc);
-                umma_commit<2>(&bar.empty[s]);
-                umma_commit<2>(&bar.dfull[d]);
+                umma_commit<2>(&bar.empty[s], 3u << lead);
+                umma_commit<2>(&bar.dfull[d], 3u << lead);
                 da += STAGE >> 4, db += STAGE >> 4;
                 if (++s == STAGES) s = 0, phase ^= 1, da = da0, db = db0;
             }
             if (i < total) {
                 *dead = 1;
                 // what was issued ends before the tensor memory is given back
-                umma_commit<2>(&bar.done);
+                umma_commit<2>(&bar.done, 3u << lead);
                 (void)mbar_wait(&bar.done, 0, nullptr);
             }
         }
@@ -452,7 +458,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
         regs_take<kTileRegs>();
         const int col = (warp >> 2) * CW;
         const uint32_t from = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + col;
-        const uint32_t empty0 = peer_addr(&bar.dempty[0], 0);
+        const uint32_t empty0 = peer_addr(&bar.dempty[0], lead);
         float* stage = reinterpret_cast<float*>(ring + STAGES * STAGE + warp * 4096);
         float* xs_sh = reinterpret_cast<float*>(ring + STAGES * STAGE + kTileWarps * 4096 + warp * kTileScales);
         pdl_wait_trigger();
@@ -472,8 +478,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
                 }
                 cp_async_commit();
             };
-            request(0, 0);
-            request(kTileChunk, 1);
+            request(b0, 0);
+            request(b0 + kTileChunk, 1);
             // the warp's columns lie in one or two blocks of 128 rows of W, whose scales are requested two blocks ahead
             const int nb = n0 >> 7, last = (p.N - 1) >> 7;
             const float* w0row = p.ws + static_cast<int64_t>(min(nb, last)) * p.kb;
@@ -481,12 +487,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
             uint64_t acc[CW / 2];
 #pragma unroll
             for (int m = 0; m < CW / 2; ++m) acc[m] = 0;
-            float wa0 = __ldg(w0row), wa1 = __ldg(w0row + min(1, p.kb - 1)), wb0 = 0.f, wb1 = 0.f;
-            if (128 % CW) wb0 = __ldg(w0row + to_b), wb1 = __ldg(w0row + to_b + min(1, p.kb - 1));
-            for (int b = 0; b < p.kb; ++b, ++i) {
-                const int c = b & (2 * kTileChunk - 1);
-                if ((b & (kTileChunk - 1)) == 0) {
-                    if (b > 0) {   // the half that is behind takes the blocks after the next ones
+            const int second = min(b0 + 1, p.kb - 1);
+            float wa0 = __ldg(w0row + b0), wa1 = __ldg(w0row + second), wb0 = 0.f, wb1 = 0.f;
+            if (128 % CW) wb0 = __ldg(w0row + to_b + b0), wb1 = __ldg(w0row + to_b + second);
+            for (int b = b0; b < b1; ++b, ++i) {
+                const int c = (b - b0) & (2 * kTileChunk - 1);
+                if ((c & (kTileChunk - 1)) == 0) {
+                    if (b > b0) {   // the half that is behind takes the blocks after the next ones
                         __syncwarp();
                         request(b + kTileChunk, (c / kTileChunk) ^ 1);
                     }
@@ -528,10 +535,18 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
             }
             cp_async_wait<0>();
             if (!ok) break;
+            if constexpr (SPLIT) {   // to where the ring was: all products are done.  [row][column], 16-byte pieces turned by the row
+                const int row = (warp & 3) * 32 + lane;
+#pragma unroll
+                for (int q = 0; q < CW / 4; ++q) {
+                    const float2 lo = pair_get(acc[2 * q]), hi = pair_get(acc[2 * q + 1]);
+                    reinterpret_cast<float4*>(ring)[row * (BN / 4) + ((col / 4 + q) ^ (row & 7))] = make_float4(lo.x, lo.y, hi.x, hi.y);
+                }
+            }
             // out through the warp's piece of shared memory, 32 columns at a time: rows of 128 bytes, whose
             // 16-byte pieces are turned by the row, so that neither side meets itself in a bank
 #pragma unroll
-            for (int c0 = 0; c0 < CW; c0 += 32) {
+            for (int c0 = 0; c0 < (SPLIT ? 0 : CW); c0 += 32) {
                 tma_store_wait_read<0>();   // the elected lane's copies of what stood here before
                 __syncwarp();
 #pragma unroll
@@ -574,6 +589,40 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
         tma_store_wait_read<0>();
     }
     __syncwarp();
+    if constexpr (SPLIT) {
+        // the parts of the cluster's one tile: each CTA adds up a share of its half's rows, in order of k
+        cluster_sync();
+        const int mt = pair % p.mtiles, nt = pair / p.mtiles;
+        if (warp < kTileWarps) {
+            const int first = 128 * part / split, end = 128 * (part + 1) / split;
+            for (int i = first * (BN / 4) + tid; i < end * (BN / 4); i += kTileWarps * 32) {
+                const int row = i / (BN / 4), q = i % (BN / 4);
+                const int m = mt * 256 + static_cast<int>(rank) * 128 + row, n = nt * BN + 4 * q;
+                if (m >= p.M || n >= p.N) continue;
+                const float4* at = reinterpret_cast<const float4*>(ring) + row * (BN / 4) + (q ^ (row & 7));
+                float4 v[kTileSplit];
+#pragma unroll
+                for (int r = 0; r < kTileSplit; ++r)
+                    v[r] = r < split ? ld_peer4(peer_addr(at, 2 * r + rank)) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int r = 1; r < kTileSplit; ++r)
+                    if (r < split) v[0].x += v[r].x, v[0].y += v[r].y, v[0].z += v[r].z, v[0].w += v[r].w;
+                float* to = p.y + m * p.ldy + n;
+                const float* add = p.res ? p.res + m * p.ldy + n : nullptr;
+                if (p.wide && n + 4 <= p.N) {
+                    if (add) {
+                        const float4 a = *reinterpret_cast<const float4*>(add);
+                        v[0].x += a.x, v[0].y += a.y, v[0].z += a.z, v[0].w += a.w;
+                    }
+                    *reinterpret_cast<float4*>(to) = v[0];
+                } else {
+                    const float e[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+                    for (int j = 0; j < 4 && n + j < p.N; ++j) to[j] = add ? e[j] + add[j] : e[j];
+                }
+            }
+        }
+        __syncwarp();
+    }
     tc_fence_before();
     __syncthreads();
     // the copies of both CTAs are counted on the first one's barriers
@@ -614,15 +663,15 @@ int cluster_room(const void* fn, int threads, int s, int device) {
     return 0;
 }
 
-// The same for all sizes and a kernel, asked once a device.
-template <int NT>
-std::array<int, kMaxSplit + 1> cluster_rooms(int device) {
+// For every size of cluster of a kernel; asked once a device.
+template <auto* KERNEL>
+std::array<int, kMaxSplit + 1> cluster_rooms(int threads, int device) {
     static std::mutex mu;
     static std::map<int, std::array<int, kMaxSplit + 1>> known;
     std::lock_guard<std::mutex> lk(mu);
     auto [it, fresh] = known.try_emplace(device);
     if (fresh)
-        for (int s = 2; s <= kMaxSplit; ++s) it->second[s] = cluster_room(reinterpret_cast<const void*>(fp8_rows_kernel<NT>), kWarps<NT> * 128 + 64, s, device);
+        for (int s = 2; s <= kMaxSplit; ++s) it->second[s] = cluster_room(reinterpret_cast<const void*>(KERNEL), threads, s, device);
     return it->second;
 }
 
@@ -636,7 +685,7 @@ double plan_rows(GemmParams* g, const DeviceInfo& di) {
     constexpr int J = kGroup<NT>;
     constexpr double block = NT <= 16 ? 0.12 : NT <= 32 ? 0.16 : NT <= 64 ? 0.27 : 0.42;
     const int groups = (p.kb + J - 1) / J;
-    const auto rooms = cluster_rooms<NT>(di.device);
+    const auto rooms = cluster_rooms<fp8_rows_kernel<NT>>(kWarps<NT> * 128 + 64, di.device);
     double best = 1e30;
     for (int r = 128; r >= 8; r -= 8) {
         const int tiles = (p.N + r - 1) / r;
@@ -691,9 +740,10 @@ gem_status launch_rows(GemmParams p, const void* W, int64_t K, const void* x, in
     return launch_pdl_cluster(fn, dim3(static_cast<unsigned>(grid)), dim3(kWarps<NT> * 128 + 64), smem, stream, args, p.split);
 }
 
-template <int BN>
-gem_status launch_tile(const GemmParams& g, const void* W, int64_t K, const void* x, int64_t ldx, const DeviceInfo& di, cudaStream_t stream) {
+template <int BN, bool SPLIT>
+gem_status launch_tile(const GemmParams& g, int split, const void* W, int64_t K, const void* x, int64_t ldx, const DeviceInfo& di, cudaStream_t stream) {
     TileParams p{};
+    p.split = split;
     p.ws = g.ws, p.xs = g.xs, p.ldxs = g.ldxs, p.res = g.res, p.y = g.y, p.ldy = g.ldy, p.N = g.N, p.M = g.M, p.kb = g.kb, p.status = g.status;
     p.mtiles = (p.M + 255) / 256;
     p.tiles = p.mtiles * ((p.N + BN - 1) / BN);
@@ -705,11 +755,11 @@ gem_status launch_tile(const GemmParams& g, const void* W, int64_t K, const void
     CUtensorMap tmY = tmX;
     p.copy = p.wide && !p.res;
     if (p.copy && (st = make_tensor_map_2d(&tmY, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.y, p.N, p.M, p.ldy * 4, 32, 32, CU_TENSOR_MAP_SWIZZLE_128B)) != GEM_OK) return st;
-    const void* fn = reinterpret_cast<const void*>(fp8_tile_kernel<BN>);
+    const void* fn = reinterpret_cast<const void*>(fp8_tile_kernel<BN, SPLIT>);
     if ((st = ensure_smem(fn, di.device, kTileSmem<BN>)) != GEM_OK) return st;
-    const int pairs = std::min(p.tiles, di.num_sms / 2);
+    const int pairs = split > 1 ? p.tiles * split : std::min(p.tiles, di.num_sms / 2);
     void* args[] = {&tmW, &tmX, &tmY, &p};
-    return launch_pdl_cluster(fn, dim3(static_cast<unsigned>(2 * pairs)), dim3(kTileThreads), kTileSmem<BN>, stream, args, 2);
+    return launch_pdl_cluster(fn, dim3(static_cast<unsigned>(2 * pairs)), dim3(kTileThreads), kTileSmem<BN>, stream, args, 2 * split);
 }
 
 }  // namespace
@@ -749,18 +799,25 @@ gem_status gem_fp8_gemm(const void* W, const float* ws, int64_t N, int64_t K, co
     if (M <= 16) return launch_rows<16>(p, W, K, x, ldx, di, stream);
     if (M <= 32) return launch_rows<32>(p, W, K, x, ldx, di, stream);
     if (M <= 64) return launch_rows<64>(p, W, K, x, ldx, di, stream);
-    // More rows: tiles of 256, 128 or 64 columns by their time, rounds of 76 pairs x blocks x 0.47, 0.32 or 0.24 us (a
-    // smaller tile costs more for its size and less where there are few); up to 128 rows the kernel above where it
-    // takes less (128 x 21504 x 5376: 31 us and 48, 128 x 5376 x 21504: 38 and 47; 128 x 2048 x 4096: 13 and 7.7).
+    // More rows: tiles of 256, 128 or 64 columns by their time, rounds of 76 pairs x blocks x 0.5, 0.32 or 0.24 us (a
+    // smaller tile costs more for its size and less where there are few); where few tiles have many blocks, clusters of two
+    // to four pairs share them out, which costs 4 us for the join.  Up to 128 rows the kernel above where it takes less
+    // (128 x 21504 x 5376: 31 us and 48, 128 x 5376 x 21504: 38 and 47; 128 x 2048 x 4096: 13 and 7.7).
+    struct Choice { double us = 1e30; int bn = 256, split = 1; } best;
     const int64_t mt = (M + 255) / 256, pairs = di.num_sms / 2;
-    auto tile_us = [&](int bn, double step) { return 4.0 + static_cast<double>((mt * ((N + bn - 1) / bn) + pairs - 1) / pairs) * p.kb * step; };
-    const double us256 = tile_us(256, 0.5), us128 = tile_us(128, 0.32), us64 = tile_us(64, 0.24), best = std::min(us256, std::min(us128, us64));
-    if (M <= 128) {
-        if (plan_rows<128>(&p, di) + 4.5 <= best) return launch_rows<128>(p, W, K, x, ldx, di, stream);
+    const auto rooms = cluster_rooms<fp8_tile_kernel<256, true>>(kTileThreads, di.device);
+    for (auto [bn, step] : {std::pair(256, 0.5), std::pair(128, 0.32), std::pair(64, 0.24)}) {
+        const int64_t tiles = mt * ((N + bn - 1) / bn);
+        for (int s = 1; s <= (bn > 64 ? kTileSplit : 1) && (s == 1 || s * 4 <= p.kb); ++s) {
+            if (s > 1 && tiles * 2 * s > rooms[2 * s]) break;
+            const double us = 4.0 + static_cast<double>(s > 1 ? 1 : (tiles + pairs - 1) / pairs) * ((p.kb + s - 1) / s) * step + (s > 1 ? 4.0 : 0.0);
+            if (us < best.us) best = {us, bn, s};
+        }
     }
-    if (us256 <= best) return launch_tile<256>(p, W, K, x, ldx, di, stream);
-    if (us128 <= best) return launch_tile<128>(p, W, K, x, ldx, di, stream);
-    return launch_tile<64>(p, W, K, x, ldx, di, stream);
+    if (M <= 128 && plan_rows<128>(&p, di) + 4.5 <= best.us) return launch_rows<128>(p, W, K, x, ldx, di, stream);
+    if (best.bn == 256) return best.split > 1 ? launch_tile<256, true>(p, best.split, W, K, x, ldx, di, stream) : launch_tile<256, false>(p, 1, W, K, x, ldx, di, stream);
+    if (best.bn == 128) return best.split > 1 ? launch_tile<128, true>(p, best.split, W, K, x, ldx, di, stream) : launch_tile<128, false>(p, 1, W, K, x, ldx, di, stream);
+    return launch_tile<64, false>(p, 1, W, K, x, ldx, di, stream);
 }
 
 }  // extern "C"

@@ -89,9 +89,9 @@ __device__ __forceinline__ void umma_e4m3(uint32_t d, uint64_t a, uint64_t b, ui
             "l"(a), "l"(b), "r"(idesc)
             : "memory");
 }
-// One arrival on `bar` (G 2: on both CTAs' barrier at that place) when the products issued so far are done.
+// One arrival on `bar` (G 2: on the barrier at that place of the CTAs in `mask`) when the products issued so far are done.
 template <int G>
-__device__ __forceinline__ void umma_commit(uint64_t* bar) {
+__device__ __forceinline__ void umma_commit(uint64_t* bar, uint32_t mask = 1) {
     if constexpr (G == 1)
         asm volatile(
             "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
@@ -102,7 +102,7 @@ __device__ __forceinline__ void umma_commit(uint64_t* bar) {
             "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
             " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}\n" ::"r"(
                 smem_u32(bar)),
-            "h"(static_cast<uint16_t>(3))
+            "h"(static_cast<uint16_t>(mask))
             : "memory");
 }
 __device__ __forceinline__ void warp_expect_tx(uint64_t* bar, uint32_t bytes) {
@@ -205,6 +205,11 @@ __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
 __device__ __forceinline__ float ld_peer(uint32_t addr) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_peer4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
     return v;
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {

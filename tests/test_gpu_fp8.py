@@ -292,7 +292,7 @@ def test_gemm_shows_every_product(env):
 
 
 @pytest.mark.parametrize("K", [640, 1024, 1536, 2560, 3200, 5376, 9728])
-@pytest.mark.parametrize("M", [1, 16, 31, 64, 127])
+@pytest.mark.parametrize("M", [1, 16, 31, 64, 127, 130, 300, 513])
 def test_gemm_clusters_of_every_size(env, M, K):
     """Few rows of W and long ones: clusters of one to eight CTAs, whose parts lie where their operands were."""
     for N in (40, 200, 2560):
@@ -485,7 +485,7 @@ def test_layer_in_graphs_and_on_two_streams(env):
 # ---- waits that run out ---------------------------------------------------------------------------------
 
 
-@pytest.mark.parametrize("M,K,N", [(4, 256, 64), (8, 2048, 384), (40, 1024, 700), (3, 4096, 640), (100, 2560, 19456), (300, 512, 512), (600, 1008, 1201)])
+@pytest.mark.parametrize("M,K,N", [(4, 256, 64), (8, 2048, 384), (40, 1024, 700), (3, 4096, 640), (100, 2560, 19456), (300, 512, 512), (600, 1008, 1201), (300, 4096, 512)])
 def test_gemm_wait_that_runs_out_is_reported(env, M, K, N):
     """The first stage of CTA 0 expects 16 bytes more than it gets: every wait behind it gives up after the limit, the
     call ends and says so, and the next one is right."""
