@@ -591,11 +591,11 @@ GEM_API gem_status gem_quant_fp8(const float *x, int64_t ldx, const float *up, i
  *   (GEM_ERR_UNSUPPORTED_SHAPE); M, N, K < 2^31.  Rows of y whose base and stride are multiples of 16
  *   bytes are written fastest.
  *   The products of a block are summed on the tensor cores (tcgen05, fp32 accumulation); the blocks' sums
- *   are scaled and added in fp32 in order of k (where few rows of x share out K over a cluster, its parts
- *   in order).  A NaN code or scale makes NaN of the results that it takes part in.
+ *   are scaled and added in fp32 in order of k (where a cluster's CTAs share out K, each its part, and the
+ *   parts in order).  A NaN code or scale makes NaN of the results that it takes part in.
  *   W, like every weight of the library, may be read while the kernel before this one on the stream ends:
- *   that kernel must not be the one that writes W (an event, a synchronisation or another launch between
- *   them will do).
+ *   that kernel must not be the one that writes W (a synchronisation or another launch between them will
+ *   do).
  *   A wait that runs out sets GEM_DEVFLAG_TIMEOUT in *status (nullable: the library's word); y is then
  *   unspecified.  No workspace.  Deterministic.
  */
