@@ -64,9 +64,9 @@ template <int NT>
 constexpr int kColumns = kBuffers<NT> * kGroup<NT> * NT;
 // A cluster's CTAs hold their columns until all of them are done, and an allocation waits for as long as it has to: were
 // two clusters on the same SMs, each with the columns that the other's second CTA wants, both would wait for ever (two
-// streams are enough).  So the CTAs of a cluster take at least so much shared memory that those which fit an SM fit in
-// tensor memory too: two of up to 16 rows of x (256 columns), which have two stages or more of 64 rows of W or more, or
-// a wider one alone.  Other launches hold columns only while they work.
+// streams are enough).  So the CTAs of a cluster take at least so much shared memory, used or not, that those which fit
+// an SM fit in tensor memory too: two of up to 16 rows of x (256 columns), or a wider one alone.  Other launches hold
+// columns only while they work.
 constexpr int kSmSmem = 228 << 10;
 template <int NT>
 constexpr int kClusterSmem = NT <= 16 ? 2 * kGroup<NT> * (64 + NT) * 128 : 149 << 10;
@@ -359,6 +359,8 @@ template <int BN>
 constexpr int kTileStages = BN > 128 ? 5 : BN > 64 ? 7 : 8;
 template <int BN>
 constexpr int kTileSmem = 1024 + kTileStages<BN> * kTileStage<BN> + kTileWarps * (4096 + kTileScales);
+
+static_assert(kTileSmem<256> + kClusterSmem<16> > kSmSmem && kTileSmem<64> + kClusterSmem<16> > kSmSmem);   // (as above)
 
 template <int BN, bool SPLIT>
 __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmY, const TileParams p) {
