@@ -633,16 +633,20 @@ def fp8_gemm(W: torch.Tensor, w_scales: torch.Tensor, x: torch.Tensor, x_scales:
 
 def logprobs(y: torch.Tensor, tokens: torch.Tensor | None, logp: torch.Tensor | None, entropy: torch.Tensor | None = None,
              rank: torch.Tensor | None = None, idx: torch.Tensor | None = None, val: torch.Tensor | None = None,
-             scale: float = 1.0, status: torch.Tensor | None = None, stream=None) -> None:
+             scale: float = 1.0, status: torch.Tensor | None = None, stream=None,
+             workspace: torch.Tensor | None = None) -> None:
     """Scores of the logit rows y (fp32 [T, N]): logp, entropy fp32 and rank int32 [T] of the tokens int32 [T]
     (-1: none), and the k alternatives idx int32, val fp32 [T, k] with their log probabilities.  Outputs that are
-    None are not computed."""
+    None are not computed.  workspace: uint8 bytes, as for the other calls with scratch; the call needs none and leaves
+    them as they are."""
     dev = torch._C._cuda_getDevice()
     N = y.shape[-1]
     yp, ldy, T = _rows(y, N, "y", dev)
     f32, i32 = torch.float32, torch.int32
     if (idx is None) != (val is None):
         raise ValueError("idx and val come together")
+    if workspace is not None:
+        _here(workspace, torch.uint8, "workspace", workspace.shape, dev)
     k = 0 if idx is None else idx.shape[-1]
     st = lib.gem_logprobs(yp, ldy, T, N, scale, None if tokens is None else _here(tokens, i32, "tokens", (T,), dev),
                           None if logp is None else _here(logp, f32, "logp", (T,), dev), None if rank is None else _here(rank, i32, "rank", (T,), dev),
