@@ -227,7 +227,7 @@ def run(s):
         return [s["codes"], s["scales"]]
     if op == "gemm":
         return gem.fp8_gemm(s["w"], s["ws"], s["x"], s["xs"], s["y"], residual=s["res"])
-    gem.logprobs(s["y"], s["tokens"], s["logp"], s["entropy"], s["rank"], s["idx"], s["val"])
+    gem.logprobs(s["y"], s["tokens"], s["logp"], s["entropy"], s["rank"], s["idx"], s["val"], workspace=s["scratch"])
     return [s["logp"], s["entropy"], s["rank"]] + ([s["idx"], s["val"]] if s["k"] else [])
 
 
