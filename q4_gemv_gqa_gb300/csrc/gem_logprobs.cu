@@ -210,8 +210,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
         above += count && is_above(v, i);
         if (k && (v > -INFINITY || (v == v && tid < head))) sh.held[atomicAdd(&sh.n, 1)] = key_of(v, i);
     }
-    // of entries before the given token equal ones are above it too
-    const float bound_before = target, bound_after = nextafterf(target, INFINITY);
+    // of entries before the given token equal ones are above it too; behind it nothing is above +inf, and a NaN bars all
+    const float bound_before = target, bound_after = target == INFINITY ? __int_as_float(0x7fffffff) : nextafterf(target, INFINITY);
     int turn = 0, look_at = k == 0 ? 1 << 30 : k > W ? 0 : 1;
     for (int at = 0; at < len; at += THREADS * kVec, ++turn) {
         float x[4 * kVec];
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
                 for (int j = 0; j < 4 * kVec; ++j) above += (valid >> j & 1) && is_above(pick(x, j), index(j));
             } else {
                 const float bound = tok >= high ? bound_before : bound_after;
-                if (!(most < bound)) above += __popc(at_least(bound) & valid);
+                if (most >= bound) above += __popc(at_least(bound) & valid);
             }
         }
         if (k == 0) continue;

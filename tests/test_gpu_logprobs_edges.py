@@ -20,3 +20,22 @@ def test_a_workspace_may_be_given(env):  # noqa: F811
     for bad in (scratch.float(), scratch.cpu(), scratch[::2]):
         with pytest.raises(ValueError):
             _run(env, y, [0, 1, 2, 3, 4], 7, workspace=bad)
+
+
+@pytest.mark.parametrize("T", [1, 3, 6, 400])
+@pytest.mark.parametrize("N", [5000, 30000, 100001])
+def test_rank_of_one_of_several_infinite_tokens(env, T, N):  # noqa: F811
+    """Equal entries go by lowest index, +inf among them, wherever in the row they lie."""
+    T = T if N < 100000 else min(T, 40)
+    y = _logits(T, N, 11)
+    at = [5, 17, N // 7, N // 2, N // 2 + 3, N - 2]
+    y[:, at] = np.inf
+    y[:, N // 3] = np.nan
+    for q in range(0, 6, 1 if T < 10 else 3):
+        tokens = [at[(q + t) % 6] for t in range(T)]
+        got = _run(env, y, tokens, 8)
+        assert got["rank"].tolist() == [1 + (q + t) % 6 for t in range(T)]
+        assert (got["idx"][:, :6] == at).all()
+        assert np.isnan(got["logp"]).all() and np.isnan(got["val"]).all() and np.isnan(got["entropy"]).all()
+    y[:, N // 3], y[:, at[1:]] = 0, 0
+    _check(_run(env, y, [N // 3] * T, 3), y, [N // 3] * T, 3)
