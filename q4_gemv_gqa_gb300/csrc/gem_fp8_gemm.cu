@@ -168,6 +168,7 @@ __global__ void __launch_bounds__(kWarps<NT> * 128 + 64) fp8_rows_kernel(const _
         uint64_t da = da0, db = db0;
         int i = 0, s = 0, b = b0;
         uint32_t phase = 0;
+        pdl_wait();   // the rows of x come behind it: its time is none of the bounded waits'
         for (; i < total; ++i) {
             const int d = i % NB, nj = min(J, b1 - b);
             if (i >= NB && !warp_wait(&bar.dempty[d], static_cast<uint32_t>((i / NB - 1) & 1), p.status, dead)) break;
@@ -438,6 +439,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
             uint64_t da = da0, db = db0;
             int i = 0, s = 0;
             uint32_t phase = 0;
+            pdl_wait();   // (as above)
             for (; i < total; ++i) {
                 const int d = i & (NB - 1);
                 if (i >= NB && !warp_wait(&bar.dempty[d], static_cast<uint32_t>((i / NB - 1) & 1), p.status, dead)) break;
