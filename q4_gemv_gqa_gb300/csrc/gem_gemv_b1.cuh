@@ -219,6 +219,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) q4_0_gemv_b1_kernel(const __gr
                         const int g0 = ph * gps;
                         const int ng = min(gps, Gr - g0);
                         if (s >= ns) {
+                            if (s == ns) pdl_wait();   // as the consumers do before they free a slot
                             ok = mbar_wait(&empty[slot], par, p.status);
                             if (!ok) break;
                         }

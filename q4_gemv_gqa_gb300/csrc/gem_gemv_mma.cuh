@@ -198,6 +198,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) q4_0_gemv_mma_kernel(const __g
                     const int g0 = ph * p.gps;
                     const int ng = min(p.gps, p.G - g0);
                     if (s >= p.ns) {
+                        if (s == p.ns) pdl_wait();   // as the consumers do before they free a slot
                         ok = mbar_wait(&empty[slot], par, p.status);
                         if (!ok) break;
                     }

@@ -127,6 +127,7 @@ __global__ void __launch_bounds__((kQ8mWarps + 1) * 32, 1) q8_0_gemv_mma_kernel(
             for (int64_t tl = blockIdx.x; tl < ntiles && ok; tl += gridDim.x) {
                 const int64_t r0 = tl * kQ8mRows;
                 for (int c = 0; c < p.nchunk; ++c) {
+                    if (s == ns) pdl_wait();   // as the consumers do before they free a slot
                     if (s >= ns && !(ok = mbar_wait(&empty[slot], par, p.status))) break;
                     // boxes of 8 blocks (K % 256 == 0: whole boxes); rows past N arrive as zeros
                     // and count toward the bytes like the others

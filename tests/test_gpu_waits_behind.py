@@ -53,3 +53,37 @@ def test_block_scaled_product(env, long_kernel, M, K, N):  # noqa: F811
     assert _behind(env, long_kernel, lambda: gem.fp8_gemm(*d, y)) == 0
     want, most = fp8.gemm(W, ws, x, xs)
     assert np.all(np.abs(y.cpu().numpy() - want) <= _tol(K, most))
+
+
+def _blocks(t, N, K, size):
+    """Weights of N rows in blocks of 32 values and `size` bytes, each with a scale of 2^-7."""
+    W = t.randint(0, 256, (N, K // 32, size), generator=t.Generator(device="cuda").manual_seed(0), device="cuda", dtype=t.uint8)
+    W[:, :, 0], W[:, :, 1] = 0, 0x20
+    return W.view(-1)
+
+
+@pytest.mark.parametrize("B", [1, 2, 4, 8, 16, 32])
+@pytest.mark.parametrize("K,N", [(5376, 21504), (21504, 5376)])
+def test_q4_0_products(env, long_kernel, B, K, N):  # noqa: F811
+    gem, t = env
+    W, x, y = _blocks(t, N, K, 18), t.randn(B, K, device="cuda"), t.zeros(B, N, device="cuda")
+    calls = [lambda: gem.q4_0_gemm(W, None, N, K, x, y), lambda: gem.q4_0_gemm(W, W, N, K, x, y)]
+    if B <= 8:
+        calls += [lambda: gem.q4_0_gemv(W, N, K, x, y), lambda: gem.q4_0_gemv(W, N, K, x, y, shared_records=True)]
+    for call in calls:
+        call()
+        want = y.clone()
+        assert _behind(env, long_kernel, call) == 0
+        assert t.equal(y, want)
+
+
+@pytest.mark.parametrize("B", [1, 2, 4, 8])
+def test_q8_0_products(env, long_kernel, B):  # noqa: F811
+    gem, t = env
+    N, K = 65536, 5376
+    W, x, y = _blocks(t, N, K, 34), t.randn(B, K, device="cuda"), t.zeros(B, N, device="cuda")
+    call = lambda: gem.q8_0_gemv(W, N, K, x, y)  # noqa: E731
+    call()
+    want = y.clone()
+    assert _behind(env, long_kernel, call) == 0
+    assert t.equal(y, want)
