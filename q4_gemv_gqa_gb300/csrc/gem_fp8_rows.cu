@@ -245,7 +245,9 @@ constexpr double kGelu3 = kGelu1 * 0.044715;
 
 // act(x) * u of four values, and a bound of their relative error: 9.5e-7, and for GELU, whose z is itself off by 2^-22
 // of it, 2.4e-7 max(-z, 1/2) more (above 0 the gate's own flatness holds z's error down).  e^-z is 2^(a + b), a + b = -z log2(e) as a pair, so that its error stays
-// 2^-22 for any z; then a reciprocal and two products.
+// 2^-22 for any z; then a reciprocal and two products.  The gate meets up first: it is far from 1 only where x is between
+// -83 and 17, so wherever y counts (above 2^-118, the lowest border of a code) the gate times up is a normal number, or up
+// itself.  The gate times x is not, with a tiny x and a large up.
 template <int ACT>
 __device__ __forceinline__ Four gated(Four x, Four u, float& err) {
     Four z = x;
@@ -275,7 +277,7 @@ __device__ __forceinline__ Four gated(Four x, Four u, float& err) {
     // e (1 + b ln 2) + 1; at z = -200 e is infinite and b tiny, and its inverse 0
     e = fma4(e, fma4(b, four(0.6931471805599453f), four(1.f)), four(1.f));
     const Four r{make_float2(inverse(e.a.x), inverse(e.a.y)), make_float2(inverse(e.b.x), inverse(e.b.y))};
-    return x * r * u;
+    return x * (r * u);
 }
 template <int ACT>
 __device__ __noinline__ double gated64(float x, float u) {

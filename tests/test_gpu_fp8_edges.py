@@ -1,0 +1,34 @@
+"""The 8-bit floating-point path at the edges of its calls: values, scales and strides at the ends of their ranges."""
+import numpy as np
+import pytest
+
+from oracle import fp8
+from test_gpu_fp8 import _check_rows, _dev, _operands, _product, _rows, _tol, _u8, env  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def _gated(env, x, up, act):  # noqa: F811
+    gem, t = env
+    codes, scales = _rows(t, *x.shape)
+    gem.quant_fp8(_dev(t, x), codes, scales, up=_dev(t, up), act=act)
+    return codes, scales
+
+
+@pytest.mark.parametrize("act", [0, 1])
+def test_gate_of_values_whose_product_with_it_is_below_the_least_normal_one(env, act):  # noqa: F811
+    """Blocks of tiny x (or of a tiny gate, or of tiny up) with factors that bring them back."""
+    r = np.random.RandomState(act)
+    T, H = 240, 256
+    x, up = np.zeros((2, T, H), np.float32)
+    x[:80] = (r.randint(1, 1 << r.randint(1, 23), (80, H)) * 2.0 ** -149).astype(np.float32)
+    up[:80] = (r.randn(80, H) * np.exp2(r.uniform(60, 120, (80, 1)))).astype(np.float32)
+    x[80:160] = r.uniform(*((-82.9, -75) if act == 0 else (-9.8, -9.4)), (80, H))
+    up[80:160] = (r.randn(80, H) * np.exp2(r.uniform(30, 120, (80, 1)))).astype(np.float32)
+    x[160:] = np.abs(r.randn(80, H) * np.exp2(r.uniform(50, 120, (80, 1)))).astype(np.float32)
+    up[160:] = (r.randint(1, 1 << 20, (80, H)) * 2.0 ** -149).astype(np.float32)
+    x[0], up[0] = 3 * 2.0 ** -149, 1e30
+    codes, scales = _gated(env, x, up, act)
+    y = fp8.gated(x, up, act)
+    assert (np.abs(y).max(1) >= 2.0 ** -100).sum() > 200
+    _check_rows(codes, scales, y)
