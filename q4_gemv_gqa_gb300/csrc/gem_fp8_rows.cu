@@ -239,7 +239,8 @@ struct QuantParams {
 };
 
 constexpr int kPlain = 2;            // ACT: 0 SiLU, 1 GELU-tanh, 2 the row itself
-constexpr float kGateLow = -83.f;    // the gate is 0 below it (e^83 is still finite in fp32)
+constexpr float kGateLow = -83.f;    // the gate is 0 for z below it (e^83 is still finite in fp32)
+constexpr float kGeluLow = -9.809149f;   // the least x whose exact z for GELU is not: z in fp32 falls on the wrong side next to it
 constexpr double kGelu1 = 1.5957691216057308;                  // 2 sqrt(2 / pi)
 constexpr double kGelu3 = kGelu1 * 0.044715;
 
@@ -253,8 +254,8 @@ __device__ __forceinline__ Four gated(Four x, Four u, float& err) {
     Four z = x;
     if (ACT == 1) z = x * fma4(x * x, four(static_cast<float>(kGelu3)), four(static_cast<float>(kGelu1)));
     // beyond these the gate is 0 or 1 all the same (and so for a NaN, which the product with x keeps)
-    auto held = [](float v) { return v >= kGateLow ? fminf(v, 100.f) : -200.f; };
-    z = {make_float2(held(z.a.x), held(z.a.y)), make_float2(held(z.b.x), held(z.b.y))};
+    auto held = [](float v, float x) { return x >= (ACT == 1 ? kGeluLow : kGateLow) ? fminf(v, 100.f) : -200.f; };
+    z = {make_float2(held(z.a.x, x.a.x), held(z.a.y, x.a.y)), make_float2(held(z.b.x, x.b.x), held(z.b.y, x.b.y))};
     err = 9.5e-7f;
     if (ACT == 1) {
         auto depth = [](float v) { return v > -150.f ? -v : 0.f; };   // a gate of 0 is exact

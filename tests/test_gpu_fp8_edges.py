@@ -32,3 +32,15 @@ def test_gate_of_values_whose_product_with_it_is_below_the_least_normal_one(env,
     y = fp8.gated(x, up, act)
     assert (np.abs(y).max(1) >= 2.0 ** -100).sum() > 200
     _check_rows(codes, scales, y)
+
+
+@pytest.mark.parametrize("act", [0, 1])
+def test_gate_at_its_lower_end(env, act):  # noqa: F811
+    """The values on either side of z = -83, a block of each: zeros below it, e^-83 of x at it."""
+    end = np.float32(-83) if act == 0 else np.float32(-9.809149)
+    x = (np.full(64, end).view(np.int32) + np.arange(-32, 32)).astype(np.int32).view(np.float32)
+    x = np.repeat(x[:, None], 128, 1)
+    up = np.exp2(np.resize(np.arange(40, 120, dtype=np.float32), x.shape))
+    y = fp8.gated(x, up, act)
+    assert 20 < (y != 0).any(1).sum() < 44
+    _check_rows(*_gated(env, x, up, act), y)
