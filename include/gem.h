@@ -570,7 +570,8 @@ GEM_API gem_status gem_rmsnorm_fp8(const float *x, int64_t ldx, const float *res
 /*
  * Rows in 8 bits: of the gated activation (up set) or of x itself (up NULL).
  *   y[t][i] = up ? act(x[t][i]) * up[t][i] : x[t][i], in 8 bits as above; act as gem_swiglu, taken as
- *   x / (1 + e^-z) with z = x (silu) or 2 sqrt(2/pi) (x + 0.044715 x^3) (gelu_tanh); 0 where z < -83.
+ *   x / (1 + e^-z) with z = x (silu) or 2 sqrt(2/pi) (x + 0.044715 x^3) (gelu_tanh); 0 for finite x
+ *   with z < -83.  An infinite or NaN x or up makes its block's scale NaN, whatever it is multiplied by.
  *   x [T][ldx], up [T][ldu] fp32, 16-byte aligned, strides multiples of 4 values (the two halves of a
  *   merged projection's rows will do).  codes, scales, T as gem_rmsnorm_fp8; H a multiple of 16,
  *   at most 2^24.  codes and scales must not overlap x or up.

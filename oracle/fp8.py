@@ -65,7 +65,7 @@ def gated(x, up, act):
     x, up = x.astype(np.float64), up.astype(np.float64)
     z = x if act == 0 else 2 * math.sqrt(2 / math.pi) * (x + 0.044715 * x ** 3)
     with np.errstate(over="ignore", invalid="ignore"):
-        return np.where(z < -83, 0.0 * up, x * up / (1 + np.exp(-z)))
+        return np.where(z < -83, 0.0 * x * up, x * up / (1 + np.exp(-z)))
 
 
 def gemm(W, ws, x, xs, residual=None):

@@ -44,3 +44,19 @@ def test_gate_at_its_lower_end(env, act):  # noqa: F811
     y = fp8.gated(x, up, act)
     assert 20 < (y != 0).any(1).sum() < 44
     _check_rows(*_gated(env, x, up, act), y)
+
+
+@pytest.mark.parametrize("act", [0, 1])
+def test_infinite_gate_and_up(env, act):  # noqa: F811
+    """A block with an infinity or a NaN on either side has no scale, whatever it meets; the others keep theirs."""
+    r = np.random.RandomState(9)
+    x, up = r.randn(12, 384).astype(np.float32), r.randn(12, 384).astype(np.float32)
+    bad = np.zeros((12, 3), bool)
+    for t, (a, b) in enumerate([(np.inf, 1), (-np.inf, 1), (np.nan, 1), (1, np.inf), (1, -np.inf), (1, np.nan), (-np.inf, 0), (np.inf, 0),
+                                (-200, np.inf), (0, np.inf), (-np.inf, np.inf)]):
+        x[t, 128 * (t % 3) + 7 * t], up[t, 128 * (t % 3) + 7 * t] = a, b
+        bad[t, t % 3] = True
+    codes, scales = _gated(env, x, up, act)
+    assert np.array_equal(np.isnan(scales.cpu().numpy()), bad)
+    with np.errstate(invalid="ignore"):
+        _check_rows(codes, scales, fp8.gated(x, up, act))
