@@ -543,7 +543,7 @@ GEM_API gem_status gem_kv4_attn(const float *q, int64_t ldq, int64_t T, const in
  * block of 128 (the last block may be shorter).  For a block with largest magnitude m
  *     scale = the smallest power of two with m <= 448 * scale,   code = e4m3(value / scale),
  * rounded to nearest even; dividing by a power of two rounds nothing, so a code depends on the value
- * alone.  m < 2^-100: scale 0, codes 0.  m not finite: scale NaN, codes 0.
+ * alone.  m < 2^-100: scale 0, codes 0.  m NaN or past fp32's largest number: scale NaN, codes 0.
  * A layer on T rows: gem_rmsnorm_fp8, gem_fp8_gemm (QKV), attention, gem_quant_fp8, gem_fp8_gemm (O);
  * gem_rmsnorm_fp8, gem_fp8_gemm (gate and up as one matrix), gem_quant_fp8, gem_fp8_gemm (down).
  */

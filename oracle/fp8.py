@@ -38,7 +38,7 @@ def quantise(y: np.ndarray):
         v = y[:, 128 * b:128 * b + 128]
         for t in range(T):
             m = np.max(np.abs(v[t]))
-            if not np.isfinite(m):
+            if not m <= np.finfo(np.float32).max:
                 scales[t, b] = np.nan
             elif m >= 2.0 ** -100:
                 k = math.frexp(m)[1] - 10

@@ -12,3 +12,10 @@ def test_gate_of_what_is_not_finite(act):
     up = np.array([[1, 1, 1, np.inf, np.nan, 0, np.inf, -np.inf, 5, 5]], np.float32)
     y = fp8.gated(x, up, act)
     assert not np.isfinite(y[0, :8]).any() and np.array_equal(y[0, 8:], [0, 0])
+
+
+def test_scales_end_with_the_largest_number():
+    y = np.zeros((2, 256))
+    y[0, 3], y[1, 3] = np.finfo(np.float32).max, -2.0 ** 128
+    codes, scales = fp8.quantise(y)
+    assert scales[0, 0] == 2.0 ** 120 and np.isnan(scales[1, 0]) and not codes[1].any() and not scales[:, 1].any()

@@ -60,3 +60,14 @@ def test_infinite_gate_and_up(env, act):  # noqa: F811
     assert np.array_equal(np.isnan(scales.cpu().numpy()), bad)
     with np.errstate(invalid="ignore"):
         _check_rows(codes, scales, fp8.gated(x, up, act))
+
+
+@pytest.mark.parametrize("act", [0, 1])
+def test_gated_values_past_the_largest_number(env, act):  # noqa: F811
+    """Finite x and up whose product fp32 does not hold: the block has no scale.  Up to there it has."""
+    x, up = np.full((40, 256), 3.0, np.float32), np.ones((40, 256), np.float32)
+    x[:, 5] = np.exp2(np.arange(100, 120, 0.5)).astype(np.float32)
+    up[:, 5] = -1.5 * 2.0 ** 17
+    codes, scales = _gated(env, x, up, act)
+    assert 10 < np.isnan(scales.cpu().numpy()[:, 0]).sum() < 30 and np.isfinite(scales.cpu().numpy()[:, 1]).all()
+    _check_rows(codes, scales, fp8.gated(x, up, act))
