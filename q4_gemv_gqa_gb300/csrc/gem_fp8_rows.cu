@@ -111,10 +111,13 @@ __device__ __forceinline__ Pair inv_rms(Pair s, Pair one_h, float eps) {
     const float q0 = s.hi * one_h.hi, q1 = fmaf(s.hi, one_h.hi, -q0) + fmaf(s.hi, one_h.lo, s.lo * one_h.hi);
     Pair q = two_sum(q0, eps);
     q.lo += q1;
+    // brought near 1 by a power of 4: the products below then neither overflow nor lose bits
+    const float to = q.hi < 0x1p-60f ? 0x1p64f : q.hi > 0x1p60f ? 0x1p-64f : 1.f, back = q.hi < 0x1p-60f ? 0x1p32f : q.hi > 0x1p60f ? 0x1p-32f : 1.f;
+    q.hi *= to, q.lo *= to;
     const float r = rsqrtf(q.hi), a = r * r, b = fmaf(r, r, -a);
     const float t = fmaf(q.hi, a, -1.f) + fmaf(q.hi, b, q.lo * a);   // q r^2 - 1
     const float c = -0.5f * r * t, hi = r + c;                        // one Newton step, kept as a pair
-    return {hi, (r - hi) + c};
+    return {hi * back, ((r - hi) + c) * back};
 }
 
 // ---- RMSNorm with the residual's addition ------------------------------------------------------

@@ -71,3 +71,29 @@ def test_gated_values_past_the_largest_number(env, act):  # noqa: F811
     codes, scales = _gated(env, x, up, act)
     assert 10 < np.isnan(scales.cpu().numpy()[:, 0]).sum() < 30 and np.isfinite(scales.cpu().numpy()[:, 1]).all()
     _check_rows(codes, scales, fp8.gated(x, up, act))
+
+
+@pytest.mark.parametrize("H", [128, 1280, 5376])
+def test_norm_of_rows_over_the_whole_range(env, H):  # noqa: F811
+    """gamma chosen so that every y is within fp32's last place of a border; rows are one row times powers of two, from squares
+    of 2^-100 to sums of squares next to the largest number."""
+    gem, t = env
+    r = np.random.RandomState(H)
+    base = r.uniform(1, 2, H).astype(np.float32) * r.choice([-1, 1], H)
+    _, y = fp8.rmsnorm(base[None].astype(np.float32), None, None, 0.0)
+    gamma = (r.choice(fp8._MID[70:126], H) / np.abs(y[0])).astype(np.float32)
+    gamma[::128] = (440 / np.abs(y[0, ::128])).astype(np.float32)
+    top = (127 - int(np.ceil(np.log2(4 * H)))) // 2
+    k = np.arange(-48, top + 1)
+    x = (base[None].astype(np.float64) * np.exp2(k.astype(np.float64))[:, None]).astype(np.float32)
+    codes, scales = _rows(t, k.size, H)
+    gem.rmsnorm_fp8(_dev(t, x), _dev(t, gamma), 0.0, codes, scales)
+    _check_rows(codes, scales, fp8.rmsnorm(x, None, gamma, 0.0)[1])
+
+
+def test_norm_of_zeros_with_the_least_eps(env):  # noqa: F811
+    gem, t = env
+    for eps in (1e-6, 1e-30, 1.2e-38, 1e-38, 1e-40, 1e-45):
+        codes, scales = _rows(t, 3, 256)
+        gem.rmsnorm_fp8(t.zeros(3, 256, device="cuda"), None, eps, codes, scales)
+        assert not _u8(codes).any() and not scales.cpu().numpy().any()
