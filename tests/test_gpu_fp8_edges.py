@@ -97,3 +97,18 @@ def test_norm_of_zeros_with_the_least_eps(env):  # noqa: F811
         codes, scales = _rows(t, 3, 256)
         gem.rmsnorm_fp8(t.zeros(3, 256, device="cuda"), None, eps, codes, scales)
         assert not _u8(codes).any() and not scales.cpu().numpy().any()
+
+
+def test_norm_product_with_gamma_past_the_largest_number(env):  # noqa: F811
+    """h * gamma is formed in fp32: a block where it is not finite has no scale, up to there the codes are the exact ones."""
+    gem, t = env
+    r = np.random.RandomState(3)
+    x = (r.uniform(1, 1.9, (4, 512)) * 2.0 ** 50).astype(np.float32)
+    gamma = r.uniform(0.5, 1, 512).astype(np.float32)
+    gamma[128:256] *= np.float32(2.0 ** 77)                 # products up to 1.9 * 2^127
+    gamma[300] = 2.0 ** 78                                  # at least 2^128
+    codes, scales = _rows(t, 4, 512)
+    gem.rmsnorm_fp8(_dev(t, x), _dev(t, gamma), 1e-6, codes, scales)
+    y = fp8.rmsnorm(x, None, gamma, 1e-6)[1]
+    y[:, 300] = np.inf
+    _check_rows(codes, scales, y)
