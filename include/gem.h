@@ -586,7 +586,8 @@ GEM_API gem_status gem_quant_fp8(const float *x, int64_t ldx, const float *up, i
  *   y[m][n] = sum_b xs[m][b] * ws[n / 128][b] * (sum_{k in block b} x[m][k] * W[n][k])  (+ residual[m][n])
  *   W   [N][K] e4m3, rows contiguous;   ws [ceil(N / 128)][ceil(K / 128)] fp32, any values.
  *   x   [M][ldx] e4m3, ldx >= K;  xs [M][ldxs] fp32, ldxs >= ceil(K / 128), any values
- *          (xs * ws is rounded to fp32 before it scales the sum: it loses bits below 2^-126).
+ *          (xs * ws is rounded to fp32 before it scales the sum: it loses bits below 2^-126, and past the
+ *          largest number results are infinite or NaN, that of a block whose sum is 0 too).
  *   y   [M][ldy] fp32, ldy >= N;  residual nullable, [M][ldy], may be y.  y must not overlap the rest.
  *   W and x 16-byte aligned, ldx a multiple of 16 (GEM_ERR_MISALIGNED); K a multiple of 16
  *   (GEM_ERR_UNSUPPORTED_SHAPE); M, N, K < 2^31.  Rows of y whose base and stride are multiples of 16

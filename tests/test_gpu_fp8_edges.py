@@ -112,3 +112,21 @@ def test_norm_product_with_gamma_past_the_largest_number(env):  # noqa: F811
     y = fp8.rmsnorm(x, None, gamma, 1e-6)[1]
     y[:, 300] = np.inf
     _check_rows(codes, scales, y)
+
+
+@pytest.mark.parametrize("M", [3, 40, 100, 300])
+def test_product_of_the_scales_at_its_ends(env, M):  # noqa: F811
+    """xs * ws is formed in fp32: up to its largest number the results are right, past it they are not finite."""
+    K, N = 384, 300
+    W, ws, x, xs = _operands(M, K, N, 5)
+    xs[1], ws[:] = xs[1] / xs[1].max() * 2.0 ** 100, ws / ws.max()
+    ws[1] *= np.float32(2.0 ** 27.9)                        # rows 128 .. 255 of W
+    x[1], W[128:256] = np.where(x[1] % 128 > 32, 8, x[1]), 1    # products of a few 2^-15
+    xs[0], ws[2, 1] = 1.0, 2.0 ** 30
+    xs[2], x[2, 128:256] = 2.0 ** 100, 0                    # nothing of row 2 in block 1
+    y = _product(env, W, ws, x, xs).cpu().numpy()
+    want, most = fp8.gemm(W, ws, x, xs)
+    fine = np.ones((M, N), bool)
+    fine[1, 256:] = fine[2, 256:] = False                   # 2^130
+    assert np.all((np.abs(y - want) <= _tol(K, most))[fine & (most < 3e38)])
+    assert not np.isfinite(y[2, 256:]).any()
