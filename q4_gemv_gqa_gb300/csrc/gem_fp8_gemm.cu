@@ -785,6 +785,7 @@ gem_status gem_fp8_gemm(const void* W, const float* ws, int64_t N, int64_t K, co
         ((reinterpret_cast<uintptr_t>(ws) | reinterpret_cast<uintptr_t>(xs) | reinterpret_cast<uintptr_t>(y) |
           reinterpret_cast<uintptr_t>(residual) | reinterpret_cast<uintptr_t>(status)) & 3))
         return GEM_ERR_MISALIGNED;
+    if (M == 1) ldx = K;   // leads nowhere, and a tensor map takes no stride of 2^40 or more
     DeviceInfo di;
     gem_status st;
     if ((st = device_info(&di)) != GEM_OK) return st;

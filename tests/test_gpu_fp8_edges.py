@@ -130,3 +130,24 @@ def test_product_of_the_scales_at_its_ends(env, M):  # noqa: F811
     fine[1, 256:] = fine[2, 256:] = False                   # 2^130
     assert np.all((np.abs(y - want) <= _tol(K, most))[fine & (most < 3e38)])
     assert not np.isfinite(y[2, 256:]).any()
+
+
+@pytest.mark.parametrize("K", [256, 400])
+def test_one_row_with_any_stride(env, K):  # noqa: F811
+    """The stride of a single row leads nowhere, whatever it is."""
+    gem, t = env
+    W, ws, x, xs = _operands(1, K, 70, 1)
+    d = [_dev(t, a) for a in (W, ws, x, xs)]
+    y = t.zeros(1, 70, device="cuda")
+    far = 1 << 45
+    st = gem.lib.gem_fp8_gemm(d[0].data_ptr(), d[1].data_ptr(), 70, K, d[2].data_ptr(), far, d[3].data_ptr(), far, 1, y.data_ptr(), far,
+                              None, None, t.cuda.current_stream().cuda_stream)
+    assert st == 0
+    want, most = fp8.gemm(W, ws, x, xs)
+    assert np.all(np.abs(y.cpu().numpy() - want) <= _tol(K, most))
+    codes, scales = _rows(t, 1, 256)
+    row = np.random.RandomState(2).randn(1, 256).astype(np.float32)
+    xd = _dev(t, row)
+    assert gem.lib.gem_quant_fp8(xd.data_ptr(), far, xd.data_ptr(), far, 1, 256, 0, codes.data_ptr(), far, scales.data_ptr(), far,
+                                 t.cuda.current_stream().cuda_stream) == 0
+    _check_rows(codes, scales, fp8.gated(row, row, 0))
