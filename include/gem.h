@@ -615,7 +615,7 @@ GEM_API gem_status gem_fp8_gemm(const void *W, const float *ws, int64_t N, int64
  *   entropy[t] = -sum_n p[n] log p[n], p = e^(l - lse), where p[n] = 0 counts 0; nullable.
  *   idx[t][r], val[t][r], r < k: gem_topk's indices and their log probabilities l[idx] - lse; k in
  *              0..64, k <= N (k 0: both may be NULL).
- *   y [T][ldy] fp32, ldy >= N, 1 <= N < 2^31; T < 2^28; scale > 0 and finite.
+ *   y [T][ldy] fp32, ldy >= N, 1 <= N < 2^31; T < 2^28; scale from 2^-100 to 2^100.
  *   tokens     [T] int32; nullable with logp and rank.  -1: none given, logp 0 and rank 0.  Any other value
  *              outside [0, N) sets GEM_DEVFLAG_POS_RANGE, logp NaN and rank 0.
  *   -inf logits (banned tokens) have probability 0.  A row with a NaN or +inf, or of -inf alone: logp,

@@ -29,6 +29,9 @@ constexpr int kMaxTop = 64;
 constexpr int kVec = 4;              // 16-byte loads of a thread in a piece of 16 values
 constexpr int kHeld = 2048;          // keys that may wait to be sorted
 constexpr float kLowest = -3.402823466e38f;
+// Of the scale.  c = scale * log2 e stays finite and normal, and a difference of logits that passes the largest number
+// has no weight at any of them.
+constexpr float kLeastScale = 7.888609052210118e-31f, kMostScale = 1.2676506002282294e30f;   // 2^-100, 2^100
 
 struct ScoreParams {
     const float* y; int64_t ldy;
@@ -370,18 +373,20 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
     sum = sh.all;
     // no finite logit, or one that is not a number
     const float log_s = sum.s > 0.f ? logf(sum.s) : __int_as_float(0x7fffffff);
+    // by halves: the difference of two logits may pass the largest number where its product with the scale does not
+    auto log_of = [&](float v) { return 2.f * (p.scale * (0.5f * v - 0.5f * sum.m)) - log_s; };
     if (tid == 0) {
         if (p.entropy) p.entropy[t] = log_s - 0.6931471805599453f * (sum.e / sum.s);
         if (p.tokens) {
             if (!given && tok != -1) atomicOr(p.status, GEM_DEVFLAG_POS_RANGE);
-            if (p.logp) p.logp[t] = given ? p.scale * (target - sum.m) - log_s : tok == -1 ? 0.f : __int_as_float(0x7fffffff);
+            if (p.logp) p.logp[t] = given ? log_of(target) : tok == -1 ? 0.f : __int_as_float(0x7fffffff);
             if (p.rank) p.rank[t] = given ? sh.total + 1 : 0;
         }
     }
     if (tid < k) {
         const unsigned long long key = sh.top[tid];
         p.idx[t * k + tid] = static_cast<int>(~static_cast<uint32_t>(key));
-        p.val[t * k + tid] = p.scale * (value_of(static_cast<uint32_t>(key >> 32)) - sum.m) - log_s;
+        p.val[t * k + tid] = log_of(value_of(static_cast<uint32_t>(key >> 32)));
     }
 }
 
@@ -394,7 +399,7 @@ gem_status gem_logprobs(const float* y, int64_t ldy, int64_t T, int64_t N, float
                         float* logp, int32_t* rank, float* entropy, int k, int32_t* idx, float* val, int32_t* status,
                         void* stream) {
     using namespace gem;
-    if (T < 0 || N < 1 || k < 0 || k > N || !(scale > 0.f) || !(scale <= 3.402823466e38f)) return GEM_ERR_INVALID_ARG;
+    if (T < 0 || N < 1 || k < 0 || k > N || !(scale >= kLeastScale && scale <= kMostScale)) return GEM_ERR_INVALID_ARG;
     if (k > kMaxTop || N >= (int64_t(1) << 31) || T >= (int64_t(1) << 28)) return GEM_ERR_UNSUPPORTED_SHAPE;
     if (T == 0) return GEM_OK;
     if (!y || ldy < N || (k && (!idx || !val)) || ((logp || rank) && !tokens)) return GEM_ERR_INVALID_ARG;

@@ -39,3 +39,35 @@ def test_rank_of_one_of_several_infinite_tokens(env, T, N):  # noqa: F811
         assert np.isnan(got["logp"]).all() and np.isnan(got["val"]).all() and np.isnan(got["entropy"]).all()
     y[:, N // 3], y[:, at[1:]] = 0, 0
     _check(_run(env, y, [N // 3] * T, 3), y, [N // 3] * T, 3)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 100, 1e20, 0.25, 1e-25, 2.0 ** -100])
+@pytest.mark.parametrize("T,N", [(3, 6001), (9, 30000)])
+def test_scales_and_logits_over_their_whole_range(env, T, N, scale):  # noqa: F811
+    """Differences of logits that pass the type's largest value before they are scaled, and scales at their limits."""
+    y = _logits(T, N, 12)
+    y[1:] = np.clip(y[1:].astype(np.float64) * 2e38, -3.4e38, 3.4e38).astype(np.float32)
+    y[2, ::3] = -np.inf
+    y[2, 4::3] = -3.4028235e38
+    tokens = [4 + 3 * t for t in range(T)]
+    got, want = _run(env, y, tokens, 12, scale), fp8.scores(y, tokens, 12, scale)
+    assert np.array_equal(got["rank"], want["rank"]) and np.array_equal(got["idx"], want["idx"])
+    # one entry has all the weight (a row of ordinary logits: all of them with the small scales, and as little with the large
+    # ones), so that log s is off by 2^-24 (128 + 4 + 4 spread) and the values by two roundings more
+    lse = 2.0 ** -24 * (128 + 4 + 4 * want["spread"])
+    for name, n in (("logp", lse), ("val", lse[:, None])):
+        with np.errstate(over="ignore"):
+            w = want[name].astype(np.float32).astype(np.float64)  # past the largest number: infinite
+        fine = np.isfinite(w)
+        assert np.array_equal(got[name][~fine], w[~fine])
+        assert np.all(np.abs(np.where(fine, got[name] - np.where(fine, w, 0), 0)) <= n + 2.0 ** -22 * np.abs(np.where(fine, w, 0)))
+    assert np.all(np.abs(got["entropy"] - want["entropy"]) <= 2.0 ** -24 * (128 + 4) * (2 + 4 * want["spread"] + want["entropy"]))
+
+
+def test_scales_out_of_range_are_refused(env):  # noqa: F811
+    gem, t = env
+    y, lp = t.zeros(2, 100, device="cuda"), t.zeros(2, device="cuda")
+    tok = t.zeros(2, dtype=t.int32, device="cuda")
+    for scale in (2.0 ** 101, 3e38, 2.0 ** -101, 1e-40):
+        with pytest.raises(gem.GemError):
+            gem.logprobs(y, tok, lp, scale=scale)
