@@ -71,7 +71,7 @@ struct Sums {
 };
 // c = scale * log2 e: e^(scale (a - b)) = 2^(c (a - b))
 __device__ __forceinline__ void raise(Sums& a, float m, float c) {
-    const float d = fmaxf((a.m - m) * c, -1e30f), f = exp2_fast(d);
+    const float d = fmaxf((a.m - m) * c, -1e28f), f = exp2_fast(d);   // a sum of 2^31 times d is finite: it meets an f of 0
     a.e = f * fmaf(a.s, d, a.e);
     a.s *= f;
     a.m = m;

@@ -71,3 +71,17 @@ def test_scales_out_of_range_are_refused(env):  # noqa: F811
     for scale in (2.0 ** 101, 3e38, 2.0 ** -101, 1e-40):
         with pytest.raises(gem.GemError):
             gem.logprobs(y, tok, lp, scale=scale)
+
+
+def test_one_entry_far_above_very_many(env):  # noqa: F811
+    """Sums of 2^29 and more that a far larger entry takes the weight from."""
+    gem, t = env
+    N = 1 << 30
+    y = t.zeros(1, N, device="cuda")
+    y[0, N - 9] = 1e38
+    for rows in (y, t.cat([y] * 5)):
+        T = rows.shape[0]
+        tokens = t.full((T,), N - 9, dtype=t.int32, device="cuda")
+        logp, ent, rank = t.full((T,), -7.0, device="cuda"), t.full((T,), -7.0, device="cuda"), t.zeros(T, dtype=t.int32, device="cuda")
+        gem.logprobs(rows, tokens, logp, ent, rank)
+        assert not logp.any() and not ent.any() and bool((rank == 1).all())
