@@ -85,3 +85,15 @@ def test_one_entry_far_above_very_many(env):  # noqa: F811
         logp, ent, rank = t.full((T,), -7.0, device="cuda"), t.full((T,), -7.0, device="cuda"), t.zeros(T, dtype=t.int32, device="cuda")
         gem.logprobs(rows, tokens, logp, ent, rank)
         assert not logp.any() and not ent.any() and bool((rank == 1).all())
+
+
+@pytest.mark.parametrize("N,k", [(32000, 5), (151669, 20)])
+def test_little_is_added_to_the_last_rounding(env, N, k):  # noqa: F811
+    """In the mean square over many rows: one rounding of the result (a unit of its last place / sqrt 12), and 2^-23 for
+    the sum, whose terms' errors of up to 2^-22 are averaged."""
+    y = _logits(300, N, 13)
+    tokens = np.random.RandomState(14).randint(0, N, 300)
+    got, want = _run(env, y, tokens, k), fp8.scores(y, tokens, k)
+    for name in ("logp", "val"):
+        last = np.spacing(np.abs(want[name]).astype(np.float32)).astype(np.float64)
+        assert np.mean((got[name] - want[name]) ** 2) <= np.mean(last ** 2) / 12 + 2.0 ** -46, name
