@@ -484,16 +484,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
             };
             request(b0, 0);
             request(b0 + kTileChunk, 1);
-            // the warp's columns lie in one or two blocks of 128 rows of W, whose scales are requested two blocks ahead
-            const int nb = n0 >> 7, last = (p.N - 1) >> 7;
-            const float* w0row = p.ws + static_cast<int64_t>(min(nb, last)) * p.kb;
-            const int to_b = nb < last ? p.kb : 0;
+            // the warp's columns lie in one block of 128 rows of W, whose scales are requested two blocks ahead
+            static_assert(128 % CW == 0);
+            const float* wrow = p.ws + static_cast<int64_t>(min(n0, p.N - 1) >> 7) * p.kb;
             uint64_t acc[CW / 2];
 #pragma unroll
             for (int m = 0; m < CW / 2; ++m) acc[m] = 0;
-            const int second = min(b0 + 1, p.kb - 1);
-            float wa0 = __ldg(w0row + b0), wa1 = __ldg(w0row + second), wb0 = 0.f, wb1 = 0.f;
-            if (128 % CW) wb0 = __ldg(w0row + to_b + b0), wb1 = __ldg(w0row + to_b + second);
+            float w0 = __ldg(wrow + b0), w1 = __ldg(wrow + min(b0 + 1, p.kb - 1));
             for (int b = b0; b < b1; ++b, ++i) {
                 const int c = (b - b0) & (2 * kTileChunk - 1);
                 if ((c & (kTileChunk - 1)) == 0) {
@@ -504,11 +501,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
                     cp_async_wait<1>();
                     __syncwarp();
                 }
-                const float x0 = xs_sh[c * kTilePitch + lane], sa = x0 * wa0, sb = 128 % CW ? x0 * wb0 : sa;
-                const int ahead = min(b + 2, p.kb - 1);
-                wa0 = wa1, wb0 = wb1;
-                wa1 = __ldg(w0row + ahead);
-                if (128 % CW) wb1 = __ldg(w0row + to_b + ahead);
+                const uint64_t s2 = pair_of(xs_sh[c * kTilePitch + lane] * w0);
+                w0 = w1;
+                w1 = __ldg(wrow + min(b + 2, p.kb - 1));
                 const int d = i & (NB - 1);
                 if (!warp_wait(&bar.dfull[d], static_cast<uint32_t>((i / NB) & 1), p.status, dead)) {
                     *dead = 1;
@@ -530,11 +525,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp8_tile_kernel(const __grid_
                         if (lane == 0) mbar_arrive_peer(empty0 + 8 * d);
                     }
 #pragma unroll
-                    for (int g = 0; g < G; ++g) {
-                        const uint64_t s2 = pair_of((n0 + 16 * (u + g)) >> 7 == nb ? sa : sb);
+                    for (int g = 0; g < G; ++g)
 #pragma unroll
                         for (int q = 0; q < 8; ++q) pair_fma(acc[8 * (u + g) + q], v[g][2 * q], v[g][2 * q + 1], s2);
-                    }
                 }
             }
             cp_async_wait<0>();
