@@ -717,6 +717,10 @@ gem_status launch_rows(GemmParams p, const void* W, int64_t K, const void* x, in
     const int64_t steps = per * ((int64_t(p.tiles) * p.split + grid - 1) / grid);   // of the busiest CTA
     p.stages = static_cast<int>(std::min(std::min<int64_t>(kMaxStages, steps),
                                          (static_cast<int64_t>(di.smem_optin) - fixed - static_cast<int>(sizeof(RowsBarriers)) - 512) / stage));
+    // a cluster's sums lie where the ring was, and the x scales behind the ring are still read by then (one stage is
+    // too short for 128 rows of x on fewer than 128 of W, two are not)
+    if (p.split > 1) p.stages = std::max(p.stages, (NT * 512 + stage - 1) / stage);
+    static_assert(1024 + 16384 + kScaleBytes + NT * 512 + kGroup<NT> * (128 + NT) * 128 + sizeof(RowsBarriers) + 512 <= 227 << 10);
     const size_t smem = std::max(static_cast<size_t>(fixed + p.stages * stage), static_cast<size_t>(p.split > 1 ? kClusterSmem<NT> : 0));
     p.whole = K % 128 == 0;
     CUtensorMap tmW, tmX;
