@@ -575,7 +575,7 @@ def rmsnorm_fp8(x: torch.Tensor, gamma: torch.Tensor | None, eps: float, codes: 
                 residual: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None):
     """RMSNorm of x (+ residual) in 8 bits: x fp32 [T, H], codes uint8 or float8_e4m3fn [T, >= H], scales fp32
     [T, >= ceil(H / 128)].  out (may be x or residual) receives x + residual."""
-    dev = torch._C._cuda_getDevice()
+    dev = torch.cuda.current_device()
     H = x.shape[-1]
     xp, ldx, T = _rows(x, H, "x", dev)
     rp, ldr, r_rows = (None, 0, T) if residual is None else _rows(residual, H, "residual", dev)
@@ -594,7 +594,7 @@ def quant_fp8(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, up: to
               act: int = ACT_SILU, stream=None):
     """act(x) * up, or x itself (up None), in 8 bits; x, up fp32 [T, H] (column ranges of a wider tensor will
     do), codes and scales as rmsnorm_fp8."""
-    dev = torch._C._cuda_getDevice()
+    dev = torch.cuda.current_device()
     H = x.shape[-1]
     xp, ldx, T = _rows(x, H, "x", dev)
     up_p, ldu, u_rows = (None, 0, T) if up is None else _rows(up, H, "up", dev)
@@ -612,7 +612,7 @@ def fp8_gemm(W: torch.Tensor, w_scales: torch.Tensor, x: torch.Tensor, x_scales:
     """y = x @ W.T (+ residual) of 8-bit rows: W [N, K] e4m3 (uint8 or float8_e4m3fn) with w_scales fp32
     [ceil(N / 128), ceil(K / 128)], x [M, >= K] with x_scales fp32 [M, >= ceil(K / 128)], y and residual (which
     may be y) fp32 [M, >= N] of the same row stride."""
-    dev = torch._C._cuda_getDevice()
+    dev = torch.cuda.current_device()
     if W.dim() != 2 or not W.is_contiguous():
         raise ValueError("W must be contiguous [N, K], got %s strides %s" % (tuple(W.shape), W.stride()))
     N, K = W.shape
@@ -639,7 +639,7 @@ def logprobs(y: torch.Tensor, tokens: torch.Tensor | None, logp: torch.Tensor | 
     (-1: none), and the k alternatives idx int32, val fp32 [T, k] with their log probabilities.  Outputs that are
     None are not computed.  workspace: uint8 bytes, as for the other calls with scratch; the call needs none and leaves
     them as they are."""
-    dev = torch._C._cuda_getDevice()
+    dev = torch.cuda.current_device()
     N = y.shape[-1]
     yp, ldy, T = _rows(y, N, "y", dev)
     f32, i32 = torch.float32, torch.int32
