@@ -403,6 +403,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const
             __syncthreads();
             if (tid == 0) sh.all = sum, sh.total = above;
         }
+        __syncwarp();
         cluster_sync();   // what the others hold has been read
         if (part != 0) return;
         if (k) sort_held(sh, listed, k);
