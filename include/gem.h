@@ -589,8 +589,8 @@ GEM_API gem_status gem_quant_fp8(const float *x, int64_t ldx, const float *up, i
  *          (xs * ws is rounded to fp32 before it scales the sum: it loses bits below 2^-126, and past the
  *          largest number results are infinite or NaN, that of a block whose sum is 0 too).
  *   y   [M][ldy] fp32, ldy >= N;  residual nullable, [M][ldy], may be y.  y must not overlap the rest.
- *   W and x 16-byte aligned, ldx a multiple of 16 (GEM_ERR_MISALIGNED); K a multiple of 16
- *   (GEM_ERR_UNSUPPORTED_SHAPE); M, N, K < 2^31.  Rows of y whose base and stride are multiples of 16
+ *   W and x 16-byte aligned, ldx a multiple of 16 (GEM_ERR_MISALIGNED); K a multiple of 16, M, N and K at
+ *   most 2^31 - 512 (GEM_ERR_UNSUPPORTED_SHAPE); K not 0, unless M or N is.  Rows of y whose base and stride are multiples of 16
  *   bytes are written fastest.
  *   The products of a block are summed on the tensor cores (tcgen05, fp32 accumulation); the blocks' sums
  *   are scaled and added in fp32 in order of k (where a cluster's CTAs share out K, each its part, and the

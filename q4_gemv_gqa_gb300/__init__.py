@@ -611,7 +611,8 @@ def fp8_gemm(W: torch.Tensor, w_scales: torch.Tensor, x: torch.Tensor, x_scales:
              residual: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """y = x @ W.T (+ residual) of 8-bit rows: W [N, K] e4m3 (uint8 or float8_e4m3fn) with w_scales fp32
     [ceil(N / 128), ceil(K / 128)], x [M, >= K] with x_scales fp32 [M, >= ceil(K / 128)], y and residual (which
-    may be y) fp32 [M, >= N] of the same row stride."""
+    may be y) fp32 [M, >= N] of the same row stride.  W is read while the kernel before this one on the stream may still run:
+    a kernel that writes it must not be that one (a synchronisation or another launch between them will do)."""
     dev = torch.cuda.current_device()
     if W.dim() != 2 or not W.is_contiguous():
         raise ValueError("W must be contiguous [N, K], got %s strides %s" % (tuple(W.shape), W.stride()))

@@ -10,11 +10,12 @@
 // of the product, the rows of x its 16..128 columns.  The tensor cores read W straight from shared memory, so nothing
 // is unpacked, and a tile may have any multiple of 8 rows of W (the rest of the 128 is whatever lies there, and not
 // used): height and CTAs a tile are chosen so that the busiest SM is done first.  8 x 5376 x 21504: 19.7 us, 5.9 TB/s
-// of W, 87 % of the copy rate; 61 x 21504 x 5376: 23.4 us, of which 17 stream (three CTAs on 128 rows of W; loads,
+// of W, 87 % of the copy rate; 61 x 21504 x 5376: 23.4 us, of which 17 stream (three CTAs on 120 rows of W; loads,
 // products and scales keep shared memory as busy as the copy keeps HBM); 1 x 2048 x 4096: 4.6 us.
 //
-// fp8_tile_kernel (more rows): pairs of CTAs, 256 rows of x by up to 256 of W.  4096 x 5376 x 21504: 388 us,
-// 2.44 PFLOP/s, tensor cores 52 % active.  Without the adds it takes 321 us, without the products 340 to 354, without
+// fp8_tile_kernel (more rows): pairs of CTAs, 256 rows of x by up to 256 of W.  4096 x 5376 x 21504: 393 us in a burst
+// (2.41 PFLOP/s, tensor cores 52 % active), 416 to 422 in a long run under the power cap.  Without the adds it takes 321 us,
+// without the products 340 to 354, without
 // both 234: reading back and adding 128 x 256 sums for each 128 of K takes as long as their product, and two buffers of
 // tensor memory do not hide all of one behind the other.  Tried and not kept: halves of 128 columns with four buffers
 // (420 us: x is read twice from shared memory); 160 columns with three (407, bound by the L2); W on the 256-row side and
@@ -674,8 +675,9 @@ std::array<int, kMaxSplit + 1> cluster_rooms(int threads, int device) {
 
 // Rows of W a tile and CTAs that share a tile's blocks by their time (returned in us, without beginning and end): the
 // blocks' products and adds, whatever the rows of W, or the read of W but for the first blocks, which are on their way
-// before the call begins.  A cluster costs its joining; of clusters there is one round.  (61 x 21504 x 5376: 3 CTAs on 128 rows 23.7 us, 2 on 72 24.9, 1 on 72 37.9;
-// 16 x 9728 x 2560: 4 on 128 6.8, 3 on 64 8.1, 2 on 64 9.1, 1 on 64 12.6.)
+// before the call begins.  A cluster costs its joining; of clusters there is one round.  (61 x 21504 x 5376: 3 CTAs on 120 rows, which it takes, 23.4 us, 3 on 128 23.7, 2 on 72 24.9,
+// 1 on 72 37.9; 16 x 9728 x 2560, three weights in turn: 5 on 96, which it takes, 7.0, 4 on 128 6.8, 3 on 64 8.1, 2 on 64 9.1,
+// 1 on 64 12.6.)
 template <int NT>
 double plan_rows(GemmParams* g, const DeviceInfo& di) {
     GemmParams& p = *g;

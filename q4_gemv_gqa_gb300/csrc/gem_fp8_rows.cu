@@ -9,9 +9,9 @@
 // which is exact.  The same holds for the scale's own border, 448 * 2^k.
 //
 // Floors are the rows' bytes; what they take besides is instructions (45 to 52 % of the issue slots) between loads
-// that few registers can hold ahead.  GB300: RMSNorm with residual 4096 x 5376 70 us (286 MB, 60 % of the copy rate),
-// 8192 x 2560 60 us (67 %); gated activation 4093 x 9728 70 us (358 MB, 75 %); a plain row 37 us (80 %); a decoding
-// step's rows 2 to 3 us.  Summing in fp32 first and deciding a row again where that leaves a code open took 75 to 98 us
+// that few registers can hold ahead.  GB300: RMSNorm with residual 4096 x 5376 69 us (286 MB, 61 % of the copy rate),
+// 8192 x 2560 59 us (68 %); SiLU 4093 x 9728 70 us (358 MB, 75 %), GELU 72 us (73 %); a plain row 36 us (81 %); a decoding
+// step's rows 2 to 3 us, of more than 32 blocks (8 x 5376) 4.7 us.  Summing in fp32 first and deciding a row again where that leaves a code open took 75 to 98 us
 // (one row of ten) and a second barrier.
 #include <cmath>
 
@@ -400,8 +400,9 @@ gem_status gem_rmsnorm_fp8(const float* x, int64_t ldx, const float* residual, i
                  {one_h_hi, static_cast<float>(one_h - static_cast<double>(one_h_hi))}, 0, codes, ldc, scales, lds};
     const int blocks = static_cast<int>((H + 127) / 128);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // few rows: a block a warp, the shortest chain; else four, in so few registers that three rows are in work on an SM
-    // (4096 x 5376: 68 us; two rows 81; one, with the next row's loads ahead in 122 registers, 76)
+    // few rows: a block a warp, the shortest chain, as far as a CTA's 32 warps go (8 x 2560: 2.6 us); else four, in so few
+    // registers that three rows are in work on an SM (8 x 5376: 4.7 us; 4096 x 5376: 69; two rows 81; one, with the next
+    // row's loads ahead in 122 registers, 76)
     if (blocks <= 32 && T <= di.num_sms) return launch_norm<1, 1024, 1>(p, blocks, s);
     if (blocks <= 48) return launch_norm<4, 384, 3>(p, blocks, s);
     if (blocks <= 128) return launch_norm<4, 1024, 1>(p, blocks, s);

@@ -12,9 +12,10 @@
 // hold enough of them; a row whose numbers run out before that (NaN) is listed again, slowly.  The rank counts values
 // only in pieces whose maximum reaches the given token's logit.
 //
-// Bound by the read of the logits where there are many: 1021 x 262144 takes 199 us (1.07 GB, 79 % of the copy rate; 192
+// Bound by the read of the logits where there are many: 1021 x 262144 takes 200 us (1.07 GB, 79 % of the copy rate; 197
 // without a list).  61 x 151669 with 20 alternatives takes 24 us, 14 of them without a list: ten pieces a CTA, so
-// beginning, listing and joining count; 1 x 262144 9.6 us.  A row is one CTA's, or a cluster's, whose CTAs join their sums and lists
+// beginning, listing and joining count; 1 x 262144 9.8 us with 5 alternatives, 7.2 without a list and 48 with 64, whose
+// 16 parts hand on up to 128 keys each.  A row is one CTA's, or a cluster's, whose CTAs join their sums and lists
 // through shared memory: no workspace, no counters, and an order that depends on the sizes alone.
 #include <cmath>
 #include <mutex>
