@@ -557,7 +557,7 @@ GEM_API gem_status gem_kv4_attn(const float *q, int64_t ldq, int64_t T, const in
  *   gamma  [H] fp32, 16-byte aligned.
  *   codes  [T][ldc] bytes, 16-byte aligned, ldc a multiple of 16;  scales [T][lds] fp32, lds >= ceil(H / 128).
  *          They must not overlap x, residual or out.
- *   eps finite and >= 0.  H a multiple of 16, at most 32768 (GEM_ERR_UNSUPPORTED_SHAPE otherwise); T < 2^31.
+ *   eps from 0 to 2^127.  H a multiple of 16, at most 32768 (GEM_ERR_UNSUPPORTED_SHAPE otherwise); T < 2^31.
  *   The mean square is summed to about 2^-40 and a value next to a border of two codes is decided in
  *   fp64, so the codes are those of the exact y (for squares, and products with gamma, above 2^-100).  A
  *   row whose sum of squares is not finite in fp32 gets NaN scales, a block where h * gamma is not one.

@@ -383,7 +383,7 @@ gem_status gem_rmsnorm_fp8(const float* x, int64_t ldx, const float* residual, i
                            int64_t T, int64_t H, const float* gamma, float eps, uint8_t* codes, int64_t ldc,
                            float* scales, int64_t lds, void* stream) {
     using namespace gem;
-    if (T < 0 || H < 0 || !(eps >= 0.f && eps <= 3.402823466e38f)) return GEM_ERR_INVALID_ARG;
+    if (T < 0 || H < 0 || !(eps >= 0.f && eps <= 0x1p127f)) return GEM_ERR_INVALID_ARG;   // plus any mean square it is finite
     if (H % 16 || H > 32768 || T >= (int64_t(1) << 31)) return GEM_ERR_UNSUPPORTED_SHAPE;
     if (T == 0 || H == 0) return GEM_OK;
     if (!x || ldx < H || (residual && ldr < H) || (out && ldo < H)) return GEM_ERR_INVALID_ARG;

@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 
 from oracle import fp8
+from test_fp8_cpu import D, INVALID, OK, lib  # noqa: F401
 
 
 @pytest.mark.parametrize("act", [0, 1])
@@ -19,3 +20,8 @@ def test_scales_end_with_the_largest_number():
     y[0, 3], y[1, 3] = np.finfo(np.float32).max, -2.0 ** 128
     codes, scales = fp8.quantise(y)
     assert scales[0, 0] == 2.0 ** 120 and np.isnan(scales[1, 0]) and not codes[1].any() and not scales[:, 1].any()
+
+
+@pytest.mark.parametrize("eps,want", [(0.0, OK), (1e-45, OK), (2.0 ** 127, OK), (2.0 ** 127.1, INVALID), (3.4e38, INVALID), (-1e-45, INVALID)])
+def test_eps(lib, eps, want):  # noqa: F811
+    assert lib.gem_rmsnorm_fp8(D, 256, None, 0, None, 0, 0, 256, None, eps, D, 256, D, 2, None) == want

@@ -151,3 +151,14 @@ def test_one_row_with_any_stride(env, K):  # noqa: F811
     assert gem.lib.gem_quant_fp8(xd.data_ptr(), far, xd.data_ptr(), far, 1, 256, 0, codes.data_ptr(), far, scales.data_ptr(), far,
                                  t.cuda.current_stream().cuda_stream) == 0
     _check_rows(codes, scales, fp8.gated(row, row, 0))
+
+
+def test_norm_with_the_largest_eps(env):  # noqa: F811
+    """Beside it a row whose squares' sum is next to the largest number."""
+    gem, t = env
+    r = np.random.RandomState(8)
+    x = (r.randn(3, 256) * np.exp2([[3.0], [40.0], [58.0]])).astype(np.float32)
+    x[2] = np.clip(x[2], -2.0 ** 59.4, 2.0 ** 59.4)
+    codes, scales = _rows(t, 3, 256)
+    gem.rmsnorm_fp8(_dev(t, x), None, 2.0 ** 127, codes, scales)
+    _check_rows(codes, scales, fp8.rmsnorm(x, None, None, 2.0 ** 127)[1])
